@@ -2,13 +2,18 @@
 
 The compute path is the C-ABI library built from ``csrc/`` (TMA + mbarrier
 stage ring + tcgen05/TMEM kernels for sm_103a).  ``binding`` marshals torch
-tensors into that library; it has no fallback of any kind.
+tensors into that library; it has no fallback of any kind.  ``experts`` is
+the same for 4-bit matrices, their product and the routing of tokens to
+experts.
 """
 _EXPORTS = ("gemm_tn_f16", "gemm_tn_f16_ex", "gemm_f16_scaled", "gemm_tn_f16_from_host",
             "get_device_error",
             "minimum_stages", "query_config", "probe_latencies", "library_path", "status_string",
             "GemmError")
-__all__ = list(_EXPORTS)
+_EXPERTS = ("Fp4Matrix", "Routing", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
+            "fp4_scale_bytes", "fp4_get_device_error", "moe_sort", "moe_dispatch",
+            "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+__all__ = list(_EXPORTS + _EXPERTS)
 
 
 def __getattr__(name):
@@ -17,4 +22,7 @@ def __getattr__(name):
     if name in _EXPORTS:
         from . import binding
         return getattr(binding, name)
+    if name in _EXPERTS:
+        from . import experts
+        return getattr(experts, name)
     raise AttributeError(name)
