@@ -1,99 +1,91 @@
-// D[r][n] = alpha * sum_k a[r][k] b[g(r)][n][k] on 4-bit matrices.
-#include <cmath>
+// Host side of fp4_gemm_tn: checks, the choice of tile, tensor maps, launch.
+#include <cuda.h>
 
-#include "fp4.cuh"
+#include <cmath>
+#include <mutex>
+
+#include "fp4_gemm_kernel.cuh"
 
 namespace gb300 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;   // rows and outputs of a block's tile
-constexpr int kDepth = 64;  // columns per step
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-// value of element k of a row: code times block scale
-template <int kFormat>
-__device__ __forceinline__ void decode_row(const Fp4View& v, int64_t row, int64_t tile, int r,
-                                           int64_t k, float (&f)[16]) {
-  const uint2 codes = *reinterpret_cast<const uint2*>(v.codes + row * v.pitch + k / 2);
-  from_e2m1(codes.x, f);
-  from_e2m1(codes.y, f + 8);
-  const float step = scale_value<kFormat>(
-      v.scales[tile * v.tile_bytes + scale_at(r, static_cast<int>(k / block_size(kFormat)))]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] *= step;
+// The first error of the launches on a given stream; 0: none.
+__device__ uint32_t g_fp4_error[kErrorWords];
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+std::mutex g_mu;
+EncodeTiledFn g_encode = nullptr;
+uintptr_t g_word_stream[kErrorWords];
+int g_words_used = 1;
+
+int get_encoder() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_encode) return GEMM_OK;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                       &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess || fn == nullptr) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+  return GEMM_OK;
 }
 
-// A block per 64 x 64 tile of D, decoded into shared memory 64 columns at a
-// time; each thread sums 4 x 4 outputs in fp32.
-template <typename T, int kFormat>
-__global__ void __launch_bounds__(kThreads)
-    fp4_gemm_kernel(uint16_t* __restrict__ d, const Fp4View a, const Fp4View b, float alpha) {
-  __shared__ float sa[kTile][kDepth + 1], sb[kTile][kDepth + 1];
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int64_t n_out = b.group_rows;
-  int64_t row, end, first;  // this tile's rows, and its group's first row
-  int g;
-  if (a.offsets) {
-    g = find_group(a.offsets, a.groups, kTile, blockIdx.x);
-    first = a.offsets[g];
-    end = g < a.groups ? a.offsets[g + 1] : a.rows;
-    row = first + (blockIdx.x - (first / kTile + g)) * static_cast<int64_t>(kTile);
-  } else {
-    const int64_t per = (a.group_rows + kTile - 1) / kTile;
-    g = static_cast<int>(blockIdx.x / per);
-    first = g * a.group_rows;
-    end = first + a.group_rows;
-    row = first + (blockIdx.x - g * per) * kTile;
+// Index of a stream's error word: 0 for the legacy default stream, one each
+// for the first 63 others, then shared by a hash.
+int error_index(cudaStream_t s) {
+  const uintptr_t h = reinterpret_cast<uintptr_t>(s);
+  if (h == 0) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (int i = 1; i < g_words_used; ++i)
+    if (g_word_stream[i] == h) return i;
+  if (g_words_used < kErrorWords) {
+    g_word_stream[g_words_used] = h;
+    return g_words_used++;
   }
-  const int count = static_cast<int>(max(min(static_cast<int64_t>(kTile), end - row), int64_t{0}));
-  if (count == 0) return;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kTile;
-  const bool live = g < a.groups;
-  const int64_t a_tile0 = a.offsets ? first / kTileRows + g
-                                    : g * ((a.group_rows + kTileRows - 1) / kTileRows);
-  const int64_t b_tile0 = g * ((n_out + kTileRows - 1) / kTileRows);
-  float acc[4][4] = {};
-  const int lr = threadIdx.x >> 2, lk = (threadIdx.x & 3) * 16;
-  for (int64_t k0 = 0; live && k0 < a.cols; k0 += kDepth) {
-    const int64_t k = k0 + lk;
-    float f[16] = {}, h[16] = {};
-    if (lr < count && k / 2 < a.pitch) {
-      const int64_t in = row + lr - first;
-      decode_row<kFormat>(a, row + lr, a_tile0 + in / kTileRows, static_cast<int>(in % kTileRows), k, f);
-    }
-    if (n0 + lr < n_out && k / 2 < b.pitch)
-      decode_row<kFormat>(b, g * n_out + n0 + lr, b_tile0 + (n0 + lr) / kTileRows,
-                          static_cast<int>((n0 + lr) % kTileRows), k, h);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      sa[lr][lk + i] = f[i];
-      sb[lr][lk + i] = h[i];
-    }
-    __syncthreads();
-    for (int i = 0; i < kDepth; ++i) {
-      float x[4], y[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[q] = sa[(threadIdx.x >> 4) + 16 * q][i];
-        y[q] = sb[(threadIdx.x & 15) + 16 * q][i];
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int p = 0; p < 4; ++p) acc[q][p] = fmaf(x[q], y[p], acc[q][p]);
-    }
+  return 1 + static_cast<int>((h >> 4) % (kErrorWords - 1));
+}
+
+// A matrix's codes as rows of bytes; a box is 128 bytes wide.
+int encode_codes(CUtensorMap* map, const fp4_matrix_t* m, uint32_t box_rows) {
+  const uint64_t pitch = static_cast<uint64_t>(code_pitch(m->cols));
+  const cuuint64_t dims[2] = {pitch, static_cast<cuuint64_t>(m->rows)};
+  const cuuint64_t strides[1] = {pitch};
+  const cuuint32_t box[2] = {kGemmBytesK, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m->codes, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
+template <typename T, int kFormat, int kBN>
+int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas, cudaStream_t s) {
+  const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);  // the count of tiles before each
+  using S = Fp4GemmShape<kFormat, kBN>;
+  p.stages = S::stages_that_fit(fixed);
+  const auto kernel = fp4_gemm_tc<T, kFormat, kBN>;
+  static std::once_flag once;  // per instantiation
+  static cudaError_t granted = cudaSuccess;
+  std::call_once(once, [&] {
+    granted = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kGemmSmemLimit);
+  });
+  if (granted != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
   }
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int r = (threadIdx.x >> 4) + 16 * q;
-      const int64_t n = n0 + (threadIdx.x & 15) + 16 * p;
-      if (r < count && n < n_out)
-        reinterpret_cast<T*>(d)[(row + r) * n_out + n] = from_float<T>(acc[q][p] * alpha);
-    }
+  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, w,
+                    x, p);
 }
 
 }  // namespace
@@ -123,28 +115,74 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   if ((rc = require_device(&sms)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->cols == 0) return write_empty_sum(D, nullptr, 0.0f, a->rows * n_out, sms, s);
+  if ((rc = get_encoder()) != GEMM_OK) return rc;
+
+  // Rows per tile: 256 where a group has more than 128 of them on average.
+  const int64_t mean = a->rows / a->groups;
+  const int bn = mean > 128 ? 256 : 128;
+  Fp4GemmParams p;
+  std::memset(&p, 0, sizeof(p));
   const Fp4View va = view_of(a), vb = view_of(b);
-  alpha *= va.up * vb.up;
-  const int64_t tiles = a->offsets ? a->rows / kTile + a->groups + 1
-                                   : a->groups * ((a->group_rows + kTile - 1) / kTile);
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((n_out + kTile - 1) / kTile));
-  const auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, s, static_cast<uint16_t*>(D), va, vb, alpha);
+  p.w_scales = vb.scales;
+  p.x_scales = va.scales;
+  p.w_tile_bytes = vb.tile_bytes;
+  p.x_tile_bytes = va.tile_bytes;
+  p.d = static_cast<uint16_t*>(D);
+  p.offsets = a->offsets;
+  p.rows = a->rows;
+  p.group_rows = a->group_rows;
+  p.n_out = n_out;
+  p.groups = a->groups;
+  p.k = static_cast<int32_t>(a->cols);
+  p.num_kb = static_cast<int32_t>(col_stages(a->cols));
+  p.m_tiles = static_cast<int32_t>((n_out + kGemmM - 1) / kGemmM);
+  // Few rows a group: boxes of 32, so that a tile loads little more than it has.
+  p.box_rows = mean > 64 ? 128 : 32;
+  p.raster = 8;
+  p.alpha = alpha * va.up * vb.up;
+  p.timeout_ns = kTimeoutNs;
+  void* words = nullptr;
+  if (cudaGetSymbolAddress(&words, g_fp4_error) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  p.error = static_cast<uint32_t*>(words) + error_index(s);
+  CUtensorMap tmW, tmX;
+  if ((rc = encode_codes(&tmW, b, kGemmM)) != GEMM_OK ||
+      (rc = encode_codes(&tmX, a, p.box_rows)) != GEMM_OK)
+    return rc;
+  // One CTA per SM, fewer where there cannot be that many tiles.
+  const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
+                                       : a->groups * ((a->group_rows + bn - 1) / bn);
+  const int ctas = static_cast<int>(std::min<int64_t>(sms, row_tiles * p.m_tiles));
+  const auto by_bn = [&](auto t, auto fmt) {
+    using T = decltype(t);
+    return bn == 256 ? launch<T, fmt(), 256>(tmW, tmX, p, ctas, s)
+                     : launch<T, fmt(), 128>(tmW, tmX, p, ctas, s);
   };
-  if (type == MOE_F16)
-    return a->format == FP4_NV ? go(fp4_gemm_kernel<__half, FP4_NV>)
-                               : go(fp4_gemm_kernel<__half, FP4_MX>);
-  return a->format == FP4_NV ? go(fp4_gemm_kernel<__nv_bfloat16, FP4_NV>)
-                             : go(fp4_gemm_kernel<__nv_bfloat16, FP4_MX>);
+  const auto by_format = [&](auto t) {
+    return a->format == FP4_NV ? by_bn(t, std::integral_constant<int, FP4_NV>{})
+                               : by_bn(t, std::integral_constant<int, FP4_MX>{});
+  };
+  return type == MOE_F16 ? by_format(__half{}) : by_format(__nv_bfloat16{});
 }
 
 extern "C" int fp4_get_device_error(void* stream, uint32_t* raw) {
   const int rc = require_device(nullptr);
   if (rc != GEMM_OK) return rc;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t word = 0;
+  const uint32_t zero = 0;
+  const size_t off = static_cast<size_t>(error_index(s)) * sizeof(uint32_t);
+  if (cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&word, g_fp4_error, sizeof(word), off, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_fp4_error, &zero, sizeof(zero), off, cudaMemcpyHostToDevice, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  if (raw) *raw = 0;
-  return GEMM_OK;
+  if (raw) *raw = word;
+  return static_cast<int>(word & 0xffu);
 }

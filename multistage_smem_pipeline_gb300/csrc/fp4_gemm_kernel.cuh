@@ -1,0 +1,485 @@
+// The 4-bit product on the tensor cores.
+//
+// D[r][n] = alpha sum_k a[r][k] b[g][n][k] for the rows r of group g.  The
+// weights are the instruction's M operand (128 rows a tile) and the
+// activations its N operand (1 to kBN rows a tile): N may be any multiple of
+// 16, so that an expert with few rows costs few columns.  A tile's
+// accumulator is then D transposed: lane = output n, column = row r.
+//
+// Inside a CTA, one per SM, each walking the list of tiles:
+//   warp 0, one thread -- producer: per 256 columns of k (128 bytes of codes a
+//       row), TMA boxes of both operands' codes and bulk copies of their
+//       scale chunks into a ring of stages;
+//   warp 1, one thread -- copies the stage's scales into tensor memory
+//       (tcgen05.cp, 512 bytes = 128 rows x 4 blocks at a time, replicated to
+//       the four lane quadrants) and issues a block-scaled MMA per 64 columns;
+//   warps 2 .. 9 -- epilogue: two warps per lane quadrant take alternate
+//       32-column chunks to registers, round them, let the accumulator go, and
+//       store.
+// Every ring slot has its own columns of tensor memory for scales: a slot's
+// copies begin after its full barrier, hence after its empty one, which the
+// commit of the MMAs that read those columns completed.
+//
+// Waits are bounded as in the fp16 kernels: on expiry the error word is set,
+// all roles leave their loops, what is in flight is drained, and tensor
+// memory is freed.
+#pragma once
+#include <cuda.h>
+
+#include "fp4.cuh"
+
+namespace gb300 {
+
+constexpr int kGemmM = 128;           // weight rows per tile
+constexpr int kGemmBytesK = 128;      // codes of a row per stage: 256 elements
+constexpr int kGemmEpiWarps = 8;
+constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
+constexpr int kGemmMaxStages = 8;
+constexpr uint32_t kWBytes = kGemmM * kGemmBytesK;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemScales = 256;  // first column of the scales
+constexpr int kErrorWords = 64;
+constexpr uint32_t kGemmSmemLimit = 232448;
+
+enum GemmWait : uint32_t { kWaitEmpty = 1, kWaitFull = 2, kWaitTmemEmpty = 3, kWaitTmemFull = 4 };
+
+struct Fp4GemmParams {
+  const uint8_t* w_scales;
+  const uint8_t* x_scales;
+  int64_t w_tile_bytes, x_tile_bytes;
+  uint16_t* d;
+  const int32_t* offsets;  // of the rows' groups; null: uniform groups
+  int64_t rows, group_rows, n_out;
+  int32_t groups, k, num_kb;
+  int32_t m_tiles;         // weight tiles per group
+  int32_t box_rows;        // activation rows per TMA box
+  int32_t stages;
+  int32_t raster;          // row tiles that share a pass over the weight tiles
+  float alpha;
+  uint64_t timeout_ns;
+  uint32_t* error;
+};
+
+template <int kFormat, int kBN>
+struct Fp4GemmShape {
+  static constexpr int kXTiles = (kBN + kTileRows - 1) / kTileRows;  // scale tiles of the rows
+  static constexpr uint32_t kScaleStage = chunks_per_stage(kFormat) * kChunkBytes;
+  static constexpr uint32_t kXBytes = kBN * kGemmBytesK;
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleStage * (1 + kXTiles);
+  static constexpr int kAccs = kBN > 128 ? 1 : 2;  // accumulators in columns 0 .. 255
+  // columns of scales per slot: 4 per chunk and 128 rows
+  static constexpr uint32_t kWCols = 4 * chunks_per_stage(kFormat);
+  static constexpr uint32_t kSlotCols = kWCols * (1 + kXTiles);
+  static constexpr int kSlots = (kTmemCols - kTmemScales) / kSlotCols;
+  static int stages_that_fit(uint32_t fixed) {
+    int s = static_cast<int>((kGemmSmemLimit - fixed) / kStageBytes);
+    if (s > kSlots) s = kSlots;
+    return s > kGemmMaxStages ? kGemmMaxStages : s;
+  }
+};
+
+// Shared memory past the ring: barriers, then the tensor memory address, the
+// abort flag, and the running count of row tiles before each group.
+constexpr uint32_t kGemmBars = 2 * kGemmMaxStages + 5;
+__host__ __device__ constexpr uint32_t gemm_fixed_bytes(int groups) {
+  return 8 * kGemmBars + 16 + 4 * (groups + 1) + 1024;  // 1 KiB to align the ring
+}
+
+// ------------------------------------------------------------------ PTX
+// Instruction descriptor of the block-scaled kinds: A and B E2M1 (bits 7-9
+// and 10-11 = 1), both K-major, N >> 3 in bits 17-22, the scales' type in bit
+// 23 (0: E4M3, 1: E8M0), M >> 4 in bits 24-28; bits 4-5 and 29-30 say which
+// bytes of a 32-bit column hold the scales of B and A.
+template <int kFormat>
+__host__ __device__ constexpr uint32_t fp4_idesc(int m, int n) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (kFormat == FP4_MX ? 1u << 23 : 0u) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t fp4_idesc_scale_bytes(int first) {
+  return (static_cast<uint32_t>(first) << 4) | (static_cast<uint32_t>(first) << 29);
+}
+
+template <int kFormat>
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t a_scales, uint32_t b_scales,
+                                         uint32_t accumulate) {
+  if (kFormat == FP4_NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory to 32 lanes x 4 columns, in all four
+// lane quadrants.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// Shared-memory descriptor of an unswizzled run of 16-byte rows: 8-row groups
+// 128 bytes apart (stride byte offset), descriptor version 1.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ waits
+__device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t site, const Fp4GemmParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > p.timeout_ns) {
+        *abort_flag = 1;
+        atomicCAS(p.error, 0u, static_cast<uint32_t>(GEMM_ERR_TIMEOUT) | (site << 8));
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void gemm_wait_drain(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((it & 31u) == 0 && global_timer_ns() - t0 > timeout_ns) return;
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+struct GemmTile {
+  int64_t x_row;    // first row of the activations (and of D)
+  int64_t x_tile;   // its scale tile
+  int32_t count;    // rows
+  int32_t group, m; // weight tile m of the group
+};
+
+// Tile t: groups in order; in a group, `raster` row tiles at a time walk over
+// the weight tiles together, so that what runs at once shares operands in L2.
+template <int kBN>
+__device__ __forceinline__ GemmTile gemm_tile(int64_t t, const Fp4GemmParams& p,
+                                              const int32_t* before) {
+  GemmTile o;
+  int64_t first, rows;
+  if (p.offsets) {
+    int lo = 0, hi = p.groups - 1;  // the last group with before[g] * m_tiles <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(before[mid]) * p.m_tiles <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    o.group = lo;
+    t -= static_cast<int64_t>(before[lo]) * p.m_tiles;
+    first = p.offsets[lo];
+    rows = p.offsets[lo + 1] - first;
+    o.x_tile = first / kTileRows + lo;
+  } else {
+    const int64_t per = (p.group_rows + kBN - 1) / kBN * p.m_tiles;
+    o.group = static_cast<int32_t>(t / per);
+    t -= o.group * per;
+    first = o.group * p.group_rows;
+    rows = p.group_rows;
+    o.x_tile = o.group * ((p.group_rows + kTileRows - 1) / kTileRows);
+  }
+  const int x_tiles = static_cast<int>((rows + kBN - 1) / kBN);
+  const int band = static_cast<int>(t / (static_cast<int64_t>(p.raster) * p.m_tiles));
+  const int in = static_cast<int>(t - static_cast<int64_t>(band) * p.raster * p.m_tiles);
+  const int wide = min(p.raster, x_tiles - band * p.raster);
+  const int xt = band * p.raster + in % wide;
+  o.m = in / wide;
+  o.x_row = first + static_cast<int64_t>(xt) * kBN;
+  o.x_tile += xt * (kBN / kTileRows);
+  o.count = static_cast<int32_t>(min(static_cast<int64_t>(kBN), rows - static_cast<int64_t>(xt) * kBN));
+  return o;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_two(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack_two<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------------------ kernel
+template <typename T, int kFormat, int kBN>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    fp4_gemm_tc(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                const Fp4GemmParams p) {
+  static_assert(kBN % kTileRows == 0, "row tiles start whole scale tiles");
+  using S = Fp4GemmShape<kFormat, kBN>;
+  constexpr int kChunks = chunks_per_stage(kFormat);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
+  const uint32_t bars = base + stages * S::kStageBytes;
+  const auto full_bar = [&](int s) { return bars + 8u * s; };
+  const auto empty_bar = [&](int s) { return bars + 8u * (kGemmMaxStages + s); };
+  const auto tfull_bar = [&](int b) { return bars + 8u * (2 * kGemmMaxStages + b); };
+  const auto tempty_bar = [&](int b) { return bars + 8u * (2 * kGemmMaxStages + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * kGemmMaxStages + 4);
+  uint8_t* const misc = smem + stages * S::kStageBytes + 8 * kGemmBars;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int32_t* const before = reinterpret_cast<int32_t*>(misc + 16);  // row tiles before each group
+
+  if (threadIdx.x == 0) {
+    grid_launch_dependents();
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), kGemmEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (p.offsets && warp == 2) {  // running count of row tiles
+    int32_t total = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + lane;
+      const int32_t n = g < p.groups ? (p.offsets[g + 1] - p.offsets[g] + kBN - 1) / kBN : 0;
+      int32_t upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      if (g < p.groups) before[g] = total + upto - n;
+      total += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) before[p.groups] = total;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t tiles =
+      (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
+      static_cast<int64_t>(p.m_tiles);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles && !*abort_flag; t += gridDim.x) {
+        const GemmTile tile = gemm_tile<kBN>(t, p, before);
+        const int boxes = (tile.count + p.box_rows - 1) / p.box_rows;
+        const int x_tiles = (tile.count + kTileRows - 1) / kTileRows;
+        const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
+                               S::kScaleStage * (1 + x_tiles);
+        const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * kGemmM);
+        const uint8_t* const w_scales =
+            p.w_scales + (static_cast<int64_t>(tile.group) * p.m_tiles + tile.m) * p.w_tile_bytes;
+        const uint8_t* const x_scales = p.x_scales + tile.x_tile * p.x_tile_bytes;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!gemm_wait(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
+            ok = false;
+            break;
+          }
+          const uint32_t w_dst = base + stage * S::kStageBytes;
+          const uint32_t x_dst = w_dst + kWBytes;
+          const uint32_t s_dst = x_dst + S::kXBytes;
+          const uint32_t full = full_bar(stage);
+          mbar_arrive_expect_tx(full, bytes);
+          tma_load_2d(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+          bulk_load(s_dst, w_scales + static_cast<int64_t>(kb) * S::kScaleStage, S::kScaleStage,
+                    full);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
+                        static_cast<int>(tile.x_row) + b * p.box_rows);
+          for (int x = 0; x < x_tiles; ++x)
+            bulk_load(s_dst + (1 + x) * S::kScaleStage,
+                      x_scales + x * p.x_tile_bytes + static_cast<int64_t>(kb) * S::kScaleStage,
+                      S::kScaleStage, full);
+          ++issued;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every load has landed before the CTA may end
+      const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+      for (uint32_t i = first; i < issued; ++i)
+        gemm_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const GemmTile tile = gemm_tile<kBN>(t, p, before);
+        const int x_tiles = (tile.count + kTileRows - 1) / kTileRows;
+        const uint32_t idesc = fp4_idesc<kFormat>(kGemmM, (tile.count + 15) & ~15);
+        if (!gemm_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kBN);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!gemm_wait(full_bar(stage), phase, abort_flag, kWaitFull, p)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t w_src = base + stage * S::kStageBytes;
+          const uint32_t s_src = w_src + kWBytes + S::kXBytes;
+          const uint32_t w_cols = tmem + kTmemScales + stage * S::kSlotCols;
+          const uint32_t x_cols = w_cols + S::kWCols;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            tmem_copy_scales(w_cols + 4 * c, scale_desc(s_src + c * kChunkBytes));
+            for (int x = 0; x < x_tiles; ++x)
+              tmem_copy_scales(x_cols + 4 * (c * S::kXTiles + x),
+                               scale_desc(s_src + (1 + x) * S::kScaleStage + c * kChunkBytes));
+          }
+          const uint64_t w_desc = sw128_kmajor_desc(w_src);
+          const uint64_t x_desc = sw128_kmajor_desc(w_src + kWBytes);
+          const int steps = min(4, (p.k - kb * kStageCols + 63) / 64);  // 64 columns each
+          for (int s = 0; s < steps; ++s) {
+            const int chunk = kFormat == FP4_NV ? s : s >> 1;
+            const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
+            umma_fp4<kFormat>(d_tmem, w_desc + 2u * s, x_desc + 2u * s,
+                              idesc | fp4_idesc_scale_bytes(byte), w_cols + 4 * chunk,
+                              x_cols + 4 * S::kXTiles * chunk, (kb | s) != 0);
+          }
+          umma_commit(empty_bar(stage));
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(tfull_bar(acc));
+        if (++acc == S::kAccs) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      umma_commit(drain_bar);
+      gemm_wait_drain(drain_bar, 0, p.timeout_ns);
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3;               // the lane quadrant this warp may read
+    const int half = (warp - 2) >> 2;     // which of the two warps on it
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      int ok = 0;
+      if (lane == 0) ok = gemm_wait(tfull_bar(acc), acc_phase, abort_flag, kWaitTmemFull, p);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after_sync();
+      constexpr int kMine = kBN / 64;     // 32-column chunks of each warp
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
+                             static_cast<uint32_t>(acc * kBN);
+      uint32_t h[kMine][16];              // columns 2i and 2i + 1 of each chunk, rounded
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) {
+        const int col = 32 * (2 * c + half);
+        if (col >= tile.count) break;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_row + col, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          h[c][i] = pack_two<T>(p.alpha * __uint_as_float(r[2 * i]),
+                                p.alpha * __uint_as_float(r[2 * i + 1]));
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      const int64_t n = static_cast<int64_t>(tile.m) * kGemmM + q * 32 + lane;
+      uint16_t* const d = p.d + tile.x_row * p.n_out + n;
+      if (n < p.n_out) {
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) {
+          const int col = 32 * (2 * c + half);
+          if (col >= tile.count) break;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (col + 2 * i < tile.count)
+              d[(col + 2 * i) * p.n_out] = static_cast<uint16_t>(h[c][i]);
+            if (col + 2 * i + 1 < tile.count)
+              d[(col + 2 * i + 1) * p.n_out] = static_cast<uint16_t>(h[c][i] >> 16);
+          }
+        }
+      }
+      if (++acc == S::kAccs) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    // rows of no group are zero
+    if (p.offsets) {
+      const int64_t from = static_cast<int64_t>(p.offsets[p.groups]) * p.n_out;
+      const int64_t end = p.rows * p.n_out;
+      const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kGemmEpiWarps);
+      for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * (32 * kGemmEpiWarps) +
+                       threadIdx.x - 64; i < end; i += step)
+        p.d[i] = 0;
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace gb300
