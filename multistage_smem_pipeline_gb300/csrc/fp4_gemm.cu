@@ -84,7 +84,7 @@ int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, w,
+  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, 1u, w,
                     x, p);
 }
 

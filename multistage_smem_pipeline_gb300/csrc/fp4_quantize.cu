@@ -9,26 +9,48 @@ namespace gb300 {
 namespace {
 
 constexpr int kSegment = 16;                            // elements a thread takes
-constexpr int kTileSegments = kStageCols / kSegment;    // 16 of them across a tile's 256 columns
+constexpr int kTileSegments = kStageCols / kSegment;    // of them across 256 columns
 constexpr int kThreads = 256;
 
-// 16 elements of a row from column c on; zeros from `cols` on.  kVec: the row
-// is 16-byte aligned.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_segment(const uint16_t* row, int64_t c, int64_t cols,
-                                             float (&f)[kSegment]) {
+// A chunk of scales, 128 rows by 4 blocks, is what a block of threads handles
+// in the kernels that go by tiles.
+template <int kFormat>
+struct Chunk {
+  static constexpr int kCols = 4 * block_size(kFormat);         // 64 or 128
+  static constexpr int kSegments = kCols / kSegment;            // across it: 4 or 8
+  static constexpr int kRowsAtOnce = kThreads / kSegments;      // 64 or 32
+  static constexpr int kSteps = kTileRows / kRowsAtOnce;        // 2 or 4
+};
+
+// 16 elements of a row as they are stored, from column c on; what lies at
+// `cols` or past it is undefined.  kVec: the row is 16-byte aligned.
+struct Raw {
+  Pack p[2];
+};
+
+template <bool kVec>
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, int64_t c, int64_t cols) {
+  Raw r;
+  std::memset(&r, 0, sizeof(r));
   if (kVec && c + kSegment <= cols) {
-    const uint4* const q = reinterpret_cast<const uint4*>(row + c);
-    const uint4 v[2] = {q[0], q[1]};
-    const T* const e = reinterpret_cast<const T*>(v);
-#pragma unroll
-    for (int i = 0; i < kSegment; ++i) f[i] = to_float(e[i]);
-    return;
+    r.p[0] = load8<true>(row, c, cols);
+    r.p[1] = load8<true>(row, c + 8, cols);
+  } else {
+    if (c < cols) r.p[0] = load8<false>(row, c, cols);
+    if (c + 8 < cols) r.p[1] = load8<false>(row, c + 8, cols);
   }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const Raw& r, int64_t c, int64_t cols, float (&f)[kSegment]) {
+  const T* const e = reinterpret_cast<const T*>(&r);
 #pragma unroll
-  for (int i = 0; i < kSegment; ++i) {
-    f[i] = 0.0f;
-    if (c + i < cols) f[i] = to_float(reinterpret_cast<const T*>(row)[c + i]);
+  for (int i = 0; i < kSegment; ++i) f[i] = to_float(e[i]);
+  if (c + kSegment > cols) {
+#pragma unroll
+    for (int i = 0; i < kSegment; ++i)
+      if (c + i >= cols) f[i] = 0.0f;
   }
 }
 
@@ -78,37 +100,47 @@ __device__ __forceinline__ Segment quantize_segment(float (&f)[kSegment], const 
   return s;
 }
 
-// A block per 128-row tile and 256 columns: thread i takes segment i % 16 of
-// rows i / 16 + 16 n.  The tile's scales are put together in shared memory and
-// written in one piece.
+// A block per tile and chunk.  All of a thread's rows are asked for before the
+// first is used; the chunk is put together in shared memory and written in
+// one piece.
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx) {
-  constexpr int kBytes = chunks_per_stage(kFormat) * kChunkBytes;
-  __shared__ __align__(16) uint8_t scales[kBytes];
+    quantize_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx, int chunks) {
+  using C = Chunk<kFormat>;
+  __shared__ __align__(16) uint8_t scales[kChunkBytes];
   grid_launch_dependents();
-  const TileRows t = tile_rows(v, blockIdx.x);
-  for (int i = threadIdx.x; i < kBytes / 16; i += kThreads)
-    reinterpret_cast<uint4*>(scales)[i] = make_uint4(0, 0, 0, 0);
+  const int chunk = static_cast<int>(blockIdx.x % chunks);
+  const TileRows t = tile_rows(v, blockIdx.x / chunks);  // uniform groups: reads nothing
+  if (threadIdx.x < kChunkBytes / 16)
+    reinterpret_cast<uint4*>(scales)[threadIdx.x] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   grid_dependency_wait();
-  const int seg = threadIdx.x % kTileSegments;
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kStageCols + seg * kSegment;
-  for (int r0 = 0; r0 < t.count; r0 += kThreads / kTileSegments) {
-    const int r = r0 + threadIdx.x / kTileSegments;
-    const bool live = r < t.count;
+  const int seg = threadIdx.x % C::kSegments;
+  const int64_t c = static_cast<int64_t>(chunk) * C::kCols + seg * kSegment;
+  const int r0 = threadIdx.x / C::kSegments;
+  Raw raw[C::kSteps];
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    const int r = r0 + i * C::kRowsAtOnce;
+    raw[i] = load_raw<kVec>(x + (t.row + r) * ldx, c, r < t.count ? v.cols : 0);
+  }
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    const int r = r0 + i * C::kRowsAtOnce;
+    if (i * C::kRowsAtOnce >= t.count) break;
     float f[kSegment];
-    load_segment<T, kVec>(x + (t.row + r) * ldx, c, live ? v.cols : 0, f);
+    widen<T>(raw[i], c, v.cols, f);
     const Segment s = quantize_segment<kFormat>(f, v);
-    if (!live) continue;
+    if (r >= t.count) continue;
     if (c / 2 < v.pitch)
       *reinterpret_cast<uint2*>(v.codes + (t.row + r) * v.pitch + c / 2) = s.codes;
     if (c < v.cols) scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)] = s.scale;
   }
   __syncthreads();
-  uint8_t* const to = v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(blockIdx.y) * kBytes;
-  for (int i = threadIdx.x; i < kBytes / 16; i += kThreads)
-    reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(scales)[i];
+  if (threadIdx.x < kChunkBytes / 16)
+    reinterpret_cast<uint4*>(v.scales + t.tile * v.tile_bytes +
+                             static_cast<int64_t>(chunk) * kChunkBytes)[threadIdx.x] =
+        reinterpret_cast<const uint4*>(scales)[threadIdx.x];
 }
 
 // A block per token and up to 4096 columns: quantised once, written to the
@@ -126,7 +158,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t c = seg * kSegment;
   const int64_t cols256 = col_stages(v.cols) * kStageCols;
   float f[kSegment];
-  load_segment<T, kVec>(x + token * ldx, c, v.cols, f);
+  widen<T>(load_raw<kVec>(x + token * ldx, c, v.cols), c, v.cols, f);
   const Segment s = quantize_segment<kFormat>(f, v);
   // bytes of the chunk's four blocks, in every thread
   constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
@@ -152,48 +184,60 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// A block per tile and chunk, and per 128 rows of no group.
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-    dequantize_kernel(uint16_t* __restrict__ y, const Fp4View v) {
-  constexpr int kBytes = chunks_per_stage(kFormat) * kChunkBytes;
-  __shared__ __align__(16) uint8_t scales[kBytes];
+    dequantize_kernel(uint16_t* __restrict__ y, const Fp4View v, int chunks) {
+  using C = Chunk<kFormat>;
+  __shared__ __align__(16) uint8_t scales[kChunkBytes];
   grid_launch_dependents();
   grid_dependency_wait();
-  const TileRows t = tile_rows(v, blockIdx.x);
+  const int chunk = static_cast<int>(blockIdx.x % chunks);
+  const TileRows t = tile_rows(v, blockIdx.x / chunks);
   if (t.count == 0) return;
-  if (t.tile >= 0) {
-    const uint8_t* const from =
-        v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(blockIdx.y) * kBytes;
-    for (int i = threadIdx.x; i < kBytes / 16; i += kThreads)
-      reinterpret_cast<uint4*>(scales)[i] = reinterpret_cast<const uint4*>(from)[i];
+  const int seg = threadIdx.x % C::kSegments;
+  const int64_t c = static_cast<int64_t>(chunk) * C::kCols + seg * kSegment;
+  const int r0 = threadIdx.x / C::kSegments;
+  uint2 codes[C::kSteps];
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    const int r = r0 + i * C::kRowsAtOnce;
+    codes[i] = make_uint2(0, 0);
+    if (t.tile >= 0 && r < t.count && c < v.cols)
+      codes[i] = *reinterpret_cast<const uint2*>(v.codes + (t.row + r) * v.pitch + c / 2);
   }
+  if (t.tile >= 0 && threadIdx.x < kChunkBytes / 16)
+    reinterpret_cast<uint4*>(scales)[threadIdx.x] = reinterpret_cast<const uint4*>(
+        v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(chunk) * kChunkBytes)[threadIdx.x];
   __syncthreads();
-  const int seg = threadIdx.x % kTileSegments;
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * kStageCols + seg * kSegment;
   if (c >= v.cols) return;
-  for (int r = threadIdx.x / kTileSegments; r < t.count; r += kThreads / kTileSegments) {
+#pragma unroll
+  for (int i = 0; i < C::kSteps; ++i) {
+    const int r = r0 + i * C::kRowsAtOnce;
+    if (r >= t.count) return;
     float f[kSegment] = {};
     if (t.tile >= 0) {
-      const uint2 codes = *reinterpret_cast<const uint2*>(v.codes + (t.row + r) * v.pitch + c / 2);
-      from_e2m1(codes.x, f);
-      from_e2m1(codes.y, f + 8);
+      from_e2m1(codes[i].x, f);
+      from_e2m1(codes[i].y, f + 8);
       const uint32_t byte = scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)];
       const float step = scale_value<kFormat>(byte) * (kFormat == FP4_NV ? v.up : 1.0f);
 #pragma unroll
-      for (int i = 0; i < kSegment; ++i) f[i] *= step;
+      for (int e = 0; e < kSegment; ++e) f[e] *= step;
     }
     uint16_t* const row = y + (t.row + r) * v.cols;
     if (kVec && c + kSegment <= v.cols) {
-      uint4 o[2];
-      T* const e = reinterpret_cast<T*>(o);
+      float lo[8], hi[8];
 #pragma unroll
-      for (int i = 0; i < kSegment; ++i) e[i] = from_float<T>(f[i]);
-      reinterpret_cast<uint4*>(row + c)[0] = o[0];
-      reinterpret_cast<uint4*>(row + c)[1] = o[1];
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = f[e];
+        hi[e] = f[8 + e];
+      }
+      store8<true>(row, c, v.cols, pack<T>(lo));
+      store8<true>(row, c + 8, v.cols, pack<T>(hi));
     } else {
 #pragma unroll
-      for (int i = 0; i < kSegment; ++i)
-        if (c + i < v.cols) reinterpret_cast<T*>(row)[c + i] = from_float<T>(f[i]);
+      for (int e = 0; e < kSegment; ++e)
+        if (c + e < v.cols) reinterpret_cast<T*>(row)[c + e] = from_float<T>(f[e]);
     }
   }
 }
@@ -268,12 +312,14 @@ extern "C" int fp4_quantize(const fp4_matrix_t* out, const void* x, int64_t ldx,
       const int64_t segments = col_stages(out->cols) * kTileSegments;
       const dim3 grid(static_cast<unsigned>(x_rows),
                       static_cast<unsigned>((segments + kThreads - 1) / kThreads));
-      return launch_pdl(quantize_routed_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0, s, v, xp,
+      return launch_pdl(quantize_routed_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0, s, 1u, v, xp,
                         ldx, routing->rows, routing->ids, routing->top_k);
     }
-    const dim3 grid(static_cast<unsigned>(tile_count(out->rows, out->groups, false)),
-                    static_cast<unsigned>(col_stages(out->cols)));
-    return launch_pdl(quantize_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0, s, v, xp, ldx);
+    const int64_t chunks = col_stages(out->cols) * chunks_per_stage(fmt());
+    const int64_t blocks = tile_count(out->rows, out->groups, false) * chunks;
+    if (blocks > INT_MAX) return static_cast<int>(GEMM_ERR_INVALID_VALUE);
+    return launch_pdl(quantize_kernel<T, fmt(), wide()>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kThreads), 0, s, 1u, v, xp, ldx, static_cast<int>(chunks));
   });
 }
 
@@ -293,12 +339,15 @@ extern "C" int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* s
   const Fp4View v = view_of(in);
   const bool vec = aligned_to(y, 16) && in->cols % 8 == 0;
   const bool by_offsets = in->offsets != nullptr;
-  const dim3 grid(
-      static_cast<unsigned>(tile_count(in->rows, in->groups, by_offsets) + (by_offsets ? 1 : 0)),
-      static_cast<unsigned>(col_stages(in->cols)));
   return dispatch_forms(type, in->format, vec, [&](auto t, auto fmt, auto wide) {
     using T = decltype(t);
-    return launch_pdl(dequantize_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0,
-                      static_cast<cudaStream_t>(stream), static_cast<uint16_t*>(y), v);
+    // only the columns that y has: padding is left out
+    const int64_t chunks = (in->cols + Chunk<fmt()>::kCols - 1) / Chunk<fmt()>::kCols;
+    const int64_t blocks =
+        (tile_count(in->rows, in->groups, by_offsets) + (by_offsets ? 1 : 0)) * chunks;
+    if (blocks > INT_MAX) return static_cast<int>(GEMM_ERR_INVALID_VALUE);
+    return launch_pdl(dequantize_kernel<T, fmt(), wide()>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kThreads), 0, static_cast<cudaStream_t>(stream), 1u,
+                      static_cast<uint16_t*>(y), v, static_cast<int>(chunks));
   });
 }

@@ -25,7 +25,7 @@ inline bool valid_type(int type) { return type == MOE_F16 || type == MOE_BF16; }
 // The routing's own fields: sizes in range, and the arrays that a call reads.
 inline int check_routing(const moe_routing_t* r) {
   if (!r || r->tokens < 0 || r->top_k < 1 || r->top_k > MOE_MAX_TOP_K || r->experts < 1 ||
-      r->experts > MOE_MAX_EXPERTS || r->tokens > INT_MAX / r->top_k)
+      r->experts > MOE_MAX_EXPERTS || r->tokens > MOE_MAX_SLOTS / r->top_k)
     return GEMM_ERR_INVALID_VALUE;
   if (r->tokens > 0 && (!r->offsets || !r->rows || !r->pairs || !r->ids))
     return GEMM_ERR_INVALID_VALUE;
@@ -38,20 +38,25 @@ inline int check_routing(const moe_routing_t* r) {
 // A launch with programmatic dependent launch: the kernel's set-up may overlap
 // the end of the one before it in the stream, and every kernel here waits for
 // that one (grid_dependency_wait) before its first access to memory.
+// `cluster` blocks form a cluster.
 template <typename... Params, typename... Args>
 int launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-               Args... args) {
+               unsigned cluster, Args... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -82,33 +87,81 @@ __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 
-// N neighbouring 16-bit elements as they are loaded and stored: 8 (16 bytes)
-// where rows are 16-byte aligned, else 1.
-template <int N>
-struct Pack;
-template <>
-struct Pack<8> {
-  uint4 v;
-};
-template <>
-struct Pack<1> {
-  uint16_t v;
+// Eight neighbouring 16-bit elements.
+struct alignas(16) Pack {
+  uint32_t w[4];
 };
 
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Pack<N>& p, float (&f)[N]) {
-  const T* e = reinterpret_cast<const T*>(&p);
+template <typename T>
+__device__ __forceinline__ void unpack(const Pack& p, float (&f)[8]) {
+  const T* const e = reinterpret_cast<const T*>(&p);
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = to_float(e[i]);
+  for (int i = 0; i < 8; ++i) f[i] = to_float(e[i]);
 }
 
-template <typename T, int N>
-__device__ __forceinline__ Pack<N> pack(const float (&f)[N]) {
-  Pack<N> p;
-  T* e = reinterpret_cast<T*>(&p);
+template <typename T>
+__device__ __forceinline__ Pack pack(const float (&f)[8]) {
+  Pack p;
+  T* const e = reinterpret_cast<T*>(&p);
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = from_float<T>(f[i]);
+  for (int i = 0; i < 8; ++i) e[i] = from_float<T>(f[i]);
   return p;
+}
+
+// Rows that do not start on 16-byte boundaries.  A row is walked in windows of
+// eight elements that are aligned where they are stored; the first begins
+// `lead` elements before the row, and only the first and the last windows hold
+// elements outside it.
+__device__ __forceinline__ int row_lead(const uint16_t* row) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) >> 1;
+}
+
+// Elements [e, e + 8) of a row of n.  Unaligned: the one or two 16-byte words
+// that hold them, shifted into place; a word without an element of the row in
+// it is not read, and what stands outside the row is undefined.
+template <bool kAligned>
+__device__ __forceinline__ Pack load8(const uint16_t* row, int64_t e, int64_t n) {
+  if (kAligned) return *reinterpret_cast<const Pack*>(row + e);
+  const uintptr_t start = reinterpret_cast<uintptr_t>(row);
+  const uintptr_t at = start + 2 * e;  // may lie before the row
+  const uintptr_t word = at & ~static_cast<uintptr_t>(15);
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  if (word + 16 > start && word < start + 2 * n) lo = *reinterpret_cast<const uint4*>(word);
+  if (word != at && word + 16 < start + 2 * n) hi = *reinterpret_cast<const uint4*>(word + 16);
+  const uint32_t off = static_cast<uint32_t>(at & 15);
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  Pack p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p.w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+  return p;
+}
+
+// The same window to a row that it is aligned in; elements outside are left out.
+template <bool kAligned>
+__device__ __forceinline__ void store8(uint16_t* row, int64_t e, int64_t n, const Pack& p) {
+  if (kAligned || (e >= 0 && e + 8 <= n)) {
+    *reinterpret_cast<Pack*>(row + e) = p;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i >= 0 && e + i < n) row[e + i] = static_cast<uint16_t>(p.w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Zeroes what a window holds outside a row of n elements.
+__device__ __forceinline__ void clip8(float (&f)[8], int64_t e, int64_t n) {
+  if (e >= 0 && e + 8 <= n) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (e + i < 0 || e + i >= n) f[i] = 0.0f;
 }
 
 }  // namespace gb300

@@ -8,6 +8,8 @@
 //                                               dw(p) = <dO[t], Y[rows(p)]>
 // All but the sort move rows and are bound by memory: each kernel reads its
 // inputs once and writes its outputs once, 16 bytes a thread.
+#include <mutex>
+
 #include "moe_common.cuh"
 
 namespace gb300 {
@@ -26,37 +28,74 @@ struct RouteParams {
 };
 
 // ------------------------------------------------------------------ sort
-// One block: each warp owns a run of slots, in order.  Counts per warp and
-// key in shared memory, then their sums over (key, warp) in that order: the
-// first row of each warp's slots of each key.  A second walk gives each slot
-// its place: the lanes of a warp that hold equal keys are ranked by lane.
+// A cluster of 1 to 8 blocks; the slots are cut into one run per warp, in
+// order.  Counts per key and warp in shared memory, turned into what lies
+// before each warp's slots of a key: within the block by a scan over its
+// warps, across blocks from the other blocks' totals (distributed shared
+// memory), across keys by a scan over the keys, which is `offsets`.  A second
+// walk places the slots: lanes of a warp that hold equal keys are ranked by
+// lane.  Slots are read twice (the second time from cache) and everything is
+// written once; what bounds it is latency, hence one launch and few steps.
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(int32_t* __restrict__ offsets, int32_t* __restrict__ rows,
                 int32_t* __restrict__ pairs, const int32_t* __restrict__ ids, int n, int experts) {
-  extern __shared__ int32_t count[];  // [kSortWarps][experts + 1], then [kSortWarps] sums
+  extern __shared__ int32_t count[];  // [kSortWarps][keys], then [keys] totals, [kSortWarps] sums
   const int keys = experts + 1;
-  int32_t* const sums = count + kSortWarps * keys;
+  int32_t* const totals = count + kSortWarps * keys;
+  int32_t* const sums = totals + keys;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int blocks = static_cast<int>(gridDim.x);  // one cluster is the grid
   grid_launch_dependents();
   for (int i = threadIdx.x; i < kSortWarps * keys; i += kSortThreads) count[i] = 0;
   __syncthreads();
   grid_dependency_wait();
-  const int per_warp = ((n + kSortThreads - 1) / kSortThreads) * 32;
-  const int begin = min(warp * per_warp, n), end = min(begin + per_warp, n);
+  const int warps = blocks * kSortWarps;
+  const int per_warp = ((n + 32 * warps - 1) / (32 * warps)) * 32;
+  const int64_t at = static_cast<int64_t>(rank * kSortWarps + warp) * per_warp;
+  const int begin = static_cast<int>(min(at, static_cast<int64_t>(n)));
+  const int end = static_cast<int>(min(at + per_warp, static_cast<int64_t>(n)));
   int32_t* const mine = count + warp * keys;
   const auto key_of = [&](int p) {
     const int32_t e = ids[p];
     return (e < 0 || e >= experts) ? experts : e;
   };
+#pragma unroll 4
   for (int p = begin + lane; p < end; p += 32) atomicAdd(&mine[key_of(p)], 1);
   __syncthreads();
-  // exclusive sums, keys outermost: each thread sums a run of keys
+  // over the block's warps: a warp per key, a lane per warp
+  for (int k = warp; k < keys; k += kSortWarps) {
+    const int c = count[lane * keys + k];
+    int upto = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    count[lane * keys + k] = upto - c;
+    if (lane == 31) totals[k] = upto;
+  }
+  if (blocks > 1) cluster_sync();
+  else __syncthreads();
+  // over blocks and keys: a thread per key, two of them where there are more
   const int per_thread = (keys + kSortThreads - 1) / kSortThreads;
-  const int k0 = min(static_cast<int>(threadIdx.x) * per_thread, keys);
-  const int k1 = min(k0 + per_thread, keys);
-  int total = 0;
-  for (int k = k0; k < k1; ++k)
-    for (int w = 0; w < kSortWarps; ++w) total += count[w * keys + k];
+  int all[2] = {0, 0}, lower[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = static_cast<int>(threadIdx.x) * per_thread + i;
+    if (i >= per_thread || k >= keys) continue;
+    for (int b = 0; b < blocks; ++b) {
+      int c = totals[k];
+      if (b != rank)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                     : "=r"(c)
+                     : "r"(mapa_shared(smem_u32(totals + k), b))
+                     : "memory");
+      all[i] += c;
+      if (b < rank) lower[i] += c;
+    }
+  }
+  const int total = all[0] + all[1];
   int upto = total;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -64,27 +103,30 @@ __global__ void __launch_bounds__(kSortThreads)
     if (lane >= d) upto += v;
   }
   if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  int before = upto - total;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  for (int k = k0; k < k1; ++k) {
-    offsets[k] = before;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = count[w * keys + k];
-      count[w * keys + k] = before;
-      before += c;
-    }
+  if (blocks > 1) cluster_sync();  // the others have read this block's totals
+  else __syncthreads();
+  int before = lane < warp ? sums[lane] : 0;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+  before += upto - total;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = static_cast<int>(threadIdx.x) * per_thread + i;
+    if (i >= per_thread || k >= keys) continue;
+    if (rank == 0) offsets[k] = before;
+    totals[k] = before + lower[i];  // the first row of this block's slots of the key
+    before += all[i];
   }
   __syncthreads();
   for (int p0 = begin; p0 < end; p0 += 32) {
     const int p = p0 + lane;
     const int key = p < end ? key_of(p) : keys;  // past the run: a key of its own
     const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int in = __popc(same & ((1u << lane) - 1u));
     int row = 0;
-    if (key < keys) row = mine[key] + rank;
+    if (key < keys) row = mine[key] + in + totals[key];
     __syncwarp();
-    if (key < keys && rank == 0) mine[key] += __popc(same);
+    if (key < keys && in == 0) mine[key] += __popc(same);
     __syncwarp();
     if (key < keys) {
       rows[p] = row;
@@ -94,8 +136,10 @@ __global__ void __launch_bounds__(kSortThreads)
 }
 
 // ------------------------------------------------------------------ rows out
-// One block per token: its row is read once and written top_k times.
-template <int N>
+// One block per token: its row is read once and written top_k times.  Rows
+// that are not aligned each have windows of their own, and read the token's
+// row again, from cache.
+template <bool kAligned>
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(uint16_t* __restrict__ y, const uint16_t* __restrict__ x, int64_t ldx,
                     const RouteParams r) {
@@ -104,40 +148,81 @@ __global__ void __launch_bounds__(kRowThreads)
   const int64_t t = blockIdx.x;
   const int32_t kept = r.offsets[r.experts];
   const int32_t* const rows = r.rows + t * r.top_k;
-  for (int64_t h = threadIdx.x * N; h < r.hidden; h += kRowThreads * N) {
-    const Pack<N> v = *reinterpret_cast<const Pack<N>*>(x + t * ldx + h);
+  const uint16_t* const from = x + t * ldx;
+  const Pack zero = {{0, 0, 0, 0}};
+  if (kAligned) {
+    for (int64_t h = threadIdx.x * 8; h < r.hidden; h += kRowThreads * 8) {
+      const Pack v = load8<true>(from, h, r.hidden);
+      for (int j = 0; j < r.top_k; ++j) {
+        const int32_t row = rows[j];
+        store8<true>(y + row * r.hidden, h, r.hidden, row < kept ? v : zero);
+      }
+    }
+  } else {
     for (int j = 0; j < r.top_k; ++j) {
       const int32_t row = rows[j];
-      Pack<N> w = v;
-      if (row >= kept) std::memset(&w, 0, sizeof(w));
-      *reinterpret_cast<Pack<N>*>(y + row * r.hidden + h) = w;
+      uint16_t* const to = y + row * r.hidden;
+      const int lead = row_lead(to);
+      for (int64_t h = static_cast<int64_t>(threadIdx.x) * 8 - lead; h < r.hidden;
+           h += kRowThreads * 8)
+        store8<false>(to, h, r.hidden, row < kept ? load8<false>(from, h, r.hidden) : zero);
     }
   }
 }
 
 // ------------------------------------------------------------------ rows back
-// One block per token; kWeighted: the sum takes weights.
-template <typename T, int N, bool kWeighted>
+// One block per token; kWeighted: the sum takes weights.  The rows of kFlight
+// slots are asked for before the first is used; the sum keeps slot order.
+template <typename T, bool kAligned, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(uint16_t* __restrict__ out, const uint16_t* __restrict__ y,
                    const float* __restrict__ weights, const RouteParams r) {
+  constexpr int kFlight = 4;
+  __shared__ int32_t s_row[MOE_MAX_TOP_K];
+  __shared__ float s_weight[MOE_MAX_TOP_K];
+  __shared__ int s_live;
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t t = blockIdx.x;
-  const int32_t kept = r.offsets[r.experts];
-  const int32_t* const rows = r.rows + t * r.top_k;
-  for (int64_t h = threadIdx.x * N; h < r.hidden; h += kRowThreads * N) {
-    float acc[N] = {};
-    for (int j = 0; j < r.top_k; ++j) {
-      const int32_t row = rows[j];
-      if (row >= kept) continue;
-      float v[N];
-      unpack<T>(*reinterpret_cast<const Pack<N>*>(y + row * r.hidden + h), v);
-      const float w = kWeighted ? weights[t * r.top_k + j] : 1.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = kWeighted ? fmaf(w, v[i], acc[i]) : acc[i] + v[i];
+  if (threadIdx.x < 32) {  // the kept slots, in order
+    const int32_t kept = r.offsets[r.experts];
+    int live = 0;
+    for (int j0 = 0; j0 < r.top_k; j0 += 32) {
+      const int j = j0 + static_cast<int>(threadIdx.x);
+      const int32_t row = j < r.top_k ? r.rows[t * r.top_k + j] : kept;
+      const unsigned in = __ballot_sync(0xffffffffu, row < kept);
+      if (row < kept) {
+        const int at = live + __popc(in & ((1u << threadIdx.x) - 1u));
+        s_row[at] = row;
+        if (kWeighted) s_weight[at] = weights[t * r.top_k + j];
+      }
+      live += __popc(in);
     }
-    *reinterpret_cast<Pack<N>*>(out + t * r.hidden + h) = pack<T>(acc);
+    if (threadIdx.x == 0) s_live = live;
+  }
+  __syncthreads();
+  const int live = s_live;
+  uint16_t* const to = out + t * r.hidden;
+  const int lead = kAligned ? 0 : row_lead(to);
+  for (int64_t h = static_cast<int64_t>(threadIdx.x) * 8 - lead; h < r.hidden;
+       h += kRowThreads * 8) {
+    float acc[8] = {};
+    for (int j = 0; j < live; j += kFlight) {
+      Pack v[kFlight];
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q)
+        if (j + q < live) v[q] = load8<kAligned>(y + s_row[j + q] * r.hidden, h, r.hidden);
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) {
+        if (j + q >= live) break;
+        float f[8];
+        unpack<T>(v[q], f);
+        const float w = kWeighted ? s_weight[j + q] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = kWeighted ? fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+      }
+    }
+    store8<kAligned>(to, h, r.hidden, pack<T>(acc));
   }
 }
 
@@ -145,11 +230,12 @@ __global__ void __launch_bounds__(kRowThreads)
 // One warp per slot: it scales the token's gradient into the slot's row and
 // takes its product with the row the slot had.  The warps of a block share
 // the token's gradient through L1.
-template <typename T, int N>
+template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kRowThreads)
     combine_backward_kernel(uint16_t* __restrict__ grad_y, float* __restrict__ grad_weights,
                             const uint16_t* __restrict__ grad_out, const uint16_t* __restrict__ y,
                             const float* __restrict__ weights, const RouteParams r) {
+  constexpr int kFlight = 4;
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
@@ -160,20 +246,39 @@ __global__ void __launch_bounds__(kRowThreads)
   const float w = kept ? weights[p] : 0.0f;
   const uint16_t* const g_row = grad_out + (p / r.top_k) * r.hidden;
   const uint16_t* const y_row = y + row * r.hidden;
+  uint16_t* const to = grad_y ? grad_y + row * r.hidden : nullptr;
+  const int lead = kAligned || !to ? 0 : row_lead(to);
   float dot = 0.0f;
-  for (int64_t h = lane * N; h < r.hidden; h += 32 * N) {
-    float g[N] = {}, v[N];
-    if (kept) {
-      unpack<T>(*reinterpret_cast<const Pack<N>*>(g_row + h), g);
-      if (grad_weights) {
-        unpack<T>(*reinterpret_cast<const Pack<N>*>(y_row + h), v);
+  for (int64_t h0 = static_cast<int64_t>(lane) * 8 - lead; h0 < r.hidden; h0 += 32 * 8 * kFlight) {
+    Pack g[kFlight], v[kFlight];
 #pragma unroll
-        for (int i = 0; i < N; ++i) dot = fmaf(g[i], v[i], dot);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) g[i] *= w;
+    for (int q = 0; q < kFlight; ++q) {
+      const int64_t h = h0 + q * 32 * 8;
+      if (h >= r.hidden || !kept) continue;
+      if (grad_weights) v[q] = load8<kAligned>(y_row, h, r.hidden);
+      g[q] = load8<kAligned>(g_row, h, r.hidden);
     }
-    if (grad_y) *reinterpret_cast<Pack<N>*>(grad_y + row * r.hidden + h) = pack<T>(g);
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const int64_t h = h0 + q * 32 * 8;
+      if (h >= r.hidden) break;
+      float a[8] = {}, b[8];
+      if (kept) {
+        unpack<T>(g[q], a);
+        if (grad_weights) {
+          unpack<T>(v[q], b);
+          if (!kAligned) {
+            clip8(a, h, r.hidden);
+            clip8(b, h, r.hidden);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = fmaf(a[i], b[i], dot);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= w;
+      }
+      if (to) store8<kAligned>(to, h, r.hidden, pack<T>(a));
+    }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
@@ -231,14 +336,15 @@ int run_combine(void* out, const void* y, const float* weights, int64_t hidden, 
   if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
   const bool wide = rows_aligned({out, y}, hidden, hidden);
   const auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(r->tokens)), dim3(kRowThreads), 0, s,
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(r->tokens)), dim3(kRowThreads), 0, s, 1u,
                       static_cast<uint16_t*>(out), static_cast<const uint16_t*>(y), weights,
                       route_params(r, hidden));
   };
   if (type == MOE_F16)
-    return wide ? go(combine_kernel<__half, 8, kWeighted>) : go(combine_kernel<__half, 1, kWeighted>);
-  return wide ? go(combine_kernel<__nv_bfloat16, 8, kWeighted>)
-              : go(combine_kernel<__nv_bfloat16, 1, kWeighted>);
+    return wide ? go(combine_kernel<__half, true, kWeighted>)
+                : go(combine_kernel<__half, false, kWeighted>);
+  return wide ? go(combine_kernel<__nv_bfloat16, true, kWeighted>)
+              : go(combine_kernel<__nv_bfloat16, false, kWeighted>);
 }
 
 }  // namespace
@@ -248,7 +354,7 @@ using namespace gb300;
 
 extern "C" int moe_sort_workspace_bytes(int64_t tokens, int top_k, int experts, uint64_t* bytes) {
   if (!bytes || tokens < 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || experts < 1 ||
-      experts > MOE_MAX_EXPERTS || tokens > INT_MAX / top_k)
+      experts > MOE_MAX_EXPERTS || tokens > MOE_MAX_SLOTS / top_k)
     return GEMM_ERR_INVALID_VALUE;
   *bytes = 0;
   return GEMM_OK;
@@ -268,15 +374,24 @@ extern "C" int moe_sort(int32_t* offsets, int32_t* rows, int32_t* pairs, const i
   if (need > 0 && !aligned_to(workspace, 16)) return GEMM_ERR_MISALIGNED;
   if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
   const int n = static_cast<int>(tokens * top_k);
-  const size_t smem = sizeof(int32_t) * kSortWarps * (experts + 2);
-  if (cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(int32_t) * kSortWarps * (MOE_MAX_EXPERTS + 2))) !=
-      cudaSuccess) {
+  const auto bytes = [](int keys) { return sizeof(int32_t) * ((kSortWarps + 1) * keys + kSortWarps); };
+  static std::once_flag once;
+  static cudaError_t granted = cudaSuccess;
+  std::call_once(once, [&] {
+    granted = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(bytes(MOE_MAX_EXPERTS + 1)));
+  });
+  if (granted != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  return launch_pdl(sort_kernel, dim3(1), dim3(kSortThreads), smem,
-                    static_cast<cudaStream_t>(stream), offsets, rows, pairs, ids, n, experts);
+  // One block walks up to 4 slots a thread; past that the runs are spread over
+  // a cluster (doubling up to 8 blocks).
+  unsigned blocks = 1;
+  while (blocks < 8 && n > static_cast<int>(4 * kSortThreads * blocks)) blocks *= 2;
+  return launch_pdl(sort_kernel, dim3(blocks), dim3(kSortThreads), bytes(experts + 1),
+                    static_cast<cudaStream_t>(stream), blocks, offsets, rows, pairs, ids, n,
+                    experts);
 }
 
 extern "C" int moe_dispatch(void* y, const void* x, int64_t ldx, int64_t hidden, int type,
@@ -289,9 +404,9 @@ extern "C" int moe_dispatch(void* y, const void* x, int64_t ldx, int64_t hidden,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RouteParams p = route_params(r, hidden);
   return rows_aligned({y, x}, hidden, ldx)
-             ? launch_pdl(dispatch_kernel<8>, grid, block, 0, s, static_cast<uint16_t*>(y),
+             ? launch_pdl(dispatch_kernel<true>, grid, block, 0, s, 1u, static_cast<uint16_t*>(y),
                           static_cast<const uint16_t*>(x), ldx, p)
-             : launch_pdl(dispatch_kernel<1>, grid, block, 0, s, static_cast<uint16_t*>(y),
+             : launch_pdl(dispatch_kernel<false>, grid, block, 0, s, 1u, static_cast<uint16_t*>(y),
                           static_cast<const uint16_t*>(x), ldx, p);
 }
 
@@ -323,12 +438,13 @@ extern "C" int moe_combine_backward(void* grad_y, float* grad_weights, const voi
   const int64_t blocks = (n + kRowThreads / 32 - 1) / (kRowThreads / 32);
   const auto go = [&](auto kernel) {
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRowThreads), 0,
-                      static_cast<cudaStream_t>(stream), static_cast<uint16_t*>(grad_y),
+                      static_cast<cudaStream_t>(stream), 1u, static_cast<uint16_t*>(grad_y),
                       grad_weights, static_cast<const uint16_t*>(grad_out),
                       static_cast<const uint16_t*>(y), weights, route_params(r, hidden));
   };
   if (type == MOE_F16)
-    return wide ? go(combine_backward_kernel<__half, 8>) : go(combine_backward_kernel<__half, 1>);
-  return wide ? go(combine_backward_kernel<__nv_bfloat16, 8>)
-              : go(combine_backward_kernel<__nv_bfloat16, 1>);
+    return wide ? go(combine_backward_kernel<__half, true>)
+                : go(combine_backward_kernel<__half, false>);
+  return wide ? go(combine_backward_kernel<__nv_bfloat16, true>)
+              : go(combine_backward_kernel<__nv_bfloat16, false>);
 }

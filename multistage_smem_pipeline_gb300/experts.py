@@ -13,7 +13,6 @@ Tensors given as `out` are written in place; without it one is allocated.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
 
 import torch
 
@@ -44,6 +43,9 @@ class _MatrixC(ctypes.Structure):
                 ("offsets", ctypes.c_void_p)]
 
 
+_FUNCTIONS = {}
+
+
 def _declare():
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     pr, pm, pu = ctypes.POINTER(_RoutingC), ctypes.POINTER(_MatrixC), ctypes.POINTER(ctypes.c_uint64)
@@ -62,34 +64,39 @@ def _declare():
             "moe_combine_backward": [vp, vp, vp, vp, vp, i64, i32, pr, vp]}.items():
         f = getattr(LIB, name)
         f.argtypes, f.restype = args, i32
+        _FUNCTIONS[name] = f
 
 
 _declare()
 
 
-def _call(name: str, device: torch.device, *args):
-    """The C function with the stream's device current."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        rc = getattr(LIB, name)(*args)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
+
+
+def _call(name: str, x: torch.Tensor, stream, *args):
+    """The C function on `stream` (default: the current one of x's device), with that device
+    current."""
+    index = x.get_device()
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = _FUNCTIONS[name](*args, handle)
     else:
-        with torch.cuda.device(device):
-            rc = getattr(LIB, name)(*args)
-    if rc != GEMM_OK:
+        with torch.cuda.device(index):
+            rc = _FUNCTIONS[name](*args, handle)
+    if rc:
         raise GemmError(rc, name)
 
 
-def _stream(stream, device: torch.device) -> int:
-    return int((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
-
-
-def _matrix(x: torch.Tensor, what: str) -> None:
-    """x is a CUDA matrix of a supported type with contiguous rows."""
-    if x.dtype not in TYPES:
+def _matrix(x: torch.Tensor, what: str) -> int:
+    """x's type number; x must be a CUDA matrix of a supported type with contiguous rows."""
+    kind = TYPES.get(x.dtype)
+    if kind is None:
         raise TypeError(f"{what} must be float16 or bfloat16")
     if x.dim() != 2 or not x.is_cuda:
         raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    if not x.is_contiguous() and x.shape[1] > 1 and x.stride(1) != 1:
         raise ValueError(f"{what}'s rows must be contiguous")
+    return kind
 
 
 def _out(out, shape, dtype, device, what: str) -> torch.Tensor:
@@ -102,41 +109,95 @@ def _out(out, shape, dtype, device, what: str) -> torch.Tensor:
     return out
 
 
-def _row_stride(x: torch.Tensor) -> int:
+def _row_stride(x: torch.Tensor, cols: int) -> int:
     """Elements between rows (a tensor of one row may report any stride)."""
-    return max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
+    return max(x.stride(0), cols) if x.shape[0] > 1 else cols
 
 
-@dataclass
 class Routing:
     """Where each slot (token, j) went: rows[token, j] is its row in expert order, pairs the
     inverse, and expert e has rows offsets[e] to offsets[e + 1] - 1.  Dropped slots have the
-    rows from offsets[-1] on.  All int32, on the device."""
-    offsets: torch.Tensor
-    rows: torch.Tensor
-    pairs: torch.Tensor
-    ids: torch.Tensor
+    rows from offsets[-1] on.  All int32, on the device.  moe_sort makes one; a program with a
+    router of its own can give the tensors itself."""
+
+    __slots__ = ("ids", "tokens", "top_k", "experts", "_buffer", "_offsets", "_rows", "_pairs",
+                 "_c", "_ref")
+
+    def __init__(self, offsets: torch.Tensor, rows: torch.Tensor, pairs: torch.Tensor,
+                 ids: torch.Tensor):
+        for t, what in ((offsets, "offsets"), (rows, "rows"), (pairs, "pairs"), (ids, "ids")):
+            if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() \
+                    or t.device != ids.device:
+                raise ValueError(f"{what} must be a contiguous int32 CUDA tensor on ids's device")
+        if ids.dim() != 2 or rows.shape != ids.shape or pairs.numel() != ids.numel() \
+                or offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("ids and rows must be tokens x top_k, pairs as many, and offsets "
+                             "experts + 1")
+        self._offsets, self._rows, self._pairs, self._buffer = offsets, rows, pairs, None
+        self._set(ids, offsets.numel() - 1, offsets.data_ptr(), rows.data_ptr(), pairs.data_ptr())
+
+    def _set(self, ids, experts, offsets, rows, pairs):
+        self.ids, self.experts = ids, experts
+        self.tokens, self.top_k = ids.shape
+        self._c = _RoutingC(self.tokens, self.top_k, experts, offsets, rows, pairs, ids.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def _empty(cls, ids: torch.Tensor, experts: int) -> "Routing":
+        """Unwritten: one allocation for the three arrays, each on a 16-byte boundary; the
+        tensors are made when they are asked for."""
+        self = cls.__new__(cls)
+        n, head = ids.numel() + 3 & ~3, experts + 4 & ~3
+        self._buffer = torch.empty(head + 2 * n, dtype=torch.int32, device=ids.device)
+        self._offsets = self._rows = self._pairs = None
+        at = self._buffer.data_ptr()
+        self._set(ids, experts, at, at + 4 * head, at + 4 * (head + n))
+        return self
 
     @property
-    def tokens(self) -> int:
-        return self.ids.shape[0]
+    def offsets(self) -> torch.Tensor:
+        if self._offsets is None:
+            self._offsets = self._buffer[:self.experts + 1]
+        return self._offsets
 
     @property
-    def top_k(self) -> int:
-        return self.ids.shape[1]
+    def rows(self) -> torch.Tensor:
+        if self._rows is None:
+            head = self.experts + 4 & ~3
+            self._rows = self._buffer.as_strided((self.tokens, self.top_k), (self.top_k, 1), head)
+        return self._rows
 
     @property
-    def experts(self) -> int:
-        return self.offsets.shape[0] - 1
+    def pairs(self) -> torch.Tensor:
+        if self._pairs is None:
+            head, n = self.experts + 4 & ~3, self.slots + 3 & ~3
+            self._pairs = self._buffer[head + n:head + n + self.slots]
+        return self._pairs
 
     @property
     def slots(self) -> int:
-        return self.ids.numel()
+        return self.tokens * self.top_k
 
-    def _c(self) -> _RoutingC:
-        return _RoutingC(self.ids.shape[0], self.ids.shape[1], self.offsets.shape[0] - 1,
-                         self.offsets.data_ptr(), self.rows.data_ptr(), self.pairs.data_ptr(),
-                         self.ids.data_ptr())
+    @property
+    def device(self) -> torch.device:
+        return self.ids.device
+
+
+def _layout(rows: int, cols: int, form: str, group_rows: int | None, routing: Routing | None):
+    """(groups, rows of a uniform group, bytes of a row's codes, tiles, chunks of a tile)."""
+    if form not in FORMATS:
+        raise ValueError(f"unknown format {form!r}")
+    chunks = -(-cols // 256) * (4 if form == "nvfp4" else 2)
+    pitch = (cols + 31) // 32 * 16
+    if routing is not None:
+        if group_rows is not None or rows != routing.tokens * routing.top_k:
+            raise ValueError("a matrix in expert order has a row per slot and no group_rows")
+        return routing.experts, 0, pitch, rows // 128 + routing.experts, chunks
+    g = rows if group_rows is None else int(group_rows)
+    if g < 0 or (rows % g if g else rows):
+        raise ValueError(f"{rows} rows are not whole groups of {g}")
+    groups = max(rows // g, 1) if g else 1
+    return groups, g, pitch, groups * -(-g // 128), chunks
 
 
 class Fp4Matrix:
@@ -146,55 +207,66 @@ class Fp4Matrix:
     group_rows: rows of each group (for weights of several experts, one expert's outputs; default:
     all rows are one group).  Instead, `routing` marks rows in expert order."""
 
-    __slots__ = ("codes", "scales", "cols", "format", "exponent", "group_rows", "routing", "groups")
+    __slots__ = ("rows", "cols", "format", "exponent", "group_rows", "routing", "groups", "_shape",
+                 "_buffer", "_codes", "_scales", "_c", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, *, cols: int,
                  format: str = "nvfp4", exponent: int = 0, group_rows: int | None = None,
                  routing: Routing | None = None):
-        if format not in FORMATS:
-            raise ValueError(f"unknown format {format!r}")
         if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
             raise TypeError("codes and scales must be uint8")
         if not (codes.is_cuda and scales.is_cuda) or codes.device != scales.device:
             raise ValueError("codes and scales must be CUDA tensors on one device")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        pitch = (cols + 31) // 32 * 16
-        if codes.dim() != 2 or codes.shape[1] != pitch:
-            raise ValueError(f"codes must be rows x {pitch}, got {tuple(codes.shape)}")
-        rows = codes.shape[0]
-        if routing is not None:
-            if group_rows is not None or rows != routing.slots:
-                raise ValueError("a matrix in expert order has a row per slot and no group_rows")
-            self.groups, group_rows = routing.experts, 0
-            tiles = rows // 128 + self.groups
-        else:
-            group_rows = rows if group_rows is None else int(group_rows)
-            if group_rows < 0 or (rows % group_rows if group_rows else rows):
-                raise ValueError(f"{rows} rows are not whole groups of {group_rows}")
-            self.groups = max(rows // group_rows, 1) if group_rows else 1
-            tiles = self.groups * -(-group_rows // 128)
-        need = tiles * -(-cols // 256) * (4 if format == "nvfp4" else 2) * 512
-        if scales.numel() < need:
-            raise ValueError(f"scales must have {need} bytes, got {scales.numel()}")
-        self.codes, self.scales, self.cols = codes, scales, int(cols)
-        self.format, self.exponent = format, int(exponent)
-        self.group_rows, self.routing = group_rows, routing
+        if codes.dim() != 2:
+            raise ValueError("codes must be a matrix")
+        shape = _layout(codes.shape[0], cols, format, group_rows, routing)
+        if codes.shape[1] != shape[2]:
+            raise ValueError(f"codes must be rows x {shape[2]}, got {tuple(codes.shape)}")
+        if scales.numel() < shape[3] * shape[4] * 512:
+            raise ValueError(f"scales must have {shape[3] * shape[4] * 512} bytes, "
+                             f"got {scales.numel()}")
+        self._codes, self._scales, self._buffer = codes, scales, None
+        self._set(codes.shape[0], cols, format, exponent, routing, shape, codes.data_ptr(),
+                  scales.data_ptr())
+
+    def _set(self, rows, cols, form, exponent, routing, shape, codes, scales):
+        self.rows, self.cols, self.format, self.exponent = rows, int(cols), form, int(exponent)
+        self.groups, self.group_rows, self.routing, self._shape = shape[0], shape[1], routing, shape
+        self._c = _MatrixC(codes, scales, rows, self.cols, FORMATS[form], self.exponent, shape[0],
+                           0, shape[1], None if routing is None else routing._c.offsets)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def _empty(cls, rows, cols, form, exponent, group_rows, routing, device) -> "Fp4Matrix":
+        """Unwritten: one allocation for scales and codes; the tensors are made when asked for."""
+        self = cls.__new__(cls)
+        shape = _layout(rows, cols, form, group_rows, routing)
+        scales = shape[3] * shape[4] * 512
+        self._buffer = torch.empty(scales + rows * shape[2], dtype=torch.uint8, device=device)
+        self._codes = self._scales = None
+        at = self._buffer.data_ptr()
+        self._set(rows, cols, form, exponent, routing, shape, at + scales, at)
+        return self
 
     @property
-    def rows(self) -> int:
-        return self.codes.shape[0]
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            tiles, chunks = self._shape[3:]
+            self._scales = self._buffer[:tiles * chunks * 512].view(tiles, chunks, 512)
+        return self._scales
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            tiles, chunks = self._shape[3:]
+            self._codes = self._buffer[tiles * chunks * 512:].view(self.rows, self._shape[2])
+        return self._codes
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
-
-    def _c(self) -> _MatrixC:
-        return _MatrixC(self.codes.data_ptr(), self.scales.data_ptr(), self.codes.shape[0],
-                        self.cols, FORMATS[self.format], self.exponent, self.groups, 0,
-                        self.group_rows,
-                        self.routing.offsets.data_ptr() if self.routing is not None else None)
-
+        return (self._buffer if self._buffer is not None else self._codes).device
 
 def _bytes(name: str, *args) -> int:
     n = ctypes.c_uint64(0)
@@ -216,35 +288,22 @@ def fp4_quantize(x: torch.Tensor, *, format: str = "nvfp4", exponent: int = 0,
     """x (rows x cols, float16 or bfloat16, rows contiguous) as an Fp4Matrix.
 
     With a routing, x has a row per token and the result a row per slot, in expert order."""
-    _matrix(x, "x")
-    if format not in FORMATS:
-        raise ValueError(f"unknown format {format!r}")
+    kind = _matrix(x, "x")
     rows, cols = x.shape
     if routing is not None:
         if rows != routing.tokens:
             raise ValueError(f"x has {rows} rows, the routing {routing.tokens} tokens")
-        if routing.offsets.device != x.device:
+        if routing.device != x.device:
             raise ValueError("x and the routing are on different devices")
         rows = routing.slots
     if out is None:
-        pitch = (cols + 31) // 32 * 16
-        if routing is not None:
-            tiles = rows // 128 + routing.experts
-        else:
-            g = rows if group_rows is None else int(group_rows)
-            tiles = rows // g * -(-g // 128) if g > 0 else 0
-        chunks = -(-cols // 256) * (4 if format == "nvfp4" else 2)
-        out = Fp4Matrix(torch.empty((rows, pitch), dtype=torch.uint8, device=x.device),
-                        torch.empty((tiles, chunks, 512), dtype=torch.uint8, device=x.device),
-                        cols=cols, format=format, exponent=exponent, group_rows=group_rows,
-                        routing=routing)
+        out = Fp4Matrix._empty(rows, cols, format, exponent, group_rows, routing, x.device)
     elif out.rows != rows or out.cols != cols or out.format != format \
             or out.exponent != exponent or out.routing is not routing or out.device != x.device \
             or (group_rows is not None and out.group_rows != group_rows):
         raise ValueError("out does not fit x, the format or the groups")
-    _call("fp4_quantize", x.device, ctypes.byref(out._c()), x.data_ptr(), _row_stride(x),
-          TYPES[x.dtype], ctypes.byref(routing._c()) if routing is not None else None,
-          _stream(stream, x.device))
+    _call("fp4_quantize", x, stream, out._ref, x.data_ptr(), _row_stride(x, cols), kind,
+          None if routing is None else routing._ref)
     return out
 
 
@@ -254,8 +313,7 @@ def fp4_dequantize(q: Fp4Matrix, dtype: torch.dtype = torch.float16,
     if dtype not in TYPES:
         raise TypeError("dtype must be float16 or bfloat16")
     out = _out(out, (q.rows, q.cols), dtype, q.device, "out")
-    _call("fp4_dequantize", q.device, out.data_ptr(), TYPES[dtype], ctypes.byref(q._c()),
-          _stream(stream, q.device))
+    _call("fp4_dequantize", out, stream, out.data_ptr(), TYPES[dtype], q._ref)
     return out
 
 
@@ -267,11 +325,11 @@ def fp4_gemm_tn(a: Fp4Matrix, b: Fp4Matrix, *, alpha: float = 1.0,
     zeros.  b has as many groups as a, each of b.group_rows outputs."""
     if dtype not in TYPES:
         raise TypeError("dtype must be float16 or bfloat16")
-    if a.device != b.device:
+    device = a.device
+    if device != b.device:
         raise ValueError("a and b are on different devices")
-    out = _out(out, (a.rows, b.group_rows), dtype, a.device, "out")
-    _call("fp4_gemm_tn", a.device, out.data_ptr(), TYPES[dtype], ctypes.byref(a._c()),
-          ctypes.byref(b._c()), float(alpha), _stream(stream, a.device))
+    out = _out(out, (a.rows, b.group_rows), dtype, device, "out")
+    _call("fp4_gemm_tn", out, stream, out.data_ptr(), TYPES[dtype], a._ref, b._ref, alpha)
     return out
 
 
@@ -299,34 +357,34 @@ def moe_sort(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = N
     elif workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != ids.device
                                     or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on ids's device")
-    r = Routing(torch.empty(experts + 1, dtype=torch.int32, device=ids.device),
-                torch.empty_like(ids),
-                torch.empty(ids.numel(), dtype=torch.int32, device=ids.device), ids)
-    _call("moe_sort", ids.device, r.offsets.data_ptr(), r.rows.data_ptr(), r.pairs.data_ptr(),
-          ids.data_ptr(), ids.shape[0], ids.shape[1], experts,
-          workspace.data_ptr() if workspace is not None else None,
-          workspace.numel() if workspace is not None else 0, _stream(stream, ids.device))
+    r = Routing._empty(ids, experts)
+    c = r._c
+    _call("moe_sort", ids, stream, c.offsets, c.rows, c.pairs, c.ids, c.tokens, c.top_k, experts,
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel())
     return r
 
 
-def _by_token(x: torch.Tensor, routing: Routing, what: str) -> None:
-    _matrix(x, what)
-    if x.shape[0] != routing.tokens or x.device != routing.offsets.device:
+def _by_token(x: torch.Tensor, routing: Routing, what: str) -> int:
+    kind = _matrix(x, what)
+    if x.shape[0] != routing.tokens or x.device != routing.device:
         raise ValueError(f"{what} must have the routing's {routing.tokens} rows, on its device")
+    return kind
 
 
-def _by_slot(y: torch.Tensor, routing: Routing, what: str) -> None:
-    _matrix(y, what)
-    if y.shape[0] != routing.slots or not y.is_contiguous() or y.device != routing.offsets.device:
+def _by_slot(y: torch.Tensor, routing: Routing, what: str) -> int:
+    kind = _matrix(y, what)
+    if y.shape[0] != routing.slots or not y.is_contiguous() or y.device != routing.device:
         raise ValueError(f"{what} must be contiguous with the routing's {routing.slots} rows, "
                          "on its device")
+    return kind
 
 
 def _weights(weights: torch.Tensor, routing: Routing) -> None:
     if weights.dtype != torch.float32:
         raise TypeError("weights must be float32")
     if weights.shape != routing.ids.shape or not weights.is_contiguous() \
-            or weights.device != routing.offsets.device:
+            or weights.device != routing.device:
         raise ValueError("weights must be contiguous, of the routing's tokens x top_k, "
                          "on its device")
 
@@ -334,47 +392,47 @@ def _weights(weights: torch.Tensor, routing: Routing) -> None:
 def moe_dispatch(x: torch.Tensor, routing: Routing, out: torch.Tensor | None = None,
                  stream=None) -> torch.Tensor:
     """x's rows (a row per token) in expert order, a row per slot; zeros for dropped slots."""
-    _by_token(x, routing, "x")
-    out = _out(out, (routing.slots, x.shape[1]), x.dtype, x.device, "out")
-    _call("moe_dispatch", x.device, out.data_ptr(), x.data_ptr(), _row_stride(x), x.shape[1],
-          TYPES[x.dtype], ctypes.byref(routing._c()), _stream(stream, x.device))
+    kind = _by_token(x, routing, "x")
+    hidden = x.shape[1]
+    out = _out(out, (routing.slots, hidden), x.dtype, x.device, "out")
+    _call("moe_dispatch", x, stream, out.data_ptr(), x.data_ptr(), _row_stride(x, hidden), hidden,
+          kind, routing._ref)
     return out
 
 
 def moe_dispatch_backward(grad_y: torch.Tensor, routing: Routing, out: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """moe_dispatch's gradient: each token's sum over its kept slots."""
-    _by_slot(grad_y, routing, "grad_y")
-    out = _out(out, (routing.tokens, grad_y.shape[1]), grad_y.dtype, grad_y.device, "out")
-    _call("moe_dispatch_backward", grad_y.device, out.data_ptr(), grad_y.data_ptr(),
-          grad_y.shape[1], TYPES[grad_y.dtype], ctypes.byref(routing._c()),
-          _stream(stream, grad_y.device))
+    kind = _by_slot(grad_y, routing, "grad_y")
+    hidden = grad_y.shape[1]
+    out = _out(out, (routing.tokens, hidden), grad_y.dtype, grad_y.device, "out")
+    _call("moe_dispatch_backward", out, stream, out.data_ptr(), grad_y.data_ptr(), hidden, kind,
+          routing._ref)
     return out
 
 
 def moe_combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Each token's weighted sum of its kept slots' rows of y.  weights: tokens x top_k float32."""
-    _by_slot(y, routing, "y")
+    kind = _by_slot(y, routing, "y")
     _weights(weights, routing)
-    out = _out(out, (routing.tokens, y.shape[1]), y.dtype, y.device, "out")
-    _call("moe_combine", y.device, out.data_ptr(), y.data_ptr(), weights.data_ptr(), y.shape[1],
-          TYPES[y.dtype], ctypes.byref(routing._c()), _stream(stream, y.device))
+    hidden = y.shape[1]
+    out = _out(out, (routing.tokens, hidden), y.dtype, y.device, "out")
+    _call("moe_combine", out, stream, out.data_ptr(), y.data_ptr(), weights.data_ptr(), hidden,
+          kind, routing._ref)
     return out
 
 
 def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor, routing: Routing,
                          weights: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """moe_combine's gradients: (of y, of weights); zeros for dropped slots."""
-    _by_token(grad_out, routing, "grad_out")
-    _by_slot(y, routing, "y")
-    _weights(weights, routing)
-    if grad_out.dtype != y.dtype or grad_out.shape[1] != y.shape[1] \
+    kind = _by_slot(y, routing, "y")
+    if _by_token(grad_out, routing, "grad_out") != kind or grad_out.shape[1] != y.shape[1] \
             or not grad_out.is_contiguous():
         raise ValueError("grad_out must be contiguous, of y's type and width")
+    _weights(weights, routing)
     grad_y = torch.empty_like(y)
     grad_w = torch.empty_like(weights)
-    _call("moe_combine_backward", y.device, grad_y.data_ptr(), grad_w.data_ptr(),
-          grad_out.data_ptr(), y.data_ptr(), weights.data_ptr(), y.shape[1], TYPES[y.dtype],
-          ctypes.byref(routing._c()), _stream(stream, y.device))
+    _call("moe_combine_backward", y, stream, grad_y.data_ptr(), grad_w.data_ptr(),
+          grad_out.data_ptr(), y.data_ptr(), weights.data_ptr(), y.shape[1], kind, routing._ref)
     return grad_y, grad_w
