@@ -118,12 +118,10 @@ int fp4_get_device_error(void* stream, uint32_t* raw);
  * outside [0, experts) marks a dropped slot.  rows[p] is slot p's place among
  * all slots ordered by expert, then by p, the dropped ones last; pairs is its
  * inverse; offsets[e] is the first row of expert e and offsets[experts] the
- * number of slots kept.  The workspace is 16-byte aligned, of
- * moe_sort_workspace_bytes() bytes (0: none is needed).
+ * number of slots kept.
  */
-int moe_sort_workspace_bytes(int64_t tokens, int top_k, int experts, uint64_t* bytes);
 int moe_sort(int32_t* offsets, int32_t* rows, int32_t* pairs, const int32_t* ids, int64_t tokens,
-             int top_k, int experts, void* workspace, uint64_t workspace_bytes, void* stream);
+             int top_k, int experts, void* stream);
 
 /* In what follows x, out and their gradients are tokens x hidden, y and its
  * gradient (tokens * top_k) x hidden in row order; all of `type` (2-byte

@@ -20,9 +20,10 @@ def __getattr__(name):
     # the CUDA library is loaded on first use, so that importing the package
     # (e.g. for ``synthetic``) works on machines without it
     if name in _EXPORTS:
-        from . import binding
-        return getattr(binding, name)
-    if name in _EXPERTS:
-        from . import experts
-        return getattr(experts, name)
-    raise AttributeError(name)
+        from . import binding as module
+    elif name in _EXPERTS:
+        from . import experts as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(module, name)  # the next look-up finds it here
+    return value

@@ -42,16 +42,49 @@ __device__ __forceinline__ Raw load_raw(const uint16_t* row, int64_t c, int64_t 
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void widen(const Raw& r, int64_t c, int64_t cols, float (&f)[kSegment]) {
-  const T* const e = reinterpret_cast<const T*>(&r);
+// Zeroes the elements at `cols` and past it.
+__device__ __forceinline__ void clip(Raw& r, int64_t c, int64_t cols) {
+  if (c + kSegment <= cols) return;
 #pragma unroll
-  for (int i = 0; i < kSegment; ++i) f[i] = to_float(e[i]);
-  if (c + kSegment > cols) {
-#pragma unroll
-    for (int i = 0; i < kSegment; ++i)
-      if (c + i >= cols) f[i] = 0.0f;
+  for (int i = 0; i < kSegment / 2; ++i) {
+    uint32_t& w = r.p[i >> 2].w[i & 3];
+    if (c + 2 * i >= cols) w = 0;
+    else if (c + 2 * i + 1 >= cols) w &= 0xffffu;
   }
+}
+
+// Magnitudes of two elements, and the larger of two such pairs, each half for
+// itself; a NaN in either wins.
+template <typename T>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_pair<__half>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t max_pair<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two fp32 products, or fused products and sums, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
 }
 
 struct Segment {
@@ -59,44 +92,56 @@ struct Segment {
   uint32_t scale;  // byte
 };
 
-// f / (scale 2^exponent) to codes.  FP4_MX: called by whole warps, the two
-// threads of a block being neighbours.
+// 16 elements to codes and their block's scale.  FP4_MX: called by whole
+// warps, the two threads of a block being neighbours.
 //
 // The quotient must round to E2M1 as the exact one does, ties included, and
 // x times the rounded reciprocal does not always: for scales of significand
-// 13/8 to 15/8 some exact ties move.  One residual step (Markstein) puts it
-// right: q = x r, q + r (x - q s).  Checked for every fp16 and bf16 value
-// against every scale.
-template <int kFormat>
-__device__ __forceinline__ Segment quantize_segment(float (&f)[kSegment], const Fp4View& v) {
-  float top = 0.0f;
+// 13/8 to 15/8 some exact ties move.  So the reciprocal is held in two parts,
+// hi + lo, and the quotient is fma(x, hi, x lo): within 2^-24 of the exact
+// one after a single rounding, hence equal to it at a tie (which fp32 holds),
+// and never across one, as x and a tie that differ do so by at least 2^-11.
+// Checked for every fp16 and bf16 value against every scale.  The powers of
+// two of the exponent go into the two parts.
+template <typename T, int kFormat>
+__device__ __forceinline__ Segment quantize_segment(const Raw& raw, const Fp4View& v) {
+  uint32_t both = 0;  // largest magnitudes of the even and the odd elements
 #pragma unroll
-  for (int i = 0; i < kSegment; ++i) {
-    if (kFormat == FP4_NV) f[i] *= v.down;
-    // as bits, so that a NaN is larger than everything
-    top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(f[i]) & 0x7fffffffu));
-  }
+  for (int i = 0; i < kSegment / 2; ++i)
+    both = max_pair<T>(both, raw.p[i >> 2].w[i & 3] & 0x7fff7fffu);
+  const T* const halves = reinterpret_cast<const T*>(&both);
+  // compared as bits, so that a NaN is larger than everything
+  uint32_t top = max(__float_as_uint(to_float(halves[0])), __float_as_uint(to_float(halves[1])));
   Segment s;
+  float hi, lo = 0.0f;
+  bool finite;
   if (kFormat == FP4_NV) {
-    const bool finite = __float_as_uint(top) < 0x7f800000u;
-    s.scale = finite ? to_e4m3(__fdiv_rn(top, 6.0f)) : kNanE4M3;
+    const float scaled = __uint_as_float(top) * v.down;
+    finite = __float_as_uint(scaled) < 0x7f800000u;
+    s.scale = finite ? to_e4m3(__fdiv_rn(scaled, 6.0f)) : kNanE4M3;
     const float step = finite ? from_e4m3(s.scale) : 0.0f;
-    const float inv = step > 0.0f ? __frcp_rn(step) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kSegment; ++i) {
-      const float q = f[i] * inv;
-      f[i] = finite ? fmaf(fmaf(-q, step, f[i]), inv, q) : 0.0f;
-    }
+    hi = step > 0.0f ? __frcp_rn(step) : 0.0f;
+    lo = fmaf(-hi, step, 1.0f) * hi * v.down;
+    hi *= v.down;
   } else {
-    top = __uint_as_float(max(__float_as_uint(top),
-                              __shfl_xor_sync(0xffffffffu, __float_as_uint(top), 1)));
-    const int field = static_cast<int>(__float_as_uint(top) >> 23);
-    s.scale = field == 0xff ? kNanE8M0 : static_cast<uint32_t>(max(field - 2, 0));
-    const float inv = field == 0xff ? 0.0f : __uint_as_float((254u - s.scale) << 23);
-#pragma unroll
-    for (int i = 0; i < kSegment; ++i) f[i] = field == 0xff ? 0.0f : f[i] * inv;
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const int field = static_cast<int>(top >> 23);
+    finite = field != 0xff;
+    s.scale = finite ? static_cast<uint32_t>(max(field - 2, 0)) : kNanE8M0;
+    hi = finite ? __uint_as_float((254u - s.scale) << 23) : 0.0f;
   }
-  s.codes = make_uint2(to_e2m1(f), to_e2m1(f + 8));
+  float q[kSegment];
+#pragma unroll
+  for (int i = 0; i < kSegment; i += 2) {
+    const T* const e = reinterpret_cast<const T*>(&raw.p[i >> 3].w[(i >> 1) & 3]);
+    const float2 x = make_float2(to_float(e[0]), to_float(e[1]));
+    float2 y;
+    if (kFormat == FP4_NV) y = fma2(x, make_float2(hi, hi), mul2(x, make_float2(lo, lo)));
+    else y = mul2(x, make_float2(hi, hi));
+    q[i] = y.x;
+    q[i + 1] = y.y;
+  }
+  s.codes = finite ? make_uint2(to_e2m1(q), to_e2m1(q + 8)) : make_uint2(0, 0);
   return s;
 }
 
@@ -128,9 +173,8 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < C::kSteps; ++i) {
     const int r = r0 + i * C::kRowsAtOnce;
     if (i * C::kRowsAtOnce >= t.count) break;
-    float f[kSegment];
-    widen<T>(raw[i], c, v.cols, f);
-    const Segment s = quantize_segment<kFormat>(f, v);
+    clip(raw[i], c, v.cols);
+    const Segment s = quantize_segment<T, kFormat>(raw[i], v);
     if (r >= t.count) continue;
     if (c / 2 < v.pitch)
       *reinterpret_cast<uint2*>(v.codes + (t.row + r) * v.pitch + c / 2) = s.codes;
@@ -157,9 +201,9 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t seg = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
   const int64_t c = seg * kSegment;
   const int64_t cols256 = col_stages(v.cols) * kStageCols;
-  float f[kSegment];
-  widen<T>(load_raw<kVec>(x + token * ldx, c, v.cols), c, v.cols, f);
-  const Segment s = quantize_segment<kFormat>(f, v);
+  Raw raw = load_raw<kVec>(x + token * ldx, c, v.cols);
+  clip(raw, c, v.cols);
+  const Segment s = quantize_segment<T, kFormat>(raw, v);
   // bytes of the chunk's four blocks, in every thread
   constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
   uint32_t word = (c < v.cols ? s.scale : 0u) << (8 * (seg / kPerBlock & 3));
@@ -210,11 +254,11 @@ __global__ void __launch_bounds__(kThreads)
     reinterpret_cast<uint4*>(scales)[threadIdx.x] = reinterpret_cast<const uint4*>(
         v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(chunk) * kChunkBytes)[threadIdx.x];
   __syncthreads();
-  if (c >= v.cols) return;
+  __shared__ __align__(16) uint16_t staged[kVec ? 8 : C::kRowsAtOnce * C::kCols];
 #pragma unroll
   for (int i = 0; i < C::kSteps; ++i) {
+    if (i * C::kRowsAtOnce >= t.count) break;
     const int r = r0 + i * C::kRowsAtOnce;
-    if (r >= t.count) return;
     float f[kSegment] = {};
     if (t.tile >= 0) {
       from_e2m1(codes[i].x, f);
@@ -224,20 +268,43 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int e = 0; e < kSegment; ++e) f[e] *= step;
     }
-    uint16_t* const row = y + (t.row + r) * v.cols;
-    if (kVec && c + kSegment <= v.cols) {
-      float lo[8], hi[8];
+    float half[8];
+    Pack p[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = f[e];
-        hi[e] = f[8 + e];
-      }
-      store8<true>(row, c, v.cols, pack<T>(lo));
-      store8<true>(row, c + 8, v.cols, pack<T>(hi));
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) half[e] = f[8 * h + e];
+      p[h] = pack<T>(half);
+    }
+    if (kVec) {
+      // Neighbours swap halves, so that a warp's store covers 32-byte sectors
+      // whole: first both halves of the even segment, then of the odd one.
+      const bool odd = seg & 1;
+      Pack other;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        other.w[w] = __shfl_xor_sync(0xffffffffu, odd ? p[0].w[w] : p[1].w[w], 1);
+      if (r >= t.count) continue;
+      uint16_t* const row = y + (t.row + r) * v.cols;
+      const int64_t even = c - (odd ? kSegment : 0);  // cols is a multiple of 8: pieces are whole
+      const int64_t first = even + (odd ? 8 : 0), second = first + kSegment;
+      if (first < v.cols) store8<true>(row, first, v.cols, odd ? other : p[0]);
+      if (second < v.cols) store8<true>(row, second, v.cols, odd ? p[1] : other);
     } else {
-#pragma unroll
-      for (int e = 0; e < kSegment; ++e)
-        if (c + e < v.cols) reinterpret_cast<T*>(row)[c + e] = from_float<T>(f[e]);
+      // Rows start anywhere: through shared memory, then element by element
+      // with neighbouring lanes on neighbouring elements.
+      *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment) = p[0];
+      *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment + 8) = p[1];
+      __syncthreads();
+      const int rows = min(C::kRowsAtOnce, t.count - i * C::kRowsAtOnce);
+      const int64_t c0 = static_cast<int64_t>(chunk) * C::kCols;
+      const int cols = static_cast<int>(min(static_cast<int64_t>(C::kCols), v.cols - c0));
+      uint16_t* const to = y + (t.row + i * C::kRowsAtOnce) * v.cols + c0;
+      for (int w = threadIdx.x; w < rows * C::kCols; w += kThreads) {
+        const int rr = w / C::kCols, cc = w % C::kCols;
+        if (cc < cols) to[rr * v.cols + cc] = staged[w];
+      }
+      __syncthreads();
     }
   }
 }

@@ -352,27 +352,17 @@ int run_combine(void* out, const void* y, const float* weights, int64_t hidden, 
 
 using namespace gb300;
 
-extern "C" int moe_sort_workspace_bytes(int64_t tokens, int top_k, int experts, uint64_t* bytes) {
-  if (!bytes || tokens < 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || experts < 1 ||
+extern "C" int moe_sort(int32_t* offsets, int32_t* rows, int32_t* pairs, const int32_t* ids,
+                        int64_t tokens, int top_k, int experts, void* stream) {
+  if (tokens < 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || experts < 1 ||
       experts > MOE_MAX_EXPERTS || tokens > MOE_MAX_SLOTS / top_k)
     return GEMM_ERR_INVALID_VALUE;
-  *bytes = 0;
-  return GEMM_OK;
-}
-
-extern "C" int moe_sort(int32_t* offsets, int32_t* rows, int32_t* pairs, const int32_t* ids,
-                        int64_t tokens, int top_k, int experts, void* workspace,
-                        uint64_t workspace_bytes, void* stream) {
-  uint64_t need = 0;
-  int rc = moe_sort_workspace_bytes(tokens, top_k, experts, &need);
-  if (rc != GEMM_OK) return rc;
   if (!offsets || (tokens > 0 && (!rows || !pairs || !ids))) return GEMM_ERR_INVALID_VALUE;
   if (!aligned_to(offsets, 4) || !aligned_to(rows, 4) || !aligned_to(pairs, 4) ||
       !aligned_to(ids, 4))
     return GEMM_ERR_MISALIGNED;
-  if (need > 0 && (!workspace || workspace_bytes < need)) return GEMM_ERR_INVALID_VALUE;
-  if (need > 0 && !aligned_to(workspace, 16)) return GEMM_ERR_MISALIGNED;
-  if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
+  const int rc = require_device(nullptr);
+  if (rc != GEMM_OK) return rc;
   const int n = static_cast<int>(tokens * top_k);
   const auto bytes = [](int keys) { return sizeof(int32_t) * ((kSortWarps + 1) * keys + kSortWarps); };
   static std::once_flag once;

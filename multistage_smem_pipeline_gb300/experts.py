@@ -20,8 +20,7 @@ from . import binding as _b
 from .binding import GEMM_OK, GemmError, LIB
 
 EXPORTED = ("fp4_code_bytes", "fp4_scale_bytes", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
-            "fp4_get_device_error", "moe_sort_workspace_bytes", "moe_sort", "moe_dispatch",
-            "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+            "fp4_get_device_error", "moe_sort", "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
 
 TYPES = {torch.float16: 0, torch.bfloat16: 1}
 FORMATS = {"nvfp4": 0, "mxfp4": 1}
@@ -56,8 +55,7 @@ def _declare():
             "fp4_dequantize": [vp, i32, pm, vp],
             "fp4_gemm_tn": [vp, i32, pm, pm, ctypes.c_float, vp],
             "fp4_get_device_error": [vp, ctypes.POINTER(ctypes.c_uint32)],
-            "moe_sort_workspace_bytes": [i64, i32, i32, pu],
-            "moe_sort": [vp, vp, vp, vp, i64, i32, i32, vp, ctypes.c_uint64, vp],
+            "moe_sort": [vp, vp, vp, vp, i64, i32, i32, vp],
             "moe_dispatch": [vp, vp, i64, i64, i32, pr, vp],
             "moe_dispatch_backward": [vp, vp, i64, i32, pr, vp],
             "moe_combine": [vp, vp, vp, i64, i32, pr, vp],
@@ -71,6 +69,7 @@ _declare()
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index, without a Stream object
+_current_device = torch._C._cuda_getDevice
 
 
 def _call(name: str, x: torch.Tensor, stream, *args):
@@ -78,7 +77,7 @@ def _call(name: str, x: torch.Tensor, stream, *args):
     current."""
     index = x.get_device()
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = _FUNCTIONS[name](*args, handle)
     else:
         with torch.cuda.device(index):
@@ -120,8 +119,8 @@ class Routing:
     rows from offsets[-1] on.  All int32, on the device.  moe_sort makes one; a program with a
     router of its own can give the tensors itself."""
 
-    __slots__ = ("ids", "tokens", "top_k", "experts", "_buffer", "_offsets", "_rows", "_pairs",
-                 "_c", "_ref")
+    __slots__ = ("ids", "tokens", "top_k", "experts", "slots", "device", "_buffer", "_offsets",
+                 "_rows", "_pairs", "_c", "_ref")
 
     def __init__(self, offsets: torch.Tensor, rows: torch.Tensor, pairs: torch.Tensor,
                  ids: torch.Tensor):
@@ -137,8 +136,9 @@ class Routing:
         self._set(ids, offsets.numel() - 1, offsets.data_ptr(), rows.data_ptr(), pairs.data_ptr())
 
     def _set(self, ids, experts, offsets, rows, pairs):
-        self.ids, self.experts = ids, experts
+        self.ids, self.experts, self.device = ids, experts, ids.device
         self.tokens, self.top_k = ids.shape
+        self.slots = self.tokens * self.top_k
         self._c = _RoutingC(self.tokens, self.top_k, experts, offsets, rows, pairs, ids.data_ptr())
         self._ref = ctypes.byref(self._c)
 
@@ -174,14 +174,6 @@ class Routing:
             self._pairs = self._buffer[head + n:head + n + self.slots]
         return self._pairs
 
-    @property
-    def slots(self) -> int:
-        return self.tokens * self.top_k
-
-    @property
-    def device(self) -> torch.device:
-        return self.ids.device
-
 
 def _layout(rows: int, cols: int, form: str, group_rows: int | None, routing: Routing | None):
     """(groups, rows of a uniform group, bytes of a row's codes, tiles, chunks of a tile)."""
@@ -207,8 +199,8 @@ class Fp4Matrix:
     group_rows: rows of each group (for weights of several experts, one expert's outputs; default:
     all rows are one group).  Instead, `routing` marks rows in expert order."""
 
-    __slots__ = ("rows", "cols", "format", "exponent", "group_rows", "routing", "groups", "_shape",
-                 "_buffer", "_codes", "_scales", "_c", "_ref")
+    __slots__ = ("rows", "cols", "format", "exponent", "group_rows", "routing", "groups", "device",
+                 "_shape", "_buffer", "_codes", "_scales", "_c", "_ref")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, *, cols: int,
                  format: str = "nvfp4", exponent: int = 0, group_rows: int | None = None,
@@ -227,7 +219,7 @@ class Fp4Matrix:
         if scales.numel() < shape[3] * shape[4] * 512:
             raise ValueError(f"scales must have {shape[3] * shape[4] * 512} bytes, "
                              f"got {scales.numel()}")
-        self._codes, self._scales, self._buffer = codes, scales, None
+        self._codes, self._scales, self._buffer, self.device = codes, scales, None, codes.device
         self._set(codes.shape[0], cols, format, exponent, routing, shape, codes.data_ptr(),
                   scales.data_ptr())
 
@@ -246,6 +238,7 @@ class Fp4Matrix:
         scales = shape[3] * shape[4] * 512
         self._buffer = torch.empty(scales + rows * shape[2], dtype=torch.uint8, device=device)
         self._codes = self._scales = None
+        self.device = device
         at = self._buffer.data_ptr()
         self._set(rows, cols, form, exponent, routing, shape, at + scales, at)
         return self
@@ -263,10 +256,6 @@ class Fp4Matrix:
             tiles, chunks = self._shape[3:]
             self._codes = self._buffer[tiles * chunks * 512:].view(self.rows, self._shape[2])
         return self._codes
-
-    @property
-    def device(self) -> torch.device:
-        return (self._buffer if self._buffer is not None else self._codes).device
 
 def _bytes(name: str, *args) -> int:
     n = ctypes.c_uint64(0)
@@ -323,13 +312,13 @@ def fp4_gemm_tn(a: Fp4Matrix, b: Fp4Matrix, *, alpha: float = 1.0,
     """out[r] = alpha * a[r] @ b[g(r)]^T (fp32 accumulation): g(r) is the group of row r, so with
     activations in expert order each row meets its expert's weights; rows of dropped slots give
     zeros.  b has as many groups as a, each of b.group_rows outputs."""
-    if dtype not in TYPES:
+    kind = TYPES.get(dtype)
+    if kind is None:
         raise TypeError("dtype must be float16 or bfloat16")
-    device = a.device
-    if device != b.device:
+    if a.device != b.device:
         raise ValueError("a and b are on different devices")
-    out = _out(out, (a.rows, b.group_rows), dtype, device, "out")
-    _call("fp4_gemm_tn", out, stream, out.data_ptr(), TYPES[dtype], a._ref, b._ref, alpha)
+    out = _out(out, (a.rows, b.group_rows), dtype, a.device, "out")
+    _call("fp4_gemm_tn", out, stream, out.data_ptr(), kind, a._ref, b._ref, alpha)
     return out
 
 
@@ -340,8 +329,7 @@ def fp4_get_device_error(stream=None) -> tuple[int, int]:
     return rc, int(raw.value)
 
 
-def moe_sort(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None,
-             stream=None) -> Routing:
+def moe_sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
     """Slots sorted by expert.  ids: tokens x top_k int32; a number outside [0, experts) drops
     its slot.  The order within an expert is the slots' own."""
     if ids.dtype != torch.int32:
@@ -351,17 +339,9 @@ def moe_sort(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = N
     experts = int(experts)
     if not 1 <= experts <= MAX_EXPERTS or not 1 <= ids.shape[1] <= MAX_TOP_K:
         raise ValueError(f"1 to {MAX_EXPERTS} experts and 1 to {MAX_TOP_K} slots are supported")
-    need = _bytes("moe_sort_workspace_bytes", ids.shape[0], ids.shape[1], experts)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
-    elif workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != ids.device
-                                    or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on ids's device")
     r = Routing._empty(ids, experts)
     c = r._c
-    _call("moe_sort", ids, stream, c.offsets, c.rows, c.pairs, c.ids, c.tokens, c.top_k, experts,
-          None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else workspace.numel())
+    _call("moe_sort", ids, stream, c.offsets, c.rows, c.pairs, c.ids, r.tokens, r.top_k, experts)
     return r
 
 

@@ -63,9 +63,8 @@ def test_sizes(ex):
     for args in [(-1, 8, 0, 1, 0), (8, 2**23 + 1, 0, 1, 0), (8, 8, 2, 1, 0), (8, 8, 0, 0, 0),
                  (9, 8, 0, 2, 0), (8, 8, 0, 1025, 1), (8, 8, 0, 1, 2), (2**31, 8, 0, 1, 0)]:
         assert ex.LIB.fp4_scale_bytes(*args, ctypes.byref(n)) == E, args
-    assert ex.LIB.moe_sort_workspace_bytes(10, 2, 4, ctypes.byref(n)) == 0
     for args in [(-1, 2, 4), (10, 0, 4), (10, 65, 4), (10, 2, 0), (10, 2, 1025), (2**31, 1, 4)]:
-        assert ex.LIB.moe_sort_workspace_bytes(*args, ctypes.byref(n)) == E, args
+        assert ex.LIB.moe_sort(P[0], P[1], P[2], P[3], *args, None) == E, args
 
 
 def quantize(ex, m, x=P[2], ldx=256, type=0, r=None):
@@ -139,10 +138,10 @@ def test_gemm_refusals(ex):
 def test_routing_refusals(ex):
     E, MIS, L = 1, 2, ex.LIB
     r = ctypes.byref(routing(ex))
-    assert L.moe_sort(0, P[1], P[2], P[3], 10, 2, 4, None, 0, None) == E
-    assert L.moe_sort(P[0], 0, P[2], P[3], 10, 2, 4, None, 0, None) == E
-    assert L.moe_sort(P[0] + 2, P[1], P[2], P[3], 10, 2, 4, None, 0, None) == MIS
-    assert L.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 1025, None, 0, None) == E
+    assert L.moe_sort(0, P[1], P[2], P[3], 10, 2, 4, None) == E
+    assert L.moe_sort(P[0], 0, P[2], P[3], 10, 2, 4, None) == E
+    assert L.moe_sort(P[0] + 2, P[1], P[2], P[3], 10, 2, 4, None) == MIS
+    assert L.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 1025, None) == E
     assert L.moe_dispatch(0, P[1], 64, 64, 0, r, None) == E
     assert L.moe_dispatch(P[0], P[1], 63, 64, 0, r, None) == E
     assert L.moe_dispatch(P[0], P[1], 64, -1, 0, r, None) == E
@@ -171,7 +170,7 @@ def test_valid_calls_without_a_device_report_it(ex):
     a, b = matrix(ex), matrix(ex, rows=128, codes=P[4], scales=P[5])
     assert quantize(ex, a) in bad
     assert gemm(ex, a, b) in bad
-    assert ex.LIB.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 4, P[4], 1 << 24, None) in bad
+    assert ex.LIB.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 4, None) in bad
     assert ex.LIB.moe_combine(P[0], P[1], P[2], 64, 0, ctypes.byref(r), None) in bad
 
 
