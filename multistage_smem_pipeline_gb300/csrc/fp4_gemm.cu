@@ -4,7 +4,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "fp4_gemm_kernel.cuh"
+#include "fp4_gemm_pair_kernel.cuh"
 
 namespace gb300 {
 namespace {
@@ -68,6 +68,20 @@ int encode_codes(CUtensorMap* map, const fp4_matrix_t* m, uint32_t box_rows) {
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
+// A matrix's scales as rows of one chunk, 128 words; a box is a stage's chunks.
+int encode_scales(CUtensorMap* map, const fp4_matrix_t* m, int64_t chunks) {
+  const cuuint64_t dims[2] = {kChunkBytes / 4, static_cast<cuuint64_t>(chunks)};
+  const cuuint64_t strides[1] = {kChunkBytes};
+  const cuuint32_t box[2] = {kChunkBytes / 4,
+                             static_cast<cuuint32_t>(chunks_per_stage(m->format))};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m->scales, dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
 template <typename T, int kFormat, int kBN>
 int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas, cudaStream_t s) {
   const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);  // the count of tiles before each
@@ -86,6 +100,27 @@ int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas
   }
   return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, 1u, w,
                     x, p);
+}
+
+template <typename T, int kFormat>
+int launch_pair(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& sw,
+                const CUtensorMap& sx, Fp4GemmParams p, int ctas, cudaStream_t s) {
+  const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);
+  using S = Fp4PairShape<kFormat>;
+  p.stages = S::stages_that_fit(fixed);
+  const auto kernel = fp4_gemm_pair<T, kFormat>;
+  static std::once_flag once;  // per instantiation
+  static cudaError_t granted = cudaSuccess;
+  std::call_once(once, [&] {
+    granted = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kGemmSmemLimit);
+  });
+  if (granted != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, 2u,
+                    w, x, sw, sx, p);
 }
 
 }  // namespace
@@ -117,9 +152,6 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   if (a->cols == 0) return write_empty_sum(D, nullptr, 0.0f, a->rows * n_out, sms, s);
   if ((rc = get_encoder()) != GEMM_OK) return rc;
 
-  // Rows per tile: 256 where a group has more than 128 of them on average.
-  const int64_t mean = a->rows / a->groups;
-  const int bn = mean > 128 ? 256 : 128;
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
   const Fp4View va = view_of(a), vb = view_of(b);
@@ -135,34 +167,60 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   p.groups = a->groups;
   p.k = static_cast<int32_t>(a->cols);
   p.num_kb = static_cast<int32_t>(col_stages(a->cols));
-  p.m_tiles = static_cast<int32_t>((n_out + kGemmM - 1) / kGemmM);
-  // Few rows a group: boxes of 32, so that a tile loads little more than it has.
-  p.box_rows = mean > 64 ? 128 : 32;
-  p.raster = 8;
+  p.w_group_tiles = static_cast<int32_t>((n_out + kTileRows - 1) / kTileRows);
+  p.tile_chunks = p.num_kb * chunks_per_stage(a->format);
   p.alpha = alpha * va.up * vb.up;
   p.timeout_ns = kTimeoutNs;
+  p.raster = 8;
   void* words = nullptr;
   if (cudaGetSymbolAddress(&words, g_fp4_error) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
   p.error = static_cast<uint32_t*>(words) + error_index(s);
-  CUtensorMap tmW, tmX;
-  if ((rc = encode_codes(&tmW, b, kGemmM)) != GEMM_OK ||
-      (rc = encode_codes(&tmX, a, p.box_rows)) != GEMM_OK)
-    return rc;
+
+  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs.  Both are bound by
+  // what an SM loads (36 against 38 KiB per 256 columns), so the one with fewer
+  // waves of tiles is taken; a pair's tile does four times the work.  With
+  // groups by offsets the number of row tiles is not known here: a group is
+  // taken to have the mean number of rows.
+  const auto tiles_of = [&](int64_t bm, int64_t bn) {
+    const int64_t group = a->offsets ? (a->rows + a->groups - 1) / a->groups : a->group_rows;
+    return std::min<int64_t>(a->groups, a->rows) * ((group + bn - 1) / bn) * ((n_out + bm - 1) / bm);
+  };
+  const int64_t single_waves = (tiles_of(128, 128) + sms - 1) / sms;
+  const int64_t pair_waves = (tiles_of(256, 256) + sms / 2 - 1) / (sms / 2);
+  const int64_t x_chunks =
+      tile_count(a->rows, a->groups, a->offsets != nullptr) * p.tile_chunks;
+  const int64_t w_chunks = static_cast<int64_t>(a->groups) * p.w_group_tiles * p.tile_chunks;
+  const bool pair = pair_waves < single_waves && x_chunks <= INT_MAX && w_chunks <= INT_MAX;
+  const int bn = pair ? 256 : 128;
+  const int bm = pair ? 256 : 128;
+  p.m_tiles = static_cast<int32_t>((n_out + bm - 1) / bm);
+  // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile
+  // loads little more than it has.
+  p.box_rows = a->offsets || a->group_rows <= 64 ? 32 : 128;
   // One CTA per SM, fewer where there cannot be that many tiles.
   const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
                                        : a->groups * ((a->group_rows + bn - 1) / bn);
-  const int ctas = static_cast<int>(std::min<int64_t>(sms, row_tiles * p.m_tiles));
-  const auto by_bn = [&](auto t, auto fmt) {
+  const int64_t units = row_tiles * p.m_tiles;
+  CUtensorMap tmW, tmX, tmSW, tmSX;
+  if ((rc = encode_codes(&tmW, b, kGemmM)) != GEMM_OK ||
+      (rc = encode_codes(&tmX, a, p.box_rows)) != GEMM_OK)
+    return rc;
+  if (pair && ((rc = encode_scales(&tmSW, b, w_chunks)) != GEMM_OK ||
+               (rc = encode_scales(&tmSX, a, x_chunks)) != GEMM_OK))
+    return rc;
+  const auto go = [&](auto t, auto fmt) {
     using T = decltype(t);
-    return bn == 256 ? launch<T, fmt(), 256>(tmW, tmX, p, ctas, s)
-                     : launch<T, fmt(), 128>(tmW, tmX, p, ctas, s);
+    if (pair)
+      return launch_pair<T, fmt()>(tmW, tmX, tmSW, tmSX, p,
+                                   2 * static_cast<int>(std::min<int64_t>(sms / 2, units)), s);
+    return launch<T, fmt(), 128>(tmW, tmX, p, static_cast<int>(std::min<int64_t>(sms, units)), s);
   };
   const auto by_format = [&](auto t) {
-    return a->format == FP4_NV ? by_bn(t, std::integral_constant<int, FP4_NV>{})
-                               : by_bn(t, std::integral_constant<int, FP4_MX>{});
+    return a->format == FP4_NV ? go(t, std::integral_constant<int, FP4_NV>{})
+                               : go(t, std::integral_constant<int, FP4_MX>{});
   };
   return type == MOE_F16 ? by_format(__half{}) : by_format(__nv_bfloat16{});
 }

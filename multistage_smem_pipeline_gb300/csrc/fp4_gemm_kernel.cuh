@@ -51,7 +51,9 @@ struct Fp4GemmParams {
   const int32_t* offsets;  // of the rows' groups; null: uniform groups
   int64_t rows, group_rows, n_out;
   int32_t groups, k, num_kb;
-  int32_t m_tiles;         // weight tiles per group
+  int32_t m_tiles;         // weight tiles (of the kernel's height) per group
+  int32_t w_group_tiles;   // scale tiles of the weights per group
+  int32_t tile_chunks;     // chunks of a scale tile
   int32_t box_rows;        // activation rows per TMA box
   int32_t stages;
   int32_t raster;          // row tiles that share a pass over the weight tiles
@@ -251,6 +253,72 @@ __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// ------------------------------------------------------------------ epilogue
+// One warp's part of a tile's accumulator, lanes 32 q .. 32 q + 31 and every
+// other 32-column chunk: to registers in one go, rounded in place (element i
+// of a chunk's array then holds columns 2i and 2i + 1), the accumulator let go
+// by `release`, and stored; a lane is an output n, so a store of the warp
+// writes 32 neighbouring outputs of one row.
+template <typename T, int kBN, typename Release>
+__device__ __forceinline__ void store_tile(uint32_t t_row, int half, int count, float alpha,
+                                           uint16_t* d, bool live, int64_t n_out, Release release) {
+  constexpr int kMine = kBN / 64;
+  uint32_t r[kMine][32];
+#pragma unroll
+  for (int c = 0; c < kMine; ++c)
+    if (32 * (2 * c + half) < count) tmem_ld_32x32b_x32(t_row + 32 * (2 * c + half), r[c]);
+  tmem_ld_wait();
+  release();
+#pragma unroll
+  for (int c = 0; c < kMine; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      r[c][i] = pack_two<T>(alpha * __uint_as_float(r[c][2 * i]),
+                            alpha * __uint_as_float(r[c][2 * i + 1]));
+  if (!live) return;
+#pragma unroll
+  for (int c = 0; c < kMine; ++c) {
+    const int col = 32 * (2 * c + half);
+    if (col >= count) break;
+    uint16_t* to = d + col * n_out;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (col + i < count) *to = static_cast<uint16_t>(r[c][i >> 1] >> (16 * (i & 1)));
+      to += n_out;
+    }
+  }
+}
+
+// Rows of no group are zero: elements [from, end) of D, by every epilogue
+// thread of the grid.
+__device__ __forceinline__ void zero_tail(const Fp4GemmParams& p) {
+  if (!p.offsets) return;
+  const int64_t from = static_cast<int64_t>(p.offsets[p.groups]) * p.n_out;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kGemmEpiWarps);
+  for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * (32 * kGemmEpiWarps) + threadIdx.x - 64;
+       i < p.rows * p.n_out; i += step)
+    p.d[i] = 0;
+}
+
+// The running count of row tiles before each group, by one warp.
+template <int kBN>
+__device__ __forceinline__ void count_row_tiles(const Fp4GemmParams& p, int32_t* before, int lane) {
+  int32_t total = 0;
+  for (int g0 = 0; g0 < p.groups; g0 += 32) {
+    const int g = g0 + lane;
+    const int32_t n = g < p.groups ? (p.offsets[g + 1] - p.offsets[g] + kBN - 1) / kBN : 0;
+    int32_t upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (g < p.groups) before[g] = total + upto - n;
+    total += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) before[p.groups] = total;
+}
+
 // ------------------------------------------------------------------ kernel
 template <typename T, int kFormat, int kBN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
@@ -298,22 +366,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) {  // running count of row tiles
-    int32_t total = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      const int g = g0 + lane;
-      const int32_t n = g < p.groups ? (p.offsets[g + 1] - p.offsets[g] + kBN - 1) / kBN : 0;
-      int32_t upto = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int32_t v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-      }
-      if (g < p.groups) before[g] = total + upto - n;
-      total += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) before[p.groups] = total;
-  }
+  if (p.offsets && warp == 2) count_row_tiles<kBN>(p, before, lane);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -339,7 +392,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * kGemmM);
       const int x_row = static_cast<int>(tile.x_row);
       const uint8_t* w_scales =
-          p.w_scales + (static_cast<int64_t>(tile.group) * p.m_tiles + tile.m) * p.w_tile_bytes;
+          p.w_scales +
+          (static_cast<int64_t>(tile.group) * p.w_group_tiles + tile.m) * p.w_tile_bytes;
       const uint8_t* x_scales = p.x_scales + tile.x_tile * p.x_tile_bytes;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
@@ -457,55 +511,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after_sync();
-      constexpr int kMine = kBN / 64;     // 32-column chunks of each warp
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kBN);
-      uint32_t h[kMine][16];              // columns 2i and 2i + 1 of each chunk, rounded
-#pragma unroll
-      for (int c = 0; c < kMine; ++c) {
-        const int col = 32 * (2 * c + half);
-        if (col >= tile.count) break;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(t_row + col, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          h[c][i] = pack_two<T>(p.alpha * __uint_as_float(r[2 * i]),
-                                p.alpha * __uint_as_float(r[2 * i + 1]));
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(acc));
       const int64_t n = static_cast<int64_t>(tile.m) * kGemmM + q * 32 + lane;
-      uint16_t* const d = p.d + tile.x_row * p.n_out + n;
-      if (n < p.n_out) {
-#pragma unroll
-        for (int c = 0; c < kMine; ++c) {
-          const int col = 32 * (2 * c + half);
-          if (col >= tile.count) break;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (col + 2 * i < tile.count)
-              d[(col + 2 * i) * p.n_out] = static_cast<uint16_t>(h[c][i]);
-            if (col + 2 * i + 1 < tile.count)
-              d[(col + 2 * i + 1) * p.n_out] = static_cast<uint16_t>(h[c][i] >> 16);
-          }
-        }
-      }
+      store_tile<T, kBN>(t_row, half, tile.count, p.alpha, p.d + tile.x_row * p.n_out + n,
+                         n < p.n_out, p.n_out, [&] {
+                           tc_fence_before_sync();
+                           __syncwarp();
+                           if (lane == 0) mbar_arrive(tempty_bar(acc));
+                         });
       if (++acc == S::kAccs) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    // rows of no group are zero
-    if (p.offsets) {
-      const int64_t from = static_cast<int64_t>(p.offsets[p.groups]) * p.n_out;
-      const int64_t end = p.rows * p.n_out;
-      const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kGemmEpiWarps);
-      for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * (32 * kGemmEpiWarps) +
-                       threadIdx.x - 64; i < end; i += step)
-        p.d[i] = 0;
-    }
+    zero_tail(p);
   }
   __syncwarp();
   tc_fence_before_sync();

@@ -1,0 +1,273 @@
+// The 4-bit product over CTA pairs (tcgen05 cta_group::2).
+//
+// A pair owns 256 outputs x up to 256 rows.  Each CTA loads its own 128 rows
+// of weights, its half of the activations' rows, the scales of its weights and
+// all the activations' scales; the even CTA issues, and each CTA accumulates
+// its 128 outputs in its own tensor memory.  Per 256 columns of k an SM then
+// loads 38 KiB for 512 cycles of MMA instead of the 54 KiB of a single CTA's
+// 128 x 256 tile, which the load rate of an SM (about 60 B a cycle with all of
+// them loading) does not cover.
+//
+// Barriers as in the fp16 pair kernel: `full` in the even CTA counts both
+// CTAs' bytes; `empty` and `tfull` are in both, committed to both; `tempty` in
+// the even CTA takes every epilogue warp of both.
+#pragma once
+#include "fp4_gemm_kernel.cuh"
+
+namespace gb300 {
+
+template <int kFormat>
+struct Fp4PairShape {
+  static constexpr int kBN = 256;
+  static constexpr int kXTiles = 2;
+  static constexpr uint32_t kScaleStage = chunks_per_stage(kFormat) * kChunkBytes;
+  static constexpr uint32_t kXBytes = kBN / 2 * kGemmBytesK;
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleStage * (1 + kXTiles);
+  static constexpr uint32_t kWCols = 4 * chunks_per_stage(kFormat);
+  static constexpr uint32_t kSlotCols = kWCols * (1 + kXTiles);
+  static constexpr int kSlots = (kTmemCols - kTmemScales) / kSlotCols;
+  static int stages_that_fit(uint32_t fixed) {
+    int s = static_cast<int>((kGemmSmemLimit - fixed) / kStageBytes);
+    if (s > kSlots) s = kSlots;
+    return s > kGemmMaxStages ? kGemmMaxStages : s;
+  }
+};
+
+template <int kFormat>
+__device__ __forceinline__ void umma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t a_scales, uint32_t b_scales,
+                                              uint32_t accumulate) {
+  if (kFormat == FP4_NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)
+        : "memory");
+}
+
+// In each CTA of the pair, from its own shared memory to its own tensor memory.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// tmSW, tmSX: the scales as rows of one chunk (128 words).
+template <typename T, int kFormat>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    fp4_gemm_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ CUtensorMap tmSW,
+                  const __grid_constant__ CUtensorMap tmSX, const Fp4GemmParams p) {
+  using S = Fp4PairShape<kFormat>;
+  constexpr int kBN = S::kBN;
+  constexpr int kChunks = chunks_per_stage(kFormat);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t bars = base + stages * S::kStageBytes;
+  const auto full_bar = [&](int s) { return bars + 8u * s; };
+  const auto empty_bar = [&](int s) { return bars + 8u * (kGemmMaxStages + s); };
+  const uint32_t tfull_bar = bars + 8u * (2 * kGemmMaxStages);
+  const uint32_t tempty_bar = tfull_bar + 8;
+  const uint32_t drain_bar = tfull_bar + 16;
+  uint8_t* const misc = smem + stages * S::kStageBytes + 8 * kGemmBars;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int32_t* const before = reinterpret_cast<int32_t*>(misc + 16);
+
+  if (threadIdx.x == 0) {
+    grid_launch_dependents();
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tempty_bar, 2 * kGemmEpiWarps);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmSW);
+    tma_prefetch_desc(&tmSX);
+  }
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers exist, and both are running
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();
+  if (p.offsets && warp == 2) count_row_tiles<kBN>(p, before, lane);
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t tiles =
+      (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
+      static_cast<int64_t>(p.m_tiles);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int64_t t = pair; ok && t < tiles; t += pairs) {
+      const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      const int half_n = ((tile.count + 31) & ~31) >> 1;  // rows this CTA holds
+      const int boxes = (half_n + p.box_rows - 1) / p.box_rows;
+      const bool two = tile.count > kTileRows;
+      const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
+                             S::kScaleStage * (two ? 3 : 2);
+      const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * (2 * kGemmM) + rank * kGemmM);
+      const int x_row = static_cast<int>(tile.x_row) + rank * half_n;
+      int sw = (tile.group * p.w_group_tiles + 2 * tile.m + rank) * p.tile_chunks;
+      int sx = static_cast<int>(tile.x_tile) * p.tile_chunks;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t w_dst = base + stage * S::kStageBytes;
+          const uint32_t x_dst = w_dst + kWBytes;
+          const uint32_t s_dst = x_dst + S::kXBytes;
+          const uint32_t full = mapa_shared(full_bar(stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+          tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
+                             x_row + b * p.box_rows);
+          tma_load_2d_pair(s_dst, &tmSW, full, 0, sw);
+          tma_load_2d_pair(s_dst + S::kScaleStage, &tmSX, full, 0, sx);
+          if (two)
+            tma_load_2d_pair(s_dst + 2 * S::kScaleStage, &tmSX, full, 0, sx + p.tile_chunks);
+        }
+        __syncwarp();
+        sw += kChunks;
+        sx += kChunks;
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (rank == 0) {  // the even CTA's barriers count both CTAs' bytes
+      const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+      for (uint32_t i = first; i < issued; ++i)
+        gemm_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (even CTA)
+    if (rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t w_desc0 = sw128_kmajor_desc(base);
+      const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
+      for (int64_t t = pair; ok && t < tiles; t += pairs) {
+        const GemmTile tile = gemm_tile<kBN>(t, p, before);
+        const bool two = tile.count > kTileRows;
+        const uint32_t idesc = fp4_idesc<kFormat>(2 * kGemmM, (tile.count + 31) & ~31);
+        if (!gemm_wait_warp(tempty_bar, acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
+        tc_fence_after_sync();
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!gemm_wait_warp(full_bar(stage), phase, abort_flag, kWaitFull, p)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          if (elect_one()) {
+            const uint64_t at = static_cast<uint64_t>((stage * S::kStageBytes) >> 4);
+            const uint64_t s_desc = s_desc0 + at;
+            const uint32_t w_cols = tmem + kTmemScales + stage * S::kSlotCols;
+            const uint32_t x_cols = w_cols + S::kWCols;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              tmem_copy_scales_pair(w_cols + 4 * c, s_desc + ((c * kChunkBytes) >> 4));
+              tmem_copy_scales_pair(x_cols + 8 * c,
+                                    s_desc + ((S::kScaleStage + c * kChunkBytes) >> 4));
+              if (two)
+                tmem_copy_scales_pair(x_cols + 8 * c + 4,
+                                      s_desc + ((2 * S::kScaleStage + c * kChunkBytes) >> 4));
+            }
+            const uint64_t w_desc = w_desc0 + at;
+            const uint64_t x_desc = w_desc + (kWBytes >> 4);
+            const int left = p.k - kb * kStageCols;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              if (64 * s >= left) break;
+              const int chunk = kFormat == FP4_NV ? s : s >> 1;
+              const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
+              umma_fp4_pair<kFormat>(tmem, w_desc + 2u * s, x_desc + 2u * s,
+                                     idesc | fp4_idesc_scale_bytes(byte), w_cols + 4 * chunk,
+                                     x_cols + 8 * chunk, (kb | s) != 0);
+            }
+            umma_commit_pair_mc(empty_bar(stage), 0x3);
+          }
+          __syncwarp();
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair_mc(tfull_bar, 0x3);
+        __syncwarp();
+        acc_phase ^= 1u;
+      }
+      if (elect_one()) umma_commit_pair_mc(drain_bar, 0x1);
+      __syncwarp();
+      gemm_wait_drain(drain_bar, 0, p.timeout_ns);
+      // the last remote arrivals on this CTA's barrier have landed
+      gemm_wait_drain(tempty_bar, acc_phase ^ 1u, p.timeout_ns);
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;
+    uint32_t acc_phase = 0;
+    const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
+    for (int64_t t = pair; t < tiles; t += pairs) {
+      const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      int ok = 0;
+      if (lane == 0) ok = gemm_wait(tfull_bar, acc_phase, abort_flag, kWaitTmemFull, p);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after_sync();
+      const int64_t n = static_cast<int64_t>(tile.m) * (2 * kGemmM) + rank * kGemmM + q * 32 + lane;
+      store_tile<T, kBN>(tmem + (static_cast<uint32_t>(q * 32) << 16), half, tile.count, p.alpha,
+                         p.d + tile.x_row * p.n_out + n, n < p.n_out, p.n_out, [&] {
+                           tc_fence_before_sync();
+                           __syncwarp();
+                           if (lane == 0) mbar_arrive_cluster(leader_tempty);
+                         });
+      acc_phase ^= 1u;
+    }
+    zero_tail(p);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+}  // namespace gb300
