@@ -43,7 +43,8 @@ enum {
   FP4_MAX_COLS = 1 << 23,  /* columns of a 4-bit matrix */
   MOE_MAX_EXPERTS = 1024,  /* experts (groups) of a routing */
   MOE_MAX_TOP_K = 64,      /* slots per token */
-  MOE_MAX_SLOTS = 1 << 30  /* tokens * top_k */
+  MOE_MAX_SLOTS = 1 << 30, /* tokens * top_k */
+  MOE_MAX_HIDDEN = 1 << 30 /* elements of a row that is moved */
 };
 
 /* Where the slots of each token went: what moe_sort writes, as later calls

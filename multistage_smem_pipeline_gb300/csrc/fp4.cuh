@@ -108,8 +108,8 @@ inline Fp4View view_of(const fp4_matrix_t* m) {
 
 // ------------------------------------------------------------------ device
 // Byte of block `b` (counted along the row) of row r (within the tile).
-__device__ __forceinline__ int64_t scale_at(int r, int b) {
-  return static_cast<int64_t>(b >> 2) * kChunkBytes + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
+__device__ __forceinline__ int scale_at(int r, int b) {
+  return (b >> 2) * kChunkBytes + (r & 31) * 16 + (r >> 5) * 4 + (b & 3);
 }
 
 // Rows [row, row + count) and the scale tile of one 128-row tile of a matrix.
@@ -117,10 +117,7 @@ __device__ __forceinline__ int64_t scale_at(int r, int b) {
 // one more: those past the last group stand for the rows in no group, with
 // tile = -1.
 struct TileRows {
-  int64_t row;
-  int32_t count;
-  int64_t tile;
-  int32_t group;
+  int32_t row, count, tile;
 };
 
 // The last g in [0, groups] with offsets[g] / unit + g <= q.
@@ -134,24 +131,27 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, in
   return lo;
 }
 
-__device__ __forceinline__ TileRows tile_rows(const Fp4View& v, int64_t q) {
+__device__ __forceinline__ TileRows tile_rows(const Fp4View& v, int q) {
   TileRows t;
   if (!v.offsets) {
-    const int64_t per = (v.group_rows + kTileRows - 1) / kTileRows;
-    const int64_t g = q / per, in = q - g * per;
-    t.row = g * v.group_rows + in * kTileRows;
-    t.count = static_cast<int32_t>(min(static_cast<int64_t>(kTileRows), v.group_rows - in * kTileRows));
+    const int group_rows = static_cast<int>(v.group_rows);
+    int g = 0, in = q;
+    if (v.groups > 1) {
+      const int per = (group_rows + kTileRows - 1) / kTileRows;
+      g = q / per;
+      in = q - g * per;
+    }
+    t.row = g * group_rows + in * kTileRows;
+    t.count = min(kTileRows, group_rows - in * kTileRows);
     t.tile = q;
-    t.group = static_cast<int32_t>(g);
     return t;
   }
   const int g = find_group(v.offsets, v.groups, kTileRows, q);
-  const int64_t first = v.offsets[g];
-  const int64_t end = g < v.groups ? v.offsets[g + 1] : v.rows;
+  const int first = v.offsets[g];
+  const int end = g < v.groups ? v.offsets[g + 1] : static_cast<int>(v.rows);
   t.row = first + (q - (first / kTileRows + g)) * kTileRows;
-  t.count = static_cast<int32_t>(max(min(static_cast<int64_t>(kTileRows), end - t.row), int64_t{0}));
+  t.count = max(min(kTileRows, end - t.row), 0);
   t.tile = g < v.groups ? q : -1;
-  t.group = g;
   return t;
 }
 

@@ -29,7 +29,7 @@ struct Raw {
 };
 
 template <bool kVec>
-__device__ __forceinline__ Raw load_raw(const uint16_t* row, int64_t c, int64_t cols) {
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, int c, int cols) {
   Raw r;
   std::memset(&r, 0, sizeof(r));
   if (kVec && c + kSegment <= cols) {
@@ -43,7 +43,7 @@ __device__ __forceinline__ Raw load_raw(const uint16_t* row, int64_t c, int64_t 
 }
 
 // Zeroes the elements at `cols` and past it.
-__device__ __forceinline__ void clip(Raw& r, int64_t c, int64_t cols) {
+__device__ __forceinline__ void clip(Raw& r, int c, int cols) {
   if (c + kSegment <= cols) return;
 #pragma unroll
   for (int i = 0; i < kSegment / 2; ++i) {
@@ -116,11 +116,16 @@ __device__ __forceinline__ Segment quantize_segment(const Raw& raw, const Fp4Vie
   float hi, lo = 0.0f;
   bool finite;
   if (kFormat == FP4_NV) {
+    // amax / 6 in the same way: 1/6 in two parts
+    constexpr float kSixth = 1.0f / 6.0f;
+    const float sixth_lo = fmaf(-kSixth, 6.0f, 1.0f) * kSixth;
     const float scaled = __uint_as_float(top) * v.down;
     finite = __float_as_uint(scaled) < 0x7f800000u;
-    s.scale = finite ? to_e4m3(__fdiv_rn(scaled, 6.0f)) : kNanE4M3;
+    s.scale = finite ? to_e4m3(fmaf(scaled, kSixth, scaled * sixth_lo)) : kNanE4M3;
     const float step = finite ? from_e4m3(s.scale) : 0.0f;
-    hi = step > 0.0f ? __frcp_rn(step) : 0.0f;
+    // the approximate reciprocal will do: lo makes up for what it is off by
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(step));
+    if (!(step > 0.0f)) hi = 0.0f;
     lo = fmaf(-hi, step, 1.0f) * hi * v.down;
     hi *= v.down;
   } else {
@@ -145,46 +150,52 @@ __device__ __forceinline__ Segment quantize_segment(const Raw& raw, const Fp4Vie
   return s;
 }
 
-// A block per tile and chunk.  All of a thread's rows are asked for before the
-// first is used; the chunk is put together in shared memory and written in
-// one piece.
+// A block per chunk, going down the tiles.  All of a thread's rows of a tile
+// are asked for before the first is used; the chunk is put together in shared
+// memory and written in one piece.
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-    quantize_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx, int chunks) {
+    quantize_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx, int tiles) {
   using C = Chunk<kFormat>;
   __shared__ __align__(16) uint8_t scales[kChunkBytes];
   grid_launch_dependents();
-  const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const TileRows t = tile_rows(v, blockIdx.x / chunks);  // uniform groups: reads nothing
-  if (threadIdx.x < kChunkBytes / 16)
-    reinterpret_cast<uint4*>(scales)[threadIdx.x] = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  grid_dependency_wait();
+  const int cols = static_cast<int>(v.cols);
   const int seg = threadIdx.x % C::kSegments;
-  const int64_t c = static_cast<int64_t>(chunk) * C::kCols + seg * kSegment;
+  const int c = static_cast<int>(blockIdx.x) * C::kCols + seg * kSegment;
   const int r0 = threadIdx.x / C::kSegments;
-  Raw raw[C::kSteps];
+  const bool padded = c / 2 < static_cast<int>(v.pitch);
+  grid_dependency_wait();
+  for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+    const TileRows t = tile_rows(v, tile);
+    Raw raw[C::kSteps];
+    const uint16_t* from = x + (t.row + r0) * ldx;
 #pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
-    const int r = r0 + i * C::kRowsAtOnce;
-    raw[i] = load_raw<kVec>(x + (t.row + r) * ldx, c, r < t.count ? v.cols : 0);
-  }
+    for (int i = 0; i < C::kSteps; ++i) {
+      raw[i] = load_raw<kVec>(from, c, r0 + i * C::kRowsAtOnce < t.count ? cols : 0);
+      from += C::kRowsAtOnce * ldx;
+    }
+    if (threadIdx.x < kChunkBytes / 16)
+      reinterpret_cast<uint4*>(scales)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    uint8_t* to = v.codes + (t.row + r0) * v.pitch + c / 2;
 #pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
-    const int r = r0 + i * C::kRowsAtOnce;
-    if (i * C::kRowsAtOnce >= t.count) break;
-    clip(raw[i], c, v.cols);
-    const Segment s = quantize_segment<T, kFormat>(raw[i], v);
-    if (r >= t.count) continue;
-    if (c / 2 < v.pitch)
-      *reinterpret_cast<uint2*>(v.codes + (t.row + r) * v.pitch + c / 2) = s.codes;
-    if (c < v.cols) scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)] = s.scale;
+    for (int i = 0; i < C::kSteps; ++i) {
+      const int r = r0 + i * C::kRowsAtOnce;
+      if (i * C::kRowsAtOnce >= t.count) break;
+      clip(raw[i], c, cols);
+      const Segment s = quantize_segment<T, kFormat>(raw[i], v);
+      if (r < t.count) {
+        if (padded) *reinterpret_cast<uint2*>(to) = s.codes;
+        if (c < cols) scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)] = s.scale;
+      }
+      to += C::kRowsAtOnce * v.pitch;
+    }
+    __syncthreads();
+    if (threadIdx.x < kChunkBytes / 16)
+      reinterpret_cast<uint4*>(v.scales + t.tile * v.tile_bytes +
+                               static_cast<int64_t>(blockIdx.x) * kChunkBytes)[threadIdx.x] =
+          reinterpret_cast<const uint4*>(scales)[threadIdx.x];
   }
-  __syncthreads();
-  if (threadIdx.x < kChunkBytes / 16)
-    reinterpret_cast<uint4*>(v.scales + t.tile * v.tile_bytes +
-                             static_cast<int64_t>(chunk) * kChunkBytes)[threadIdx.x] =
-        reinterpret_cast<const uint4*>(scales)[threadIdx.x];
 }
 
 // A block per token and up to 4096 columns: quantised once, written to the
@@ -198,115 +209,123 @@ __global__ void __launch_bounds__(kThreads)
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t token = blockIdx.x;
-  const int64_t seg = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x;
-  const int64_t c = seg * kSegment;
-  const int64_t cols256 = col_stages(v.cols) * kStageCols;
-  Raw raw = load_raw<kVec>(x + token * ldx, c, v.cols);
-  clip(raw, c, v.cols);
+  const int cols = static_cast<int>(v.cols);
+  const int seg = static_cast<int>(blockIdx.y) * kThreads + threadIdx.x;
+  const int c = seg * kSegment;
+  Raw raw = load_raw<kVec>(x + token * ldx, c, cols);
+  clip(raw, c, cols);
   const Segment s = quantize_segment<T, kFormat>(raw, v);
   // bytes of the chunk's four blocks, in every thread
   constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
-  uint32_t word = (c < v.cols ? s.scale : 0u) << (8 * (seg / kPerBlock & 3));
+  uint32_t word = (c < cols ? s.scale : 0u) << (8 * (seg / kPerBlock & 3));
   if (kFormat == FP4_MX && (seg & 1)) word = 0;
 #pragma unroll
   for (int d = 1; d < 4 * kPerBlock; d <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, d);
-  if (c >= cols256) return;
+  if (c >= static_cast<int>(col_stages(v.cols)) * kStageCols) return;
   const int32_t kept = v.offsets[v.groups];
   for (int j = 0; j < top_k; ++j) {
     const int32_t row = rows[token * top_k + j];
     if (row >= kept) continue;
-    if (c / 2 < v.pitch)
+    if (c / 2 < static_cast<int>(v.pitch))
       *reinterpret_cast<uint2*>(v.codes + row * v.pitch + c / 2) = s.codes;
     if (seg % (4 * kPerBlock) == 0) {
       const int32_t e = ids[token * top_k + j];
       const int32_t first = v.offsets[e];
-      const int64_t tile = first / kTileRows + e + (row - first) / kTileRows;
+      const int tile = first / kTileRows + e + (row - first) / kTileRows;
       *reinterpret_cast<uint32_t*>(v.scales + tile * v.tile_bytes +
-                                   scale_at((row - first) % kTileRows,
-                                            static_cast<int>(seg / kPerBlock))) = word;
+                                   scale_at((row - first) % kTileRows, seg / kPerBlock)) = word;
     }
   }
 }
 
-// A block per tile and chunk, and per 128 rows of no group.
+// A block per chunk and tile, or 128 rows of no group, going down them.
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
-    dequantize_kernel(uint16_t* __restrict__ y, const Fp4View v, int chunks) {
+    dequantize_kernel(uint16_t* __restrict__ y, const Fp4View v, int tiles) {
   using C = Chunk<kFormat>;
   __shared__ __align__(16) uint8_t scales[kChunkBytes];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const TileRows t = tile_rows(v, blockIdx.x / chunks);
-  if (t.count == 0) return;
-  const int seg = threadIdx.x % C::kSegments;
-  const int64_t c = static_cast<int64_t>(chunk) * C::kCols + seg * kSegment;
-  const int r0 = threadIdx.x / C::kSegments;
-  uint2 codes[C::kSteps];
-#pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
-    const int r = r0 + i * C::kRowsAtOnce;
-    codes[i] = make_uint2(0, 0);
-    if (t.tile >= 0 && r < t.count && c < v.cols)
-      codes[i] = *reinterpret_cast<const uint2*>(v.codes + (t.row + r) * v.pitch + c / 2);
-  }
-  if (t.tile >= 0 && threadIdx.x < kChunkBytes / 16)
-    reinterpret_cast<uint4*>(scales)[threadIdx.x] = reinterpret_cast<const uint4*>(
-        v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(chunk) * kChunkBytes)[threadIdx.x];
-  __syncthreads();
   __shared__ __align__(16) uint16_t staged[kVec ? 8 : C::kRowsAtOnce * C::kCols];
+  const int cols = static_cast<int>(v.cols);
+  const int seg = threadIdx.x % C::kSegments;
+  const int c = static_cast<int>(blockIdx.x) * C::kCols + seg * kSegment;
+  const int r0 = threadIdx.x / C::kSegments;
+  for (int tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+    const TileRows t = tile_rows(v, tile);
+    if (t.count == 0) continue;
+    __syncthreads();  // the last tile's scales have been read
+    uint2 codes[C::kSteps];
 #pragma unroll
-  for (int i = 0; i < C::kSteps; ++i) {
-    if (i * C::kRowsAtOnce >= t.count) break;
-    const int r = r0 + i * C::kRowsAtOnce;
-    float f[kSegment] = {};
-    if (t.tile >= 0) {
-      from_e2m1(codes[i].x, f);
-      from_e2m1(codes[i].y, f + 8);
-      const uint32_t byte = scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)];
-      const float step = scale_value<kFormat>(byte) * (kFormat == FP4_NV ? v.up : 1.0f);
-#pragma unroll
-      for (int e = 0; e < kSegment; ++e) f[e] *= step;
+    for (int i = 0; i < C::kSteps; ++i) {
+      const int r = r0 + i * C::kRowsAtOnce;
+      codes[i] = make_uint2(0, 0);
+      if (t.tile >= 0 && r < t.count && c < cols)
+        codes[i] = *reinterpret_cast<const uint2*>(v.codes + static_cast<int64_t>(t.row + r) * v.pitch + c / 2);
     }
-    float half[8];
-    Pack p[2];
+    if (t.tile >= 0 && threadIdx.x < kChunkBytes / 16)
+      reinterpret_cast<uint4*>(scales)[threadIdx.x] = reinterpret_cast<const uint4*>(
+          v.scales + t.tile * v.tile_bytes + static_cast<int64_t>(blockIdx.x) * kChunkBytes)[threadIdx.x];
+    __syncthreads();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < C::kSteps; ++i) {
+      if (i * C::kRowsAtOnce >= t.count) break;
+      const int r = r0 + i * C::kRowsAtOnce;
+      float f[kSegment] = {};
+      if (t.tile >= 0) {
+        from_e2m1(codes[i].x, f);
+        from_e2m1(codes[i].y, f + 8);
+        const uint32_t byte = scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)];
+        const float step = scale_value<kFormat>(byte) * (kFormat == FP4_NV ? v.up : 1.0f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) half[e] = f[8 * h + e];
-      p[h] = pack<T>(half);
-    }
-    if (kVec) {
-      // Neighbours swap halves, so that a warp's store covers 32-byte sectors
-      // whole: first both halves of the even segment, then of the odd one.
-      const bool odd = seg & 1;
-      Pack other;
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        other.w[w] = __shfl_xor_sync(0xffffffffu, odd ? p[0].w[w] : p[1].w[w], 1);
-      if (r >= t.count) continue;
-      uint16_t* const row = y + (t.row + r) * v.cols;
-      const int64_t even = c - (odd ? kSegment : 0);  // cols is a multiple of 8: pieces are whole
-      const int64_t first = even + (odd ? 8 : 0), second = first + kSegment;
-      if (first < v.cols) store8<true>(row, first, v.cols, odd ? other : p[0]);
-      if (second < v.cols) store8<true>(row, second, v.cols, odd ? p[1] : other);
-    } else {
-      // Rows start anywhere: through shared memory, then element by element
-      // with neighbouring lanes on neighbouring elements.
-      *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment) = p[0];
-      *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment + 8) = p[1];
-      __syncthreads();
-      const int rows = min(C::kRowsAtOnce, t.count - i * C::kRowsAtOnce);
-      const int64_t c0 = static_cast<int64_t>(chunk) * C::kCols;
-      const int cols = static_cast<int>(min(static_cast<int64_t>(C::kCols), v.cols - c0));
-      uint16_t* const to = y + (t.row + i * C::kRowsAtOnce) * v.cols + c0;
-      for (int w = threadIdx.x; w < rows * C::kCols; w += kThreads) {
-        const int rr = w / C::kCols, cc = w % C::kCols;
-        if (cc < cols) to[rr * v.cols + cc] = staged[w];
+        for (int e = 0; e < kSegment; ++e) f[e] *= step;
       }
-      __syncthreads();
+      float half[8];
+      Pack p[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) half[e] = f[8 * h + e];
+        p[h] = pack<T>(half);
+      }
+      if (kVec) {
+        // Neighbours swap halves, so that a warp's store covers 32-byte sectors
+        // whole: first both halves of the even segment, then of the odd one.
+        const bool odd = seg & 1;
+        Pack other;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          other.w[w] = __shfl_xor_sync(0xffffffffu, odd ? p[0].w[w] : p[1].w[w], 1);
+        if (r >= t.count) continue;
+        uint16_t* const row = y + (t.row + r) * v.cols;
+        const int even = c - (odd ? kSegment : 0);  // cols is a multiple of 8: pieces are whole
+        const int first = even + (odd ? 8 : 0), second = first + kSegment;
+        if (first < cols) store8<true>(row, first, cols, odd ? other : p[0]);
+        if (second < cols) store8<true>(row, second, cols, odd ? p[1] : other);
+      } else {
+        // Rows start anywhere: through shared memory, then element by element
+        // with neighbouring lanes on neighbouring elements.
+        *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment) = p[0];
+        *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment + 8) = p[1];
+        __syncthreads();
+        const int rows = min(C::kRowsAtOnce, t.count - i * C::kRowsAtOnce);
+        const int c0 = static_cast<int>(blockIdx.x) * C::kCols;
+        const int here = min(C::kCols, cols - c0);
+        uint16_t* const to = y + (t.row + i * C::kRowsAtOnce) * v.cols + c0;
+        for (int w = threadIdx.x; w < rows * C::kCols; w += kThreads) {
+          const int rr = w / C::kCols, cc = w % C::kCols;
+          if (cc < here) to[rr * v.cols + cc] = staged[w];
+        }
+        __syncthreads();
+      }
     }
   }
+}
+
+// Blocks for every chunk of every tile, but no more rows of them than a grid
+// may have: each goes down the tiles in that stride.
+dim3 tile_grid(int64_t chunks, int64_t tiles) {
+  return dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(tiles, 65535)));
 }
 
 // Calls f(T{}, format, vec) with the types and constants of this call.
@@ -382,11 +401,10 @@ extern "C" int fp4_quantize(const fp4_matrix_t* out, const void* x, int64_t ldx,
       return launch_pdl(quantize_routed_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0, s, 1u, v, xp,
                         ldx, routing->rows, routing->ids, routing->top_k);
     }
+    const int64_t tiles = tile_count(out->rows, out->groups, false);
     const int64_t chunks = col_stages(out->cols) * chunks_per_stage(fmt());
-    const int64_t blocks = tile_count(out->rows, out->groups, false) * chunks;
-    if (blocks > INT_MAX) return static_cast<int>(GEMM_ERR_INVALID_VALUE);
-    return launch_pdl(quantize_kernel<T, fmt(), wide()>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kThreads), 0, s, 1u, v, xp, ldx, static_cast<int>(chunks));
+    return launch_pdl(quantize_kernel<T, fmt(), wide()>, tile_grid(chunks, tiles), dim3(kThreads), 0,
+                      s, 1u, v, xp, ldx, static_cast<int>(tiles));
   });
 }
 
@@ -410,11 +428,9 @@ extern "C" int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* s
     using T = decltype(t);
     // only the columns that y has: padding is left out
     const int64_t chunks = (in->cols + Chunk<fmt()>::kCols - 1) / Chunk<fmt()>::kCols;
-    const int64_t blocks =
-        (tile_count(in->rows, in->groups, by_offsets) + (by_offsets ? 1 : 0)) * chunks;
-    if (blocks > INT_MAX) return static_cast<int>(GEMM_ERR_INVALID_VALUE);
-    return launch_pdl(dequantize_kernel<T, fmt(), wide()>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kThreads), 0, static_cast<cudaStream_t>(stream), 1u,
-                      static_cast<uint16_t*>(y), v, static_cast<int>(chunks));
+    const int64_t tiles = tile_count(in->rows, in->groups, by_offsets) + (by_offsets ? 1 : 0);
+    return launch_pdl(dequantize_kernel<T, fmt(), wide()>, tile_grid(chunks, tiles), dim3(kThreads),
+                      0, static_cast<cudaStream_t>(stream), 1u, static_cast<uint16_t*>(y), v,
+                      static_cast<int>(tiles));
   });
 }

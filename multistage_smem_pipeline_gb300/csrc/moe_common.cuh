@@ -120,14 +120,14 @@ __device__ __forceinline__ int row_lead(const uint16_t* row) {
 // that hold them, shifted into place; a word without an element of the row in
 // it is not read, and what stands outside the row is undefined.
 template <bool kAligned>
-__device__ __forceinline__ Pack load8(const uint16_t* row, int64_t e, int64_t n) {
+__device__ __forceinline__ Pack load8(const uint16_t* row, int e, int n) {
   if (kAligned) return *reinterpret_cast<const Pack*>(row + e);
   const uintptr_t start = reinterpret_cast<uintptr_t>(row);
-  const uintptr_t at = start + 2 * e;  // may lie before the row
+  const uintptr_t at = start + 2 * static_cast<intptr_t>(e);  // may lie before the row
   const uintptr_t word = at & ~static_cast<uintptr_t>(15);
   uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-  if (word + 16 > start && word < start + 2 * n) lo = *reinterpret_cast<const uint4*>(word);
-  if (word != at && word + 16 < start + 2 * n) hi = *reinterpret_cast<const uint4*>(word + 16);
+  if (word + 16 > start && word < start + 2 * static_cast<uintptr_t>(n)) lo = *reinterpret_cast<const uint4*>(word);
+  if (word != at && word + 16 < start + 2 * static_cast<uintptr_t>(n)) hi = *reinterpret_cast<const uint4*>(word + 16);
   const uint32_t off = static_cast<uint32_t>(at & 15);
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   if (off & 8) {
@@ -146,7 +146,7 @@ __device__ __forceinline__ Pack load8(const uint16_t* row, int64_t e, int64_t n)
 
 // The same window to a row that it is aligned in; elements outside are left out.
 template <bool kAligned>
-__device__ __forceinline__ void store8(uint16_t* row, int64_t e, int64_t n, const Pack& p) {
+__device__ __forceinline__ void store8(uint16_t* row, int e, int n, const Pack& p) {
   if (kAligned || (e >= 0 && e + 8 <= n)) {
     *reinterpret_cast<Pack*>(row + e) = p;
     return;
@@ -157,7 +157,7 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t e, int64_t n, cons
 }
 
 // Zeroes what a window holds outside a row of n elements.
-__device__ __forceinline__ void clip8(float (&f)[8], int64_t e, int64_t n) {
+__device__ __forceinline__ void clip8(float (&f)[8], int e, int n) {
   if (e >= 0 && e + 8 <= n) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i)

@@ -23,8 +23,7 @@ struct RouteParams {
   const int32_t* offsets;
   const int32_t* rows;
   int64_t tokens;
-  int32_t top_k, experts;
-  int64_t hidden;
+  int32_t top_k, experts, hidden;
 };
 
 // ------------------------------------------------------------------ sort
@@ -151,20 +150,19 @@ __global__ void __launch_bounds__(kRowThreads)
   const uint16_t* const from = x + t * ldx;
   const Pack zero = {{0, 0, 0, 0}};
   if (kAligned) {
-    for (int64_t h = threadIdx.x * 8; h < r.hidden; h += kRowThreads * 8) {
+    for (int h = threadIdx.x * 8; h < r.hidden; h += kRowThreads * 8) {
       const Pack v = load8<true>(from, h, r.hidden);
       for (int j = 0; j < r.top_k; ++j) {
         const int32_t row = rows[j];
-        store8<true>(y + row * r.hidden, h, r.hidden, row < kept ? v : zero);
+        store8<true>(y + static_cast<int64_t>(row) * r.hidden, h, r.hidden, row < kept ? v : zero);
       }
     }
   } else {
     for (int j = 0; j < r.top_k; ++j) {
       const int32_t row = rows[j];
-      uint16_t* const to = y + row * r.hidden;
+      uint16_t* const to = y + static_cast<int64_t>(row) * r.hidden;
       const int lead = row_lead(to);
-      for (int64_t h = static_cast<int64_t>(threadIdx.x) * 8 - lead; h < r.hidden;
-           h += kRowThreads * 8)
+      for (int h = static_cast<int>(threadIdx.x) * 8 - lead; h < r.hidden; h += kRowThreads * 8)
         store8<false>(to, h, r.hidden, row < kept ? load8<false>(from, h, r.hidden) : zero);
     }
   }
@@ -204,14 +202,13 @@ __global__ void __launch_bounds__(kRowThreads)
   const int live = s_live;
   uint16_t* const to = out + t * r.hidden;
   const int lead = kAligned ? 0 : row_lead(to);
-  for (int64_t h = static_cast<int64_t>(threadIdx.x) * 8 - lead; h < r.hidden;
-       h += kRowThreads * 8) {
+  for (int h = static_cast<int>(threadIdx.x) * 8 - lead; h < r.hidden; h += kRowThreads * 8) {
     float acc[8] = {};
     for (int j = 0; j < live; j += kFlight) {
       Pack v[kFlight];
 #pragma unroll
       for (int q = 0; q < kFlight; ++q)
-        if (j + q < live) v[q] = load8<kAligned>(y + s_row[j + q] * r.hidden, h, r.hidden);
+        if (j + q < live) v[q] = load8<kAligned>(y + static_cast<int64_t>(s_row[j + q]) * r.hidden, h, r.hidden);
 #pragma unroll
       for (int q = 0; q < kFlight; ++q) {
         if (j + q >= live) break;
@@ -245,22 +242,22 @@ __global__ void __launch_bounds__(kRowThreads)
   const bool kept = row < r.offsets[r.experts];
   const float w = kept ? weights[p] : 0.0f;
   const uint16_t* const g_row = grad_out + (p / r.top_k) * r.hidden;
-  const uint16_t* const y_row = y + row * r.hidden;
-  uint16_t* const to = grad_y ? grad_y + row * r.hidden : nullptr;
+  const uint16_t* const y_row = y + static_cast<int64_t>(row) * r.hidden;
+  uint16_t* const to = grad_y ? grad_y + static_cast<int64_t>(row) * r.hidden : nullptr;
   const int lead = kAligned || !to ? 0 : row_lead(to);
   float dot = 0.0f;
-  for (int64_t h0 = static_cast<int64_t>(lane) * 8 - lead; h0 < r.hidden; h0 += 32 * 8 * kFlight) {
+  for (int h0 = lane * 8 - lead; h0 < r.hidden; h0 += 32 * 8 * kFlight) {
     Pack g[kFlight], v[kFlight];
 #pragma unroll
     for (int q = 0; q < kFlight; ++q) {
-      const int64_t h = h0 + q * 32 * 8;
+      const int h = h0 + q * 32 * 8;
       if (h >= r.hidden || !kept) continue;
       if (grad_weights) v[q] = load8<kAligned>(y_row, h, r.hidden);
       g[q] = load8<kAligned>(g_row, h, r.hidden);
     }
 #pragma unroll
     for (int q = 0; q < kFlight; ++q) {
-      const int64_t h = h0 + q * 32 * 8;
+      const int h = h0 + q * 32 * 8;
       if (h >= r.hidden) break;
       float a[8] = {}, b[8];
       if (kept) {
@@ -303,7 +300,7 @@ int check_rows(std::initializer_list<Operand> ops, int64_t hidden, int64_t ldx, 
                const moe_routing_t* r) {
   int rc = check_routing(r);
   if (rc != GEMM_OK) return rc;
-  if (!valid_type(type) || hidden < 0 || hidden > INT_MAX || ldx < hidden || ldx > INT_MAX)
+  if (!valid_type(type) || hidden < 0 || hidden > MOE_MAX_HIDDEN || ldx < hidden || ldx > INT_MAX)
     return GEMM_ERR_INVALID_VALUE;
   if (r->tokens == 0 || hidden == 0) return GEMM_OK;
   const auto bytes = [&](const Operand& o) {
@@ -322,7 +319,8 @@ int check_rows(std::initializer_list<Operand> ops, int64_t hidden, int64_t ldx, 
 }
 
 RouteParams route_params(const moe_routing_t* r, int64_t hidden) {
-  return RouteParams{r->offsets, r->rows, r->tokens, r->top_k, r->experts, hidden};
+  return RouteParams{r->offsets, r->rows,    r->tokens,
+                     r->top_k,   r->experts, static_cast<int32_t>(hidden)};
 }
 
 template <bool kWeighted>
