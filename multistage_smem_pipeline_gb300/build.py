@@ -5,7 +5,9 @@
 Each translation unit under csrc/ is compiled in parallel, then linked into
 multistage_smem_pipeline_gb300/lib/libgemm_tn_f16.so (the CUDA runtime is
 linked statically; the driver's cuTensorMapEncodeTiled is fetched at run time
-through the runtime's entry-point query, so no -lcuda is needed).
+through the runtime's entry-point query, so no -lcuda is needed).  The Python
+binding of moe_fp4.h, csrc/experts_binding.cpp, is compiled beside them against
+the installed torch's headers and linked to the library.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libgemm_tn_f16.so")
+BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")
+BINDING = os.path.join(LIB_DIR, "_experts.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -44,10 +49,32 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return all(os.path.getmtime(d) <= t for d in _deps() + [BINDING_SRC])
+
+
+def _binding_command(out: str) -> list[str]:
+    """Compiles the binding of moe_fp4.h to an object file."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I" + inc,
+            "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + cuda, "-I" + INCLUDE,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-c", BINDING_SRC, "-o", out]
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    subprocess.check_call(["g++", "-shared", "-o", tmp, obj, "-L" + libs, "-lc10", "-lc10_cuda",
+                           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-L" + LIB_DIR,
+                           "-l:libgemm_tn_f16.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -64,6 +91,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [exe] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-c", src, "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
                                             text=True)))
+    binding_obj = os.path.join(OBJ_DIR, "experts_binding.cpp.o")
+    procs.append((BINDING_SRC, subprocess.Popen(_binding_command(binding_obj),
+                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                                text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -72,10 +103,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         elif verbose and out:
             sys.stdout.write(out)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
     tmp = LIB + f".{os.getpid()}.tmp"
-    subprocess.check_call([exe] + ARCH + ["-shared", "-o", tmp] + objs)
+    subprocess.check_call([exe] + ARCH + ["-shared", "-o", tmp, "-Xlinker",
+                                          "-soname=libgemm_tn_f16.so"] + objs)
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 

@@ -1,0 +1,468 @@
+// Python binding of moe_fp4.h: checks and marshals torch tensors, allocates
+// outputs, and calls the C functions on the current (or a given) stream.  It
+// is compiled because the calls it makes are a few microseconds long on the
+// GPU: marshalled from Python, a call cost the host 7 to 11 us, of which the
+// launch is 2.6 and an allocation 1.
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/utils/pybind.h>
+
+#include <ATen/ATen.h>
+
+#include <memory>
+#include <string>
+
+#include "moe_fp4.h"
+
+namespace {
+
+[[noreturn]] void value_error(const std::string& what) { throw py::value_error(what); }
+[[noreturn]] void type_error(const std::string& what) { throw py::type_error(what); }
+
+// A C function's status, as the exception the fp16 binding raises.
+void check(int status, const char* name) {
+  if (status == GEMM_OK) return;
+  const py::object error =
+      py::module_::import("multistage_smem_pipeline_gb300.binding").attr("GemmError");
+  const py::object value = error(status, name);
+  PyErr_SetObject(error.ptr(), value.ptr());
+  throw py::error_already_set();
+}
+
+// The stream a call runs on, with its device current meanwhile.
+class On {
+ public:
+  On(const at::Tensor& x, const py::object& stream) : guard_(x.device()) {
+    handle_ = stream.is_none()
+                  ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream())
+                  : reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
+  }
+  void* stream() const { return handle_; }
+
+ private:
+  c10::cuda::CUDAGuard guard_;
+  void* handle_;
+};
+
+int type_of(at::ScalarType t, const char* what) {
+  if (t == at::kHalf) return MOE_F16;
+  if (t == at::kBFloat16) return MOE_BF16;
+  type_error(std::string(what) + " must be float16 or bfloat16");
+}
+
+at::ScalarType dtype_of(const py::object& dtype) {
+  if (dtype.is_none()) return at::kHalf;
+  if (!THPDtype_Check(dtype.ptr())) type_error("dtype must be a torch.dtype");
+  return reinterpret_cast<THPDtype*>(dtype.ptr())->scalar_type;
+}
+
+int format_of(const std::string& name) {
+  if (name == "nvfp4") return FP4_NV;
+  if (name == "mxfp4") return FP4_MX;
+  value_error("unknown format '" + name + "'");
+}
+const char* format_name(int format) { return format == FP4_NV ? "nvfp4" : "mxfp4"; }
+
+// x is a CUDA matrix of a supported type with contiguous rows; its type number.
+int matrix(const at::Tensor& x, const char* what) {
+  const int type = type_of(x.scalar_type(), what);
+  if (x.dim() != 2 || !x.is_cuda())
+    value_error(std::string(what) + " must be a 2-D CUDA tensor");
+  if (x.size(1) > 1 && x.stride(1) != 1)
+    value_error(std::string(what) + "'s rows must be contiguous");
+  return type;
+}
+
+// Elements between rows (a tensor of one row may report any stride).
+int64_t row_stride(const at::Tensor& x) {
+  return x.size(0) > 1 ? std::max(x.stride(0), x.size(1)) : x.size(1);
+}
+
+using Out = std::optional<at::Tensor>;
+
+at::Tensor output(const Out& out, int64_t rows, int64_t cols, at::ScalarType type,
+                  at::Device device) {
+  if (!out) return at::empty({rows, cols}, at::TensorOptions().dtype(type).device(device));
+  if (out->scalar_type() != type || out->dim() != 2 || out->size(0) != rows ||
+      out->size(1) != cols || !out->is_contiguous() || out->device() != device)
+    value_error("out must be a contiguous " + std::to_string(rows) + " x " +
+                std::to_string(cols) + " tensor of the right type on the inputs' device");
+  return *out;
+}
+
+// ------------------------------------------------------------------ Routing
+struct Routing {
+  at::Tensor ids, buffer;            // buffer: the three arrays of moe_sort, in one piece
+  at::Tensor offsets, rows, pairs;   // made from it when they are asked for
+  moe_routing_t c{};
+
+  int64_t slots() const { return c.tokens * c.top_k; }
+  int64_t head() const { return (c.experts + 4) & ~int64_t{3}; }      // offsets, to 16 bytes
+  int64_t span() const { return (slots() + 3) & ~int64_t{3}; }
+  at::Device device() const { return ids.device(); }
+
+  void describe(int64_t experts) {
+    c.tokens = ids.size(0);
+    c.top_k = static_cast<int32_t>(ids.size(1));
+    c.experts = static_cast<int32_t>(experts);
+    c.ids = static_cast<const int32_t*>(ids.data_ptr());
+  }
+
+  const at::Tensor& get_offsets() {
+    if (!offsets.defined()) offsets = buffer.narrow(0, 0, c.experts + 1);
+    return offsets;
+  }
+  const at::Tensor& get_rows() {
+    if (!rows.defined()) rows = buffer.narrow(0, head(), slots()).view({c.tokens, c.top_k});
+    return rows;
+  }
+  const at::Tensor& get_pairs() {
+    if (!pairs.defined()) pairs = buffer.narrow(0, head() + span(), slots());
+    return pairs;
+  }
+};
+using RoutingPtr = std::shared_ptr<Routing>;
+
+RoutingPtr given_routing(const at::Tensor& offsets, const at::Tensor& rows,
+                         const at::Tensor& pairs, const at::Tensor& ids) {
+  for (const at::Tensor* t : {&offsets, &rows, &pairs, &ids})
+    if (t->scalar_type() != at::kInt || !t->is_cuda() || !t->is_contiguous() ||
+        t->device() != ids.device())
+      value_error("offsets, rows, pairs and ids must be contiguous int32 CUDA tensors on one device");
+  if (ids.dim() != 2 || rows.sizes() != ids.sizes() || pairs.numel() != ids.numel() ||
+      offsets.dim() != 1 || offsets.numel() < 2)
+    value_error("ids and rows must be tokens x top_k, pairs as many, and offsets experts + 1");
+  auto r = std::make_shared<Routing>();
+  r->ids = ids;
+  r->offsets = offsets;
+  r->rows = rows;
+  r->pairs = pairs;
+  r->describe(offsets.numel() - 1);
+  r->c.offsets = static_cast<const int32_t*>(offsets.data_ptr());
+  r->c.rows = static_cast<const int32_t*>(rows.data_ptr());
+  r->c.pairs = static_cast<const int32_t*>(pairs.data_ptr());
+  return r;
+}
+
+RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream) {
+  if (ids.scalar_type() != at::kInt) type_error("ids must be int32");
+  if (ids.dim() != 2 || !ids.is_cuda() || !ids.is_contiguous())
+    value_error("ids must be a contiguous 2-D CUDA tensor (tokens x top_k)");
+  if (experts < 1 || experts > MOE_MAX_EXPERTS || ids.size(1) < 1 || ids.size(1) > MOE_MAX_TOP_K)
+    value_error("1 to " + std::to_string(MOE_MAX_EXPERTS) + " experts and 1 to " +
+                std::to_string(MOE_MAX_TOP_K) + " slots are supported");
+  auto r = std::make_shared<Routing>();
+  r->ids = ids;
+  r->describe(experts);
+  r->buffer = at::empty({r->head() + 2 * r->span()}, ids.options());
+  int32_t* const at = static_cast<int32_t*>(r->buffer.data_ptr());
+  r->c.offsets = at;
+  r->c.rows = at + r->head();
+  r->c.pairs = at + r->head() + r->span();
+  const On on(ids, stream);
+  check(moe_sort(at, at + r->head(), at + r->head() + r->span(), r->c.ids, r->c.tokens, r->c.top_k,
+                 r->c.experts, on.stream()),
+        "moe_sort");
+  return r;
+}
+
+// ------------------------------------------------------------------ Fp4Matrix
+struct Fp4Matrix {
+  at::Tensor buffer;           // scales, then codes, in one piece
+  at::Tensor codes, scales;    // made from it when they are asked for
+  RoutingPtr routing;
+  int64_t pitch = 0, tiles = 0, chunks = 0;
+  at::Device device{at::kCUDA};
+  fp4_matrix_t c{};
+
+  // Everything but the pointers.
+  void describe(int64_t rows, int64_t cols, int format, int64_t exponent,
+                std::optional<int64_t> group_rows, const RoutingPtr& r) {
+    c.rows = rows;
+    c.cols = cols;
+    c.format = format;
+    c.exponent = static_cast<int32_t>(exponent);
+    pitch = (cols + 31) / 32 * 16;
+    chunks = (cols + 255) / 256 * (format == FP4_NV ? 4 : 2);
+    routing = r;
+    if (r) {
+      if (group_rows || rows != r->slots())
+        value_error("a matrix in expert order has a row per slot and no group_rows");
+      c.groups = r->c.experts;
+      c.offsets = r->c.offsets;
+      tiles = rows / 128 + c.groups;
+      return;
+    }
+    const int64_t g = group_rows.value_or(rows);
+    if (g < 0 || (g ? rows % g : rows) != 0)
+      value_error(std::to_string(rows) + " rows are not whole groups of " + std::to_string(g));
+    c.groups = g ? static_cast<int32_t>(std::max<int64_t>(rows / g, 1)) : 1;
+    c.group_rows = g;
+    tiles = c.groups * ((g + 127) / 128);
+  }
+
+  const at::Tensor& get_scales() {
+    if (!scales.defined())
+      scales = buffer.narrow(0, 0, tiles * chunks * 512).view({tiles, chunks, 512});
+    return scales;
+  }
+  const at::Tensor& get_codes() {
+    if (!codes.defined())
+      codes = buffer.narrow(0, tiles * chunks * 512, c.rows * pitch).view({c.rows, pitch});
+    return codes;
+  }
+};
+using MatrixPtr = std::shared_ptr<Fp4Matrix>;
+
+MatrixPtr given_matrix(const at::Tensor& codes, const at::Tensor& scales, int64_t cols,
+                       const std::string& format, int64_t exponent,
+                       std::optional<int64_t> group_rows, const RoutingPtr& routing) {
+  const int fmt = format_of(format);
+  if (codes.scalar_type() != at::kByte || scales.scalar_type() != at::kByte)
+    type_error("codes and scales must be uint8");
+  if (!codes.is_cuda() || !scales.is_cuda() || codes.device() != scales.device())
+    value_error("codes and scales must be CUDA tensors on one device");
+  if (!codes.is_contiguous() || !scales.is_contiguous())
+    value_error("codes and scales must be contiguous");
+  if (codes.dim() != 2 || cols < 0) value_error("codes must be a matrix of 0 or more columns");
+  auto m = std::make_shared<Fp4Matrix>();
+  m->describe(codes.size(0), cols, fmt, exponent, group_rows, routing);
+  if (codes.size(1) != m->pitch)
+    value_error("codes must have " + std::to_string(m->pitch) + " bytes a row, got " +
+                std::to_string(codes.size(1)));
+  if (scales.numel() < m->tiles * m->chunks * 512)
+    value_error("scales must have " + std::to_string(m->tiles * m->chunks * 512) +
+                " bytes, got " + std::to_string(scales.numel()));
+  m->codes = codes;
+  m->scales = scales;
+  m->device = codes.device();
+  m->c.codes = codes.data_ptr();
+  m->c.scales = scales.data_ptr();
+  return m;
+}
+
+MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t exponent,
+                   std::optional<int64_t> group_rows, const RoutingPtr& routing,
+                   const MatrixPtr& out, const py::object& stream) {
+  const int type = matrix(x, "x");
+  const int fmt = format_of(format);
+  int64_t rows = x.size(0);
+  const int64_t cols = x.size(1);
+  if (routing) {
+    if (rows != routing->c.tokens)
+      value_error("x has " + std::to_string(rows) + " rows, the routing " +
+                  std::to_string(routing->c.tokens) + " tokens");
+    if (routing->device() != x.device()) value_error("x and the routing are on different devices");
+    rows = routing->slots();
+  }
+  MatrixPtr m = out;
+  if (!m) {
+    m = std::make_shared<Fp4Matrix>();
+    m->describe(rows, cols, fmt, exponent, group_rows, routing);
+    const int64_t scales = m->tiles * m->chunks * 512;
+    m->buffer = at::empty({scales + rows * m->pitch}, x.options().dtype(at::kByte));
+    m->device = x.device();
+    m->c.scales = m->buffer.data_ptr();
+    m->c.codes = static_cast<uint8_t*>(m->buffer.data_ptr()) + scales;
+  } else if (m->c.rows != rows || m->c.cols != cols || m->c.format != fmt ||
+             m->c.exponent != exponent || m->routing != routing || m->device != x.device() ||
+             (group_rows && m->c.group_rows != *group_rows)) {
+    value_error("out does not fit x, the format or the groups");
+  }
+  const On on(x, stream);
+  check(fp4_quantize(&m->c, x.data_ptr(), row_stride(x), type, routing ? &routing->c : nullptr,
+                     on.stream()),
+        "fp4_quantize");
+  return m;
+}
+
+at::Tensor dequantize(const Fp4Matrix& q, const py::object& dtype, const Out& out,
+                      const py::object& stream) {
+  const at::ScalarType t = dtype_of(dtype);
+  const int type = type_of(t, "dtype");
+  const at::Tensor y = output(out, q.c.rows, q.c.cols, t, q.device);
+  const On on(y, stream);
+  check(fp4_dequantize(y.data_ptr(), type, &q.c, on.stream()), "fp4_dequantize");
+  return y;
+}
+
+at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::object& dtype,
+                const Out& out, const py::object& stream) {
+  const at::ScalarType t = dtype_of(dtype);
+  const int type = type_of(t, "dtype");
+  if (a.device != b.device) value_error("a and b are on different devices");
+  const at::Tensor d = output(out, a.c.rows, b.c.group_rows, t, a.device);
+  const On on(d, stream);
+  check(fp4_gemm_tn(d.data_ptr(), type, &a.c, &b.c, static_cast<float>(alpha), on.stream()),
+        "fp4_gemm_tn");
+  return d;
+}
+
+py::tuple device_error(const py::object& stream) {
+  void* const s = stream.is_none()
+                      ? static_cast<void*>(c10::cuda::getCurrentCUDAStream().stream())
+                      : reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
+  uint32_t raw = 0;
+  const int status = fp4_get_device_error(s, &raw);
+  return py::make_tuple(status, raw);
+}
+
+int64_t scale_bytes(int64_t rows, int64_t cols, const std::string& format, int groups,
+                    bool by_offsets) {
+  uint64_t n = 0;
+  check(fp4_scale_bytes(rows, cols, format_of(format), groups, by_offsets, &n), "fp4_scale_bytes");
+  return static_cast<int64_t>(n);
+}
+
+// ------------------------------------------------------------------ rows
+int by_token(const at::Tensor& x, const Routing& r, const char* what) {
+  const int type = matrix(x, what);
+  if (x.size(0) != r.c.tokens || x.device() != r.device())
+    value_error(std::string(what) + " must have a row for each of the routing's " +
+                std::to_string(r.c.tokens) + " tokens, on its device");
+  return type;
+}
+
+int by_slot(const at::Tensor& y, const Routing& r, const char* what) {
+  const int type = matrix(y, what);
+  if (y.size(0) != r.slots() || !y.is_contiguous() || y.device() != r.device())
+    value_error(std::string(what) + " must be contiguous with a row for each of the routing's " +
+                std::to_string(r.slots()) + " slots, on its device");
+  return type;
+}
+
+const float* weights_of(const at::Tensor& w, const Routing& r) {
+  if (w.scalar_type() != at::kFloat) type_error("weights must be float32");
+  if (w.sizes() != r.ids.sizes() || !w.is_contiguous() || w.device() != r.device())
+    value_error("weights must be contiguous, of the routing's tokens x top_k, on its device");
+  return static_cast<const float*>(w.data_ptr());
+}
+
+at::Tensor dispatch(const at::Tensor& x, const Routing& r, const Out& out,
+                    const py::object& stream) {
+  const int type = by_token(x, r, "x");
+  const at::Tensor y = output(out, r.slots(), x.size(1), x.scalar_type(), x.device());
+  const On on(x, stream);
+  check(moe_dispatch(y.data_ptr(), x.data_ptr(), row_stride(x), x.size(1), type, &r.c, on.stream()),
+        "moe_dispatch");
+  return y;
+}
+
+at::Tensor dispatch_backward(const at::Tensor& grad_y, const Routing& r, const Out& out,
+                             const py::object& stream) {
+  const int type = by_slot(grad_y, r, "grad_y");
+  const at::Tensor x =
+      output(out, r.c.tokens, grad_y.size(1), grad_y.scalar_type(), grad_y.device());
+  const On on(grad_y, stream);
+  check(moe_dispatch_backward(x.data_ptr(), grad_y.data_ptr(), grad_y.size(1), type, &r.c,
+                              on.stream()),
+        "moe_dispatch_backward");
+  return x;
+}
+
+at::Tensor combine(const at::Tensor& y, const Routing& r, const at::Tensor& weights,
+                   const Out& out, const py::object& stream) {
+  const int type = by_slot(y, r, "y");
+  const float* const w = weights_of(weights, r);
+  const at::Tensor o = output(out, r.c.tokens, y.size(1), y.scalar_type(), y.device());
+  const On on(y, stream);
+  check(moe_combine(o.data_ptr(), y.data_ptr(), w, y.size(1), type, &r.c, on.stream()),
+        "moe_combine");
+  return o;
+}
+
+std::pair<at::Tensor, at::Tensor> combine_backward(const at::Tensor& grad_out, const at::Tensor& y,
+                                                   const Routing& r, const at::Tensor& weights,
+                                                   const py::object& stream) {
+  const int type = by_slot(y, r, "y");
+  if (by_token(grad_out, r, "grad_out") != type || grad_out.size(1) != y.size(1) ||
+      !grad_out.is_contiguous())
+    value_error("grad_out must be contiguous, of y's type and width");
+  const float* const w = weights_of(weights, r);
+  const at::Tensor grad_y = at::empty({y.size(0), y.size(1)}, y.options());
+  const at::Tensor grad_w = at::empty({r.c.tokens, r.c.top_k}, weights.options());
+  const On on(y, stream);
+  check(moe_combine_backward(grad_y.data_ptr(), static_cast<float*>(grad_w.data_ptr()),
+                             grad_out.data_ptr(), y.data_ptr(), w, y.size(1), type, &r.c,
+                             on.stream()),
+        "moe_combine_backward");
+  return {grad_y, grad_w};
+}
+
+}  // namespace
+
+PYBIND11_MODULE(_experts, m) {
+  const auto none = py::none();
+  py::class_<Routing, RoutingPtr>(m, "Routing",
+                                  "Where each slot (token, j) went: rows[token, j] is its row in "
+                                  "expert order, pairs the inverse, and expert e has rows "
+                                  "offsets[e] to offsets[e + 1] - 1.  Dropped slots have the rows "
+                                  "from offsets[-1] on.  All int32, on the device.  moe_sort makes "
+                                  "one; a program with a router of its own can give the tensors "
+                                  "itself.")
+      .def(py::init(&given_routing), py::arg("offsets"), py::arg("rows"), py::arg("pairs"),
+           py::arg("ids"))
+      .def_property_readonly("offsets", &Routing::get_offsets)
+      .def_property_readonly("rows", &Routing::get_rows)
+      .def_property_readonly("pairs", &Routing::get_pairs)
+      .def_readonly("ids", &Routing::ids)
+      .def_property_readonly("tokens", [](const Routing& r) { return r.c.tokens; })
+      .def_property_readonly("top_k", [](const Routing& r) { return r.c.top_k; })
+      .def_property_readonly("experts", [](const Routing& r) { return r.c.experts; })
+      .def_property_readonly("slots", &Routing::slots);
+  py::class_<Fp4Matrix, MatrixPtr>(
+      m, "Fp4Matrix",
+      "A matrix of 4-bit blocks in the layout of include/moe_fp4.h.\n\n"
+      "codes: rows x (cols rounded up to 32) / 2 bytes.  scales: tiles x chunks x 512 bytes.\n"
+      "group_rows: rows of each group (for weights of several experts, one expert's outputs;\n"
+      "default: all rows are one group).  Instead, `routing` marks rows in expert order.")
+      .def(py::init(&given_matrix), py::arg("codes"), py::arg("scales"), py::kw_only(),
+           py::arg("cols"), py::arg("format") = "nvfp4", py::arg("exponent") = 0,
+           py::arg("group_rows") = none, py::arg("routing") = none)
+      .def_property_readonly("codes", &Fp4Matrix::get_codes)
+      .def_property_readonly("scales", &Fp4Matrix::get_scales)
+      .def_readonly("routing", &Fp4Matrix::routing)
+      .def_property_readonly("rows", [](const Fp4Matrix& q) { return q.c.rows; })
+      .def_property_readonly("cols", [](const Fp4Matrix& q) { return q.c.cols; })
+      .def_property_readonly("format", [](const Fp4Matrix& q) { return format_name(q.c.format); })
+      .def_property_readonly("exponent", [](const Fp4Matrix& q) { return q.c.exponent; })
+      .def_property_readonly("groups", [](const Fp4Matrix& q) { return q.c.groups; })
+      .def_property_readonly("group_rows", [](const Fp4Matrix& q) { return q.c.group_rows; });
+
+  m.def("fp4_quantize", &quantize, py::arg("x"), py::kw_only(), py::arg("format") = "nvfp4",
+        py::arg("exponent") = 0, py::arg("group_rows") = none, py::arg("routing") = none,
+        py::arg("out") = none, py::arg("stream") = none,
+        "x (rows x cols, float16 or bfloat16, rows contiguous) as an Fp4Matrix.\n\n"
+        "With a routing, x has a row per token and the result a row per slot, in expert order.");
+  m.def("fp4_dequantize", &dequantize, py::arg("q"), py::arg("dtype") = none,
+        py::arg("out") = none, py::arg("stream") = none,
+        "The values of q, rows x cols (float16 unless dtype says bfloat16); rows of dropped slots "
+        "are zero.");
+  m.def("fp4_gemm_tn", &gemm, py::arg("a"), py::arg("b"), py::kw_only(), py::arg("alpha") = 1.0,
+        py::arg("dtype") = none, py::arg("out") = none, py::arg("stream") = none,
+        "out[r] = alpha * a[r] @ b[g(r)]^T (fp32 accumulation; float16 unless dtype says bfloat16): "
+        "g(r) is the group of row r, so with activations in expert order each row meets its "
+        "expert's weights; rows of dropped slots give zeros.  b has as many groups as a, each of "
+        "b.group_rows outputs.");
+  m.def("fp4_get_device_error", &device_error, py::arg("stream") = none,
+        "(status, raw word) of the stream's error word of fp4_gemm_tn; synchronises the stream.");
+  m.def("fp4_scale_bytes", &scale_bytes, py::arg("rows"), py::arg("cols"),
+        py::arg("format") = "nvfp4", py::arg("groups") = 1, py::arg("by_offsets") = false,
+        "Bytes of an Fp4Matrix's scales.");
+  m.def("moe_sort", &sort, py::arg("ids"), py::arg("experts"), py::arg("stream") = none,
+        "Slots sorted by expert.  ids: tokens x top_k int32; a number outside [0, experts) drops "
+        "its slot.  The order within an expert is the slots' own.");
+  m.def("moe_dispatch", &dispatch, py::arg("x"), py::arg("routing"), py::arg("out") = none,
+        py::arg("stream") = none,
+        "x's rows (a row per token) in expert order, a row per slot; zeros for dropped slots.");
+  m.def("moe_dispatch_backward", &dispatch_backward, py::arg("grad_y"), py::arg("routing"),
+        py::arg("out") = none, py::arg("stream") = none,
+        "moe_dispatch's gradient: each token's sum over its kept slots.");
+  m.def("moe_combine", &combine, py::arg("y"), py::arg("routing"), py::arg("weights"),
+        py::arg("out") = none, py::arg("stream") = none,
+        "Each token's weighted sum of its kept slots' rows of y.  weights: tokens x top_k float32.");
+  m.def("moe_combine_backward", &combine_backward, py::arg("grad_out"), py::arg("y"),
+        py::arg("routing"), py::arg("weights"), py::arg("stream") = none,
+        "moe_combine's gradients: (of y, of weights); zeros for dropped slots.");
+}

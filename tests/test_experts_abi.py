@@ -14,11 +14,42 @@ HEADER = os.path.join(ROOT, "include", "moe_fp4.h")
 P = [0x10000000 * (i + 1) for i in range(8)]   # never dereferenced
 
 
+class RoutingC(ctypes.Structure):          # moe_routing_t
+    _fields_ = [("tokens", ctypes.c_int64), ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("offsets", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("pairs", ctypes.c_void_p), ("ids", ctypes.c_void_p)]
+
+
+class MatrixC(ctypes.Structure):           # fp4_matrix_t
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("exponent", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("group_rows", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p)]
+
+
 @pytest.fixture(scope="module")
 def ex():
+    """The binding, with the library's C functions declared as `LIB`."""
     from multistage_smem_pipeline_gb300 import build
     build.build()
     from multistage_smem_pipeline_gb300 import experts
+    lib = ctypes.CDLL(build.LIB)
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    pr, pm, pu = (ctypes.POINTER(t) for t in (RoutingC, MatrixC, ctypes.c_uint64))
+    for name, args in {
+            "fp4_code_bytes": [i64, i64, pu],
+            "fp4_scale_bytes": [i64, i64, i32, i32, i32, pu],
+            "fp4_quantize": [pm, vp, i64, i32, pr, vp],
+            "fp4_dequantize": [vp, i32, pm, vp],
+            "fp4_gemm_tn": [vp, i32, pm, pm, ctypes.c_float, vp],
+            "moe_sort": [vp, vp, vp, vp, i64, i32, i32, vp],
+            "moe_dispatch": [vp, vp, i64, i64, i32, pr, vp],
+            "moe_dispatch_backward": [vp, vp, i64, i32, pr, vp],
+            "moe_combine": [vp, vp, vp, i64, i32, pr, vp],
+            "moe_combine_backward": [vp, vp, vp, vp, vp, i64, i32, pr, vp]}.items():
+        getattr(lib, name).argtypes = args
+    experts.LIB = lib
     return experts
 
 
@@ -39,12 +70,12 @@ def test_package_exports(ex):
 def routing(ex, tokens=10, top_k=2, experts=4, **kw):
     v = dict(offsets=P[4], rows=P[5], pairs=P[6], ids=P[7])
     v.update(kw)
-    return ex._RoutingC(tokens, top_k, experts, v["offsets"], v["rows"], v["pairs"], v["ids"])
+    return RoutingC(tokens, top_k, experts, v["offsets"], v["rows"], v["pairs"], v["ids"])
 
 
 def matrix(ex, rows=64, cols=256, format=0, exponent=0, groups=1, group_rows=None, offsets=None,
            codes=P[0], scales=P[1], reserved=0):
-    return ex._MatrixC(codes, scales, rows, cols, format, exponent, groups, reserved,
+    return MatrixC(codes, scales, rows, cols, format, exponent, groups, reserved,
                        rows // max(groups, 1) if group_rows is None else group_rows, offsets)
 
 
