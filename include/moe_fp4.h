@@ -54,7 +54,6 @@ typedef struct {
   int32_t top_k, experts;
   const int32_t* offsets;  /* experts + 1: expert e has rows offsets[e] .. offsets[e+1] - 1 */
   const int32_t* rows;     /* tokens * top_k: the row of each slot */
-  const int32_t* pairs;    /* tokens * top_k: the slot of each row */
   const int32_t* ids;      /* tokens * top_k: the expert of each slot, as given to moe_sort */
 } moe_routing_t;
 
@@ -117,12 +116,16 @@ int fp4_get_device_error(void* stream, uint32_t* raw);
 /*
  * moe_sort: slots sorted by expert.  ids: tokens * top_k expert numbers; any
  * outside [0, experts) marks a dropped slot.  rows[p] is slot p's place among
- * all slots ordered by expert, then by p, the dropped ones last; pairs is its
- * inverse; offsets[e] is the first row of expert e and offsets[experts] the
- * number of slots kept.
+ * all slots ordered by expert, then by p, the dropped ones last; offsets[e] is
+ * the first row of expert e and offsets[experts] the number of slots kept.
+ * No two of the arrays overlap.
  */
-int moe_sort(int32_t* offsets, int32_t* rows, int32_t* pairs, const int32_t* ids, int64_t tokens,
-             int top_k, int experts, void* stream);
+int moe_sort(int32_t* offsets, int32_t* rows, const int32_t* ids, int64_t tokens, int top_k,
+             int experts, void* stream);
+
+/* moe_pairs: the inverse of rows: pairs[rows[p]] = p, for a program that walks
+ * rows (none of the calls below needs it). */
+int moe_pairs(int32_t* pairs, const moe_routing_t* routing, void* stream);
 
 /* In what follows x, out and their gradients are tokens x hidden, y and its
  * gradient (tokens * top_k) x hidden in row order; all of `type` (2-byte

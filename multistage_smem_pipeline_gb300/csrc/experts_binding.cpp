@@ -93,13 +93,12 @@ at::Tensor output(const Out& out, int64_t rows, int64_t cols, at::ScalarType typ
 
 // ------------------------------------------------------------------ Routing
 struct Routing {
-  at::Tensor ids, buffer;            // buffer: the three arrays of moe_sort, in one piece
-  at::Tensor offsets, rows, pairs;   // made from it when they are asked for
+  at::Tensor ids, buffer;     // buffer: the two arrays of moe_sort, in one piece
+  at::Tensor offsets, rows;   // made from it when they are asked for
   moe_routing_t c{};
 
   int64_t slots() const { return c.tokens * c.top_k; }
   int64_t head() const { return (c.experts + 4) & ~int64_t{3}; }      // offsets, to 16 bytes
-  int64_t span() const { return (slots() + 3) & ~int64_t{3}; }
   at::Device device() const { return ids.device(); }
 
   void describe(int64_t experts) {
@@ -117,31 +116,24 @@ struct Routing {
     if (!rows.defined()) rows = buffer.narrow(0, head(), slots()).view({c.tokens, c.top_k});
     return rows;
   }
-  const at::Tensor& get_pairs() {
-    if (!pairs.defined()) pairs = buffer.narrow(0, head() + span(), slots());
-    return pairs;
-  }
 };
 using RoutingPtr = std::shared_ptr<Routing>;
 
 RoutingPtr given_routing(const at::Tensor& offsets, const at::Tensor& rows,
-                         const at::Tensor& pairs, const at::Tensor& ids) {
-  for (const at::Tensor* t : {&offsets, &rows, &pairs, &ids})
+                         const at::Tensor& ids) {
+  for (const at::Tensor* t : {&offsets, &rows, &ids})
     if (t->scalar_type() != at::kInt || !t->is_cuda() || !t->is_contiguous() ||
         t->device() != ids.device())
-      value_error("offsets, rows, pairs and ids must be contiguous int32 CUDA tensors on one device");
-  if (ids.dim() != 2 || rows.sizes() != ids.sizes() || pairs.numel() != ids.numel() ||
-      offsets.dim() != 1 || offsets.numel() < 2)
-    value_error("ids and rows must be tokens x top_k, pairs as many, and offsets experts + 1");
+      value_error("offsets, rows and ids must be contiguous int32 CUDA tensors on one device");
+  if (ids.dim() != 2 || rows.sizes() != ids.sizes() || offsets.dim() != 1 || offsets.numel() < 2)
+    value_error("ids and rows must be tokens x top_k, and offsets experts + 1");
   auto r = std::make_shared<Routing>();
   r->ids = ids;
   r->offsets = offsets;
   r->rows = rows;
-  r->pairs = pairs;
   r->describe(offsets.numel() - 1);
   r->c.offsets = static_cast<const int32_t*>(offsets.data_ptr());
   r->c.rows = static_cast<const int32_t*>(rows.data_ptr());
-  r->c.pairs = static_cast<const int32_t*>(pairs.data_ptr());
   return r;
 }
 
@@ -155,16 +147,21 @@ RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream
   auto r = std::make_shared<Routing>();
   r->ids = ids;
   r->describe(experts);
-  r->buffer = at::empty({r->head() + 2 * r->span()}, ids.options());
+  r->buffer = at::empty({r->head() + r->slots()}, ids.options());
   int32_t* const at = static_cast<int32_t*>(r->buffer.data_ptr());
   r->c.offsets = at;
   r->c.rows = at + r->head();
-  r->c.pairs = at + r->head() + r->span();
   const On on(ids, stream);
-  check(moe_sort(at, at + r->head(), at + r->head() + r->span(), r->c.ids, r->c.tokens, r->c.top_k,
-                 r->c.experts, on.stream()),
+  check(moe_sort(at, at + r->head(), r->c.ids, r->c.tokens, r->c.top_k, r->c.experts, on.stream()),
         "moe_sort");
   return r;
+}
+
+at::Tensor pairs_of(const Routing& r, const py::object& stream) {
+  const at::Tensor pairs = at::empty({r.slots()}, r.ids.options());
+  const On on(pairs, stream);
+  check(moe_pairs(static_cast<int32_t*>(pairs.data_ptr()), &r.c, on.stream()), "moe_pairs");
+  return pairs;
 }
 
 // ------------------------------------------------------------------ Fp4Matrix
@@ -396,16 +393,14 @@ PYBIND11_MODULE(_experts, m) {
   const auto none = py::none();
   py::class_<Routing, RoutingPtr>(m, "Routing",
                                   "Where each slot (token, j) went: rows[token, j] is its row in "
-                                  "expert order, pairs the inverse, and expert e has rows "
+                                  "expert order, and expert e has rows "
                                   "offsets[e] to offsets[e + 1] - 1.  Dropped slots have the rows "
                                   "from offsets[-1] on.  All int32, on the device.  moe_sort makes "
                                   "one; a program with a router of its own can give the tensors "
                                   "itself.")
-      .def(py::init(&given_routing), py::arg("offsets"), py::arg("rows"), py::arg("pairs"),
-           py::arg("ids"))
+      .def(py::init(&given_routing), py::arg("offsets"), py::arg("rows"), py::arg("ids"))
       .def_property_readonly("offsets", &Routing::get_offsets)
       .def_property_readonly("rows", &Routing::get_rows)
-      .def_property_readonly("pairs", &Routing::get_pairs)
       .def_readonly("ids", &Routing::ids)
       .def_property_readonly("tokens", [](const Routing& r) { return r.c.tokens; })
       .def_property_readonly("top_k", [](const Routing& r) { return r.c.top_k; })
@@ -453,6 +448,8 @@ PYBIND11_MODULE(_experts, m) {
   m.def("moe_sort", &sort, py::arg("ids"), py::arg("experts"), py::arg("stream") = none,
         "Slots sorted by expert.  ids: tokens x top_k int32; a number outside [0, experts) drops "
         "its slot.  The order within an expert is the slots' own.");
+  m.def("moe_pairs", &pairs_of, py::arg("routing"), py::arg("stream") = none,
+        "The slot (token * top_k + j) of each row: the inverse of the routing's rows.");
   m.def("moe_dispatch", &dispatch, py::arg("x"), py::arg("routing"), py::arg("out") = none,
         py::arg("stream") = none,
         "x's rows (a row per token) in expert order, a row per slot; zeros for dropped slots.");

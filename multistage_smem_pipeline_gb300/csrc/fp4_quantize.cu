@@ -198,14 +198,16 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// A block per token and up to 4096 columns: quantised once, written to the
-// row of each of its slots.  Neighbouring threads join the four scale bytes
-// of a chunk.
+// A block per token and up to 4096 columns: quantised once, written to the row
+// of each of its kept slots, whose places the first threads look up.
+// Neighbouring threads join the four scale bytes of a chunk.
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
     quantize_routed_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx,
                            const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
                            int top_k) {
+  constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
+  __shared__ int64_t s_codes[MOE_MAX_TOP_K], s_scales[MOE_MAX_TOP_K];  // -1: dropped
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t token = blockIdx.x;
@@ -213,28 +215,37 @@ __global__ void __launch_bounds__(kThreads)
   const int seg = static_cast<int>(blockIdx.y) * kThreads + threadIdx.x;
   const int c = seg * kSegment;
   Raw raw = load_raw<kVec>(x + token * ldx, c, cols);
+  if (threadIdx.x < top_k) {
+    const int32_t row = rows[token * top_k + threadIdx.x];
+    const int32_t e = ids[token * top_k + threadIdx.x];
+    int64_t codes = -1;
+    if (row < v.offsets[v.groups]) {  // then e is an expert
+      const int32_t first = v.offsets[e];
+      codes = row * v.pitch;
+      s_scales[threadIdx.x] = (first / kTileRows + e + (row - first) / kTileRows) * v.tile_bytes +
+                              scale_at((row - first) % kTileRows, 0);
+    }
+    s_codes[threadIdx.x] = codes;
+  }
   clip(raw, c, cols);
   const Segment s = quantize_segment<T, kFormat>(raw, v);
   // bytes of the chunk's four blocks, in every thread
-  constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
   uint32_t word = (c < cols ? s.scale : 0u) << (8 * (seg / kPerBlock & 3));
   if (kFormat == FP4_MX && (seg & 1)) word = 0;
 #pragma unroll
   for (int d = 1; d < 4 * kPerBlock; d <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, d);
+  __syncthreads();
   if (c >= static_cast<int>(col_stages(v.cols)) * kStageCols) return;
-  const int32_t kept = v.offsets[v.groups];
+  const bool padded = c / 2 < static_cast<int>(v.pitch);
+  const bool leads = seg % (4 * kPerBlock) == 0;
+  uint8_t* const codes = v.codes + c / 2;
+  uint8_t* const scales = v.scales + static_cast<int64_t>(seg / (4 * kPerBlock)) * kChunkBytes;
+#pragma unroll 4
   for (int j = 0; j < top_k; ++j) {
-    const int32_t row = rows[token * top_k + j];
-    if (row >= kept) continue;
-    if (c / 2 < static_cast<int>(v.pitch))
-      *reinterpret_cast<uint2*>(v.codes + row * v.pitch + c / 2) = s.codes;
-    if (seg % (4 * kPerBlock) == 0) {
-      const int32_t e = ids[token * top_k + j];
-      const int32_t first = v.offsets[e];
-      const int tile = first / kTileRows + e + (row - first) / kTileRows;
-      *reinterpret_cast<uint32_t*>(v.scales + tile * v.tile_bytes +
-                                   scale_at((row - first) % kTileRows, seg / kPerBlock)) = word;
-    }
+    const int64_t at = s_codes[j];
+    if (at < 0) continue;
+    if (padded) *reinterpret_cast<uint2*>(codes + at) = s.codes;
+    if (leads) *reinterpret_cast<uint32_t*>(scales + s_scales[j]) = word;
   }
 }
 

@@ -27,10 +27,9 @@ inline int check_routing(const moe_routing_t* r) {
   if (!r || r->tokens < 0 || r->top_k < 1 || r->top_k > MOE_MAX_TOP_K || r->experts < 1 ||
       r->experts > MOE_MAX_EXPERTS || r->tokens > MOE_MAX_SLOTS / r->top_k)
     return GEMM_ERR_INVALID_VALUE;
-  if (r->tokens > 0 && (!r->offsets || !r->rows || !r->pairs || !r->ids))
+  if (r->tokens > 0 && (!r->offsets || !r->rows || !r->ids))
     return GEMM_ERR_INVALID_VALUE;
-  if (!aligned_to(r->offsets, 4) || !aligned_to(r->rows, 4) || !aligned_to(r->pairs, 4) ||
-      !aligned_to(r->ids, 4))
+  if (!aligned_to(r->offsets, 4) || !aligned_to(r->rows, 4) || !aligned_to(r->ids, 4))
     return GEMM_ERR_MISALIGNED;
   return GEMM_OK;
 }

@@ -17,7 +17,7 @@ P = [0x10000000 * (i + 1) for i in range(8)]   # never dereferenced
 class RoutingC(ctypes.Structure):          # moe_routing_t
     _fields_ = [("tokens", ctypes.c_int64), ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32),
                 ("offsets", ctypes.c_void_p), ("rows", ctypes.c_void_p),
-                ("pairs", ctypes.c_void_p), ("ids", ctypes.c_void_p)]
+                ("ids", ctypes.c_void_p)]
 
 
 class MatrixC(ctypes.Structure):           # fp4_matrix_t
@@ -43,7 +43,8 @@ def ex():
             "fp4_quantize": [pm, vp, i64, i32, pr, vp],
             "fp4_dequantize": [vp, i32, pm, vp],
             "fp4_gemm_tn": [vp, i32, pm, pm, ctypes.c_float, vp],
-            "moe_sort": [vp, vp, vp, vp, i64, i32, i32, vp],
+            "moe_sort": [vp, vp, vp, i64, i32, i32, vp],
+            "moe_pairs": [vp, pr, vp],
             "moe_dispatch": [vp, vp, i64, i64, i32, pr, vp],
             "moe_dispatch_backward": [vp, vp, i64, i32, pr, vp],
             "moe_combine": [vp, vp, vp, i64, i32, pr, vp],
@@ -68,9 +69,9 @@ def test_package_exports(ex):
 
 
 def routing(ex, tokens=10, top_k=2, experts=4, **kw):
-    v = dict(offsets=P[4], rows=P[5], pairs=P[6], ids=P[7])
+    v = dict(offsets=P[4], rows=P[5], ids=P[7])
     v.update(kw)
-    return RoutingC(tokens, top_k, experts, v["offsets"], v["rows"], v["pairs"], v["ids"])
+    return RoutingC(tokens, top_k, experts, v["offsets"], v["rows"], v["ids"])
 
 
 def matrix(ex, rows=64, cols=256, format=0, exponent=0, groups=1, group_rows=None, offsets=None,
@@ -95,7 +96,7 @@ def test_sizes(ex):
                  (9, 8, 0, 2, 0), (8, 8, 0, 1025, 1), (8, 8, 0, 1, 2), (2**31, 8, 0, 1, 0)]:
         assert ex.LIB.fp4_scale_bytes(*args, ctypes.byref(n)) == E, args
     for args in [(-1, 2, 4), (10, 0, 4), (10, 65, 4), (10, 2, 0), (10, 2, 1025), (2**31, 1, 4)]:
-        assert ex.LIB.moe_sort(P[0], P[1], P[2], P[3], *args, None) == E, args
+        assert ex.LIB.moe_sort(P[0], P[1], P[3], *args, None) == E, args
 
 
 def quantize(ex, m, x=P[2], ldx=256, type=0, r=None):
@@ -169,10 +170,14 @@ def test_gemm_refusals(ex):
 def test_routing_refusals(ex):
     E, MIS, L = 1, 2, ex.LIB
     r = ctypes.byref(routing(ex))
-    assert L.moe_sort(0, P[1], P[2], P[3], 10, 2, 4, None) == E
-    assert L.moe_sort(P[0], 0, P[2], P[3], 10, 2, 4, None) == E
-    assert L.moe_sort(P[0] + 2, P[1], P[2], P[3], 10, 2, 4, None) == MIS
-    assert L.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 1025, None) == E
+    assert L.moe_sort(0, P[1], P[3], 10, 2, 4, None) == E
+    assert L.moe_sort(P[0], 0, P[3], 10, 2, 4, None) == E
+    assert L.moe_sort(P[0] + 2, P[1], P[3], 10, 2, 4, None) == MIS
+    assert L.moe_sort(P[0], P[1], P[3], 10, 2, 1025, None) == E
+    assert L.moe_sort(P[0], P[1], P[1] + 16, 10, 2, 4, None) == E
+    assert L.moe_sort(P[0], P[0] + 16, P[3], 10, 2, 4, None) == E
+    assert L.moe_pairs(0, r, None) == E and L.moe_pairs(P[5], r, None) == E
+    assert L.moe_pairs(P[0] + 1, r, None) == MIS and L.moe_pairs(P[0], None, None) == E
     assert L.moe_dispatch(0, P[1], 64, 64, 0, r, None) == E
     assert L.moe_dispatch(P[0], P[1], 63, 64, 0, r, None) == E
     assert L.moe_dispatch(P[0], P[1], 64, -1, 0, r, None) == E
@@ -187,7 +192,7 @@ def test_routing_refusals(ex):
     assert L.moe_combine_backward(P[0], P[1], P[2], P[0] + 64, P[3], 64, 0, r, None) == E
     assert L.moe_combine_backward(P[0], P[1], P[2], P[3], 0, 64, 0, r, None) == E
     assert L.moe_combine_backward(P[0], P[1], 0, P[3], P[2], 64, 0, r, None) == E
-    empty = ctypes.byref(routing(ex, tokens=0, offsets=0, rows=0, pairs=0, ids=0))
+    empty = ctypes.byref(routing(ex, tokens=0, offsets=0, rows=0, ids=0))
     assert L.moe_dispatch(0, 0, 64, 64, 0, empty, None) == 0
     assert L.moe_combine(0, 0, 0, 64, 0, empty, None) == 0
     assert L.moe_combine_backward(0, 0, 0, 0, 0, 64, 0, empty, None) == 0
@@ -201,7 +206,7 @@ def test_valid_calls_without_a_device_report_it(ex):
     a, b = matrix(ex), matrix(ex, rows=128, codes=P[4], scales=P[5])
     assert quantize(ex, a) in bad
     assert gemm(ex, a, b) in bad
-    assert ex.LIB.moe_sort(P[0], P[1], P[2], P[3], 10, 2, 4, None) in bad
+    assert ex.LIB.moe_sort(P[0], P[1], P[3], 10, 2, 4, None) in bad
     assert ex.LIB.moe_combine(P[0], P[1], P[2], 64, 0, ctypes.byref(r), None) in bad
 
 

@@ -142,7 +142,7 @@ def test_quantise_into_expert_order(lib, form, tokens, top_k, experts, dropped, 
     r = lib.moe_sort(ids, experts)
     q = lib.fp4_quantize(x, format=form, routing=r)
     q.scales  # a row per slot, tiles by offsets
-    pairs, off = r.pairs.cpu().numpy(), r.offsets.cpu().numpy()
+    pairs, off = lib.moe_pairs(r).cpu().numpy(), r.offsets.cpu().numpy()
     want = ref.to_numpy(x)[pairs // top_k]
     live = check_stored(q, want, form)
     np.testing.assert_array_equal(live, np.arange(len(pairs)) < off[-1])
@@ -256,7 +256,7 @@ def test_products_by_expert(lib, form, tokens, top_k, experts, dropped, only, n,
     r = lib.moe_sort(ids, experts)
     out = torch.full((r.slots, n), float("nan"), dtype=dtype, device="cuda")
     lib.fp4_gemm_tn(lib.fp4_quantize(x, format=form, routing=r), qw, dtype=dtype, out=out)
-    off, pairs = r.offsets.cpu().numpy(), r.pairs.cpu().numpy()
+    off, pairs = r.offsets.cpu().numpy(), lib.moe_pairs(r).cpu().numpy()
     for e in range(experts):
         if off[e] < off[e + 1]:
             seg = slice(off[e], off[e + 1])
