@@ -82,12 +82,12 @@ int encode_scales(CUtensorMap* map, const fp4_matrix_t* m, int64_t chunks) {
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
-template <typename T, int kFormat, int kBN>
-int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas, cudaStream_t s) {
+template <typename T, int kFormat>
+int launch_single(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas, cudaStream_t s) {
   const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);  // the count of tiles before each
-  using S = Fp4GemmShape<kFormat, kBN>;
+  using S = Fp4GemmShape<kFormat>;
   p.stages = S::stages_that_fit(fixed);
-  const auto kernel = fp4_gemm_tc<T, kFormat, kBN>;
+  const auto kernel = fp4_gemm_tc<T, kFormat>;
   static std::once_flag once;  // per instantiation
   static cudaError_t granted = cudaSuccess;
   std::call_once(once, [&] {
@@ -102,25 +102,27 @@ int launch(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas
                     x, p);
 }
 
+struct PairMaps {
+  CUtensorMap w, x, sw, sx;
+};
+
 template <typename T, int kFormat>
-int launch_pair(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& sw,
-                const CUtensorMap& sx, Fp4GemmParams p, int ctas, cudaStream_t s) {
+int launch_pair(const PairMaps& m, Fp4GemmParams p, int pairs, cudaStream_t s) {
   const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);
   using S = Fp4PairShape<kFormat>;
   p.stages = S::stages_that_fit(fixed);
-  const auto kernel = fp4_gemm_pair<T, kFormat>;
   static std::once_flag once;  // per instantiation
   static cudaError_t granted = cudaSuccess;
-  std::call_once(once, [&] {
-    granted = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   kGemmSmemLimit);
+  std::call_once(once, [] {
+    granted = cudaFuncSetAttribute(fp4_gemm_pair<T, kFormat>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemLimit);
   });
   if (granted != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, 2u,
-                    w, x, sw, sx, p);
+  return launch_pdl(fp4_gemm_pair<T, kFormat>, dim3(2 * pairs), dim3(kGemmThreads),
+                    fixed + p.stages * S::kStageBytes, s, 2u, m.w, m.x, m.sw, m.sx, p);
 }
 
 }  // namespace
@@ -179,44 +181,43 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   }
   p.error = static_cast<uint32_t*>(words) + error_index(s);
 
-  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs.  Both are bound by
-  // what an SM loads (36 against 38 KiB per 256 columns), so the one with fewer
-  // waves of tiles is taken; a pair's tile does four times the work.  With
-  // groups by offsets the number of row tiles is not known here: a group is
-  // taken to have the mean number of rows.
+  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs, which do four times
+  // the work in about the time (an SM takes in 36 and 38 KiB per 256 columns):
+  // the one with fewer waves of tiles, single CTAs if equal (128 x 14336 x 4096
+  // mxfp4: 8.6 against 10.0 us; 8192^3: 261 against 170).  With groups by
+  // offsets the number of row tiles is not known here: a group is taken to
+  // have the mean number of rows.
   const auto tiles_of = [&](int64_t bm, int64_t bn) {
     const int64_t group = a->offsets ? (a->rows + a->groups - 1) / a->groups : a->group_rows;
     return std::min<int64_t>(a->groups, a->rows) * ((group + bn - 1) / bn) * ((n_out + bm - 1) / bm);
   };
-  const int64_t single_waves = (tiles_of(128, 128) + sms - 1) / sms;
-  const int64_t pair_waves = (tiles_of(256, 256) + sms / 2 - 1) / (sms / 2);
+  const auto waves = [](int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slots; };
   const int64_t x_chunks =
       tile_count(a->rows, a->groups, a->offsets != nullptr) * p.tile_chunks;
   const int64_t w_chunks = static_cast<int64_t>(a->groups) * p.w_group_tiles * p.tile_chunks;
-  const bool pair = pair_waves < single_waves && x_chunks <= INT_MAX && w_chunks <= INT_MAX;
-  const int bn = pair ? 256 : 128;
-  const int bm = pair ? 256 : 128;
+  const bool pair = waves(tiles_of(256, 256), sms / 2) < waves(tiles_of(128, 128), sms) &&
+                    x_chunks <= INT_MAX && w_chunks <= INT_MAX;  // counted in 32 bits there
+  const int bm = pair ? 256 : 128, bn = bm;
   p.m_tiles = static_cast<int32_t>((n_out + bm - 1) / bm);
   // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile
-  // loads little more than it has.
+  // loads little more than it has (8 tokens over 64 experts: 21 us against 27
+  // with boxes of 128).
   p.box_rows = a->offsets || a->group_rows <= 64 ? 32 : 128;
   // One CTA per SM, fewer where there cannot be that many tiles.
   const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
                                        : a->groups * ((a->group_rows + bn - 1) / bn);
-  const int64_t units = row_tiles * p.m_tiles;
-  CUtensorMap tmW, tmX, tmSW, tmSX;
-  if ((rc = encode_codes(&tmW, b, kGemmM)) != GEMM_OK ||
-      (rc = encode_codes(&tmX, a, p.box_rows)) != GEMM_OK)
+  const int units = static_cast<int>(std::min<int64_t>(pair ? sms / 2 : sms, row_tiles * p.m_tiles));
+  PairMaps m;
+  if ((rc = encode_codes(&m.w, b, kGemmM)) != GEMM_OK ||
+      (rc = encode_codes(&m.x, a, p.box_rows)) != GEMM_OK)
     return rc;
-  if (pair && ((rc = encode_scales(&tmSW, b, w_chunks)) != GEMM_OK ||
-               (rc = encode_scales(&tmSX, a, x_chunks)) != GEMM_OK))
+  if (pair && ((rc = encode_scales(&m.sw, b, w_chunks)) != GEMM_OK ||
+               (rc = encode_scales(&m.sx, a, x_chunks)) != GEMM_OK))
     return rc;
   const auto go = [&](auto t, auto fmt) {
     using T = decltype(t);
-    if (pair)
-      return launch_pair<T, fmt()>(tmW, tmX, tmSW, tmSX, p,
-                                   2 * static_cast<int>(std::min<int64_t>(sms / 2, units)), s);
-    return launch<T, fmt(), 128>(tmW, tmX, p, static_cast<int>(std::min<int64_t>(sms, units)), s);
+    return pair ? launch_pair<T, fmt()>(m, p, units, s)
+                : launch_single<T, fmt()>(m.w, m.x, p, units, s);
   };
   const auto by_format = [&](auto t) {
     return a->format == FP4_NV ? go(t, std::integral_constant<int, FP4_NV>{})

@@ -2,15 +2,16 @@
 //
 // D[r][n] = alpha sum_k a[r][k] b[g][n][k] for the rows r of group g.  The
 // weights are the instruction's M operand (128 rows a tile) and the
-// activations its N operand (1 to kBN rows a tile): N may be any multiple of
+// activations its N operand (1 to 128 rows a tile here, to 256 in the kernel
+// over CTA pairs): N may be any multiple of
 // 16, so that an expert with few rows costs few columns.  A tile's
 // accumulator is then D transposed: lane = output n, column = row r.
 //
 // Inside a CTA, one per SM, each walking the list of tiles:
-//   warp 0, one thread -- producer: per 256 columns of k (128 bytes of codes a
-//       row), TMA boxes of both operands' codes and bulk copies of their
-//       scale chunks into a ring of stages;
-//   warp 1, one thread -- copies the stage's scales into tensor memory
+//   warps 0 and 10 -- producers, of the weights and of the rows: per 256 columns
+//       of k (128 bytes of codes a row), TMA boxes of codes and a bulk copy of
+//       the scale chunks into a ring of stages;
+//   warp 1 -- copies the stage's scales into tensor memory
 //       (tcgen05.cp, 512 bytes = 128 rows x 4 blocks at a time, replicated to
 //       the four lane quadrants) and issues a block-scaled MMA per 64 columns;
 //   warps 2 .. 9 -- epilogue: two warps per lane quadrant take alternate
@@ -33,7 +34,8 @@ namespace gb300 {
 constexpr int kGemmM = 128;           // weight rows per tile
 constexpr int kGemmBytesK = 128;      // codes of a row per stage: 256 elements
 constexpr int kGemmEpiWarps = 8;
-constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
+constexpr int kGemmRowWarp = 2 + kGemmEpiWarps;  // the second producer
+constexpr int kGemmThreads = 96 + 32 * kGemmEpiWarps;
 constexpr int kGemmMaxStages = 8;
 constexpr uint32_t kWBytes = kGemmM * kGemmBytesK;
 constexpr uint32_t kTmemCols = 512;
@@ -62,21 +64,20 @@ struct Fp4GemmParams {
   uint32_t* error;
 };
 
-template <int kFormat, int kBN>
+constexpr int kGemmBN = 128;  // activation rows per tile, at most
+
+template <int kFormat>
 struct Fp4GemmShape {
-  static constexpr int kXTiles = (kBN + kTileRows - 1) / kTileRows;  // scale tiles of the rows
   static constexpr uint32_t kScaleStage = chunks_per_stage(kFormat) * kChunkBytes;
-  static constexpr uint32_t kXBytes = kBN * kGemmBytesK;
-  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleStage * (1 + kXTiles);
-  static constexpr int kAccs = kBN > 128 ? 1 : 2;  // accumulators in columns 0 .. 255
+  static constexpr uint32_t kXBytes = kGemmBN * kGemmBytesK;
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + 2 * kScaleStage;
   // columns of scales per slot: 4 per chunk and 128 rows
   static constexpr uint32_t kWCols = 4 * chunks_per_stage(kFormat);
-  static constexpr uint32_t kSlotCols = kWCols * (1 + kXTiles);
+  static constexpr uint32_t kSlotCols = 2 * kWCols;
   static constexpr int kSlots = (kTmemCols - kTmemScales) / kSlotCols;
   static int stages_that_fit(uint32_t fixed) {
-    int s = static_cast<int>((kGemmSmemLimit - fixed) / kStageBytes);
-    if (s > kSlots) s = kSlots;
-    return s > kGemmMaxStages ? kGemmMaxStages : s;
+    return std::min<int>({static_cast<int>((kGemmSmemLimit - fixed) / kStageBytes), kSlots,
+                          kGemmMaxStages});
   }
 };
 
@@ -320,12 +321,13 @@ __device__ __forceinline__ void count_row_tiles(const Fp4GemmParams& p, int32_t*
 }
 
 // ------------------------------------------------------------------ kernel
-template <typename T, int kFormat, int kBN>
+template <typename T, int kFormat>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     fp4_gemm_tc(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const Fp4GemmParams p) {
-  static_assert(kBN % kTileRows == 0, "row tiles start whole scale tiles");
-  using S = Fp4GemmShape<kFormat, kBN>;
+  constexpr int kBN = kGemmBN;
+  static_assert(kBN == kTileRows, "a row tile is a scale tile");
+  using S = Fp4GemmShape<kFormat>;
   constexpr int kChunks = chunks_per_stage(kFormat);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -375,8 +377,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
       static_cast<int64_t>(p.m_tiles);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
+  if (warp == 0 || warp == kGemmRowWarp) {
+    // ---------------------------------------------------------- producers
+    // Warp 0 loads the weights and their scales, the other the rows and theirs:
+    // what a copy costs its issuer bounds one warp alone.
     // The whole warp runs the loop and one lane issues: the values that the
     // copies take are then the same in every lane, which costs the issue of a
     // copy far less than a loop inside one lane's branch does.
@@ -386,9 +390,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const int boxes = (tile.count + p.box_rows - 1) / p.box_rows;
-      const int x_tiles = (tile.count + kTileRows - 1) / kTileRows;
       const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
-                             S::kScaleStage * (1 + x_tiles);
+                             2 * S::kScaleStage;
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * kGemmM);
       const int x_row = static_cast<int>(tile.x_row);
       const uint8_t* w_scales =
@@ -405,15 +408,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t x_dst = w_dst + kWBytes;
           const uint32_t s_dst = x_dst + S::kXBytes;
           const uint32_t full = full_bar(stage);
-          mbar_arrive_expect_tx(full, bytes);
-          tma_load_2d(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
-                        x_row + b * p.box_rows);
-          bulk_load(s_dst, w_scales, S::kScaleStage, full);
-          bulk_load(s_dst + S::kScaleStage, x_scales, S::kScaleStage, full);
-          if (S::kXTiles > 1 && x_tiles > 1)
-            bulk_load(s_dst + 2 * S::kScaleStage, x_scales + p.x_tile_bytes, S::kScaleStage, full);
+          if (warp == 0) {
+            mbar_arrive_expect_tx(full, bytes);
+            tma_load_2d(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+            bulk_load(s_dst, w_scales, S::kScaleStage, full);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
+                          x_row + b * p.box_rows);
+            bulk_load(s_dst + S::kScaleStage, x_scales, S::kScaleStage, full);
+          }
         }
         __syncwarp();
         w_scales += S::kScaleStage;
@@ -442,7 +446,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
     for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
-      const bool two = S::kXTiles > 1 && tile.count > kTileRows;  // scale tiles of the rows
       const uint32_t idesc = fp4_idesc<kFormat>(kGemmM, (tile.count + 15) & ~15);
       if (!gemm_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
       tc_fence_after_sync();
@@ -461,11 +464,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             tmem_copy_scales(w_cols + 4 * c, s_desc + ((c * kChunkBytes) >> 4));
-            tmem_copy_scales(x_cols + 4 * (c * S::kXTiles),
-                             s_desc + ((S::kScaleStage + c * kChunkBytes) >> 4));
-            if (two)
-              tmem_copy_scales(x_cols + 4 * (c * S::kXTiles + 1),
-                               s_desc + ((2 * S::kScaleStage + c * kChunkBytes) >> 4));
+            tmem_copy_scales(x_cols + 4 * c, s_desc + ((S::kScaleStage + c * kChunkBytes) >> 4));
           }
           const uint64_t w_desc = w_desc0 + at;
           const uint64_t x_desc = w_desc + (kWBytes >> 4);
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
             umma_fp4<kFormat>(d_tmem, w_desc + 2u * s, x_desc + 2u * s,
                               idesc | fp4_idesc_scale_bytes(byte), w_cols + 4 * chunk,
-                              x_cols + 4 * S::kXTiles * chunk, (kb | s) != 0);
+                              x_cols + 4 * chunk, (kb | s) != 0);
           }
           umma_commit(empty_bar(stage));
         }
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!ok) break;
       if (elect_one()) umma_commit(tfull_bar(acc));
       __syncwarp();
-      if (++acc == S::kAccs) {
+      if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
@@ -520,7 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                            __syncwarp();
                            if (lane == 0) mbar_arrive(tempty_bar(acc));
                          });
-      if (++acc == S::kAccs) {
+      if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }

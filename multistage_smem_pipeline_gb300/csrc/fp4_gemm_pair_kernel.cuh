@@ -1,12 +1,19 @@
 // The 4-bit product over CTA pairs (tcgen05 cta_group::2).
 //
-// A pair owns 256 outputs x up to 256 rows.  Each CTA loads its own 128 rows
-// of weights, its half of the activations' rows, the scales of its weights and
-// all the activations' scales; the even CTA issues, and each CTA accumulates
-// its 128 outputs in its own tensor memory.  Per 256 columns of k an SM then
-// loads 38 KiB for 512 cycles of MMA instead of the 54 KiB of a single CTA's
-// 128 x 256 tile, which the load rate of an SM (about 60 B a cycle with all of
-// them loading) does not cover.
+// A pair owns 256 outputs x up to 256 rows.  Each CTA loads its own 128 rows of
+// weights, its half of the activations' rows, the scales of its weights and one
+// of the two tiles of the activations' scales, which goes to both; the even CTA
+// issues, and each CTA accumulates its 128 outputs in its own tensor memory.
+//
+// What bounds it is shared memory: per 256 columns of k an SM takes in 38 KiB
+// and its MMAs read 32 KiB of codes and 6 KiB of scales in 512 cycles, more
+// than its 128 bytes a cycle; a single CTA's 128 x 256 tile would take in 54
+// and read 54.  At 8192^3 the loads alone take 120 us, the MMAs alone 136 (of
+// which 14 are the accumulator changing hands, as there is no room for two of
+// 256 columns and the scales), both 162, and the stores make it 170
+// (6.5 PFLOP/s).  Tried and no faster: 384 rows a tile (176 us: 10 waves where
+// 9.3 would do), two pairs sharing the rows by multicast (177: 36 such clusters
+// fit where 38 would fill the SMs), L2 prefetch of the weights (194).
 //
 // Barriers as in the fp16 pair kernel: `full` in the even CTA counts both
 // CTAs' bytes; `empty` and `tfull` are in both, committed to both; `tempty` in
@@ -55,6 +62,18 @@ __device__ __forceinline__ void umma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
+// One box into the shared memory of every CTA of `cta_mask`, at the same
+// offset; its bytes complete on the barrier at `bar`'s offset in the even CTA of
+// each of those CTAs' pairs (`bar`: the address in this CTA's).
+__device__ __forceinline__ void tma_load_2d_pair_mc(uint32_t dst, const void* tmap, uint32_t bar,
+                                                    int32_t x, int32_t y, uint16_t cta_mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "h"(cta_mask)
+      : "memory");
+}
+
 // In each CTA of the pair, from its own shared memory to its own tensor memory.
 __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
@@ -78,6 +97,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int stages = p.stages;
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  constexpr uint16_t kBoth = 0x3;
   const uint32_t bars = base + stages * S::kStageBytes;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kGemmMaxStages + s); };
@@ -121,8 +141,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
       static_cast<int64_t>(p.m_tiles);
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer (both CTAs)
+  if (warp == 0 || warp == kGemmRowWarp) {
+    // ---------------------------------------------------------- producers (both CTAs)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
@@ -136,7 +156,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * (2 * kGemmM) + rank * kGemmM);
       const int x_row = static_cast<int>(tile.x_row) + rank * half_n;
       int sw = (tile.group * p.w_group_tiles + 2 * tile.m + rank) * p.tile_chunks;
-      int sx = static_cast<int>(tile.x_tile) * p.tile_chunks;
+      // each CTA loads one tile of the rows' scales, for both
+      int sx = (static_cast<int>(tile.x_tile) + rank) * p.tile_chunks;
+      const bool loads_sx = rank == 0 || two;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
           ok = false;
@@ -147,15 +169,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t x_dst = w_dst + kWBytes;
           const uint32_t s_dst = x_dst + S::kXBytes;
           const uint32_t full = mapa_shared(full_bar(stage), 0);
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-          tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
-                             x_row + b * p.box_rows);
-          tma_load_2d_pair(s_dst, &tmSW, full, 0, sw);
-          tma_load_2d_pair(s_dst + S::kScaleStage, &tmSX, full, 0, sx);
-          if (two)
-            tma_load_2d_pair(s_dst + 2 * S::kScaleStage, &tmSX, full, 0, sx + p.tile_chunks);
+          if (warp == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+            tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+            tma_load_2d_pair(s_dst, &tmSW, full, 0, sw);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
+                               x_row + b * p.box_rows);
+            if (loads_sx)
+              tma_load_2d_pair_mc(s_dst + (1 + rank) * S::kScaleStage, &tmSX, full, 0, sx, kBoth);
+          }
         }
         __syncwarp();
         sw += kChunks;
@@ -167,7 +191,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
-    if (rank == 0) {  // the even CTA's barriers count both CTAs' bytes
+    if (rank == 0 && warp == 0) {  // the even CTA's barriers count both CTAs' bytes
       const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
       for (uint32_t i = first; i < issued; ++i)
         gemm_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
@@ -218,7 +242,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                      idesc | fp4_idesc_scale_bytes(byte), w_cols + 4 * chunk,
                                      x_cols + 8 * chunk, (kb | s) != 0);
             }
-            umma_commit_pair_mc(empty_bar(stage), 0x3);
+            umma_commit_pair_mc(empty_bar(stage), kBoth);
           }
           __syncwarp();
           if (++stage == stages) {
@@ -227,7 +251,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) umma_commit_pair_mc(tfull_bar, 0x3);
+        if (elect_one()) umma_commit_pair_mc(tfull_bar, kBoth);
         __syncwarp();
         acc_phase ^= 1u;
       }

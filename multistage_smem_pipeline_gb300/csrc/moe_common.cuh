@@ -125,9 +125,16 @@ __device__ __forceinline__ Pack load8(const uint16_t* row, int e, int n) {
   const uintptr_t at = start + 2 * static_cast<intptr_t>(e);  // may lie before the row
   const uintptr_t word = at & ~static_cast<uintptr_t>(15);
   uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-  if (word + 16 > start && word < start + 2 * static_cast<uintptr_t>(n)) lo = *reinterpret_cast<const uint4*>(word);
-  if (word != at && word + 16 < start + 2 * static_cast<uintptr_t>(n)) hi = *reinterpret_cast<const uint4*>(word + 16);
+  if (word + 16 > start && word < start + 2 * static_cast<uintptr_t>(n))
+    lo = *reinterpret_cast<const uint4*>(word);
+  Pack p;
   const uint32_t off = static_cast<uint32_t>(at & 15);
+  if (off == 0) {  // for the whole row: it is aligned as the windows are
+    *reinterpret_cast<uint4*>(&p) = lo;
+    return p;
+  }
+  if (word + 16 < start + 2 * static_cast<uintptr_t>(n))
+    hi = *reinterpret_cast<const uint4*>(word + 16);
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   if (off & 8) {
 #pragma unroll
@@ -137,7 +144,6 @@ __device__ __forceinline__ Pack load8(const uint16_t* row, int e, int n) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
-  Pack p;
 #pragma unroll
   for (int i = 0; i < 4; ++i) p.w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
   return p;
