@@ -109,11 +109,11 @@ struct Routing {
   }
 
   const at::Tensor& get_offsets() {
-    if (!offsets.defined()) offsets = buffer.narrow(0, 0, c.experts + 1);
+    if (!offsets.defined()) offsets = buffer.as_strided({c.experts + 1}, {1}, 0);
     return offsets;
   }
   const at::Tensor& get_rows() {
-    if (!rows.defined()) rows = buffer.narrow(0, head(), slots()).view({c.tokens, c.top_k});
+    if (!rows.defined()) rows = buffer.as_strided({c.tokens, c.top_k}, {c.top_k, 1}, head());
     return rows;
   }
 };

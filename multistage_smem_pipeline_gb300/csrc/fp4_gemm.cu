@@ -167,7 +167,6 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   p.group_rows = a->group_rows;
   p.n_out = n_out;
   p.groups = a->groups;
-  p.k = static_cast<int32_t>(a->cols);
   p.num_kb = static_cast<int32_t>(col_stages(a->cols));
   p.w_group_tiles = static_cast<int32_t>((n_out + kTileRows - 1) / kTileRows);
   p.tile_chunks = p.num_kb * chunks_per_stage(a->format);

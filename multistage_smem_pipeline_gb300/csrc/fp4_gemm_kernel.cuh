@@ -52,7 +52,7 @@ struct Fp4GemmParams {
   uint16_t* d;
   const int32_t* offsets;  // of the rows' groups; null: uniform groups
   int64_t rows, group_rows, n_out;
-  int32_t groups, k, num_kb;
+  int32_t groups, num_kb;
   int32_t m_tiles;         // weight tiles (of the kernel's height) per group
   int32_t w_group_tiles;   // scale tiles of the weights per group
   int32_t tile_chunks;     // chunks of a scale tile
@@ -468,10 +468,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           const uint64_t w_desc = w_desc0 + at;
           const uint64_t x_desc = w_desc + (kWBytes >> 4);
-          const int left = p.k - kb * kStageCols;
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {  // 64 columns each
-            if (64 * s >= left) break;
+          for (int s = 0; s < 4; ++s) {  // 64 columns each; past k codes and scales are zero
             const int chunk = kFormat == FP4_NV ? s : s >> 1;
             const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
             umma_fp4<kFormat>(d_tmem, w_desc + 2u * s, x_desc + 2u * s,

@@ -10,8 +10,8 @@
 // than its 128 bytes a cycle; a single CTA's 128 x 256 tile would take in 54
 // and read 54.  At 8192^3 the loads alone take 120 us, the MMAs alone 136 (of
 // which 14 are the accumulator changing hands, as there is no room for two of
-// 256 columns and the scales), both 162, and the stores make it 170
-// (6.5 PFLOP/s).  Tried and no faster: 384 rows a tile (176 us: 10 waves where
+// 256 columns and the scales), both 158, and the stores make it 166
+// (6.6 PFLOP/s).  Tried and no faster: 384 rows a tile (176 us: 10 waves where
 // 9.3 would do), two pairs sharing the rows by multicast (177: 36 such clusters
 // fit where 38 would fill the SMs), L2 prefetch of the weights (194).
 //
@@ -206,7 +206,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
       for (int64_t t = pair; ok && t < tiles; t += pairs) {
         const GemmTile tile = gemm_tile<kBN>(t, p, before);
-        const bool two = tile.count > kTileRows;
         const uint32_t idesc = fp4_idesc<kFormat>(2 * kGemmM, (tile.count + 31) & ~31);
         if (!gemm_wait_warp(tempty_bar, acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
         tc_fence_after_sync();
@@ -216,6 +215,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           tc_fence_after_sync();
+          // No branches in here: leaving out the second tile of scales where the
+          // rows have one, or the steps past k, made the issue the bound (170 us
+          // at 8192^3 against 166; what is copied for nothing is not used).
           if (elect_one()) {
             const uint64_t at = static_cast<uint64_t>((stage * S::kStageBytes) >> 4);
             const uint64_t s_desc = s_desc0 + at;
@@ -226,16 +228,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               tmem_copy_scales_pair(w_cols + 4 * c, s_desc + ((c * kChunkBytes) >> 4));
               tmem_copy_scales_pair(x_cols + 8 * c,
                                     s_desc + ((S::kScaleStage + c * kChunkBytes) >> 4));
-              if (two)
-                tmem_copy_scales_pair(x_cols + 8 * c + 4,
-                                      s_desc + ((2 * S::kScaleStage + c * kChunkBytes) >> 4));
+              tmem_copy_scales_pair(x_cols + 8 * c + 4,
+                                    s_desc + ((2 * S::kScaleStage + c * kChunkBytes) >> 4));
             }
             const uint64_t w_desc = w_desc0 + at;
             const uint64_t x_desc = w_desc + (kWBytes >> 4);
-            const int left = p.k - kb * kStageCols;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              if (64 * s >= left) break;
+            for (int s = 0; s < 4; ++s) {  // 64 columns each; past k codes and scales are zero
               const int chunk = kFormat == FP4_NV ? s : s >> 1;
               const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
               umma_fp4_pair<kFormat>(tmem, w_desc + 2u * s, x_desc + 2u * s,
