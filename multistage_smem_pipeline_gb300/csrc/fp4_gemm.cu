@@ -82,24 +82,68 @@ int encode_scales(CUtensorMap* map, const fp4_matrix_t* m, int64_t chunks) {
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
-template <typename T, int kFormat>
-int launch_single(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int ctas, cudaStream_t s) {
-  const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);  // the count of tiles before each
+template <typename T, int kFormat, bool kSplit>
+int launch_single(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, int tiles,
+                  int device, cudaStream_t s) {
+  const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0) + (kSplit ? kSplitBytes : 0u);
   using S = Fp4GemmShape<kFormat>;
   p.stages = S::stages_that_fit(fixed);
-  const auto kernel = fp4_gemm_tc<T, kFormat>;
-  static std::once_flag once;  // per instantiation
-  static cudaError_t granted = cudaSuccess;
+  const auto kernel = fp4_gemm_tc<T, kFormat, kSplit>;
+  static std::atomic<uint64_t> granted{0};  // per instantiation
+  if (!grant_smem(kernel, kGemmSmemLimit, device, granted)) return GEMM_ERR_CUDA;
+  return launch_pdl(kernel, dim3(tiles * p.split), dim3(kGemmThreads),
+                    fixed + p.stages * S::kStageBytes, s, static_cast<unsigned>(p.split), w, x, p);
+}
+
+// Clusters of `size` CTAs that the device holds at once, a CTA an SM (clusters
+// lie within a GPC, so some SMs may be left out).
+int resident_clusters(int size, int sms, int device) {
+  static std::once_flag once;
+  static int held[3] = {0, 0, 0};  // of 2, 4 and 8
   std::call_once(once, [&] {
-    granted = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   kGemmSmemLimit);
+    const auto kernel = fp4_gemm_tc<__half, FP4_NV, true>;
+    static std::atomic<uint64_t> granted{0};
+    if (!grant_smem(kernel, kGemmSmemLimit, device, granted)) return;
+    for (int i = 0; i < 3; ++i) {
+      cudaLaunchConfig_t cfg;
+      std::memset(&cfg, 0, sizeof(cfg));
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((2u << i) * (sms / (2 << i)));
+      cfg.blockDim = dim3(kGemmThreads);
+      cfg.dynamicSmemBytes = kGemmSmemLimit;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        held[i] = 0;
+      }
+    }
   });
-  if (granted != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
+  return held[size == 2 ? 0 : size == 4 ? 1 : 2];
+}
+
+// CTAs that share each of `tiles` tiles' k.  Measured on GB300: a 256-column
+// block of k takes a lone CTA about 0.28 us (the latency of its loads), and
+// meeting the others 0.6 us and, for the partial sums, up to 3 us for 128 rows.
+// 1 x 4096 x 14336: 17.5 us by one, 10.2 by four; 128 x 512 x 1024: 4.7 and 8.3
+// by two.  All of the clusters have to fit at once (16 tiles by eight: 12.0 us
+// where four take 7.5).
+int choose_split(int64_t tiles, int64_t rows, int num_kb, int sms, int device) {
+  int best = 1;
+  double least = 0.28 * num_kb;
+  for (int split = 2; split <= 8 && 2 * split <= num_kb; split *= 2) {
+    if (tiles > resident_clusters(split, sms, device)) break;
+    const double t = 0.28 * num_kb / split + 0.6 + 3.0 * std::min<int64_t>(rows, 128) / 128;
+    if (t < least) {
+      least = t;
+      best = split;
+    }
   }
-  return launch_pdl(kernel, dim3(ctas), dim3(kGemmThreads), fixed + p.stages * S::kStageBytes, s, 1u, w,
-                    x, p);
+  return best;
 }
 
 struct PairMaps {
@@ -107,20 +151,12 @@ struct PairMaps {
 };
 
 template <typename T, int kFormat>
-int launch_pair(const PairMaps& m, Fp4GemmParams p, int pairs, cudaStream_t s) {
+int launch_pair(const PairMaps& m, Fp4GemmParams p, int pairs, int device, cudaStream_t s) {
   const uint32_t fixed = gemm_fixed_bytes(p.offsets ? p.groups : 0);
   using S = Fp4PairShape<kFormat>;
   p.stages = S::stages_that_fit(fixed);
-  static std::once_flag once;  // per instantiation
-  static cudaError_t granted = cudaSuccess;
-  std::call_once(once, [] {
-    granted = cudaFuncSetAttribute(fp4_gemm_pair<T, kFormat>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmemLimit);
-  });
-  if (granted != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
+  static std::atomic<uint64_t> granted{0};  // per instantiation
+  if (!grant_smem(fp4_gemm_pair<T, kFormat>, kGemmSmemLimit, device, granted)) return GEMM_ERR_CUDA;
   return launch_pdl(fp4_gemm_pair<T, kFormat>, dim3(2 * pairs), dim3(kGemmThreads),
                     fixed + p.stages * S::kStageBytes, s, 2u, m.w, m.x, m.sw, m.sx, p);
 }
@@ -148,8 +184,8 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
     if (m->cols > 0 && (overlaps(D, dbytes, m->codes, code_bytes(m)) ||
                         overlaps(D, dbytes, m->scales, scale_bytes(m))))
       return GEMM_ERR_INVALID_VALUE;
-  int sms = 0;
-  if ((rc = require_device(&sms)) != GEMM_OK) return rc;
+  int sms = 0, device = 0;
+  if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->cols == 0) return write_empty_sum(D, nullptr, 0.0f, a->rows * n_out, sms, s);
   if ((rc = get_encoder()) != GEMM_OK) return rc;
@@ -206,6 +242,10 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
                                        : a->groups * ((a->group_rows + bn - 1) / bn);
   const int units = static_cast<int>(std::min<int64_t>(pair ? sms / 2 : sms, row_tiles * p.m_tiles));
+  // rows of a tile, in the mean: of the groups that there can be
+  const int64_t tile_rows =
+      a->offsets ? (a->rows + a->groups - 1) / a->groups : std::min<int64_t>(a->group_rows, 128);
+  p.split = pair ? 1 : choose_split(row_tiles * p.m_tiles, tile_rows, p.num_kb, sms, device);
   PairMaps m;
   if ((rc = encode_codes(&m.w, b, kGemmM)) != GEMM_OK ||
       (rc = encode_codes(&m.x, a, p.box_rows)) != GEMM_OK)
@@ -215,8 +255,9 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
     return rc;
   const auto go = [&](auto t, auto fmt) {
     using T = decltype(t);
-    return pair ? launch_pair<T, fmt()>(m, p, units, s)
-                : launch_single<T, fmt()>(m.w, m.x, p, units, s);
+    if (pair) return launch_pair<T, fmt()>(m, p, units, device, s);
+    return p.split > 1 ? launch_single<T, fmt(), true>(m.w, m.x, p, units, device, s)
+                       : launch_single<T, fmt(), false>(m.w, m.x, p, units, device, s);
   };
   const auto by_format = [&](auto t) {
     return a->format == FP4_NV ? go(t, std::integral_constant<int, FP4_NV>{})

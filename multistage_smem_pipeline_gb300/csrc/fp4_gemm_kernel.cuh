@@ -43,7 +43,8 @@ constexpr uint32_t kTmemScales = 256;  // first column of the scales
 constexpr int kErrorWords = 64;
 constexpr uint32_t kGemmSmemLimit = 232448;
 
-enum GemmWait : uint32_t { kWaitEmpty = 1, kWaitFull = 2, kWaitTmemEmpty = 3, kWaitTmemFull = 4 };
+enum GemmWait : uint32_t { kWaitEmpty = 1, kWaitFull = 2, kWaitTmemEmpty = 3, kWaitTmemFull = 4,
+                          kWaitParts = 5 };
 
 struct Fp4GemmParams {
   const uint8_t* w_scales;
@@ -58,6 +59,7 @@ struct Fp4GemmParams {
   int32_t tile_chunks;     // chunks of a scale tile
   int32_t box_rows;        // activation rows per TMA box
   int32_t stages;
+  int32_t split;           // CTAs that share a tile's k; 1: none do
   int32_t raster;          // row tiles that share a pass over the weight tiles
   float alpha;
   uint64_t timeout_ns;
@@ -81,9 +83,12 @@ struct Fp4GemmShape {
   }
 };
 
-// Shared memory past the ring: barriers, then the tensor memory address, the
+// A split tile's partial sums: 128 outputs x 128 rows in fp32.
+constexpr uint32_t kSplitBytes = kGemmM * kGemmBN * 4;
+
+// Shared memory past the ring (and the partial sums): barriers, then the tensor memory address, the
 // abort flag, and the running count of row tiles before each group.
-constexpr uint32_t kGemmBars = 2 * kGemmMaxStages + 5;
+constexpr uint32_t kGemmBars = 2 * kGemmMaxStages + 6;
 __host__ __device__ constexpr uint32_t gemm_fixed_bytes(int groups) {
   return 8 * kGemmBars + 16 + 4 * (groups + 1) + 1024;  // 1 KiB to align the ring
 }
@@ -158,6 +163,25 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatil
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > p.timeout_ns) {
+        *abort_flag = 1;
+        atomicCAS(p.error, 0u, static_cast<uint32_t>(GEMM_ERR_TIMEOUT) | (site << 8));
+        return false;
+      }
+    }
+  }
+}
+
+// A wait for data from other CTAs of the cluster.
+__device__ __forceinline__ bool gemm_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag, uint32_t site,
+                                                  const Fp4GemmParams& p) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 31u) == 0) {
       if (*abort_flag) return false;
       if (global_timer_ns() - t0 > p.timeout_ns) {
@@ -290,6 +314,67 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, int half, int count, 
   }
 }
 
+// A CTA's part of a split tile: thread `out` of 128 (its output) and the 32-column
+// chunks of its warp.  Slot s of `partial` holds part s's sums for this CTA's
+// columns: [s][chunk][output][32 / split].
+template <typename T>
+__device__ __forceinline__ void store_split_tile(uint32_t t_row, int out, int half, int count,
+                                                 int part, const Fp4GemmParams& p, uint32_t partial,
+                                                 uint32_t parts_bar, volatile int* abort_flag,
+                                                 uint16_t* d, bool live) {
+  const int quads = 8 / p.split;  // groups of four columns a CTA has of a chunk
+  const auto slot = [&](int s, int chunk) {
+    return partial + static_cast<uint32_t>(((s * 4 + chunk) * kGemmM + out) * quads) * 16u;
+  };
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int chunk = 2 * c + half;
+    if (32 * chunk >= count) break;
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(t_row + 32 * chunk, r);
+    tmem_ld_wait();
+    const uint32_t mine = slot(part, chunk);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const int to = g / quads;
+      const uint32_t at = mine + (g - to * quads) * 16u;
+      if (to == part)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[4 * g]),
+                     "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
+                     : "memory");
+      else
+        st_async_cluster_v4(mapa_shared(at, to), r[4 * g], r[4 * g + 1], r[4 * g + 2],
+                            r[4 * g + 3], mapa_shared(parts_bar, to));
+    }
+  }
+  if (!gemm_wait_cluster(parts_bar, 0, abort_flag, kWaitParts, p)) return;
+  if (!live) return;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int chunk = 2 * c + half;
+    for (int g = 0; g < quads; ++g) {
+      const int col = 32 * chunk + 4 * (part * quads + g);
+      if (col >= count) break;
+      float sum[4] = {};
+      for (int s = 0; s < p.split; ++s) {
+        float v[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(slot(s, chunk) + g * 16u)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += v[i];
+      }
+      const uint32_t w[2] = {pack_two<T>(p.alpha * sum[0], p.alpha * sum[1]),
+                             pack_two<T>(p.alpha * sum[2], p.alpha * sum[3])};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < count)
+          d[(col + i) * p.n_out] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
 // Rows of no group are zero: elements [from, end) of D, by every epilogue
 // thread of the grid.
 __device__ __forceinline__ void zero_tail(const Fp4GemmParams& p) {
@@ -321,7 +406,13 @@ __device__ __forceinline__ void count_row_tiles(const Fp4GemmParams& p, int32_t*
 }
 
 // ------------------------------------------------------------------ kernel
-template <typename T, int kFormat>
+// kSplit: few tiles.  A cluster of p.split CTAs (2, 4 or 8) shares one tile, each
+// taking its part of k; then every CTA sends each other one its partial sums
+// for that one's 32 / split columns of each chunk of 32, straight from
+// registers into its shared memory, and adds up what it receives for its own
+// in the order of the parts.  No sum depends on who came first.  The grid has a
+// cluster for every tile there may be.
+template <typename T, int kFormat, bool kSplit>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     fp4_gemm_tc(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const Fp4GemmParams p) {
@@ -335,13 +426,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* const smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
-  const uint32_t bars = base + stages * S::kStageBytes;
+  const uint32_t partial = base + stages * S::kStageBytes;
+  const uint32_t bars = partial + (kSplit ? kSplitBytes : 0u);
+  const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
+  const int64_t tile_step = kSplit ? INT64_MAX / 2 : gridDim.x;
+  const int kb_first = kSplit ? part * p.num_kb / p.split : 0;
+  const int kb_end = kSplit ? (part + 1) * p.num_kb / p.split : p.num_kb;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kGemmMaxStages + s); };
   const auto tfull_bar = [&](int b) { return bars + 8u * (2 * kGemmMaxStages + b); };
   const auto tempty_bar = [&](int b) { return bars + 8u * (2 * kGemmMaxStages + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * kGemmMaxStages + 4);
-  uint8_t* const misc = smem + stages * S::kStageBytes + 8 * kGemmBars;
+  const uint32_t parts_bar = drain_bar + 8;  // the other parts' sums have come
+  uint8_t* const misc = smem + (bars - base) + 8 * kGemmBars;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   int32_t* const before = reinterpret_cast<int32_t*>(misc + 16);  // row tiles before each group
@@ -357,6 +455,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_init(tempty_bar(b), kGemmEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(parts_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmW);
@@ -370,7 +469,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   grid_dependency_wait();
   if (p.offsets && warp == 2) count_row_tiles<kBN>(p, before, lane);
   tc_fence_before_sync();
-  __syncthreads();
+  if (kSplit) cluster_sync();  // the others' barriers exist
+  else __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int64_t tiles =
@@ -387,7 +487,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const int boxes = (tile.count + p.box_rows - 1) / p.box_rows;
       const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
@@ -396,9 +496,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int x_row = static_cast<int>(tile.x_row);
       const uint8_t* w_scales =
           p.w_scales +
-          (static_cast<int64_t>(tile.group) * p.w_group_tiles + tile.m) * p.w_tile_bytes;
-      const uint8_t* x_scales = p.x_scales + tile.x_tile * p.x_tile_bytes;
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+          (static_cast<int64_t>(tile.group) * p.w_group_tiles + tile.m) * p.w_tile_bytes +
+          static_cast<int64_t>(kb_first) * S::kScaleStage;
+      const uint8_t* x_scales = p.x_scales + tile.x_tile * p.x_tile_bytes +
+                                static_cast<int64_t>(kb_first) * S::kScaleStage;
+      for (int kb = kb_first; kb < kb_end; ++kb) {
         if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
           ok = false;
           break;
@@ -444,13 +546,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
     const uint64_t w_desc0 = sw128_kmajor_desc(base);
     const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
-    for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const uint32_t idesc = fp4_idesc<kFormat>(kGemmM, (tile.count + 15) & ~15);
       if (!gemm_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
       tc_fence_after_sync();
       const uint32_t d_tmem = tmem + static_cast<uint32_t>(acc * kBN);
-      for (int kb = 0; kb < p.num_kb; ++kb) {
+      for (int kb = kb_first; kb < kb_end; ++kb) {
         if (!gemm_wait_warp(full_bar(stage), phase, abort_flag, kWaitFull, p)) {
           ok = false;
           break;
@@ -474,7 +576,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int byte = kFormat == FP4_NV ? 0 : (s & 1) * 2;
             umma_fp4<kFormat>(d_tmem, w_desc + 2u * s, x_desc + 2u * s,
                               idesc | fp4_idesc_scale_bytes(byte), w_cols + 4 * chunk,
-                              x_cols + 4 * chunk, (kb | s) != 0);
+                              x_cols + 4 * chunk, kb != kb_first || s != 0);
           }
           umma_commit(empty_bar(stage));
         }
@@ -501,7 +603,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int half = (warp - 2) >> 2;     // which of the two warps on it
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int64_t t = first_tile; t < tiles; t += tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       int ok = 0;
       if (lane == 0) ok = gemm_wait(tfull_bar(acc), acc_phase, abort_flag, kWaitTmemFull, p);
@@ -511,6 +613,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kBN);
       const int64_t n = static_cast<int64_t>(tile.m) * kGemmM + q * 32 + lane;
+      if (kSplit) {
+        if (warp == 2 && lane == 0)  // 128 outputs x 32 / split columns of each chunk, from each
+          mbar_arrive_expect_tx(parts_bar, (p.split - 1) * ((tile.count + 31) / 32) *
+                                               (kGemmM * 128 / p.split));
+        store_split_tile<T>(t_row, q * 32 + lane, half, tile.count, part, p, partial, parts_bar,
+                            abort_flag, p.d + tile.x_row * p.n_out + n, n < p.n_out);
+        continue;
+      }
       store_tile<T, kBN>(t_row, half, tile.count, p.alpha, p.d + tile.x_row * p.n_out + n,
                          n < p.n_out, p.n_out, [&] {
                            tc_fence_before_sync();
@@ -526,7 +636,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   __syncwarp();
   tc_fence_before_sync();
-  __syncthreads();
+  if (kSplit) cluster_sync();  // no CTA's shared memory goes while another may write to it
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cstring>
@@ -63,12 +64,29 @@ int launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cu
   return GEMM_OK;
 }
 
-inline int require_device(int* sms) {
+// The current device, checked; its SM count and number where asked for.
+inline int require_device(int* sms, int* device = nullptr) {
   int dev = 0;
   DeviceState* st = nullptr;
   const int rc = current_device(&dev, &st);
   if (rc == GEMM_OK && sms) *sms = device_sm_count(st);
+  if (device) *device = dev;
   return rc;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on a device, once for
+// each; `done` has a bit per device (the library knows up to 64).
+template <typename Kernel>
+bool grant_smem(Kernel kernel, size_t bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = uint64_t{1} << device;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 // ------------------------------------------------------------------ device

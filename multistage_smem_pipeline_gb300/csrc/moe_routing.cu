@@ -8,8 +8,6 @@
 //                                               dw(p) = <dO[t], Y[rows(p)]>
 // All but the sort move rows and are bound by memory: each kernel reads its
 // inputs once and writes its outputs once, 16 bytes a thread.
-#include <mutex>
-
 #include "moe_common.cuh"
 
 namespace gb300 {
@@ -429,20 +427,13 @@ extern "C" int moe_sort(int32_t* offsets, int32_t* rows, const int32_t* ids, int
   if (tokens > 0 && (overlaps(rows, bytes, ids, bytes) || overlaps(offsets, offset_bytes, ids, bytes) ||
                      overlaps(offsets, offset_bytes, rows, bytes)))
     return GEMM_ERR_INVALID_VALUE;
-  const int rc = require_device(nullptr);
+  int device = 0;
+  const int rc = require_device(nullptr, &device);
   if (rc != GEMM_OK) return rc;
   const int n = static_cast<int>(tokens * top_k);
   const auto smem = [](int keys) { return sizeof(int32_t) * ((kSortWarps + 1) * keys + kSortWarps); };
-  static std::once_flag once;
-  static cudaError_t granted = cudaSuccess;
-  std::call_once(once, [&] {
-    granted = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(smem(MOE_MAX_EXPERTS + 1)));
-  });
-  if (granted != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
+  static std::atomic<uint64_t> granted{0};
+  if (!grant_smem(sort_kernel, smem(MOE_MAX_EXPERTS + 1), device, granted)) return GEMM_ERR_CUDA;
   // A slot a thread on one block, and past that a cluster of the largest
   // portable size: a step of a block's warps costs more than the cluster's
   // two meetings: 6,126 slots take 5.8 us on one block and 4.1 on eight, 1,024

@@ -187,6 +187,37 @@ def test_product(lib, form, m, n, k):
     assert lib.fp4_get_device_error() == (0, 0)
 
 
+# Few tiles and a long k: several CTAs share a tile.
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 4096), (33, 130, 5000), (100, 300, 9000),
+                                   (128, 128, 16384), (127, 257, 2049), (260, 100, 6000),
+                                   (16, 2500, 4100), (96, 20, 1024)])
+def test_product_with_k_shared(lib, form, m, n, k):
+    dtype = DTYPES[m % 2]
+    x, qw, a, b = product_case(lib, m * 5 + n, m, n, k, form, dtype)
+    q = lib.fp4_quantize(x, format=form)
+    got = lib.fp4_gemm_tn(q, qw, dtype=dtype)
+    check_product(got, a, b[0], k, dtype)
+    assert torch.equal(got, lib.fp4_gemm_tn(q, qw, dtype=dtype))
+    assert lib.fp4_get_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("tokens,top_k,experts,dropped", [(1, 2, 4, 0.0), (3, 2, 5, 0.4),
+                                                          (90, 1, 3, 0.1), (5, 3, 2, 1.0)])
+def test_products_by_expert_with_k_shared(lib, tokens, top_k, experts, dropped):
+    n, k = 200, 4360
+    ids = random_ids(tokens, tokens, top_k, experts, dropped)
+    x, qw, a, b = product_case(lib, tokens, tokens, n, k, "nvfp4", torch.float16, groups=experts)
+    r = lib.moe_sort(ids, experts)
+    out = lib.fp4_gemm_tn(lib.fp4_quantize(x, routing=r), qw)
+    off, pairs = r.offsets.cpu().numpy(), lib.moe_pairs(r).cpu().numpy()
+    for e in range(experts):
+        if off[e] < off[e + 1]:
+            seg = slice(off[e], off[e + 1])
+            check_product(out[seg], a[pairs[seg] // top_k], b[e], k, torch.float16)
+    assert not out[off[-1]:].any()
+
+
 @pytest.mark.parametrize("form", FORMATS)
 @pytest.mark.parametrize("m,n,k", [(3, 40, 256), (130, 260, 512), (513, 390, 960)])
 def test_product_of_small_integers_is_exact(lib, form, m, n, k):
