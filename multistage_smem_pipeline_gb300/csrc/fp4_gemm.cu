@@ -11,22 +11,19 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-// The first error of the launches on a given stream; 0: none.
-__device__ uint32_t g_fp4_error[kErrorWords];
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 std::mutex g_mu;
-EncodeTiledFn g_encode = nullptr;
+std::atomic<EncodeTiledFn> g_encode{nullptr};
 uintptr_t g_word_stream[kErrorWords];
 int g_words_used = 1;
 
-int get_encoder() {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_encode) return GEMM_OK;
+int get_encoder(EncodeTiledFn* encode) {
+  *encode = g_encode.load(std::memory_order_acquire);
+  if (*encode) return GEMM_OK;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
@@ -35,7 +32,8 @@ int get_encoder() {
     cudaGetLastError();
     return GEMM_ERR_CUDA;
   }
-  g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+  *encode = reinterpret_cast<EncodeTiledFn>(fn);
+  g_encode.store(*encode, std::memory_order_release);
   return GEMM_OK;
 }
 
@@ -55,28 +53,28 @@ int error_index(cudaStream_t s) {
 }
 
 // A matrix's codes as rows of bytes; a box is 128 bytes wide.
-int encode_codes(CUtensorMap* map, const fp4_matrix_t* m, uint32_t box_rows) {
+int encode_codes(EncodeTiledFn encode, CUtensorMap* map, const fp4_matrix_t* m, uint32_t box_rows) {
   const uint64_t pitch = static_cast<uint64_t>(code_pitch(m->cols));
   const cuuint64_t dims[2] = {pitch, static_cast<cuuint64_t>(m->rows)};
   const cuuint64_t strides[1] = {pitch};
   const cuuint32_t box[2] = {kGemmBytesK, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m->codes, dims, strides, box, estr,
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, m->codes, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
 // A matrix's scales as rows of one chunk, 128 words; a box is a stage's chunks.
-int encode_scales(CUtensorMap* map, const fp4_matrix_t* m, int64_t chunks) {
+int encode_scales(EncodeTiledFn encode, CUtensorMap* map, const fp4_matrix_t* m, int64_t chunks) {
   const cuuint64_t dims[2] = {kChunkBytes / 4, static_cast<cuuint64_t>(chunks)};
   const cuuint64_t strides[1] = {kChunkBytes};
   const cuuint32_t box[2] = {kChunkBytes / 4,
                              static_cast<cuuint32_t>(chunks_per_stage(m->format))};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r =
-      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m->scales, dims, strides, box, estr,
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, m->scales, dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
@@ -188,7 +186,8 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->cols == 0) return write_empty_sum(D, nullptr, 0.0f, a->rows * n_out, sms, s);
-  if ((rc = get_encoder()) != GEMM_OK) return rc;
+  EncodeTiledFn encode = nullptr;
+  if ((rc = get_encoder(&encode)) != GEMM_OK) return rc;
 
   Fp4GemmParams p;
   std::memset(&p, 0, sizeof(p));
@@ -209,12 +208,7 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   p.alpha = alpha * va.up * vb.up;
   p.timeout_ns = kTimeoutNs;
   p.raster = 8;
-  void* words = nullptr;
-  if (cudaGetSymbolAddress(&words, g_fp4_error) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
-  p.error = static_cast<uint32_t*>(words) + error_index(s);
+  p.error_word = error_index(s);
 
   // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs, which do four times
   // the work in about the time (an SM takes in 36 and 38 KiB per 256 columns):
@@ -247,11 +241,11 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
       a->offsets ? (a->rows + a->groups - 1) / a->groups : std::min<int64_t>(a->group_rows, 128);
   p.split = pair ? 1 : choose_split(row_tiles * p.m_tiles, tile_rows, p.num_kb, sms, device);
   PairMaps m;
-  if ((rc = encode_codes(&m.w, b, kGemmM)) != GEMM_OK ||
-      (rc = encode_codes(&m.x, a, p.box_rows)) != GEMM_OK)
+  if ((rc = encode_codes(encode, &m.w, b, kGemmM)) != GEMM_OK ||
+      (rc = encode_codes(encode, &m.x, a, p.box_rows)) != GEMM_OK)
     return rc;
-  if (pair && ((rc = encode_scales(&m.sw, b, w_chunks)) != GEMM_OK ||
-               (rc = encode_scales(&m.sx, a, x_chunks)) != GEMM_OK))
+  if (pair && ((rc = encode_scales(encode, &m.sw, b, w_chunks)) != GEMM_OK ||
+               (rc = encode_scales(encode, &m.sx, a, x_chunks)) != GEMM_OK))
     return rc;
   const auto go = [&](auto t, auto fmt) {
     using T = decltype(t);

@@ -63,7 +63,7 @@ struct Fp4GemmParams {
   int32_t raster;          // row tiles that share a pass over the weight tiles
   float alpha;
   uint64_t timeout_ns;
-  uint32_t* error;
+  int32_t error_word;      // where this call's errors go
 };
 
 constexpr int kGemmBN = 128;  // activation rows per tile, at most
@@ -157,6 +157,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // ------------------------------------------------------------------ waits
+// The first error of the launches on a given stream (the host maps streams to
+// words); 0: none.
+__device__ uint32_t g_fp4_error[kErrorWords];
+
+__device__ __forceinline__ void record_timeout(volatile int* abort_flag, uint32_t site,
+                                               const Fp4GemmParams& p) {
+  *abort_flag = 1;
+  atomicCAS(&g_fp4_error[p.error_word], 0u,
+            static_cast<uint32_t>(GEMM_ERR_TIMEOUT) | (site << 8));
+}
+
 __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t site, const Fp4GemmParams& p) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -166,8 +177,7 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatil
     if ((it & 31u) == 0) {
       if (*abort_flag) return false;
       if (global_timer_ns() - t0 > p.timeout_ns) {
-        *abort_flag = 1;
-        atomicCAS(p.error, 0u, static_cast<uint32_t>(GEMM_ERR_TIMEOUT) | (site << 8));
+        record_timeout(abort_flag, site, p);
         return false;
       }
     }
@@ -185,8 +195,7 @@ __device__ __forceinline__ bool gemm_wait_cluster(uint32_t bar, uint32_t parity,
     if ((it & 31u) == 0) {
       if (*abort_flag) return false;
       if (global_timer_ns() - t0 > p.timeout_ns) {
-        *abort_flag = 1;
-        atomicCAS(p.error, 0u, static_cast<uint32_t>(GEMM_ERR_TIMEOUT) | (site << 8));
+        record_timeout(abort_flag, site, p);
         return false;
       }
     }
