@@ -108,6 +108,12 @@ int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* stream);
 int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b, float alpha,
                 void* stream);
 
+/* The same with a limit of its own for the kernel's waits (timeout_ns, 0: 2 s),
+ * and inject = 1 for tests: the first stage of every CTA is never loaded, so that
+ * a wait runs out, the call's result is undefined and the error word is set. */
+int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b, float alpha,
+                   uint64_t timeout_ns, int inject, void* stream);
+
 /* Waits for `stream`, then reads and clears its error word of fp4_gemm_tn:
  * GEMM_OK or GEMM_ERR_TIMEOUT; `raw` (may be NULL) gets code | site << 8.
  * Streams have a word each up to 63 of them, beyond that they share. */

@@ -285,13 +285,14 @@ at::Tensor dequantize(const Fp4Matrix& q, const py::object& dtype, const Out& ou
 }
 
 at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::object& dtype,
-                const Out& out, const py::object& stream) {
+                const Out& out, const py::object& stream, uint64_t timeout_ns, int inject) {
   const at::ScalarType t = dtype_of(dtype);
   const int type = type_of(t, "dtype");
   if (a.device != b.device) value_error("a and b are on different devices");
   const at::Tensor d = output(out, a.c.rows, b.c.group_rows, t, a.device);
   const On on(d, stream);
-  check(fp4_gemm_tn(d.data_ptr(), type, &a.c, &b.c, static_cast<float>(alpha), on.stream()),
+  check(fp4_gemm_tn_ex(d.data_ptr(), type, &a.c, &b.c, static_cast<float>(alpha), timeout_ns, inject,
+                       on.stream()),
         "fp4_gemm_tn");
   return d;
 }
@@ -436,10 +437,11 @@ PYBIND11_MODULE(_experts, m) {
         "are zero.");
   m.def("fp4_gemm_tn", &gemm, py::arg("a"), py::arg("b"), py::kw_only(), py::arg("alpha") = 1.0,
         py::arg("dtype") = none, py::arg("out") = none, py::arg("stream") = none,
+        py::arg("timeout_ns") = 0, py::arg("inject") = 0,
         "out[r] = alpha * a[r] @ b[g(r)]^T (fp32 accumulation; float16 unless dtype says bfloat16): "
         "g(r) is the group of row r, so with activations in expert order each row meets its "
         "expert's weights; rows of dropped slots give zeros.  b has as many groups as a, each of "
-        "b.group_rows outputs.");
+        "b.group_rows outputs.  timeout_ns and inject: see fp4_gemm_tn_ex in moe_fp4.h.");
   m.def("fp4_get_device_error", &device_error, py::arg("stream") = none,
         "(status, raw word) of the stream's error word of fp4_gemm_tn; synchronises the stream.");
   m.def("fp4_scale_bytes", &scale_bytes, py::arg("rows"), py::arg("cols"),

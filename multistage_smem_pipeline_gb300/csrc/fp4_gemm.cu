@@ -166,11 +166,16 @@ using namespace gb300;
 
 extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b,
                            float alpha, void* stream) {
+  return fp4_gemm_tn_ex(D, type, a, b, alpha, 0, 0, stream);
+}
+
+extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b,
+                              float alpha, uint64_t timeout_ns, int inject, void* stream) {
   bool any_a = false, any_b = false;
   int rc = check_matrix(a, &any_a);
   if (rc != GEMM_OK) return rc;
   if ((rc = check_matrix(b, &any_b)) != GEMM_OK) return rc;
-  if (!valid_type(type) || !std::isfinite(alpha) || a->format != b->format || a->cols != b->cols ||
+  if (!valid_type(type) || !std::isfinite(alpha) || inject < 0 || inject > 1 || a->format != b->format || a->cols != b->cols ||
       a->groups != b->groups || b->offsets)
     return GEMM_ERR_INVALID_VALUE;
   const int64_t n_out = b->group_rows;
@@ -206,7 +211,8 @@ extern "C" int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_m
   p.w_group_tiles = static_cast<int32_t>((n_out + kTileRows - 1) / kTileRows);
   p.tile_chunks = p.num_kb * chunks_per_stage(a->format);
   p.alpha = alpha * va.up * vb.up;
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = timeout_ns ? timeout_ns : kTimeoutNs;
+  p.inject = inject;
   p.raster = 8;
   p.error_word = error_index(s);
 

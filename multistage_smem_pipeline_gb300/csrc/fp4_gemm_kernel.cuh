@@ -63,6 +63,7 @@ struct Fp4GemmParams {
   int32_t raster;          // row tiles that share a pass over the weight tiles
   float alpha;
   uint64_t timeout_ns;
+  int32_t inject;          // 1: leave out each CTA's first loads
   int32_t error_word;      // where this call's errors go
 };
 
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t full = full_bar(stage);
           if (warp == 0) {
             mbar_arrive_expect_tx(full, bytes);
-            tma_load_2d(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+            if (!(p.inject && issued == 0))
+              tma_load_2d(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
             bulk_load(s_dst, w_scales, S::kScaleStage, full);
           } else {
             for (int b = 0; b < boxes; ++b)

@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           const uint32_t full = mapa_shared(full_bar(stage), 0);
           if (warp == 0) {
             if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-            tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+            if (!(p.inject && issued == 0))
+              tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
             tma_load_2d_pair(s_dst, &tmSW, full, 0, sw);
           } else {
             for (int b = 0; b < boxes; ++b)

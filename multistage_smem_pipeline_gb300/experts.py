@@ -28,5 +28,5 @@ from .lib._experts import (  # noqa: E402,F401
 
 # The C functions of moe_fp4.h.
 EXPORTED = ("fp4_code_bytes", "fp4_scale_bytes", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
-            "fp4_get_device_error", "moe_sort", "moe_pairs", "moe_dispatch",
+            "fp4_gemm_tn_ex", "fp4_get_device_error", "moe_sort", "moe_pairs", "moe_dispatch",
             "moe_dispatch_backward", "moe_combine", "moe_combine_backward")

@@ -43,6 +43,7 @@ def ex():
             "fp4_quantize": [pm, vp, i64, i32, pr, vp],
             "fp4_dequantize": [vp, i32, pm, vp],
             "fp4_gemm_tn": [vp, i32, pm, pm, ctypes.c_float, vp],
+            "fp4_gemm_tn_ex": [vp, i32, pm, pm, ctypes.c_float, ctypes.c_uint64, i32, vp],
             "moe_sort": [vp, vp, vp, i64, i32, i32, vp],
             "moe_pairs": [vp, pr, vp],
             "moe_dispatch": [vp, vp, i64, i64, i32, pr, vp],
@@ -159,6 +160,9 @@ def test_gemm_refusals(ex):
     assert gemm(ex, a, b, type=2) == E
     assert gemm(ex, a, b, alpha=float("nan")) == E
     assert gemm(ex, a, b, alpha=float("inf")) == E
+    for inject in (-1, 2):
+        assert ex.LIB.fp4_gemm_tn_ex(P[2], 0, ctypes.byref(a), ctypes.byref(b), 1.0, 0, inject,
+                                     None) == E
     assert gemm(ex, a, b, d=P[0]) == E and gemm(ex, a, b, d=P[5] + 32) == E      # overlaps
     for other in [dict(cols=255), dict(format=1), dict(groups=2, rows=128),
                   dict(offsets=P[6], rows=128), dict(codes=0)]:

@@ -323,6 +323,22 @@ def test_other_stream_and_repeats(lib):
     assert torch.equal(first, d)
 
 
+@pytest.mark.parametrize("m,n,k", [(4, 100, 256), (8, 300, 4096), (600, 4096, 512)])
+def test_a_wait_that_runs_out_is_reported(lib, m, n, k):
+    """On one CTA a tile, on a tile shared by several, and on pairs: loads that never come end in
+    an error word of that stream, and the next call is right again."""
+    x, qw, a, b = product_case(lib, m, m, n, k, "nvfp4", torch.float16)
+    q = lib.fp4_quantize(x)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    lib.fp4_gemm_tn(q, qw, timeout_ns=20_000_000, inject=1, stream=s)
+    assert lib.fp4_get_device_error() == (0, 0)
+    status, raw = lib.fp4_get_device_error(s)
+    assert status == 5 and raw >> 8 in (1, 2, 3, 4, 5)
+    assert lib.fp4_get_device_error(s) == (0, 0)
+    check_product(lib.fp4_gemm_tn(q, qw), a, b[0], k, torch.float16)
+
+
 def test_captured_into_a_graph(lib):
     x, qw, a, b = product_case(lib, 41, 24, 520, 1024, "nvfp4", torch.float16, groups=4)
     ids = random_ids(5, 24, 2, 4)
