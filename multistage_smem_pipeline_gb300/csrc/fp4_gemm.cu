@@ -213,24 +213,25 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.alpha = alpha * va.up * vb.up;
   p.timeout_ns = timeout_ns ? timeout_ns : kTimeoutNs;
   p.inject = inject;
-  p.raster = 8;
   p.error_word = error_index(s);
 
-  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs, which do four times
-  // the work in about the time (an SM takes in 36 and 38 KiB per 256 columns):
-  // the one with fewer waves of tiles, single CTAs if equal (128 x 14336 x 4096
-  // mxfp4: 8.6 against 10.0 us; 8192^3: 261 against 170).  With groups by
-  // offsets the number of row tiles is not known here: a group is taken to
-  // have the mean number of rows.
-  const auto tiles_of = [&](int64_t bm, int64_t bn) {
+  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs: the form whose waves
+  // of tiles take fewer cycles.  A tile takes a single CTA about 1400 + 580 per
+  // 256 columns of k, and a pair 5700 + 520: four times the work in about the
+  // time, but with one accumulator, so that a tile's stores are not all hidden
+  // (8192^3: 261 us by single CTAs, 166 by pairs; 8192 x 4096 x 256: 16 and 24;
+  // 128 x 14336 x 4096 mxfp4: 7.8 and 10).  With groups by offsets the number of
+  // row tiles is not known here: a group is taken to have the mean number of rows.
+  const auto cycles = [&](int64_t tile, int64_t slots, int64_t fixed, int64_t per_block) {
     const int64_t group = a->offsets ? (a->rows + a->groups - 1) / a->groups : a->group_rows;
-    return std::min<int64_t>(a->groups, a->rows) * ((group + bn - 1) / bn) * ((n_out + bm - 1) / bm);
+    const int64_t tiles = std::min<int64_t>(a->groups, a->rows) * ((group + tile - 1) / tile) *
+                          ((n_out + tile - 1) / tile);
+    return (tiles + slots - 1) / slots * (fixed + per_block * p.num_kb);
   };
-  const auto waves = [](int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slots; };
   const int64_t x_chunks =
       tile_count(a->rows, a->groups, a->offsets != nullptr) * p.tile_chunks;
   const int64_t w_chunks = static_cast<int64_t>(a->groups) * p.w_group_tiles * p.tile_chunks;
-  const bool pair = waves(tiles_of(256, 256), sms / 2) < waves(tiles_of(128, 128), sms) &&
+  const bool pair = cycles(256, sms / 2, 5700, 520) < cycles(128, sms, 1400, 580) &&
                     x_chunks <= INT_MAX && w_chunks <= INT_MAX;  // counted in 32 bits there
   const int bm = pair ? 256 : 128, bn = bm;
   p.m_tiles = static_cast<int32_t>((n_out + bm - 1) / bm);
@@ -241,6 +242,8 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   // One CTA per SM, fewer where there cannot be that many tiles.
   const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
                                        : a->groups * ((a->group_rows + bn - 1) / bn);
+  // counted in 32 bits, with room for a grid's stride past the last
+  if (row_tiles * p.m_tiles > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
   const int units = static_cast<int>(std::min<int64_t>(pair ? sms / 2 : sms, row_tiles * p.m_tiles));
   // rows of a tile, in the mean: of the groups that there can be
   const int64_t tile_rows =

@@ -14,9 +14,9 @@
 //   warp 1 -- copies the stage's scales into tensor memory
 //       (tcgen05.cp, 512 bytes = 128 rows x 4 blocks at a time, replicated to
 //       the four lane quadrants) and issues a block-scaled MMA per 64 columns;
-//   warps 2 .. 9 -- epilogue: two warps per lane quadrant take alternate
-//       32-column chunks to registers, round them, let the accumulator go, and
-//       store.
+//   warps 2 .. 9 -- epilogue: four warps, one per lane quadrant, for each of the
+//       two accumulators; they take a tile to registers, round it, let the
+//       accumulator go, and store.
 // Every ring slot has its own columns of tensor memory for scales: a slot's
 // copies begin after its full barrier, hence after its empty one, which the
 // commit of the MMAs that read those columns completed.
@@ -60,7 +60,6 @@ struct Fp4GemmParams {
   int32_t box_rows;        // activation rows per TMA box
   int32_t stages;
   int32_t split;           // CTAs that share a tile's k; 1: none do
-  int32_t raster;          // row tiles that share a pass over the weight tiles
   float alpha;
   uint64_t timeout_ns;
   int32_t inject;          // 1: leave out each CTA's first loads
@@ -230,48 +229,66 @@ __device__ __forceinline__ void gemm_wait_drain(uint32_t bar, uint32_t parity, u
 
 // ------------------------------------------------------------------ tiles
 struct GemmTile {
-  int64_t x_row;    // first row of the activations (and of D)
-  int64_t x_tile;   // its scale tile
+  int32_t x_row;    // first row of the activations (and of D)
+  int32_t x_tile;   // its scale tile
   int32_t count;    // rows
   int32_t group, m; // weight tile m of the group
 };
 
-// Tile t: groups in order; in a group, `raster` row tiles at a time walk over
-// the weight tiles together, so that what runs at once shares operands in L2.
+// Tile t: groups in order; in a group, kRaster row tiles at a time walk over the
+// weight tiles together, so that what runs at once shares operands in L2.  (The
+// host keeps the number of tiles within 32 bits: every role works this out for
+// every tile, and with short k loops it shows.)
+constexpr int kRaster = 8;
+
 template <int kBN>
-__device__ __forceinline__ GemmTile gemm_tile(int64_t t, const Fp4GemmParams& p,
-                                              const int32_t* before) {
+__device__ __forceinline__ GemmTile gemm_tile(int t, const Fp4GemmParams& p, const int32_t* before) {
   GemmTile o;
-  int64_t first, rows;
+  int first, rows;
   if (p.offsets) {
     int lo = 0, hi = p.groups - 1;  // the last group with before[g] * m_tiles <= t
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(before[mid]) * p.m_tiles <= t) lo = mid;
+      if (before[mid] * p.m_tiles <= t) lo = mid;
       else hi = mid - 1;
     }
     o.group = lo;
-    t -= static_cast<int64_t>(before[lo]) * p.m_tiles;
+    t -= before[lo] * p.m_tiles;
     first = p.offsets[lo];
     rows = p.offsets[lo + 1] - first;
     o.x_tile = first / kTileRows + lo;
   } else {
-    const int64_t per = (p.group_rows + kBN - 1) / kBN * p.m_tiles;
-    o.group = static_cast<int32_t>(t / per);
-    t -= o.group * per;
-    first = o.group * p.group_rows;
-    rows = p.group_rows;
-    o.x_tile = o.group * ((p.group_rows + kTileRows - 1) / kTileRows);
+    rows = static_cast<int>(p.group_rows);
+    o.group = 0;
+    if (p.groups > 1) {
+      const int per = (rows + kBN - 1) / kBN * p.m_tiles;
+      o.group = t / per;
+      t -= o.group * per;
+    }
+    first = o.group * rows;
+    o.x_tile = o.group * ((rows + kTileRows - 1) / kTileRows);
   }
-  const int x_tiles = static_cast<int>((rows + kBN - 1) / kBN);
-  const int band = static_cast<int>(t / (static_cast<int64_t>(p.raster) * p.m_tiles));
-  const int in = static_cast<int>(t - static_cast<int64_t>(band) * p.raster * p.m_tiles);
-  const int wide = min(p.raster, x_tiles - band * p.raster);
-  const int xt = band * p.raster + in % wide;
-  o.m = in / wide;
-  o.x_row = first + static_cast<int64_t>(xt) * kBN;
+  int xt;
+  if (rows <= kBN) {
+    xt = 0;
+    o.m = t;
+  } else {
+    const int x_tiles = (rows + kBN - 1) / kBN;
+    const int band = t / (kRaster * p.m_tiles);
+    const int in = t - band * kRaster * p.m_tiles;
+    const int wide = min(kRaster, x_tiles - band * kRaster);
+    if (wide == kRaster) {
+      xt = in % kRaster;
+      o.m = in / kRaster;
+    } else {
+      o.m = in / wide;
+      xt = in - o.m * wide;
+    }
+    xt += band * kRaster;
+  }
+  o.x_row = first + xt * kBN;
   o.x_tile += xt * (kBN / kTileRows);
-  o.count = static_cast<int32_t>(min(static_cast<int64_t>(kBN), rows - static_cast<int64_t>(xt) * kBN));
+  o.count = min(kBN, rows - xt * kBN);
   return o;
 }
 
@@ -289,19 +306,20 @@ __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
 }
 
 // ------------------------------------------------------------------ epilogue
-// One warp's part of a tile's accumulator, lanes 32 q .. 32 q + 31 and every
-// other 32-column chunk: to registers in one go, rounded in place (element i
+// One warp's part of a tile's accumulator, lanes 32 q .. 32 q + 31 and four
+// 32-column chunks (first, first + kStep ...): to registers in one go, rounded in place (element i
 // of a chunk's array then holds columns 2i and 2i + 1), the accumulator let go
 // by `release`, and stored; a lane is an output n, so a store of the warp
 // writes 32 neighbouring outputs of one row.
-template <typename T, int kBN, typename Release>
-__device__ __forceinline__ void store_tile(uint32_t t_row, int half, int count, float alpha,
+template <typename T, int kStep, typename Release>
+__device__ __forceinline__ void store_tile(uint32_t t_row, int first, int count, float alpha,
                                            uint16_t* d, bool live, int64_t n_out, Release release) {
-  constexpr int kMine = kBN / 64;
+  constexpr int kMine = 4;
   uint32_t r[kMine][32];
 #pragma unroll
   for (int c = 0; c < kMine; ++c)
-    if (32 * (2 * c + half) < count) tmem_ld_32x32b_x32(t_row + 32 * (2 * c + half), r[c]);
+    if (32 * (kStep * c + first) < count)
+      tmem_ld_32x32b_x32(t_row + 32 * (kStep * c + first), r[c]);
   tmem_ld_wait();
   release();
 #pragma unroll
@@ -313,7 +331,7 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, int half, int count, 
   if (!live) return;
 #pragma unroll
   for (int c = 0; c < kMine; ++c) {
-    const int col = 32 * (2 * c + half);
+    const int col = 32 * (kStep * c + first);
     if (col >= count) break;
     uint16_t* to = d + col * n_out;
 #pragma unroll
@@ -439,8 +457,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t partial = base + stages * S::kStageBytes;
   const uint32_t bars = partial + (kSplit ? kSplitBytes : 0u);
   const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
-  const int64_t first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
-  const int64_t tile_step = kSplit ? INT64_MAX / 2 : gridDim.x;
+  const int first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
+  const int tile_step = kSplit ? INT_MAX / 4 : gridDim.x;  // kSplit: one tile
   const int kb_first = kSplit ? part * p.num_kb / p.split : 0;
   const int kb_end = kSplit ? (part + 1) * p.num_kb / p.split : p.num_kb;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
@@ -462,7 +480,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), kGemmEpiWarps);
+      mbar_init(tempty_bar(b), kGemmEpiWarps / 2);
     }
     mbar_init(drain_bar, 1);
     mbar_init(parts_bar, 1);
@@ -483,9 +501,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   else __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int64_t tiles =
-      (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
-      static_cast<int64_t>(p.m_tiles);
+  const int tiles =
+      (p.offsets ? before[p.groups]
+                 : p.groups * ((static_cast<int>(p.group_rows) + kBN - 1) / kBN)) * p.m_tiles;
 
   if (warp == 0 || warp == kGemmRowWarp) {
     // ---------------------------------------------------------- producers
@@ -497,13 +515,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+    for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const int boxes = (tile.count + p.box_rows - 1) / p.box_rows;
       const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
                              2 * S::kScaleStage;
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * kGemmM);
-      const int x_row = static_cast<int>(tile.x_row);
+      const int x_row = tile.x_row;
       const uint8_t* w_scales =
           p.w_scales +
           (static_cast<int64_t>(tile.group) * p.w_group_tiles + tile.m) * p.w_tile_bytes +
@@ -557,7 +575,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
     const uint64_t w_desc0 = sw128_kmajor_desc(base);
     const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
-    for (int64_t t = first_tile; ok && t < tiles; t += tile_step) {
+    for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const uint32_t idesc = fp4_idesc<kFormat>(kGemmM, (tile.count + 15) & ~15);
       if (!gemm_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
@@ -610,12 +628,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_wait_drain(drain_bar, 0, p.timeout_ns);
   } else {
     // ---------------------------------------------------------- epilogue
+    // Two groups of four warps, one per accumulator: while one stores a tile the
+    // other reads the next.  (A split tile is shared by both, by chunks.)
     const int q = warp & 3;               // the lane quadrant this warp may read
-    const int half = (warp - 2) >> 2;     // which of the two warps on it
-    int acc = 0;
+    const int group = (warp - 2) >> 2;
     uint32_t acc_phase = 0;
-    for (int64_t t = first_tile; t < tiles; t += tile_step) {
+    for (int t = first_tile + (kSplit ? 0 : group * tile_step); t < tiles;
+         t += (kSplit ? 1 : 2) * tile_step) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      const int acc = kSplit ? 0 : group;
       int ok = 0;
       if (lane == 0) ok = gemm_wait(tfull_bar(acc), acc_phase, abort_flag, kWaitTmemFull, p);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -624,24 +645,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(acc * kBN);
       const int64_t n = static_cast<int64_t>(tile.m) * kGemmM + q * 32 + lane;
+      uint16_t* const d = p.d + tile.x_row * p.n_out + n;
       if (kSplit) {
         if (warp == 2 && lane == 0)  // 128 outputs x 32 / split columns of each chunk, from each
           mbar_arrive_expect_tx(parts_bar, (p.split - 1) * ((tile.count + 31) / 32) *
                                                (kGemmM * 128 / p.split));
-        store_split_tile<T>(t_row, q * 32 + lane, half, tile.count, part, p, partial, parts_bar,
-                            abort_flag, p.d + tile.x_row * p.n_out + n, n < p.n_out);
+        store_split_tile<T>(t_row, q * 32 + lane, group, tile.count, part, p, partial, parts_bar,
+                            abort_flag, d, n < p.n_out);
         continue;
       }
-      store_tile<T, kBN>(t_row, half, tile.count, p.alpha, p.d + tile.x_row * p.n_out + n,
-                         n < p.n_out, p.n_out, [&] {
-                           tc_fence_before_sync();
-                           __syncwarp();
-                           if (lane == 0) mbar_arrive(tempty_bar(acc));
-                         });
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
-      }
+      store_tile<T, 1>(t_row, 0, tile.count, p.alpha, d, n < p.n_out, p.n_out, [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
+      });
+      acc_phase ^= 1u;
     }
     zero_tail(p);
   }

@@ -137,16 +137,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int64_t tiles =
-      (p.offsets ? before[p.groups] : p.groups * ((p.group_rows + kBN - 1) / kBN)) *
-      static_cast<int64_t>(p.m_tiles);
+  const int tiles =
+      (p.offsets ? before[p.groups]
+                 : p.groups * ((static_cast<int>(p.group_rows) + kBN - 1) / kBN)) * p.m_tiles;
 
   if (warp == 0 || warp == kGemmRowWarp) {
     // ---------------------------------------------------------- producers (both CTAs)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
-    for (int64_t t = pair; ok && t < tiles; t += pairs) {
+    for (int t = pair; ok && t < tiles; t += pairs) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       const int half_n = ((tile.count + 31) & ~31) >> 1;  // rows this CTA holds
       const int boxes = (half_n + p.box_rows - 1) / p.box_rows;
@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint32_t bytes = kWBytes + static_cast<uint32_t>(boxes * p.box_rows) * kGemmBytesK +
                              S::kScaleStage * (two ? 3 : 2);
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * (2 * kGemmM) + rank * kGemmM);
-      const int x_row = static_cast<int>(tile.x_row) + rank * half_n;
+      const int x_row = tile.x_row + rank * half_n;
       int sw = (tile.group * p.w_group_tiles + 2 * tile.m + rank) * p.tile_chunks;
       // each CTA loads one tile of the rows' scales, for both
-      int sx = (static_cast<int>(tile.x_tile) + rank) * p.tile_chunks;
+      int sx = (tile.x_tile + rank) * p.tile_chunks;
       const bool loads_sx = rank == 0 || two;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       bool ok = true;
       const uint64_t w_desc0 = sw128_kmajor_desc(base);
       const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
-      for (int64_t t = pair; ok && t < tiles; t += pairs) {
+      for (int t = pair; ok && t < tiles; t += pairs) {
         const GemmTile tile = gemm_tile<kBN>(t, p, before);
         const uint32_t idesc = fp4_idesc<kFormat>(2 * kGemmM, (tile.count + 31) & ~31);
         if (!gemm_wait_warp(tempty_bar, acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int half = (warp - 2) >> 2;
     uint32_t acc_phase = 0;
     const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
-    for (int64_t t = pair; t < tiles; t += pairs) {
+    for (int t = pair; t < tiles; t += pairs) {
       const GemmTile tile = gemm_tile<kBN>(t, p, before);
       int ok = 0;
       if (lane == 0) ok = gemm_wait(tfull_bar, acc_phase, abort_flag, kWaitTmemFull, p);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const int64_t n = static_cast<int64_t>(tile.m) * (2 * kGemmM) + rank * kGemmM + q * 32 + lane;
-      store_tile<T, kBN>(tmem + (static_cast<uint32_t>(q * 32) << 16), half, tile.count, p.alpha,
+      store_tile<T, 2>(tmem + (static_cast<uint32_t>(q * 32) << 16), half, tile.count, p.alpha,
                          p.d + tile.x_row * p.n_out + n, n < p.n_out, p.n_out, [&] {
                            tc_fence_before_sync();
                            __syncwarp();
