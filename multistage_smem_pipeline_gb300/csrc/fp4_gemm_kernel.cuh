@@ -3,9 +3,18 @@
 // D[r][n] = alpha sum_k a[r][k] b[g][n][k] for the rows r of group g.  The
 // weights are the instruction's M operand (128 rows a tile) and the
 // activations its N operand (1 to 128 rows a tile here, to 256 in the kernel
-// over CTA pairs): N may be any multiple of
-// 16, so that an expert with few rows costs few columns.  A tile's
-// accumulator is then D transposed: lane = output n, column = row r.
+// over CTA pairs): N may be any multiple of 16, so that an expert with few rows
+// costs few columns.  A tile's accumulator is then D transposed: lane = output
+// n, column = row r.
+//
+// With few rows what bounds it are the weights' bytes from memory: 1 x 155648 x
+// 4096 nvfp4 takes 55 us (6.5 TB/s), 1 x 14336 x 4096 7.3 (4.5 TB/s, of which
+// 2.5 us are a launch's beginning and end), 8 tokens over 64 experts (32 of
+// them at most, 2048 x 4096 each) 19.5.  With many rows and a short k it is the
+// stores, two bytes a lane: 8192 x 4096 x 256 in 16 us.  Staged through shared
+// memory for 16 bytes a lane, with the barriers between warps that takes, they
+// were slower (128 x 14336 x 4096 8.7 us against 8.2, and twice as long where
+// D's rows are not aligned).
 //
 // Inside a CTA, one per SM, each walking the list of tiles:
 //   warps 0 and 10 -- producers, of the weights and of the rows: per 256 columns

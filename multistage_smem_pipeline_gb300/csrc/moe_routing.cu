@@ -34,7 +34,8 @@ struct RouteParams {
 // memory), across keys by a scan over the keys, which is `offsets`.  Ranks and
 // keys of a warp's first 256 slots stay in registers; those of later ones wait
 // in `rows`.  Everything is read and written once or twice; what bounds the
-// sort is latency, hence one launch and few steps.
+// sort is latency, hence one launch and few steps: 64 slots take 3.1 us, 32,792
+// 7.1 and 65,536 (of 128 experts) 8.9.
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(int32_t* __restrict__ offsets, int32_t* rows, const int32_t* __restrict__ ids, int n,
                 int experts) {
@@ -173,7 +174,8 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // ------------------------------------------------------------------ rows out
 // Aligned rows: one block per token, whose row is read once and written top_k
-// times.
+// times, so that the traffic is what it has to be.  8192 x 8 rows of 4096 in
+// 93 us: 6.5 TB/s, nearly all of it writes.
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_kernel(uint16_t* __restrict__ y, const uint16_t* __restrict__ x, int64_t ldx,
                     const RouteParams r) {
@@ -193,7 +195,9 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // Other rows: one warp per slot, as each of a token's rows has windows of its
-// own; the token's row comes from cache after the first.
+// own; the token's row comes from cache after the first.  1021 x 6 rows of 1411
+// in 5.7 us (7.1 by blocks of a token), of 1408 aligned in 3.8; the shifts and
+// the second load of a window are the difference.
 __global__ void __launch_bounds__(kRowThreads)
     dispatch_slots_kernel(uint16_t* __restrict__ y, const uint16_t* __restrict__ x, int64_t ldx,
                           const RouteParams r) {
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // ------------------------------------------------------------------ rows back
 // One block per token; kWeighted: the sum takes weights.  The rows of kFlight
 // slots are asked for before the first is used; the sum keeps slot order.
-// 8192 x 8 rows of 4096 in 90 us: 6.7 TB/s.
+// 8192 x 8 rows of 4096 in 89 us: 6.8 TB/s; four in flight against two: 89 and 100.
 template <typename T, bool kAligned, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads)
     combine_kernel(uint16_t* __restrict__ out, const uint16_t* __restrict__ y,
