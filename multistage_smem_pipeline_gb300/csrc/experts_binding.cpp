@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 
 #include <memory>
+#include <optional>
 #include <string>
 
 #include "moe_fp4.h"
@@ -30,19 +31,26 @@ void check(int status, const char* name) {
   throw py::error_already_set();
 }
 
-// The stream a call runs on, with its device current meanwhile.
+// The stream a call runs on, current meanwhile together with its device: what is
+// allocated then belongs to that stream, and is not memory that work queued on
+// another one may still be using.
 class On {
  public:
-  On(const at::Tensor& x, const py::object& stream) : guard_(x.device()) {
-    handle_ = stream.is_none()
-                  ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(x.get_device()).stream())
-                  : reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
+  On(at::Device device, const py::object& stream) {
+    if (stream.is_none()) {
+      device_.emplace(device);
+      handle_ = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    } else {
+      handle_ = reinterpret_cast<cudaStream_t>(stream.attr("cuda_stream").cast<uintptr_t>());
+      stream_.emplace(c10::cuda::getStreamFromExternal(handle_, device.index()));
+    }
   }
   void* stream() const { return handle_; }
 
  private:
-  c10::cuda::CUDAGuard guard_;
-  void* handle_;
+  std::optional<c10::cuda::CUDAGuard> device_;
+  std::optional<c10::cuda::CUDAStreamGuard> stream_;
+  cudaStream_t handle_ = nullptr;
 };
 
 int type_of(at::ScalarType t, const char* what) {
@@ -144,6 +152,7 @@ RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream
   if (experts < 1 || experts > MOE_MAX_EXPERTS || ids.size(1) < 1 || ids.size(1) > MOE_MAX_TOP_K)
     value_error("1 to " + std::to_string(MOE_MAX_EXPERTS) + " experts and 1 to " +
                 std::to_string(MOE_MAX_TOP_K) + " slots are supported");
+  const On on(ids.device(), stream);
   auto r = std::make_shared<Routing>();
   r->ids = ids;
   r->describe(experts);
@@ -151,15 +160,14 @@ RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream
   int32_t* const at = static_cast<int32_t*>(r->buffer.data_ptr());
   r->c.offsets = at;
   r->c.rows = at + r->head();
-  const On on(ids, stream);
   check(moe_sort(at, at + r->head(), r->c.ids, r->c.tokens, r->c.top_k, r->c.experts, on.stream()),
         "moe_sort");
   return r;
 }
 
 at::Tensor pairs_of(const Routing& r, const py::object& stream) {
+  const On on(r.device(), stream);
   const at::Tensor pairs = at::empty({r.slots()}, r.ids.options());
-  const On on(pairs, stream);
   check(moe_pairs(static_cast<int32_t*>(pairs.data_ptr()), &r.c, on.stream()), "moe_pairs");
   return pairs;
 }
@@ -253,6 +261,7 @@ MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t expon
     if (routing->device() != x.device()) value_error("x and the routing are on different devices");
     rows = routing->slots();
   }
+  const On on(x.device(), stream);
   MatrixPtr m = out;
   if (!m) {
     m = std::make_shared<Fp4Matrix>();
@@ -267,7 +276,6 @@ MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t expon
              (group_rows && m->c.group_rows != *group_rows)) {
     value_error("out does not fit x, the format or the groups");
   }
-  const On on(x, stream);
   check(fp4_quantize(&m->c, x.data_ptr(), row_stride(x), type, routing ? &routing->c : nullptr,
                      on.stream()),
         "fp4_quantize");
@@ -278,8 +286,8 @@ at::Tensor dequantize(const Fp4Matrix& q, const py::object& dtype, const Out& ou
                       const py::object& stream) {
   const at::ScalarType t = dtype_of(dtype);
   const int type = type_of(t, "dtype");
+  const On on(q.device, stream);
   const at::Tensor y = output(out, q.c.rows, q.c.cols, t, q.device);
-  const On on(y, stream);
   check(fp4_dequantize(y.data_ptr(), type, &q.c, on.stream()), "fp4_dequantize");
   return y;
 }
@@ -289,8 +297,8 @@ at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::
   const at::ScalarType t = dtype_of(dtype);
   const int type = type_of(t, "dtype");
   if (a.device != b.device) value_error("a and b are on different devices");
+  const On on(a.device, stream);
   const at::Tensor d = output(out, a.c.rows, b.c.group_rows, t, a.device);
-  const On on(d, stream);
   check(fp4_gemm_tn_ex(d.data_ptr(), type, &a.c, &b.c, static_cast<float>(alpha), timeout_ns, inject,
                        on.stream()),
         "fp4_gemm_tn");
@@ -340,8 +348,8 @@ const float* weights_of(const at::Tensor& w, const Routing& r) {
 at::Tensor dispatch(const at::Tensor& x, const Routing& r, const Out& out,
                     const py::object& stream) {
   const int type = by_token(x, r, "x");
+  const On on(x.device(), stream);
   const at::Tensor y = output(out, r.slots(), x.size(1), x.scalar_type(), x.device());
-  const On on(x, stream);
   check(moe_dispatch(y.data_ptr(), x.data_ptr(), row_stride(x), x.size(1), type, &r.c, on.stream()),
         "moe_dispatch");
   return y;
@@ -350,9 +358,9 @@ at::Tensor dispatch(const at::Tensor& x, const Routing& r, const Out& out,
 at::Tensor dispatch_backward(const at::Tensor& grad_y, const Routing& r, const Out& out,
                              const py::object& stream) {
   const int type = by_slot(grad_y, r, "grad_y");
+  const On on(grad_y.device(), stream);
   const at::Tensor x =
       output(out, r.c.tokens, grad_y.size(1), grad_y.scalar_type(), grad_y.device());
-  const On on(grad_y, stream);
   check(moe_dispatch_backward(x.data_ptr(), grad_y.data_ptr(), grad_y.size(1), type, &r.c,
                               on.stream()),
         "moe_dispatch_backward");
@@ -363,8 +371,8 @@ at::Tensor combine(const at::Tensor& y, const Routing& r, const at::Tensor& weig
                    const Out& out, const py::object& stream) {
   const int type = by_slot(y, r, "y");
   const float* const w = weights_of(weights, r);
+  const On on(y.device(), stream);
   const at::Tensor o = output(out, r.c.tokens, y.size(1), y.scalar_type(), y.device());
-  const On on(y, stream);
   check(moe_combine(o.data_ptr(), y.data_ptr(), w, y.size(1), type, &r.c, on.stream()),
         "moe_combine");
   return o;
@@ -378,9 +386,9 @@ std::pair<at::Tensor, at::Tensor> combine_backward(const at::Tensor& grad_out, c
       !grad_out.is_contiguous())
     value_error("grad_out must be contiguous, of y's type and width");
   const float* const w = weights_of(weights, r);
+  const On on(y.device(), stream);
   const at::Tensor grad_y = at::empty({y.size(0), y.size(1)}, y.options());
   const at::Tensor grad_w = at::empty({r.c.tokens, r.c.top_k}, weights.options());
-  const On on(y, stream);
   check(moe_combine_backward(grad_y.data_ptr(), static_cast<float*>(grad_w.data_ptr()),
                              grad_out.data_ptr(), y.data_ptr(), w, y.size(1), type, &r.c,
                              on.stream()),

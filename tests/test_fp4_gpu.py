@@ -339,6 +339,25 @@ def test_a_wait_that_runs_out_is_reported(lib, m, n, k):
     check_product(lib.fp4_gemm_tn(q, qw), a, b[0], k, torch.float16)
 
 
+def test_outputs_belong_to_the_stream_of_the_call(lib):
+    """Memory that work queued on the current stream still reads is not handed to a call that runs
+    on another stream at once."""
+    x, qw, a, b = product_case(lib, 33, 64, 512, 256, "nvfp4", torch.float16)
+    q = lib.fp4_quantize(x)
+    want = lib.fp4_gemm_tn(q, qw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kept = torch.full((64, 512), 7.0, dtype=torch.float16, device="cuda")
+    address = kept.data_ptr()
+    torch.cuda._sleep(20_000_000)                 # about 10 ms of the current stream
+    copy = kept.clone()                           # reads `kept` after that
+    del kept                                      # ... which the allocator may now reuse
+    got = lib.fp4_gemm_tn(q, qw, stream=s)
+    assert got.data_ptr() != address
+    torch.cuda.synchronize()
+    assert (copy == 7).all() and torch.equal(got, want)
+
+
 def test_captured_into_a_graph(lib):
     x, qw, a, b = product_case(lib, 41, 24, 520, 1024, "nvfp4", torch.float16, groups=4)
     ids = random_ids(5, 24, 2, 4)
