@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // slots are asked for before the first is used; the sum keeps slot order.
 // 8192 x 8 rows of 4096 in 89 us: 6.8 TB/s; four in flight against two: 89 and 100.
 template <typename T, bool kAligned, bool kWeighted>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kAligned ? 1 : 5)
     combine_kernel(uint16_t* __restrict__ out, const uint16_t* __restrict__ y,
                    const float* __restrict__ weights, const RouteParams r) {
   constexpr int kFlight = 4;
@@ -284,12 +284,14 @@ __global__ void __launch_bounds__(kRowThreads)
 // One warp per slot: it scales the token's gradient into the slot's row and
 // takes its product with the row the slot had.  The warps of a block share
 // the token's gradient through L1.  8192 x 8 rows of 4096 in 167 us: 6.8 TB/s.
+// Rows that are not aligned need registers for their shifts, and do better with
+// fewer windows in flight and more warps: 8000 x 2 of 4095 in 76 us against 87.
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kAligned ? 1 : 4)
     combine_backward_kernel(uint16_t* __restrict__ grad_y, float* __restrict__ grad_weights,
                             const uint16_t* __restrict__ grad_out, const uint16_t* __restrict__ y,
                             const float* __restrict__ weights, const RouteParams r) {
-  constexpr int kFlight = 4;
+  constexpr int kFlight = kAligned ? 4 : 2;
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
