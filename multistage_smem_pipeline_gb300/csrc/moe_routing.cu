@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // slots are asked for before the first is used; the sum keeps slot order.
 // 8192 x 8 rows of 4096 in 89 us: 6.8 TB/s; four in flight against two: 89 and 100.
 template <typename T, bool kAligned, bool kWeighted>
-__global__ void __launch_bounds__(kRowThreads, kAligned ? 1 : 5)
+__global__ void __launch_bounds__(kRowThreads, 5)
     combine_kernel(uint16_t* __restrict__ out, const uint16_t* __restrict__ y,
                    const float* __restrict__ weights, const RouteParams r) {
   constexpr int kFlight = 4;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kRowThreads, kAligned ? 1 : 5)
 // Rows that are not aligned need registers for their shifts, and do better with
 // fewer windows in flight and more warps: 8000 x 2 of 4095 in 76 us against 87.
 template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads, kAligned ? 1 : 4)
+__global__ void __launch_bounds__(kRowThreads, 4)
     combine_backward_kernel(uint16_t* __restrict__ grad_y, float* __restrict__ grad_weights,
                             const uint16_t* __restrict__ grad_out, const uint16_t* __restrict__ y,
                             const float* __restrict__ weights, const RouteParams r) {
