@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint8_t* const misc = smem + stages * S::kStageBytes + 8 * kGemmBars;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  int32_t* const before = reinterpret_cast<int32_t*>(misc + 16);
+  GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 16);
 
   if (threadIdx.x == 0) {
     grid_launch_dependents();
@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish_pair();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) count_row_tiles<kBN>(p, before, lane);
+  if (p.offsets && warp == 2) find_groups<kBN>(p, start, lane);
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int tiles =
-      (p.offsets ? before[p.groups]
+      (p.offsets ? start[p.groups].tiles
                  : p.groups * ((static_cast<int>(p.group_rows) + kBN - 1) / kBN)) * p.m_tiles;
 
   if (warp == 0 || warp == kGemmRowWarp) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t phase = 0, issued = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
-      const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      const GemmTile tile = gemm_tile<kBN>(t, p, start);
       const int half_n = ((tile.count + 31) & ~31) >> 1;  // rows this CTA holds
       const int boxes = (half_n + p.box_rows - 1) / p.box_rows;
       const bool two = tile.count > kTileRows;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const uint64_t w_desc0 = sw128_kmajor_desc(base);
       const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
       for (int t = pair; ok && t < tiles; t += pairs) {
-        const GemmTile tile = gemm_tile<kBN>(t, p, before);
+        const GemmTile tile = gemm_tile<kBN>(t, p, start);
         const uint32_t idesc = fp4_idesc<kFormat>(2 * kGemmM, (tile.count + 31) & ~31);
         if (!gemm_wait_warp(tempty_bar, acc_phase ^ 1u, abort_flag, kWaitTmemEmpty, p)) break;
         tc_fence_after_sync();
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t acc_phase = 0;
     const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
     for (int t = pair; t < tiles; t += pairs) {
-      const GemmTile tile = gemm_tile<kBN>(t, p, before);
+      const GemmTile tile = gemm_tile<kBN>(t, p, start);
       int ok = 0;
       if (lane == 0) ok = gemm_wait(tfull_bar, acc_phase, abort_flag, kWaitTmemFull, p);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                          });
       acc_phase ^= 1u;
     }
-    zero_tail(p);
+    zero_tail(p, start);
   }
   __syncwarp();
   tc_fence_before_sync();
