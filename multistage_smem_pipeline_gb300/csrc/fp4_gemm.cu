@@ -156,7 +156,7 @@ int launch_pair(const PairMaps& m, Fp4GemmParams p, int pairs, int device, cudaS
   static std::atomic<uint64_t> granted{0};  // per instantiation
   if (!grant_smem(fp4_gemm_pair<T, kFormat>, kGemmSmemLimit, device, granted)) return GEMM_ERR_CUDA;
   return launch_pdl(fp4_gemm_pair<T, kFormat>, dim3(2 * pairs), dim3(kGemmThreads),
-                    fixed + p.stages * S::kStageBytes, s, 2u, m.w, m.x, m.sw, m.sx, p);
+                    fixed + S::ring_bytes(p.stages), s, 2u, m.w, m.x, m.sw, m.sx, p);
 }
 
 }  // namespace

@@ -8,12 +8,19 @@
 // What bounds it is shared memory: per 256 columns of k an SM takes in 38 KiB
 // and its MMAs read 32 KiB of codes and 6 KiB of scales in 512 cycles, more
 // than its 128 bytes a cycle; a single CTA's 128 x 256 tile would take in 54
-// and read 54.  At 8192^3 the loads alone take 120 us, the MMAs alone 136 (of
+// and read 54.  At 8192^3 the loads alone take 124 us, the MMAs alone 136 (of
 // which 14 are the accumulator changing hands, as there is no room for two of
-// 256 columns and the scales), both 158, and the stores make it 166
-// (6.6 PFLOP/s).  Tried and no faster: 384 rows a tile (176 us: 10 waves where
-// 9.3 would do), two pairs sharing the rows by multicast (177: 36 such clusters
-// fit where 38 would fill the SMs), L2 prefetch of the weights (194).
+// 256 columns and the scales), both 151, and the stores make it 164
+// (6.7 PFLOP/s).  Codes and scales have rings of their own because tensor memory
+// has room for five blocks' nvfp4 scales and shared memory for six of codes: with
+// 3, 4, 5 and 6 blocks of codes 8192^3 takes 208, 177, 165 and 164 us, and 4096
+// tokens x 8 of 64 experts, 4096 -> 2048, 153, 134, 129 and 125.
+// Tried and no faster: 384 rows a tile (176 us: 10 waves where 9.3 would do), two
+// pairs sharing the rows by multicast (177: 36 such clusters fit where 38 would
+// fill the SMs), L2 prefetch of the weights (194).  With ragged groups, tiles
+// handed out as pairs get free (clusters not yet begun taken over): 131 us for the
+// 4096 tokens where the fixed stride took 128, though the stride leaves the last
+// pair 13 % more work than the mean; pairs that run in step share operands in L2.
 //
 // Barriers as in the fp16 pair kernel: `full` in the even CTA counts both
 // CTAs' bytes; `empty` and `tfull` are in both, committed to both; `tempty` in
@@ -29,14 +36,17 @@ struct Fp4PairShape {
   static constexpr int kXTiles = 2;
   static constexpr uint32_t kScaleStage = chunks_per_stage(kFormat) * kChunkBytes;
   static constexpr uint32_t kXBytes = kBN / 2 * kGemmBytesK;
-  static constexpr uint32_t kStageBytes = kWBytes + kXBytes + kScaleStage * (1 + kXTiles);
+  static constexpr uint32_t kStageBytes = kWBytes + kXBytes;  // codes
+  static constexpr uint32_t kSlotBytes = kScaleStage * (1 + kXTiles);
   static constexpr uint32_t kWCols = 4 * chunks_per_stage(kFormat);
   static constexpr uint32_t kSlotCols = kWCols * (1 + kXTiles);
   static constexpr int kSlots = (kTmemCols - kTmemScales) / kSlotCols;
+  static __host__ __device__ int slots(int stages) { return stages < kSlots ? stages : kSlots; }
+  static uint32_t ring_bytes(int stages) { return stages * kStageBytes + slots(stages) * kSlotBytes; }
   static int stages_that_fit(uint32_t fixed) {
-    int s = static_cast<int>((kGemmSmemLimit - fixed) / kStageBytes);
-    if (s > kSlots) s = kSlots;
-    return s > kGemmMaxStages ? kGemmMaxStages : s;
+    int s = kGemmMaxStages;
+    while (ring_bytes(s) + fixed > kGemmSmemLimit) --s;
+    return s;
   }
 };
 
@@ -94,17 +104,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = p.stages;
+  const int stages = p.stages, slots = S::slots(stages);
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   constexpr uint16_t kBoth = 0x3;
-  const uint32_t bars = base + stages * S::kStageBytes;
+  const uint32_t scales = base + stages * S::kStageBytes;
+  const uint32_t bars = scales + slots * S::kSlotBytes;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kGemmMaxStages + s); };
   const uint32_t tfull_bar = bars + 8u * (2 * kGemmMaxStages);
   const uint32_t tempty_bar = tfull_bar + 8;
   const uint32_t drain_bar = tfull_bar + 16;
-  uint8_t* const misc = smem + stages * S::kStageBytes + 8 * kGemmBars;
+  uint8_t* const misc = smem + (bars - base) + 8 * kGemmBars;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 16);
@@ -141,8 +152,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       (p.offsets ? start[p.groups].tiles
                  : p.groups * ((static_cast<int>(p.group_rows) + kBN - 1) / kBN)) * p.m_tiles;
 
-  if (warp == 0 || warp == kGemmRowWarp) {
-    // ---------------------------------------------------------- producers (both CTAs)
+  if (warp == 0) {
+    // ---------------------------------------------------------- codes (both CTAs)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
@@ -155,10 +166,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                              S::kScaleStage * (two ? 3 : 2);
       const int w_row = static_cast<int>(tile.group * p.n_out + tile.m * (2 * kGemmM) + rank * kGemmM);
       const int x_row = tile.x_row + rank * half_n;
-      int sw = (tile.group * p.w_group_tiles + 2 * tile.m + rank) * p.tile_chunks;
-      // each CTA loads one tile of the rows' scales, for both
-      int sx = (tile.x_tile + rank) * p.tile_chunks;
-      const bool loads_sx = rank == 0 || two;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!gemm_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kWaitEmpty, p)) {
           ok = false;
@@ -167,24 +174,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (elect_one()) {
           const uint32_t w_dst = base + stage * S::kStageBytes;
           const uint32_t x_dst = w_dst + kWBytes;
-          const uint32_t s_dst = x_dst + S::kXBytes;
           const uint32_t full = mapa_shared(full_bar(stage), 0);
-          if (warp == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
-            if (!(p.inject && issued == 0))
-              tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
-            tma_load_2d_pair(s_dst, &tmSW, full, 0, sw);
-          } else {
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d_pair(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
-                               x_row + b * p.box_rows);
-            if (loads_sx)
-              tma_load_2d_pair_mc(s_dst + (1 + rank) * S::kScaleStage, &tmSX, full, 0, sx, kBoth);
-          }
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * bytes);
+          if (!(p.inject && issued == 0))
+            tma_load_2d_pair(w_dst, &tmW, full, kb * kGemmBytesK, w_row);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair(x_dst + b * p.box_rows * kGemmBytesK, &tmX, full, kb * kGemmBytesK,
+                             x_row + b * p.box_rows);
         }
         __syncwarp();
-        sw += kChunks;
-        sx += kChunks;
         ++issued;
         if (++stage == stages) {
           stage = 0;
@@ -192,19 +190,58 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
-    if (rank == 0 && warp == 0) {  // the even CTA's barriers count both CTAs' bytes
+    if (rank == 0) {  // the even CTA's barriers count both CTAs' bytes
       const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
       for (uint32_t i = first; i < issued; ++i)
         gemm_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
     }
+  } else if (warp == kGemmRowWarp) {
+    // ---------------------------------------------------------- scales (both CTAs)
+    // Block i's go where block i - slots' were, whose MMAs have then read theirs
+    // from tensor memory too.
+    int stage = 0, slot = 0, freed = 0;
+    uint32_t freed_phase = 0, issued = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const GemmTile tile = gemm_tile<kBN>(t, p, start);
+      int sw = (tile.group * p.w_group_tiles + 2 * tile.m + rank) * p.tile_chunks;
+      // each CTA loads one tile of the rows' scales, for both
+      int sx = (tile.x_tile + rank) * p.tile_chunks;
+      const bool loads_sx = rank == 0 || tile.count > kTileRows;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (issued >= static_cast<uint32_t>(slots)) {
+          if (!gemm_wait_warp(empty_bar(freed), freed_phase, abort_flag, kWaitEmpty, p)) {
+            ok = false;
+            break;
+          }
+          if (++freed == stages) {
+            freed = 0;
+            freed_phase ^= 1u;
+          }
+        }
+        if (elect_one()) {
+          const uint32_t dst = scales + slot * S::kSlotBytes;
+          const uint32_t full = mapa_shared(full_bar(stage), 0);
+          tma_load_2d_pair(dst, &tmSW, full, 0, sw);
+          if (loads_sx)
+            tma_load_2d_pair_mc(dst + (1 + rank) * S::kScaleStage, &tmSX, full, 0, sx, kBoth);
+        }
+        __syncwarp();
+        sw += kChunks;
+        sx += kChunks;
+        ++issued;
+        if (++stage == stages) stage = 0;
+        if (++slot == slots) slot = 0;
+      }
+    }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer (even CTA)
     if (rank == 0) {
-      int stage = 0;
+      int stage = 0, slot = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       const uint64_t w_desc0 = sw128_kmajor_desc(base);
-      const uint64_t s_desc0 = scale_desc(base + kWBytes + S::kXBytes);
+      const uint64_t s_desc0 = scale_desc(scales);
       for (int t = pair; ok && t < tiles; t += pairs) {
         const GemmTile tile = gemm_tile<kBN>(t, p, start);
         const uint32_t idesc = fp4_idesc<kFormat>(2 * kGemmM, (tile.count + 31) & ~31);
@@ -221,8 +258,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           // at 8192^3 against 166; what is copied for nothing is not used).
           if (elect_one()) {
             const uint64_t at = static_cast<uint64_t>((stage * S::kStageBytes) >> 4);
-            const uint64_t s_desc = s_desc0 + at;
-            const uint32_t w_cols = tmem + kTmemScales + stage * S::kSlotCols;
+            const uint64_t s_desc =
+                s_desc0 + static_cast<uint64_t>((slot * S::kSlotBytes) >> 4);
+            const uint32_t w_cols = tmem + kTmemScales + slot * S::kSlotCols;
             const uint32_t x_cols = w_cols + S::kWCols;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -245,6 +283,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             umma_commit_pair_mc(empty_bar(stage), kBoth);
           }
           __syncwarp();
+          if (++slot == slots) slot = 0;
           if (++stage == stages) {
             stage = 0;
             phase ^= 1u;

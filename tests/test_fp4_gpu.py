@@ -296,6 +296,36 @@ def test_products_by_expert(lib, form, tokens, top_k, experts, dropped, only, n,
     assert lib.fp4_get_device_error() == (0, 0)
 
 
+# Enough rows an expert that CTA pairs share a tile; with 600 experts what a CTA keeps of the
+# groups leaves its ring a stage less.
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("slots,experts,n,k", [(6000, 5, 1500, 2048), (84000, 600, 520, 512)])
+def test_large_products_by_expert_are_exact(lib, form, slots, experts, n, k):
+    """Small integers with scale 1, as above: the fp32 sums are exact in any order."""
+    g = torch.Generator(device="cuda").manual_seed(slots)
+    values = torch.tensor([0, 1, 2, 3, 4, 6, -1, -3], dtype=torch.float16, device="cuda")
+    x = values[torch.randint(8, (slots, k), device="cuda", generator=g)]
+    w = values[torch.randint(8, (experts * n, k), device="cuda", generator=g)]
+    x[:, ::16] = 6
+    w[:, ::16] = 6
+    # uneven, one expert without rows, some slots dropped
+    weight = torch.rand(experts, device="cuda", generator=g) + 0.5
+    weight[1] = 0
+    ids = torch.multinomial(weight, slots, replacement=True, generator=g).int()
+    ids[torch.rand(slots, device="cuda", generator=g) < 0.02] = -1
+    r = lib.moe_sort(ids.view(-1, 1), experts)
+    qw = lib.fp4_quantize(w, format=form, group_rows=n)
+    out = torch.full((slots, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lib.fp4_gemm_tn(lib.fp4_quantize(x, format=form, routing=r), qw, dtype=torch.bfloat16, out=out)
+    off, order = r.offsets.tolist(), lib.moe_pairs(r).long()
+    for e in range(experts):
+        seg = slice(off[e], off[e + 1])
+        want = x[order[seg]].double() @ w[e * n:(e + 1) * n].double().T
+        assert torch.equal(out[seg], want.to(torch.bfloat16)), e
+    assert not out[off[-1]:].any()
+    assert lib.fp4_get_device_error() == (0, 0)
+
+
 @pytest.mark.parametrize("m,n", [(3, 50), (200, 70)])
 def test_uniform_groups(lib, m, n):
     """A batch of products: the same number of rows for every weight."""
