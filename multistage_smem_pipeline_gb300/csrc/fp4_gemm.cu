@@ -216,22 +216,27 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.error_word = error_index(s);
 
   // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs: the form whose waves
-  // of tiles take fewer cycles.  A tile takes a single CTA about 1400 + 580 per
-  // 256 columns of k, and a pair 5700 + 520: four times the work in about the
+  // of tiles take fewer cycles.  A tile takes a single CTA about 1200 + 580 per
+  // 256 columns of k, and a pair 4500 + 500: four times the work in about the
   // time, but with one accumulator, so that a tile's stores are not all hidden
-  // (8192^3: 261 us by single CTAs, 166 by pairs; 8192 x 4096 x 256: 16 and 24;
+  // (8192^3: 261 us by single CTAs, 164 by pairs; 8192 x 4096 x 256: 16 and 24;
   // 128 x 14336 x 4096 mxfp4: 7.8 and 10).  With groups by offsets the number of
-  // row tiles is not known here: a group is taken to have the mean number of rows.
+  // row tiles is not known here: a group is taken to end half way through its
+  // last.  Fitted to 200 shapes measured both ways: 0.5 % over the better form of
+  // each in the mean, at worst, where a tile more starts another wave, 30 % (1326
+  // rows of 18 groups, 3022 -> 958: 13.4 us where pairs take 10.1).
   const auto cycles = [&](int64_t tile, int64_t slots, int64_t fixed, int64_t per_block) {
-    const int64_t group = a->offsets ? (a->rows + a->groups - 1) / a->groups : a->group_rows;
-    const int64_t tiles = std::min<int64_t>(a->groups, a->rows) * ((group + tile - 1) / tile) *
-                          ((n_out + tile - 1) / tile);
+    const int64_t live = std::min<int64_t>(a->groups, a->rows);
+    const int64_t row_tiles = a->offsets
+                                  ? std::max(live, (2 * a->rows + live * tile) / (2 * tile))
+                                  : a->groups * ((a->group_rows + tile - 1) / tile);
+    const int64_t tiles = row_tiles * ((n_out + tile - 1) / tile);
     return (tiles + slots - 1) / slots * (fixed + per_block * p.num_kb);
   };
   const int64_t x_chunks =
       tile_count(a->rows, a->groups, a->offsets != nullptr) * p.tile_chunks;
   const int64_t w_chunks = static_cast<int64_t>(a->groups) * p.w_group_tiles * p.tile_chunks;
-  const bool pair = cycles(256, sms / 2, 5700, 520) < cycles(128, sms, 1400, 580) &&
+  const bool pair = cycles(256, sms / 2, 4500, 500) < cycles(128, sms, 1200, 580) &&
                     x_chunks <= INT_MAX && w_chunks <= INT_MAX;  // counted in 32 bits there
   const int bm = pair ? 256 : 128, bn = bm;
   p.m_tiles = static_cast<int32_t>((n_out + bm - 1) / bm);

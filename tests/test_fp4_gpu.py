@@ -299,7 +299,7 @@ def test_products_by_expert(lib, form, tokens, top_k, experts, dropped, only, n,
 # Enough rows an expert that CTA pairs share a tile; with 600 experts what a CTA keeps of the
 # groups leaves its ring a stage less.
 @pytest.mark.parametrize("form", FORMATS)
-@pytest.mark.parametrize("slots,experts,n,k", [(6000, 5, 1500, 2048), (84000, 600, 520, 512)])
+@pytest.mark.parametrize("slots,experts,n,k", [(6000, 5, 1500, 2048), (153600, 600, 512, 2048)])
 def test_large_products_by_expert_are_exact(lib, form, slots, experts, n, k):
     """Small integers with scale 1, as above: the fp32 sums are exact in any order."""
     g = torch.Generator(device="cuda").manual_seed(slots)
