@@ -72,7 +72,7 @@ def _link_binding(obj: str) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".{os.getpid()}.tmp"
     subprocess.check_call(["g++", "-shared", "-o", tmp, obj, "-L" + libs, "-lc10", "-lc10_cuda",
-                           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-L" + LIB_DIR,
+                           "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", "-L" + LIB_DIR,
                            "-l:libgemm_tn_f16.so", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BINDING)
 

@@ -9,6 +9,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 
 #include <memory>
 #include <optional>
@@ -87,16 +88,34 @@ int64_t row_stride(const at::Tensor& x) {
   return x.size(0) > 1 ? std::max(x.stride(0), x.size(1)) : x.size(1);
 }
 
+// at::empty for the GPU, without the dispatcher's part of its time.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, at::Device device) {
+  return at::detail::empty_cuda(sizes, type, device, std::nullopt);
+}
+
 using Out = std::optional<at::Tensor>;
 
 at::Tensor output(const Out& out, int64_t rows, int64_t cols, at::ScalarType type,
                   at::Device device) {
-  if (!out) return at::empty({rows, cols}, at::TensorOptions().dtype(type).device(device));
+  if (!out) return fresh({rows, cols}, type, device);
   if (out->scalar_type() != type || out->dim() != 2 || out->size(0) != rows ||
       out->size(1) != cols || !out->is_contiguous() || out->device() != device)
     value_error("out must be a contiguous " + std::to_string(rows) + " x " +
                 std::to_string(cols) + " tensor of the right type on the inputs' device");
   return *out;
+}
+
+// Part of a buffer from element `first` on, contiguous: a tensor over the same
+// storage, made directly (through the dispatcher a view costs the host 1 to 5 us,
+// which is as long as some of the kernels).
+at::Tensor part(const at::Tensor& buffer, int64_t first, at::IntArrayRef sizes) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_version_counter(buffer.unsafeGetTensorImpl()->version_counter());
+  impl->set_storage_offset(first);
+  impl->set_sizes_contiguous(sizes);
+  return t;
 }
 
 // ------------------------------------------------------------------ Routing
@@ -117,11 +136,11 @@ struct Routing {
   }
 
   const at::Tensor& get_offsets() {
-    if (!offsets.defined()) offsets = buffer.as_strided({c.experts + 1}, {1}, 0);
+    if (!offsets.defined()) offsets = part(buffer, 0, {c.experts + 1});
     return offsets;
   }
   const at::Tensor& get_rows() {
-    if (!rows.defined()) rows = buffer.as_strided({c.tokens, c.top_k}, {c.top_k, 1}, head());
+    if (!rows.defined()) rows = part(buffer, head(), {c.tokens, c.top_k});
     return rows;
   }
 };
@@ -156,7 +175,7 @@ RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream
   auto r = std::make_shared<Routing>();
   r->ids = ids;
   r->describe(experts);
-  r->buffer = at::empty({r->head() + r->slots()}, ids.options());
+  r->buffer = fresh({r->head() + r->slots()}, at::kInt, ids.device());
   int32_t* const at = static_cast<int32_t*>(r->buffer.data_ptr());
   r->c.offsets = at;
   r->c.rows = at + r->head();
@@ -167,7 +186,7 @@ RoutingPtr sort(const at::Tensor& ids, int64_t experts, const py::object& stream
 
 at::Tensor pairs_of(const Routing& r, const py::object& stream) {
   const On on(r.device(), stream);
-  const at::Tensor pairs = at::empty({r.slots()}, r.ids.options());
+  const at::Tensor pairs = fresh({r.slots()}, at::kInt, r.device());
   check(moe_pairs(static_cast<int32_t*>(pairs.data_ptr()), &r.c, on.stream()), "moe_pairs");
   return pairs;
 }
@@ -209,12 +228,12 @@ struct Fp4Matrix {
 
   const at::Tensor& get_scales() {
     if (!scales.defined())
-      scales = buffer.narrow(0, 0, tiles * chunks * 512).view({tiles, chunks, 512});
+      scales = part(buffer, 0, {tiles, chunks, 512});
     return scales;
   }
   const at::Tensor& get_codes() {
     if (!codes.defined())
-      codes = buffer.narrow(0, tiles * chunks * 512, c.rows * pitch).view({c.rows, pitch});
+      codes = part(buffer, tiles * chunks * 512, {c.rows, pitch});
     return codes;
   }
 };
@@ -267,7 +286,7 @@ MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t expon
     m = std::make_shared<Fp4Matrix>();
     m->describe(rows, cols, fmt, exponent, group_rows, routing);
     const int64_t scales = m->tiles * m->chunks * 512;
-    m->buffer = at::empty({scales + rows * m->pitch}, x.options().dtype(at::kByte));
+    m->buffer = fresh({scales + rows * m->pitch}, at::kByte, x.device());
     m->device = x.device();
     m->c.scales = m->buffer.data_ptr();
     m->c.codes = static_cast<uint8_t*>(m->buffer.data_ptr()) + scales;
@@ -387,8 +406,8 @@ std::pair<at::Tensor, at::Tensor> combine_backward(const at::Tensor& grad_out, c
     value_error("grad_out must be contiguous, of y's type and width");
   const float* const w = weights_of(weights, r);
   const On on(y.device(), stream);
-  const at::Tensor grad_y = at::empty({y.size(0), y.size(1)}, y.options());
-  const at::Tensor grad_w = at::empty({r.c.tokens, r.c.top_k}, weights.options());
+  const at::Tensor grad_y = fresh(y.sizes(), y.scalar_type(), y.device());
+  const at::Tensor grad_w = fresh({r.c.tokens, r.c.top_k}, at::kFloat, y.device());
   check(moe_combine_backward(grad_y.data_ptr(), static_cast<float*>(grad_w.data_ptr()),
                              grad_out.data_ptr(), y.data_ptr(), w, y.size(1), type, &r.c,
                              on.stream()),
