@@ -110,7 +110,7 @@ at::Tensor output(const Out& out, int64_t rows, int64_t cols, at::ScalarType typ
 // which is as long as some of the kernels).
 at::Tensor part(const at::Tensor& buffer, int64_t first, at::IntArrayRef sizes) {
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-      c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+      c10::TensorImpl::VIEW, c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
   c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
   impl->set_version_counter(buffer.unsafeGetTensorImpl()->version_counter());
   impl->set_storage_offset(first);

@@ -198,6 +198,28 @@ def test_same_bits_every_time(lib):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("make_in", [False, True])
+@pytest.mark.parametrize("read_in", [False, True])
+def test_arrays_inside_and_outside_inference_mode(lib, make_in, read_in):
+    """A routing's and a matrix's tensors are parts of one buffer, whichever mode asks for them."""
+    ids = torch.tensor([[2, 0], [1, 2], [-1, 2]], dtype=torch.int32, device="cuda")
+    x = torch.arange(3 * 40, device="cuda").view(3, 40).half()
+    with torch.inference_mode(make_in):
+        r = lib.moe_sort(ids, 3)
+        q = lib.fp4_quantize(x, format="mxfp4", routing=r)
+    with torch.inference_mode(read_in):
+        offsets, rows, codes, scales = r.offsets, r.rows, q.codes, q.scales
+        same = lib.Routing(offsets, rows, ids)
+        again = lib.Fp4Matrix(codes, scales, cols=40, format="mxfp4", routing=same)
+        assert torch.equal(lib.fp4_dequantize(again), lib.fp4_dequantize(q))
+    assert offsets.tolist() == [0, 1, 2, 5]
+    assert rows.tolist() == [[2, 0], [1, 3], [5, 4]]
+    assert codes.shape == (6, 32) and scales.shape == (6 // 128 + 3, 2, 512)
+    assert offsets.untyped_storage().data_ptr() == rows.untyped_storage().data_ptr()
+    del r, q, same, again
+    assert offsets.tolist() == [0, 1, 2, 5]
+
+
 def test_refusals(lib):
     ids = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
     r = lib.moe_sort(ids, 3)
