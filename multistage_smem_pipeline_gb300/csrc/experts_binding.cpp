@@ -1,8 +1,8 @@
 // Python binding of moe_fp4.h: checks and marshals torch tensors, allocates
 // outputs, and calls the C functions on the current (or a given) stream.  It
 // is compiled because the calls it makes are a few microseconds long on the
-// GPU: marshalled from Python, a call cost the host 7 to 11 us, of which the
-// launch is 2.6 and an allocation 1.
+// GPU: marshalled from Python, a call cost the host 7 to 11 us; compiled, 2.6 to
+// 4.3, of which a launch is 1.5 and an allocation 0.6.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
