@@ -16,6 +16,7 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRowThreads = 256;
+constexpr int kSlotThreads = 128;  // a warp per slot
 
 struct RouteParams {
   const int32_t* offsets;
@@ -197,14 +198,16 @@ __global__ void __launch_bounds__(kRowThreads)
 // Other rows: one warp per slot, as each of a token's rows has windows of its
 // own; the token's row comes from cache after the first.  1021 x 6 rows of 1411
 // in 5.7 us (7.1 by blocks of a token), of 1408 aligned in 3.8; the shifts and
-// the second load of a window are the difference.
-__global__ void __launch_bounds__(kRowThreads)
+// the second load of a window are the difference.  Where the slots fill the SMs
+// more than once, two windows in flight and more warps do better than four
+// (8000 x 2 x 4095: 40.0 against 44.6 us; 1021 x 6 x 1411: 6.7 and 5.7).
+template <int kFlight>
+__global__ void __launch_bounds__(kSlotThreads)
     dispatch_slots_kernel(uint16_t* __restrict__ y, const uint16_t* __restrict__ x, int64_t ldx,
                           const RouteParams r) {
-  constexpr int kFlight = 4;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int64_t p = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int64_t p = static_cast<int64_t>(blockIdx.x) * (kSlotThreads / 32) + (threadIdx.x >> 5);
   if (p >= r.tokens * r.top_k) return;
   const int32_t row = r.rows[p];
   const bool kept = row < r.offsets[r.experts];
@@ -285,9 +288,11 @@ __global__ void __launch_bounds__(kRowThreads, 5)
 // takes its product with the row the slot had.  The warps of a block share
 // the token's gradient through L1.  8192 x 8 rows of 4096 in 167 us: 6.8 TB/s.
 // Rows that are not aligned need registers for their shifts, and do better with
-// fewer windows in flight and more warps: 8000 x 2 of 4095 in 76 us against 87.
-template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads, 4)
+// fewer windows in flight (8000 x 2 of 4095: 76 us against 87); kMany: and, where
+// the slots fill the SMs more than once, with fewer registers and 36 warps on an
+// SM instead of 32 (65 us; 300 x 8 of 777, where they do not: 5.2 against 4.4).
+template <typename T, bool kAligned, bool kMany>
+__global__ void __launch_bounds__(kSlotThreads, kMany ? 9 : 8)
     combine_backward_kernel(uint16_t* __restrict__ grad_y, float* __restrict__ grad_weights,
                             const uint16_t* __restrict__ grad_out, const uint16_t* __restrict__ y,
                             const float* __restrict__ weights, const RouteParams r) {
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t p = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int64_t p = static_cast<int64_t>(blockIdx.x) * (kSlotThreads / 32) + (threadIdx.x >> 5);
   if (p >= r.tokens * r.top_k) return;
   const int32_t row = r.rows[p];
   const bool kept = row < r.offsets[r.experts];
@@ -384,7 +389,7 @@ RouteParams route_params(const moe_routing_t* r, int64_t hidden) {
 
 // Blocks of warps, one for each slot.
 unsigned slot_blocks(const moe_routing_t* r) {
-  constexpr int kWarps = kRowThreads / 32;
+  constexpr int kWarps = kSlotThreads / 32;
   return static_cast<unsigned>((r->tokens * r->top_k + kWarps - 1) / kWarps);
 }
 
@@ -473,7 +478,8 @@ extern "C" int moe_dispatch(void* y, const void* x, int64_t ldx, int64_t hidden,
   int rc = check_rows({{y, true, true, false}, {x, false, false, false}}, hidden, ldx, type, r);
   if (rc != GEMM_OK) return rc;
   if (r->tokens == 0 || hidden == 0) return GEMM_OK;
-  if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
+  int sms = 0;
+  if ((rc = require_device(&sms)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RouteParams p = route_params(r, hidden);
   uint16_t* const to = static_cast<uint16_t*>(y);
@@ -481,8 +487,11 @@ extern "C" int moe_dispatch(void* y, const void* x, int64_t ldx, int64_t hidden,
   if (rows_aligned({y, x}, hidden, ldx))
     return launch_pdl(dispatch_kernel, dim3(static_cast<unsigned>(r->tokens)), dim3(kRowThreads), 0,
                       s, 1u, to, from, ldx, p);
-  return launch_pdl(dispatch_slots_kernel, dim3(slot_blocks(r)), dim3(kRowThreads), 0, s, 1u, to,
-                    from, ldx, p);
+  const auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(slot_blocks(r)), dim3(kSlotThreads), 0, s, 1u, to, from, ldx, p);
+  };
+  return r->tokens * r->top_k > 64 * static_cast<int64_t>(sms) ? go(dispatch_slots_kernel<2>)
+                                                               : go(dispatch_slots_kernel<4>);
 }
 
 extern "C" int moe_dispatch_backward(void* grad_x, const void* grad_y, int64_t hidden, int type,
@@ -508,17 +517,21 @@ extern "C" int moe_combine_backward(void* grad_y, float* grad_weights, const voi
   if (n == 0 || (!grad_y && !grad_weights)) return GEMM_OK;
   if (!weights) return GEMM_ERR_INVALID_VALUE;
   if (!aligned_to(weights, 4) || !aligned_to(grad_weights, 4)) return GEMM_ERR_MISALIGNED;
-  if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
+  int sms = 0;
+  if ((rc = require_device(&sms)) != GEMM_OK) return rc;
   const bool wide = rows_aligned({grad_y, grad_out, y}, hidden, hidden);
   const auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(slot_blocks(r)), dim3(kRowThreads), 0,
+    return launch_pdl(kernel, dim3(slot_blocks(r)), dim3(kSlotThreads), 0,
                       static_cast<cudaStream_t>(stream), 1u, static_cast<uint16_t*>(grad_y),
                       grad_weights, static_cast<const uint16_t*>(grad_out),
                       static_cast<const uint16_t*>(y), weights, route_params(r, hidden));
   };
-  if (type == MOE_F16)
-    return wide ? go(combine_backward_kernel<__half, true>)
-                : go(combine_backward_kernel<__half, false>);
-  return wide ? go(combine_backward_kernel<__nv_bfloat16, true>)
-              : go(combine_backward_kernel<__nv_bfloat16, false>);
+  const bool many = n > 32 * static_cast<int64_t>(sms);
+  const auto by_form = [&](auto t) {
+    using T = decltype(t);
+    if (wide) return go(combine_backward_kernel<T, true, false>);
+    return many ? go(combine_backward_kernel<T, false, true>)
+                : go(combine_backward_kernel<T, false, false>);
+  };
+  return type == MOE_F16 ? by_form(__half{}) : by_form(__nv_bfloat16{});
 }

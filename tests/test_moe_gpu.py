@@ -16,7 +16,8 @@ DTYPES = [torch.float16, torch.bfloat16]
 SHAPES = [  # tokens, top_k, experts, hidden, dropped
     (1, 1, 1, 8, 0.0), (1, 8, 64, 2048, 0.0), (3, 2, 5, 1, 0.0), (16, 4, 64, 1411, 0.2),
     (77, 6, 60, 136, 0.0), (130, 3, 7, 7, 0.5), (500, 2, 1024, 64, 0.0), (1021, 6, 60, 250, 0.05),
-    (40, 64, 100, 40, 0.1), (2048, 8, 128, 32, 0.0), (50, 4, 8, 96, 1.0), (4099, 8, 256, 16, 0.02)]
+    (40, 64, 100, 40, 0.1), (2048, 8, 128, 32, 0.0), (50, 4, 8, 96, 1.0), (4099, 8, 256, 16, 0.02),
+    (3000, 4, 16, 45, 0.03), (1300, 8, 5, 2051, 0.1)]
 
 
 @pytest.fixture(scope="module")
