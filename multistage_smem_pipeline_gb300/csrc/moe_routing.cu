@@ -405,11 +405,12 @@ int run_combine(void* out, const void* y, const float* weights, int64_t hidden, 
   if ((rc = require_device(&sms)) != GEMM_OK) return rc;
   const bool wide = rows_aligned({out, y}, hidden, hidden);
   // Smaller blocks where there are blocks enough to fill the SMs several times
-  // (4096 x 8 x 2048: 25.5 against 27.1 us), larger ones where a token's row is
-  // what one block has to do (16 x 4 x 2048: 1.9 against 2.3); and no threads
-  // without a window of the row (1021 x 6 x 1411: 5.9 against 6.5 with 256,
-  // 2000 x 4 x 256: 2.5 against 3.6 with 128, 8192 x 8 x 1408: 34.9 and 36.4).
-  const int64_t most = r->tokens > 8 * sms ? kRowThreads / 2 : kRowThreads;
+  // (4096 x 8 x 2048: 25.5 against 27.1 us; 2000 x 8 x 3001: 32.5 and 26.7, so
+  // not yet there), larger ones where a token's row is what one block has to do
+  // (16 x 4 x 2048: 1.9 against 2.3); and no threads without a window of the row
+  // (1021 x 6 x 1411: 5.9 against 6.5 with 256, 2000 x 4 x 256: 2.5 against 3.6
+  // with 128, 8192 x 8 x 1408: 34.9 and 36.4).
+  const int64_t most = r->tokens > 16 * sms ? kRowThreads / 2 : kRowThreads;
   const int64_t windows = (hidden + (wide ? 7 : 14)) / 8;
   const int64_t passes = (windows + most - 1) / most;
   const unsigned threads =
