@@ -178,6 +178,8 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   if (!valid_type(type) || !std::isfinite(alpha) || inject < 0 || inject > 1 || a->format != b->format || a->cols != b->cols ||
       a->groups != b->groups || b->offsets)
     return GEMM_ERR_INVALID_VALUE;
+  const double scale = std::ldexp(static_cast<double>(alpha), a->exponent + b->exponent);
+  if (!std::isfinite(static_cast<float>(scale))) return GEMM_ERR_INVALID_VALUE;
   const int64_t n_out = b->group_rows;
   if (a->rows == 0 || n_out == 0) return GEMM_OK;
   if (!D) return GEMM_ERR_INVALID_VALUE;
@@ -210,7 +212,7 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.num_kb = static_cast<int32_t>(col_stages(a->cols));
   p.w_group_tiles = static_cast<int32_t>((n_out + kTileRows - 1) / kTileRows);
   p.tile_chunks = p.num_kb * chunks_per_stage(a->format);
-  p.alpha = alpha * va.up * vb.up;
+  p.alpha = static_cast<float>(scale);  // one rounding, whatever the exponents' order
   p.timeout_ns = timeout_ns ? timeout_ns : kTimeoutNs;
   p.inject = inject;
   p.error_word = error_index(s);

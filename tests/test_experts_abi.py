@@ -230,3 +230,14 @@ def test_python_refusals_on_cpu_tensors(ex):
         ex.moe_sort(torch.zeros(4, 2, dtype=torch.int32), 4)
     with pytest.raises(TypeError):
         ex.moe_sort(torch.zeros(4, 2), 4)
+
+
+def test_gemm_refuses_a_scale_beyond_fp32(ex):
+    """alpha 2^(exponents) is one fp32 factor: infinite, it would turn sums of zero into NaN."""
+    E = 1
+    none = dict(rows=0, codes=0, scales=0)      # valid, and nothing to launch
+    for ea, eb, alpha, want in [(100, 100, 1.0, E), (100, 28, 1.0, E), (100, 27, 1.0, 0),
+                                (100, 100, 2.0 ** -80, 0), (100, -100, 2.0 ** 127, 0),
+                                (60, 0, -2.0 ** 68, E), (-100, -100, 1.0, 0)]:
+        a, b = matrix(ex, exponent=ea, **none), matrix(ex, rows=128, exponent=eb, codes=P[4], scales=P[5])
+        assert gemm(ex, a, b, alpha=alpha) == want, (ea, eb, alpha)
