@@ -76,17 +76,17 @@ const char* format_name(int format) { return format == FP4_NV ? "nvfp4" : "mxfp4
 // x is a CUDA matrix of a supported type with contiguous rows; its type number.
 int matrix(const at::Tensor& x, const char* what) {
   const int type = type_of(x.scalar_type(), what);
-  if (x.dim() != 2 || !x.is_cuda())
-    value_error(std::string(what) + " must be a 2-D CUDA tensor");
-  if (x.size(1) > 1 && x.stride(1) != 1)
-    value_error(std::string(what) + "'s rows must be contiguous");
+  const std::string name(what);
+  if (x.dim() != 2) value_error(name + " must be a 2-D CUDA tensor");
+  if (x.size(1) > 1 && x.stride(1) != 1) value_error(name + "'s rows must be contiguous");
+  if (x.size(0) > 1 && x.stride(0) < x.size(1))  // an expanded row, or windows over one
+    value_error(name + "'s rows must not overlap");
+  if (!x.is_cuda()) value_error(name + " must be a 2-D CUDA tensor");
   return type;
 }
 
 // Elements between rows (a tensor of one row may report any stride).
-int64_t row_stride(const at::Tensor& x) {
-  return x.size(0) > 1 ? std::max(x.stride(0), x.size(1)) : x.size(1);
-}
+int64_t row_stride(const at::Tensor& x) { return x.size(0) > 1 ? x.stride(0) : x.size(1); }
 
 // at::empty for the GPU, without the dispatcher's part of its time.
 at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, at::Device device) {

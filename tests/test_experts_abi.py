@@ -241,3 +241,12 @@ def test_gemm_refuses_a_scale_beyond_fp32(ex):
                                 (60, 0, -2.0 ** 68, E), (-100, -100, 1.0, 0)]:
         a, b = matrix(ex, exponent=ea, **none), matrix(ex, rows=128, exponent=eb, codes=P[4], scales=P[5])
         assert gemm(ex, a, b, alpha=alpha) == want, (ea, eb, alpha)
+
+
+def test_rows_that_overlap_are_refused(ex):
+    """The kernels step by the row's width at least: an expanded row would be read past its end."""
+    row = torch.zeros(1, 32, dtype=torch.float16)
+    windows = torch.zeros(64, dtype=torch.float16).unfold(0, 32, 8)
+    for x in (row.expand(4, 32), windows, torch.zeros(1, 1, dtype=torch.float16).expand(4, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            ex.fp4_quantize(x)
