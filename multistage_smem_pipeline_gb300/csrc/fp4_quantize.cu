@@ -150,6 +150,23 @@ __device__ __forceinline__ Segment quantize_segment(const Raw& raw, const Fp4Vie
   return s;
 }
 
+// Codes and their block's scale to 16 elements.
+template <typename T, int kFormat>
+__device__ __forceinline__ void dequantize_segment(Pack (&p)[2], uint2 codes, uint32_t scale,
+                                                   const Fp4View& v) {
+  float f[kSegment];
+  from_e2m1(codes.x, f);
+  from_e2m1(codes.y, f + 8);
+  const float step = scale_value<kFormat>(scale) * (kFormat == FP4_NV ? v.up : 1.0f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float half[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) half[e] = f[8 * h + e] * step;
+    p[h] = pack<T>(half);
+  }
+}
+
 // A block per chunk, going down the tiles.  All of a thread's rows of a tile
 // are asked for before the first is used; the chunk is put together in shared
 // memory and written in one piece.  Six blocks an SM for FP4_NV and four for
@@ -257,14 +274,13 @@ __global__ void __launch_bounds__(kThreads)
 
 // A block per chunk and tile, or 128 rows of no group, going down them.  8192 x
 // 8192 nvfp4 to bf16 in 28 us (6.1 TB/s).
-template <typename T, int kFormat, bool kVec>
+template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(uint16_t* __restrict__ y, const Fp4View v, int tiles) {
   using C = Chunk<kFormat>;
   __shared__ __align__(16) uint8_t scales[kChunkBytes];
   grid_launch_dependents();
   grid_dependency_wait();
-  __shared__ __align__(16) uint16_t staged[kVec ? 8 : C::kRowsAtOnce * C::kCols];
   const int cols = static_cast<int>(v.cols);
   const int seg = threadIdx.x % C::kSegments;
   const int c = static_cast<int>(blockIdx.x) * C::kCols + seg * kSegment;
@@ -289,53 +305,97 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < C::kSteps; ++i) {
       if (i * C::kRowsAtOnce >= t.count) break;
       const int r = r0 + i * C::kRowsAtOnce;
-      float f[kSegment] = {};
-      if (t.tile >= 0) {
-        from_e2m1(codes[i].x, f);
-        from_e2m1(codes[i].y, f + 8);
-        const uint32_t byte = scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)];
-        const float step = scale_value<kFormat>(byte) * (kFormat == FP4_NV ? v.up : 1.0f);
+      Pack p[2] = {};
+      if (t.tile >= 0)
+        dequantize_segment<T, kFormat>(p, codes[i],
+                                       scales[scale_at(r, kFormat == FP4_NV ? seg : seg >> 1)], v);
+      // Neighbours swap halves, so that a warp's store covers 32-byte sectors
+      // whole: first both halves of the even segment, then of the odd one.
+      const bool odd = seg & 1;
+      Pack other;
 #pragma unroll
-        for (int e = 0; e < kSegment; ++e) f[e] *= step;
-      }
-      float half[8];
-      Pack p[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) half[e] = f[8 * h + e];
-        p[h] = pack<T>(half);
-      }
-      if (kVec) {
-        // Neighbours swap halves, so that a warp's store covers 32-byte sectors
-        // whole: first both halves of the even segment, then of the odd one.
-        const bool odd = seg & 1;
-        Pack other;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          other.w[w] = __shfl_xor_sync(0xffffffffu, odd ? p[0].w[w] : p[1].w[w], 1);
-        if (r >= t.count) continue;
-        uint16_t* const row = y + (t.row + r) * v.cols;
-        const int even = c - (odd ? kSegment : 0);  // cols is a multiple of 8: pieces are whole
-        const int first = even + (odd ? 8 : 0), second = first + kSegment;
-        if (first < cols) store8<true>(row, first, cols, odd ? other : p[0]);
-        if (second < cols) store8<true>(row, second, cols, odd ? p[1] : other);
-      } else {
-        // Rows start anywhere: through shared memory, then element by element
-        // with neighbouring lanes on neighbouring elements.
-        *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment) = p[0];
-        *reinterpret_cast<Pack*>(staged + r0 * C::kCols + seg * kSegment + 8) = p[1];
-        __syncthreads();
-        const int rows = min(C::kRowsAtOnce, t.count - i * C::kRowsAtOnce);
-        const int c0 = static_cast<int>(blockIdx.x) * C::kCols;
-        const int here = min(C::kCols, cols - c0);
-        uint16_t* const to = y + (t.row + i * C::kRowsAtOnce) * v.cols + c0;
-        for (int w = threadIdx.x; w < rows * C::kCols; w += kThreads) {
-          const int rr = w / C::kCols, cc = w % C::kCols;
-          if (cc < here) to[rr * v.cols + cc] = staged[w];
-        }
-        __syncthreads();
-      }
+      for (int w = 0; w < 4; ++w)
+        other.w[w] = __shfl_xor_sync(0xffffffffu, odd ? p[0].w[w] : p[1].w[w], 1);
+      if (r >= t.count) continue;
+      uint16_t* const row = y + (t.row + r) * v.cols;
+      const int even = c - (odd ? kSegment : 0);  // cols is a multiple of 8: pieces are whole
+      const int first = even + (odd ? 8 : 0), second = first + kSegment;
+      if (first < cols) store8<true>(row, first, cols, odd ? other : p[0]);
+      if (second < cols) store8<true>(row, second, cols, odd ? p[1] : other);
+    }
+  }
+}
+
+// Rows that start anywhere.  A block takes 16 rows of 256 columns at a time, so
+// that there are blocks enough for the smaller matrices and few ends of rows, and
+// puts them together in shared memory; from there they leave in windows of 16
+// bytes that are aligned in the output's row, and what lies before the first and
+// after the last one by one.  The next rows are asked for before that.
+template <typename T, int kFormat>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_unaligned_kernel(uint16_t* __restrict__ y, const Fp4View v, int64_t steps) {
+  constexpr int kRows = kThreads / kTileSegments;  // 16
+  constexpr int kSteps = kTileRows / kRows;        // to a tile
+  constexpr int kWindows = kStageCols / 8;         // of a row, at most
+  __shared__ __align__(16) uint16_t staged[kRows * kStageCols];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int cols = static_cast<int>(v.cols);
+  const int seg = threadIdx.x % kTileSegments;
+  const int c0 = static_cast<int>(blockIdx.x) * kStageCols;
+  const int c = c0 + seg * kSegment;
+  const int r0 = threadIdx.x / kTileSegments;
+  const int here = min(kStageCols, cols - c0);
+  struct Rows {
+    int first, count;  // of the matrix, and how many (none: 0 or less)
+    bool live;         // this thread's segment has codes
+    uint2 codes;
+    uint32_t scale;
+  };
+  const auto load = [&](int64_t step) {
+    Rows n;
+    n.count = 0;
+    n.live = false;
+    if (step >= steps) return n;
+    const TileRows t = tile_rows(v, static_cast<int>(step / kSteps));
+    const int in = static_cast<int>(step % kSteps) * kRows;
+    n.first = t.row + in;
+    n.count = min(kRows, t.count - in);
+    n.live = t.tile >= 0 && r0 < n.count && c < cols;
+    if (n.live) {
+      n.codes = *reinterpret_cast<const uint2*>(v.codes + (n.first + r0) * v.pitch + c / 2);
+      const int64_t at = t.tile * v.tile_bytes +
+                         static_cast<int64_t>(blockIdx.x) * chunks_per_stage(kFormat) * kChunkBytes;
+      n.scale = v.scales[at + scale_at(in + r0, kFormat == FP4_NV ? seg : seg >> 1)];
+    }
+    return n;
+  };
+  Rows next = load(blockIdx.y);
+  for (int64_t step = blockIdx.y; step < steps; step += gridDim.y) {
+    const Rows now = next;
+    next = load(step + gridDim.y);
+    if (now.count <= 0) continue;
+    Pack p[2] = {};
+    if (now.live) dequantize_segment<T, kFormat>(p, now.codes, now.scale, v);
+    __syncthreads();  // the last rows have left
+    *reinterpret_cast<Pack*>(staged + r0 * kStageCols + seg * kSegment) = p[0];
+    *reinterpret_cast<Pack*>(staged + r0 * kStageCols + seg * kSegment + 8) = p[1];
+    __syncthreads();
+    uint16_t* const to = y + now.first * v.cols + c0;
+    for (int w = threadIdx.x; w < now.count * kWindows; w += kThreads) {
+      const int r = w / kWindows;
+      uint16_t* const row = to + r * v.cols;
+      const int e = w % kWindows * 8 + (-row_lead(row) & 7);
+      if (e + 8 <= here) store8<true>(row, e, here, load8<false>(staged + r * kStageCols, e, here));
+    }
+    if (threadIdx.x < now.count * 16) {
+      const int r = threadIdx.x / 16, k = threadIdx.x % 8;
+      const bool ahead = threadIdx.x % 16 < 8;
+      uint16_t* const row = to + r * v.cols;
+      const int head = min(-row_lead(row) & 7, here);
+      const int tail = head + (here - head) / 8 * 8;  // past the last whole window
+      const int e = ahead ? k : tail + k;
+      if (e < (ahead ? head : here)) row[e] = staged[r * kStageCols + e];
     }
   }
 }
@@ -447,11 +507,18 @@ extern "C" int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* s
   const bool by_offsets = in->offsets != nullptr;
   return dispatch_forms(type, in->format, vec, [&](auto t, auto fmt, auto wide) {
     using T = decltype(t);
-    // only the columns that y has: padding is left out
-    const int64_t chunks = (in->cols + Chunk<fmt()>::kCols - 1) / Chunk<fmt()>::kCols;
     const int64_t tiles = tile_count(in->rows, in->groups, by_offsets) + (by_offsets ? 1 : 0);
-    return launch_pdl(dequantize_kernel<T, fmt(), wide()>, tile_grid(chunks, tiles, sms), dim3(kThreads),
-                      0, static_cast<cudaStream_t>(stream), 1u, static_cast<uint16_t*>(y), v,
-                      static_cast<int>(tiles));
+    uint16_t* const to = static_cast<uint16_t*>(y);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (wide()) {
+      // only the columns that y has: padding is left out
+      const int64_t chunks = (in->cols + Chunk<fmt()>::kCols - 1) / Chunk<fmt()>::kCols;
+      return launch_pdl(dequantize_kernel<T, fmt()>, tile_grid(chunks, tiles, sms), dim3(kThreads), 0,
+                        s, 1u, to, v, static_cast<int>(tiles));
+    }
+    const int64_t steps = tiles * (kTileRows * kTileSegments / kThreads);
+    return launch_pdl(dequantize_unaligned_kernel<T, fmt()>,
+                      tile_grid(col_stages(in->cols), steps, sms), dim3(kThreads), 0, s, 1u, to, v,
+                      steps);
   });
 }
