@@ -445,3 +445,20 @@ def test_refusals(lib):
     r = lib.moe_sort(torch.zeros(9, 1, dtype=torch.int32, device="cuda"), 2)
     with pytest.raises(ValueError):
         lib.fp4_quantize(x, routing=r)
+
+
+@pytest.mark.parametrize("form", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,cols", [(3, 1), (33, 7), (17, 9), (130, 255), (16, 257), (40, 264),
+                                    (129, 1000), (21, 1411)])
+def test_values_at_any_alignment(lib, form, dtype, n, cols):
+    """Outputs that start at any 2-byte address, and nothing around them is written."""
+    x = rows(n + cols, n, cols, torch.float16)
+    q = lib.fp4_quantize(x, format=form)
+    want = torch.from_numpy(ref.values(ref.to_numpy(x), form)).to(dtype)   # exact in either type
+    for first in range(8):
+        flat = torch.full((n * cols + 16,), 7.25, dtype=dtype, device="cuda")
+        lib.fp4_dequantize(q, dtype=dtype, out=flat[first:first + n * cols].view(n, cols))
+        got = flat.cpu()
+        assert torch.equal(got[first:first + n * cols].view(n, cols), want)
+        assert (got[:first] == 7.25).all() and (got[first + n * cols:] == 7.25).all()
