@@ -331,16 +331,16 @@ __global__ void __launch_bounds__(kThreads)
 // puts them together in shared memory; from there they leave in windows of 16
 // bytes that are aligned in the output's row, and what lies before the first and
 // after the last one by one.  The next rows are asked for before that.  2411 x
-// 1169 mxfp4 to fp16 in 3.7 us, where blocks of a whole tile that store single
-// elements take 8.6 (aligned, 1168: 3.5); 8191 x 8191 nvfp4 in 48.6 (3.5 TB/s;
-// by whole tiles 47.4, aligned 28): the shifts and the rows' ends.
+// 1169 mxfp4 to fp16 in 3.3 us, where blocks of a whole tile that store single
+// elements take 8.6 (aligned, 1168: 3.5); 8191 x 8191 nvfp4 in 41 (4.2 TB/s; by
+// whole tiles 47, aligned 28), bound by instruction issue: shifts and rows' ends.
 template <typename T, int kFormat>
 __global__ void __launch_bounds__(kThreads)
     dequantize_unaligned_kernel(uint16_t* __restrict__ y, const Fp4View v, int64_t steps) {
   constexpr int kRows = kThreads / kTileSegments;  // 16
   constexpr int kSteps = kTileRows / kRows;        // to a tile
   constexpr int kWindows = kStageCols / 8;         // of a row, at most
-  __shared__ __align__(16) uint16_t staged[kRows * kStageCols];
+  __shared__ __align__(16) uint16_t staged[kRows * kStageCols + 8];  // 8: read past the last
   grid_launch_dependents();
   grid_dependency_wait();
   const int cols = static_cast<int>(v.cols);
@@ -385,11 +385,12 @@ __global__ void __launch_bounds__(kThreads)
     *reinterpret_cast<Pack*>(staged + r0 * kStageCols + seg * kSegment + 8) = p[1];
     __syncthreads();
     uint16_t* const to = y + now.first * v.cols + c0;
-    for (int w = threadIdx.x; w < now.count * kWindows; w += kThreads) {
-      const int r = w / kWindows;
+    for (int r = threadIdx.x / kWindows; r < now.count; r += kThreads / kWindows) {
       uint16_t* const row = to + r * v.cols;
-      const int e = w % kWindows * 8 + (-row_lead(row) & 7);
-      if (e + 8 <= here) store8<true>(row, e, here, load8<false>(staged + r * kStageCols, e, here));
+      const int head = -row_lead(row) & 7, at = threadIdx.x % kWindows * 8;
+      if (at + head + 8 > here) continue;
+      const uint4* const from = reinterpret_cast<const uint4*>(staged + r * kStageCols + at);
+      *reinterpret_cast<Pack*>(row + at + head) = shift8(from[0], from[1], 2 * head);
     }
     if (threadIdx.x < now.count * 16) {
       const int r = threadIdx.x / 16, k = threadIdx.x % 8;

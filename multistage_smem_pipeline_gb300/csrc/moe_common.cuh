@@ -133,6 +133,23 @@ __device__ __forceinline__ int row_lead(const uint16_t* row) {
   return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) >> 1;
 }
 
+// The 16 bytes from byte `off` (even, below 16) of the 32 of two words on.
+__device__ __forceinline__ Pack shift8(const uint4& lo, const uint4& hi, uint32_t off) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  Pack p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p.w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+  return p;
+}
+
 // Elements [e, e + 8) of a row of n.  Unaligned: the one or two 16-byte words
 // that hold them, shifted into place; a word without an element of the row in
 // it is not read, and what stands outside the row is undefined.
@@ -145,26 +162,15 @@ __device__ __forceinline__ Pack load8(const uint16_t* row, int e, int n) {
   uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
   if (word + 16 > start && word < start + 2 * static_cast<uintptr_t>(n))
     lo = *reinterpret_cast<const uint4*>(word);
-  Pack p;
   const uint32_t off = static_cast<uint32_t>(at & 15);
   if (off == 0) {  // for the whole row: it is aligned as the windows are
+    Pack p;
     *reinterpret_cast<uint4*>(&p) = lo;
     return p;
   }
   if (word + 16 < start + 2 * static_cast<uintptr_t>(n))
     hi = *reinterpret_cast<const uint4*>(word + 16);
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (off & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (off & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p.w[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
-  return p;
+  return shift8(lo, hi, off);
 }
 
 // The same window to a row that it is aligned in; elements outside are left out.

@@ -231,11 +231,13 @@ __global__ void __launch_bounds__(kSlotThreads)
 // One block per token; kWeighted: the sum takes weights.  The rows of kFlight
 // slots are asked for before the first is used; the sum keeps slot order.
 // 8192 x 8 rows of 4096 in 89 us: 6.8 TB/s; four in flight against two: 89 and 100.
+// Unaligned rows do as well with two as with four (4096 x 8 x 2047: 40 us) as long
+// as a thread has at most 40 registers; with 42 it was 48.7.  Two leave room.
 template <typename T, bool kAligned, bool kWeighted>
 __global__ void __launch_bounds__(kRowThreads, 5)
     combine_kernel(uint16_t* __restrict__ out, const uint16_t* __restrict__ y,
                    const float* __restrict__ weights, const RouteParams r) {
-  constexpr int kFlight = 4;
+  constexpr int kFlight = kAligned ? 4 : 2;
   __shared__ int32_t s_row[MOE_MAX_TOP_K];
   __shared__ float s_weight[MOE_MAX_TOP_K];
   __shared__ int s_live;
