@@ -48,13 +48,18 @@ enum {
 };
 
 /* Where the slots of each token went: what moe_sort writes, as later calls
- * take it.  A slot p = token * top_k + j is one (token, expert) pair. */
+ * take it.  A slot p = token * top_k + j is one (token, expert) pair.  A program
+ * that fills the arrays itself keeps to what moe_sort writes: `rows` a
+ * permutation of 0 .. tokens * top_k - 1, `offsets` non-decreasing from 0 to at
+ * most tokens * top_k, the rows from the last offset on those of dropped slots.
+ * They are read on the device and not checked. */
 typedef struct {
   int64_t tokens;
   int32_t top_k, experts;
   const int32_t* offsets;  /* experts + 1: expert e has rows offsets[e] .. offsets[e+1] - 1 */
   const int32_t* rows;     /* tokens * top_k: the row of each slot */
-  const int32_t* ids;      /* tokens * top_k: the expert of each slot, as given to moe_sort */
+  const int32_t* ids;      /* tokens * top_k: the expert of each slot, as given to moe_sort.  No call
+                              reads them after it: what they hold by then does not matter */
 } moe_routing_t;
 
 /* A 4-bit matrix. */

@@ -425,7 +425,9 @@ PYBIND11_MODULE(_experts, m) {
                                   "offsets[e] to offsets[e + 1] - 1.  Dropped slots have the rows "
                                   "from offsets[-1] on.  All int32, on the device.  moe_sort makes "
                                   "one; a program with a router of its own can give the tensors "
-                                  "itself.")
+                                  "itself (rows: a permutation of the slots; offsets: from 0, "
+                                  "non-decreasing; neither is checked).  What ids holds "
+                                  "after that does not matter: no call reads it again.")
       .def(py::init(&given_routing), py::arg("offsets"), py::arg("rows"), py::arg("ids"))
       .def_property_readonly("offsets", &Routing::get_offsets)
       .def_property_readonly("rows", &Routing::get_rows)

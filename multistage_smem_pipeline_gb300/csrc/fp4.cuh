@@ -131,6 +131,18 @@ __device__ __forceinline__ int find_group(const int32_t* offsets, int groups, in
   return lo;
 }
 
+// The group of a row below offsets[groups]: the last one that starts at or
+// before it (those before that start there too are empty).
+__device__ __forceinline__ int group_of_row(const int32_t* offsets, int groups, int32_t row) {
+  int lo = 0, hi = groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (offsets[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ TileRows tile_rows(const Fp4View& v, int q) {
   TileRows t;
   if (!v.offsets) {

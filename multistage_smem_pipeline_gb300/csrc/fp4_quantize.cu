@@ -219,7 +219,10 @@ __global__ void __launch_bounds__(kThreads, kFormat == FP4_NV ? 6 : 4)
 }
 
 // A block per token and up to 4096 columns: quantised once, written to the row
-// of each of its kept slots, whose places the first threads look up.
+// of each of its kept slots, whose places the first threads look up: the expert
+// of a row is the group it lies in, found among the offsets in shared memory
+// (one latency for all of them; the caller's list of experts is not read again,
+// which may hold the next step's by now).
 // Neighbouring threads join the four scale bytes of a chunk.  4096 tokens of
 // 4096 columns into 8 slots each take 23 us (4.8 TB/s); what it waits on are
 // the scales, 4 bytes of a row in each 512-byte chunk, as writing codes 16 bytes
@@ -227,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, kFormat == FP4_NV ? 6 : 4)
 template <typename T, int kFormat, bool kVec>
 __global__ void __launch_bounds__(kThreads)
     quantize_routed_kernel(const Fp4View v, const uint16_t* __restrict__ x, int64_t ldx,
-                           const int32_t* __restrict__ rows, const int32_t* __restrict__ ids,
-                           int top_k) {
+                           const int32_t* __restrict__ rows, int top_k) {
   constexpr int kPerBlock = kFormat == FP4_NV ? 1 : 2;
   __shared__ int64_t s_codes[MOE_MAX_TOP_K], s_scales[MOE_MAX_TOP_K];  // -1: dropped
+  __shared__ int32_t s_first[MOE_MAX_EXPERTS + 1];
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t token = blockIdx.x;
@@ -238,12 +241,14 @@ __global__ void __launch_bounds__(kThreads)
   const int seg = static_cast<int>(blockIdx.y) * kThreads + threadIdx.x;
   const int c = seg * kSegment;
   Raw raw = load_raw<kVec>(x + token * ldx, c, cols);
+  for (int g = threadIdx.x; g <= v.groups; g += kThreads) s_first[g] = v.offsets[g];
+  const int32_t row = threadIdx.x < top_k ? rows[token * top_k + threadIdx.x] : -1;
+  __syncthreads();
   if (threadIdx.x < top_k) {
-    const int32_t row = rows[token * top_k + threadIdx.x];
-    const int32_t e = ids[token * top_k + threadIdx.x];
     int64_t codes = -1;
-    if (row < v.offsets[v.groups]) {  // then e is an expert
-      const int32_t first = v.offsets[e];
+    if (row >= 0 && row < s_first[v.groups]) {
+      const int e = group_of_row(s_first, v.groups, row);
+      const int32_t first = s_first[e];
       codes = row * v.pitch;
       s_scales[threadIdx.x] = (first / kTileRows + e + (row - first) / kTileRows) * v.tile_bytes +
                               scale_at((row - first) % kTileRows, 0);
@@ -483,7 +488,7 @@ extern "C" int fp4_quantize(const fp4_matrix_t* out, const void* x, int64_t ldx,
       const dim3 grid(static_cast<unsigned>(x_rows),
                       static_cast<unsigned>((segments + kThreads - 1) / kThreads));
       return launch_pdl(quantize_routed_kernel<T, fmt(), wide()>, grid, dim3(kThreads), 0, s, 1u, v, xp,
-                        ldx, routing->rows, routing->ids, routing->top_k);
+                        ldx, routing->rows, routing->top_k);
     }
     const int64_t tiles = tile_count(out->rows, out->groups, false);
     const int64_t chunks = col_stages(out->cols) * chunks_per_stage(fmt());
