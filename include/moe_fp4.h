@@ -120,6 +120,19 @@ int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b,
 int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b, float alpha,
                    uint64_t timeout_ns, int inject, void* stream);
 
+/* The form that fp4_gemm_tn takes for `rows` rows in `groups` groups (uniform, or by
+ * offsets) with n outputs each.  Host only, no GPU work; needs a current device
+ * only to read its SM and cluster counts (with none, a GB300's are assumed). */
+typedef struct {
+  int cta_pair;            /* 1: tiles on CTA pairs */
+  int split_k;             /* CTAs that share a tile's k; 1: none do */
+  int tile;                /* outputs, and rows at most, of a tile */
+  int box_rows;            /* rows of activations that one copy loads */
+  int ctas;                /* launched */
+} fp4_config_t;
+int fp4_query_config(int64_t rows, int64_t n, int64_t cols, int format, int groups, int by_offsets,
+                     fp4_config_t* out);
+
 /* Waits for `stream`, then reads and clears its error word of fp4_gemm_tn:
  * GEMM_OK or GEMM_ERR_TIMEOUT; `raw` (may be NULL) gets code | site << 8.
  * Streams have a word each up to 63 of them, beyond that they share. */

@@ -11,8 +11,8 @@ _EXPORTS = ("gemm_tn_f16", "gemm_tn_f16_ex", "gemm_f16_scaled", "gemm_tn_f16_fro
             "minimum_stages", "query_config", "probe_latencies", "library_path", "status_string",
             "GemmError")
 _EXPERTS = ("Fp4Matrix", "Routing", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
-            "fp4_scale_bytes", "fp4_get_device_error", "moe_sort", "moe_pairs", "moe_dispatch",
-            "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+            "fp4_query_config", "fp4_scale_bytes", "fp4_get_device_error", "moe_sort", "moe_pairs",
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
 __all__ = list(_EXPORTS + _EXPERTS)
 
 

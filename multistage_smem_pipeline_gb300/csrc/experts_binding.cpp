@@ -340,6 +340,20 @@ int64_t scale_bytes(int64_t rows, int64_t cols, const std::string& format, int g
   return static_cast<int64_t>(n);
 }
 
+py::dict query_config(int64_t rows, int64_t n, int64_t cols, const std::string& format, int groups,
+                      bool by_offsets) {
+  fp4_config_t c{};
+  check(fp4_query_config(rows, n, cols, format_of(format), groups, by_offsets, &c),
+        "fp4_query_config");
+  py::dict d;
+  d["cta_pair"] = c.cta_pair;
+  d["split_k"] = c.split_k;
+  d["tile"] = c.tile;
+  d["box_rows"] = c.box_rows;
+  d["ctas"] = c.ctas;
+  return d;
+}
+
 // ------------------------------------------------------------------ rows
 int by_token(const at::Tensor& x, const Routing& r, const char* what) {
   const int type = matrix(x, what);
@@ -476,6 +490,9 @@ PYBIND11_MODULE(_experts, m) {
   m.def("fp4_scale_bytes", &scale_bytes, py::arg("rows"), py::arg("cols"),
         py::arg("format") = "nvfp4", py::arg("groups") = 1, py::arg("by_offsets") = false,
         "Bytes of an Fp4Matrix's scales.");
+  m.def("fp4_query_config", &query_config, py::arg("rows"), py::arg("n"), py::arg("cols"),
+        py::arg("format") = "nvfp4", py::arg("groups") = 1, py::arg("by_offsets") = false,
+        "The form that fp4_gemm_tn takes for a product of these sizes, without running it.");
   m.def("moe_sort", &sort, py::arg("ids"), py::arg("experts"), py::arg("stream") = none,
         "Slots sorted by expert.  ids: tokens x top_k int32; a number outside [0, experts) drops "
         "its slot.  The order within an expert is the slots' own.");

@@ -93,11 +93,16 @@ int launch_single(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, i
                     fixed + p.stages * S::kStageBytes, s, static_cast<unsigned>(p.split), w, x, p);
 }
 
-// Clusters of `size` CTAs that the device holds at once, a CTA an SM (clusters
-// lie within a GPC, so some SMs may be left out).
-int resident_clusters(int size, int sms, int device) {
+// What the choice of a form needs to know of the device.
+struct Machine {
+  int sms;
+  int clusters[3];  // of 2, 4 and 8 CTAs, held at once, a CTA an SM (clusters lie
+                    // within a GPC, so some SMs may be left out)
+};
+
+Machine machine_of(int sms, int device) {
   static std::once_flag once;
-  static int held[3] = {0, 0, 0};  // of 2, 4 and 8
+  static int held[3] = {0, 0, 0};
   std::call_once(once, [&] {
     const auto kernel = fp4_gemm_tc<__half, FP4_NV, true>;
     static std::atomic<uint64_t> granted{0};
@@ -121,20 +126,21 @@ int resident_clusters(int size, int sms, int device) {
       }
     }
   });
-  return held[size == 2 ? 0 : size == 4 ? 1 : 2];
+  return Machine{sms, {held[0], held[1], held[2]}};
 }
 
 // CTAs that share each of `tiles` tiles' k.  Measured on GB300: a 256-column
 // block of k takes a lone CTA about 0.28 us (the latency of its loads), and
 // meeting the others 0.6 us and, for the partial sums, up to 3 us for 128 rows.
-// 1 x 4096 x 14336: 17.5 us by one, 10.2 by four; 128 x 512 x 1024: 4.7 and 8.3
-// by two.  All of the clusters have to fit at once (16 tiles by eight: 12.0 us
-// where four take 7.5).
-int choose_split(int64_t tiles, int64_t rows, int num_kb, int sms, int device) {
+// Weights from memory, by one and by two, four or eight: 1 x 4096 x 14336 16.9 us and
+// 12.7, 9.9, -; 128 x 128 x 32768 35.4 and 23.7, 15.4, 9.8; 128 x 512 x 1024, from
+// cache, 4.7 and 8.3.  All of the clusters have to fit at once (16 tiles by eight:
+// 12.0 us where four take 7.5).
+int choose_split(int64_t tiles, int64_t rows, int num_kb, const Machine& machine) {
   int best = 1;
   double least = 0.28 * num_kb;
-  for (int split = 2; split <= 8 && 2 * split <= num_kb; split *= 2) {
-    if (tiles > resident_clusters(split, sms, device)) break;
+  for (int i = 0; i < 3 && 4 << i <= num_kb && tiles <= machine.clusters[i]; ++i) {
+    const int split = 2 << i;
     const double t = 0.28 * num_kb / split + 0.6 + 3.0 * std::min<int64_t>(rows, 128) / 128;
     if (t < least) {
       least = t;
@@ -142,6 +148,70 @@ int choose_split(int64_t tiles, int64_t rows, int num_kb, int sms, int device) {
     }
   }
   return best;
+}
+
+struct Plan {
+  bool pair;
+  int tile;           // outputs and rows of one
+  int m_tiles;        // of a group
+  int box_rows;
+  int split;
+  int units;          // CTAs, pairs or clusters
+  int64_t x_chunks, w_chunks;
+};
+
+// The form of a product of `rows` rows in `groups` groups with `n` outputs each:
+// 128 x 128 tiles on single CTAs, those tiles' k shared by clusters, or 256 x 256
+// on pairs.  Where single CTAs have a tile each at most, they are it, split where
+// there are few: pairs would leave more SMs idle (256 x 8192 x 14336: 22.4 us where
+// single CTAs take 19.5; 1 x 4096 x 14336: 17.8, 16.9, and 9.9 split).  Past
+// that, whichever's waves of tiles take fewer cycles: a tile takes a single CTA about
+// 1200 + 580 per 256 columns of k, and a pair, four times the work, 4500 + 500,
+// with one accumulator, so that a tile's stores are not all hidden (8192^3: 261 us
+// by single CTAs, 164 by pairs; 8192 x 4096 x 256: 16 and 24).  With groups by
+// offsets the number of row tiles is not known here: a group is taken to end half
+// way through its last.  150 dense shapes (1 to 512 rows, 128 to 8192 outputs, k
+// 2048 to 32768, weights from memory) take 0.8 % over the best form of each in the
+// mean, at worst 30 (16 x 8192 x 2048: 7.3 us by two, 5.6 by one).
+int make_plan(int64_t rows, int64_t n, int64_t cols, int format, int64_t groups, bool by_offsets,
+              const Machine& machine, Plan* o) {
+  const int num_kb = static_cast<int>(col_stages(cols));
+  const int64_t group_rows = by_offsets ? 0 : rows / groups;
+  const int64_t tile_chunks = static_cast<int64_t>(num_kb) * chunks_per_stage(format);
+  const int64_t live = std::min(groups, rows);
+  const auto m_tiles = [&](int64_t tile) { return (n + tile - 1) / tile; };
+  const auto expected = [&](int64_t tile) {  // tiles
+    return m_tiles(tile) * (by_offsets ? std::max(live, (2 * rows + live * tile) / (2 * tile))
+                                       : groups * ((group_rows + tile - 1) / tile));
+  };
+  const auto most = [&](int64_t tile) {
+    return m_tiles(tile) *
+           (by_offsets ? rows / tile + live : groups * ((group_rows + tile - 1) / tile));
+  };
+  // rows of a tile, in the mean: of the groups that there can be
+  const int64_t tile_rows =
+      by_offsets ? (rows + groups - 1) / groups : std::min<int64_t>(group_rows, 128);
+  // counted in 32 bits by the kernel over pairs
+  o->x_chunks = tile_count(rows, groups, by_offsets) * tile_chunks;
+  o->w_chunks = groups * ((n + kTileRows - 1) / kTileRows) * tile_chunks;
+  const auto waves = [&](int64_t tile, int64_t slots) { return (expected(tile) + slots - 1) / slots; };
+  o->pair = waves(128, machine.sms) > 1 &&
+            waves(256, machine.sms / 2) * (4500 + 500 * num_kb) <
+                waves(128, machine.sms) * (1200 + 580 * num_kb) &&
+            o->x_chunks <= INT_MAX && o->w_chunks <= INT_MAX;
+  o->split = o->pair ? 1 : choose_split(most(128), tile_rows, num_kb, machine);
+  o->tile = o->pair ? 256 : 128;
+  // counted in 32 bits, with room for a grid's stride past the last
+  if (most(o->tile) > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
+  o->m_tiles = static_cast<int>(m_tiles(o->tile));
+  // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile
+  // loads little more than it has (8 tokens over 64 experts: 21 us against 27
+  // with boxes of 128).
+  o->box_rows = by_offsets || group_rows <= 64 ? 32 : 128;
+  // One CTA per SM, fewer where there cannot be that many tiles.
+  o->units = static_cast<int>(
+      std::min<int64_t>(o->pair ? machine.sms / 2 : machine.sms, most(o->tile)));
+  return GEMM_OK;
 }
 
 struct PairMaps {
@@ -217,63 +287,49 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.inject = inject;
   p.error_word = error_index(s);
 
-  // 128 x 128 tiles on single CTAs, or 256 x 256 on pairs: the form whose waves
-  // of tiles take fewer cycles.  A tile takes a single CTA about 1200 + 580 per
-  // 256 columns of k, and a pair 4500 + 500: four times the work in about the
-  // time, but with one accumulator, so that a tile's stores are not all hidden
-  // (8192^3: 261 us by single CTAs, 164 by pairs; 8192 x 4096 x 256: 16 and 24;
-  // 128 x 14336 x 4096 mxfp4: 7.8 and 10).  With groups by offsets the number of
-  // row tiles is not known here: a group is taken to end half way through its
-  // last.  Fitted to 200 shapes measured both ways: 0.5 % over the better form of
-  // each in the mean, at worst, where a tile more starts another wave, 30 % (1326
-  // rows of 18 groups, 3022 -> 958: 13.4 us where pairs take 10.1).
-  const auto cycles = [&](int64_t tile, int64_t slots, int64_t fixed, int64_t per_block) {
-    const int64_t live = std::min<int64_t>(a->groups, a->rows);
-    const int64_t row_tiles = a->offsets
-                                  ? std::max(live, (2 * a->rows + live * tile) / (2 * tile))
-                                  : a->groups * ((a->group_rows + tile - 1) / tile);
-    const int64_t tiles = row_tiles * ((n_out + tile - 1) / tile);
-    return (tiles + slots - 1) / slots * (fixed + per_block * p.num_kb);
-  };
-  const int64_t x_chunks =
-      tile_count(a->rows, a->groups, a->offsets != nullptr) * p.tile_chunks;
-  const int64_t w_chunks = static_cast<int64_t>(a->groups) * p.w_group_tiles * p.tile_chunks;
-  const bool pair = cycles(256, sms / 2, 4500, 500) < cycles(128, sms, 1200, 580) &&
-                    x_chunks <= INT_MAX && w_chunks <= INT_MAX;  // counted in 32 bits there
-  const int bm = pair ? 256 : 128, bn = bm;
-  p.m_tiles = static_cast<int32_t>((n_out + bm - 1) / bm);
-  // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile
-  // loads little more than it has (8 tokens over 64 experts: 21 us against 27
-  // with boxes of 128).
-  p.box_rows = a->offsets || a->group_rows <= 64 ? 32 : 128;
-  // One CTA per SM, fewer where there cannot be that many tiles.
-  const int64_t row_tiles = a->offsets ? a->rows / bn + std::min<int64_t>(a->groups, a->rows)
-                                       : a->groups * ((a->group_rows + bn - 1) / bn);
-  // counted in 32 bits, with room for a grid's stride past the last
-  if (row_tiles * p.m_tiles > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
-  const int units = static_cast<int>(std::min<int64_t>(pair ? sms / 2 : sms, row_tiles * p.m_tiles));
-  // rows of a tile, in the mean: of the groups that there can be
-  const int64_t tile_rows =
-      a->offsets ? (a->rows + a->groups - 1) / a->groups : std::min<int64_t>(a->group_rows, 128);
-  p.split = pair ? 1 : choose_split(row_tiles * p.m_tiles, tile_rows, p.num_kb, sms, device);
+  Plan plan;
+  rc = make_plan(a->rows, n_out, a->cols, a->format, a->groups, a->offsets != nullptr,
+                 machine_of(sms, device), &plan);
+  if (rc != GEMM_OK) return rc;
+  p.m_tiles = plan.m_tiles;
+  p.box_rows = plan.box_rows;
+  p.split = plan.split;
   PairMaps m;
   if ((rc = encode_codes(encode, &m.w, b, kGemmM)) != GEMM_OK ||
       (rc = encode_codes(encode, &m.x, a, p.box_rows)) != GEMM_OK)
     return rc;
-  if (pair && ((rc = encode_scales(encode, &m.sw, b, w_chunks)) != GEMM_OK ||
-               (rc = encode_scales(encode, &m.sx, a, x_chunks)) != GEMM_OK))
+  if (plan.pair && ((rc = encode_scales(encode, &m.sw, b, plan.w_chunks)) != GEMM_OK ||
+                    (rc = encode_scales(encode, &m.sx, a, plan.x_chunks)) != GEMM_OK))
     return rc;
   const auto go = [&](auto t, auto fmt) {
     using T = decltype(t);
-    if (pair) return launch_pair<T, fmt()>(m, p, units, device, s);
-    return p.split > 1 ? launch_single<T, fmt(), true>(m.w, m.x, p, units, device, s)
-                       : launch_single<T, fmt(), false>(m.w, m.x, p, units, device, s);
+    if (plan.pair) return launch_pair<T, fmt()>(m, p, plan.units, device, s);
+    return p.split > 1 ? launch_single<T, fmt(), true>(m.w, m.x, p, plan.units, device, s)
+                       : launch_single<T, fmt(), false>(m.w, m.x, p, plan.units, device, s);
   };
   const auto by_format = [&](auto t) {
     return a->format == FP4_NV ? go(t, std::integral_constant<int, FP4_NV>{})
                                : go(t, std::integral_constant<int, FP4_MX>{});
   };
   return type == MOE_F16 ? by_format(__half{}) : by_format(__nv_bfloat16{});
+}
+
+extern "C" int fp4_query_config(int64_t rows, int64_t n, int64_t cols, int format, int groups,
+                                int by_offsets, fp4_config_t* out) {
+  if (!out || rows < 1 || n < 1 || cols < 1 || !fits(rows, cols) || check_format(format) != GEMM_OK ||
+      groups < 1 || (by_offsets != 0 && by_offsets != 1) ||
+      (by_offsets ? groups > MOE_MAX_EXPERTS : rows % groups != 0) || n > INT_MAX / groups)
+    return GEMM_ERR_INVALID_VALUE;
+  Machine machine{152, {76, 36, 15}};
+  int sms = 0, device = 0;
+  if (require_device(&sms, &device) == GEMM_OK) machine = machine_of(sms, device);
+  else cudaGetLastError();
+  Plan plan;
+  const int rc = make_plan(rows, n, cols, format, groups, by_offsets != 0, machine, &plan);
+  if (rc != GEMM_OK) return rc;
+  *out = fp4_config_t{plan.pair ? 1 : 0, plan.split, plan.tile, plan.box_rows,
+                      plan.units * (plan.pair ? 2 : plan.split)};
+  return GEMM_OK;
 }
 
 extern "C" int fp4_get_device_error(void* stream, uint32_t* raw) {

@@ -23,10 +23,10 @@ if not os.path.exists(_build.BINDING):
 
 from .lib._experts import (  # noqa: E402,F401
     Fp4Matrix, Routing, fp4_dequantize, fp4_gemm_tn, fp4_get_device_error, fp4_quantize,
-    fp4_scale_bytes, moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward,
-    moe_pairs, moe_sort)
+    fp4_query_config, fp4_scale_bytes, moe_combine, moe_combine_backward, moe_dispatch,
+    moe_dispatch_backward, moe_pairs, moe_sort)
 
 # The C functions of moe_fp4.h.
 EXPORTED = ("fp4_code_bytes", "fp4_scale_bytes", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
-            "fp4_gemm_tn_ex", "fp4_get_device_error", "moe_sort", "moe_pairs", "moe_dispatch",
-            "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+            "fp4_gemm_tn_ex", "fp4_query_config", "fp4_get_device_error", "moe_sort", "moe_pairs",
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
