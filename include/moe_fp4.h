@@ -108,7 +108,8 @@ int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* stream);
  *      same format and cols as a;
  *   D  a->rows x N of `type`, contiguous, 2-byte aligned, overlapping neither.
  * Rows of `a` in no group give zeros.  cols == 0 gives zeros.  alpha *
- * 2^(a's exponent + b's) is held in fp32 and has to be finite there.
+ * 2^(a's exponent + b's) has to be finite in fp32; it is rounded to fp32's 24 bits,
+ * below its normal numbers too.
  * A pipeline wait that ran out (2 s) is reported by fp4_get_device_error().
  */
 int fp4_gemm_tn(void* D, int type, const fp4_matrix_t* a, const fp4_matrix_t* b, float alpha,

@@ -282,7 +282,12 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.num_kb = static_cast<int32_t>(col_stages(a->cols));
   p.w_group_tiles = static_cast<int32_t>((n_out + kTileRows - 1) / kTileRows);
   p.tile_chunks = p.num_kb * chunks_per_stage(a->format);
-  p.alpha = static_cast<float>(scale);  // one rounding, whatever the exponents' order
+  // One rounding, whatever the exponents' order.  Below fp32's normal numbers the
+  // factor would lose bits or be zero where the results need not be (sums reach
+  // 2^46): then it is applied in two steps, 2^120 times the factor and 2^-120.
+  const bool tiny = std::fabs(scale) < std::ldexp(1.0, -126);
+  p.pre = tiny ? static_cast<float>(std::ldexp(scale, 120)) : 1.0f;
+  p.alpha = tiny ? power_of_two(-120) : static_cast<float>(scale);
   p.timeout_ns = timeout_ns ? timeout_ns : kTimeoutNs;
   p.inject = inject;
   p.error_word = error_index(s);

@@ -69,7 +69,7 @@ struct Fp4GemmParams {
   int32_t box_rows;        // activation rows per TMA box
   int32_t stages;
   int32_t split;           // CTAs that share a tile's k; 1: none do
-  float alpha;
+  float pre, alpha;        // the sums' factor, in two where fp32 has no normal number for it
   uint64_t timeout_ns;
   int32_t inject;          // 1: leave out each CTA's first loads
   int32_t error_word;      // where this call's errors go
@@ -328,8 +328,9 @@ __device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
 // by `release`, and stored; a lane is an output n, so a store of the warp
 // writes 32 neighbouring outputs of one row.
 template <typename T, int kStep, typename Release>
-__device__ __forceinline__ void store_tile(uint32_t t_row, int first, int count, float alpha,
-                                           uint16_t* d, bool live, int64_t n_out, Release release) {
+__device__ __forceinline__ void store_tile(uint32_t t_row, int first, int count,
+                                           const Fp4GemmParams& p, uint16_t* d, bool live,
+                                           Release release) {
   constexpr int kMine = 4;
   uint32_t r[kMine][32];
 #pragma unroll
@@ -338,22 +339,28 @@ __device__ __forceinline__ void store_tile(uint32_t t_row, int first, int count,
       tmem_ld_32x32b_x32(t_row + 32 * (kStep * c + first), r[c]);
   tmem_ld_wait();
   release();
+  if (p.pre != 1.0f) {
+#pragma unroll
+    for (int c = 0; c < kMine; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[c][i] = __float_as_uint(p.pre * __uint_as_float(r[c][i]));
+  }
 #pragma unroll
   for (int c = 0; c < kMine; ++c)
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      r[c][i] = pack_two<T>(alpha * __uint_as_float(r[c][2 * i]),
-                            alpha * __uint_as_float(r[c][2 * i + 1]));
+      r[c][i] = pack_two<T>(p.alpha * __uint_as_float(r[c][2 * i]),
+                            p.alpha * __uint_as_float(r[c][2 * i + 1]));
   if (!live) return;
 #pragma unroll
   for (int c = 0; c < kMine; ++c) {
     const int col = 32 * (kStep * c + first);
     if (col >= count) break;
-    uint16_t* to = d + col * n_out;
+    uint16_t* to = d + col * p.n_out;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       if (col + i < count) *to = static_cast<uint16_t>(r[c][i >> 1] >> (16 * (i & 1)));
-      to += n_out;
+      to += p.n_out;
     }
   }
 }
@@ -408,6 +415,10 @@ __device__ __forceinline__ void store_split_tile(uint32_t t_row, int out, int ha
                      : "memory");
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] += v[i];
+      }
+      if (p.pre != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] *= p.pre;
       }
       const uint32_t w[2] = {pack_two<T>(p.alpha * sum[0], p.alpha * sum[1]),
                              pack_two<T>(p.alpha * sum[2], p.alpha * sum[3])};
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             abort_flag, d, n < p.n_out);
         continue;
       }
-      store_tile<T, 1>(t_row, 0, tile.count, p.alpha, d, n < p.n_out, p.n_out, [&] {
+      store_tile<T, 1>(t_row, 0, tile.count, p, d, n < p.n_out, [&] {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty_bar(acc));

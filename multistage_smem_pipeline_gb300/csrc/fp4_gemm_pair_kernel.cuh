@@ -314,12 +314,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       const int64_t n = static_cast<int64_t>(tile.m) * (2 * kGemmM) + rank * kGemmM + q * 32 + lane;
-      store_tile<T, 2>(tmem + (static_cast<uint32_t>(q * 32) << 16), half, tile.count, p.alpha,
-                         p.d + tile.x_row * p.n_out + n, n < p.n_out, p.n_out, [&] {
-                           tc_fence_before_sync();
-                           __syncwarp();
-                           if (lane == 0) mbar_arrive_cluster(leader_tempty);
-                         });
+      store_tile<T, 2>(tmem + (static_cast<uint32_t>(q * 32) << 16), half, tile.count, p,
+                       p.d + tile.x_row * p.n_out + n, n < p.n_out, [&] {
+                         tc_fence_before_sync();
+                         __syncwarp();
+                         if (lane == 0) mbar_arrive_cluster(leader_tempty);
+                       });
       acc_phase ^= 1u;
     }
     zero_tail(p, start);
