@@ -203,6 +203,9 @@ struct Fp4Matrix {
   // Everything but the pointers.
   void describe(int64_t rows, int64_t cols, int format, int64_t exponent,
                 std::optional<int64_t> group_rows, const RoutingPtr& r) {
+    if (exponent != static_cast<int32_t>(exponent))  // the C functions check the rest
+      value_error("exponent " + std::to_string(exponent) + " is out of range");
+    if (rows > INT32_MAX) value_error(std::to_string(rows) + " rows are too many");
     c.rows = rows;
     c.cols = cols;
     c.format = format;
@@ -249,7 +252,8 @@ MatrixPtr given_matrix(const at::Tensor& codes, const at::Tensor& scales, int64_
     value_error("codes and scales must be CUDA tensors on one device");
   if (!codes.is_contiguous() || !scales.is_contiguous())
     value_error("codes and scales must be contiguous");
-  if (codes.dim() != 2 || cols < 0) value_error("codes must be a matrix of 0 or more columns");
+  if (codes.dim() != 2 || cols < 0 || cols > FP4_MAX_COLS)
+    value_error("codes must be a matrix of 0 to " + std::to_string(FP4_MAX_COLS) + " columns");
   auto m = std::make_shared<Fp4Matrix>();
   m->describe(codes.size(0), cols, fmt, exponent, group_rows, routing);
   if (codes.size(1) != m->pitch)
@@ -280,11 +284,13 @@ MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t expon
     if (routing->device() != x.device()) value_error("x and the routing are on different devices");
     rows = routing->slots();
   }
-  const On on(x.device(), stream);
   MatrixPtr m = out;
   if (!m) {
     m = std::make_shared<Fp4Matrix>();
     m->describe(rows, cols, fmt, exponent, group_rows, routing);
+  }
+  const On on(x.device(), stream);
+  if (!out) {
     const int64_t scales = m->tiles * m->chunks * 512;
     m->buffer = fresh({scales + rows * m->pitch}, at::kByte, x.device());
     m->device = x.device();

@@ -1,0 +1,37 @@
+"""Checks of the compiled binding that need GPU tensors but no GPU: they are made on tensors that
+only say where they are."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+
+@pytest.fixture(scope="module")
+def ex():
+    from multistage_smem_pipeline_gb300 import build
+    build.build()
+    from multistage_smem_pipeline_gb300 import experts
+    return experts
+
+
+def fake(*sizes, dtype, device="cuda:0"):
+    with FakeTensorMode():
+        return torch.empty(*sizes, dtype=dtype, device=device)
+
+
+def stored(rows=4, device="cuda:0"):
+    """Codes and scales of a rows x 64 nvfp4 matrix, with scales enough for any routing of them."""
+    return (fake(rows, 32, dtype=torch.uint8, device=device),
+            fake(1 << 16, dtype=torch.uint8, device=device))
+
+
+def test_numbers_are_not_cut_to_32_bits(ex):
+    codes, scales = stored()
+    assert ex.Fp4Matrix(codes, scales, cols=64, exponent=-7).exponent == -7
+    for exponent in (2**32, 2**32 - 3, -2**32, 2**40 + 5, 2**63 - 1):
+        with pytest.raises(ValueError, match="exponent"):
+            ex.Fp4Matrix(codes, scales, cols=64, exponent=exponent)
+    for cols in (2**23 + 1, 2**62, 2**63 - 1):
+        with pytest.raises(ValueError, match="columns"):
+            ex.Fp4Matrix(codes, scales, cols=cols)
+    with pytest.raises(ValueError, match="exponent"):
+        ex.fp4_quantize(fake(4, 64, dtype=torch.float16), exponent=2**32)
