@@ -146,6 +146,12 @@ struct Routing {
 };
 using RoutingPtr = std::shared_ptr<Routing>;
 
+// A routing's arrays are where the tensor is that they speak of.
+void same_device(const at::Device& device, const RoutingPtr& r, const char* what) {
+  if (r && r->device() != device)
+    value_error(std::string(what) + " and the routing are on different devices");
+}
+
 RoutingPtr given_routing(const at::Tensor& offsets, const at::Tensor& rows,
                          const at::Tensor& ids) {
   for (const at::Tensor* t : {&offsets, &rows, &ids})
@@ -252,6 +258,7 @@ MatrixPtr given_matrix(const at::Tensor& codes, const at::Tensor& scales, int64_
     value_error("codes and scales must be CUDA tensors on one device");
   if (!codes.is_contiguous() || !scales.is_contiguous())
     value_error("codes and scales must be contiguous");
+  same_device(codes.device(), routing, "codes");
   if (codes.dim() != 2 || cols < 0 || cols > FP4_MAX_COLS)
     value_error("codes must be a matrix of 0 to " + std::to_string(FP4_MAX_COLS) + " columns");
   auto m = std::make_shared<Fp4Matrix>();
@@ -281,7 +288,7 @@ MatrixPtr quantize(const at::Tensor& x, const std::string& format, int64_t expon
     if (rows != routing->c.tokens)
       value_error("x has " + std::to_string(rows) + " rows, the routing " +
                   std::to_string(routing->c.tokens) + " tokens");
-    if (routing->device() != x.device()) value_error("x and the routing are on different devices");
+    same_device(x.device(), routing, "x");
     rows = routing->slots();
   }
   MatrixPtr m = out;

@@ -35,3 +35,21 @@ def test_numbers_are_not_cut_to_32_bits(ex):
             ex.Fp4Matrix(codes, scales, cols=cols)
     with pytest.raises(ValueError, match="exponent"):
         ex.fp4_quantize(fake(4, 64, dtype=torch.float16), exponent=2**32)
+
+
+def routing(ex, device, experts=3, tokens=2, top_k=2):
+    def ints(*sizes):
+        return fake(*sizes, dtype=torch.int32, device=device)
+    return ex.Routing(ints(experts + 1), ints(tokens, top_k), ints(tokens, top_k))
+
+
+def test_a_routing_of_another_device_is_refused(ex):
+    """A kernel would read the other GPU's offsets."""
+    codes, scales = stored()
+    assert ex.Fp4Matrix(codes, scales, cols=64, routing=routing(ex, "cuda:0")).groups == 3
+    with pytest.raises(ValueError, match="different devices"):
+        ex.Fp4Matrix(codes, scales, cols=64, routing=routing(ex, "cuda:1"))
+    with pytest.raises(ValueError, match="different devices"):
+        ex.fp4_quantize(fake(2, 64, dtype=torch.float16), routing=routing(ex, "cuda:1"))
+    with pytest.raises(ValueError, match="one device"):
+        ex.Fp4Matrix(codes, stored(device="cuda:1")[1], cols=64)
