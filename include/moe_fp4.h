@@ -134,9 +134,10 @@ typedef struct {
 int fp4_query_config(int64_t rows, int64_t n, int64_t cols, int format, int groups, int by_offsets,
                      fp4_config_t* out);
 
-/* Waits for `stream`, then reads and clears its error word of fp4_gemm_tn:
- * GEMM_OK or GEMM_ERR_TIMEOUT; `raw` (may be NULL) gets code | site << 8.
- * Streams have a word each up to 63 of them, beyond that they share. */
+/* Waits for `stream`, a stream of the current device, then reads and clears its
+ * error word of fp4_gemm_tn on that device: GEMM_OK or GEMM_ERR_TIMEOUT; `raw`
+ * (may be NULL) gets code | site << 8.  Streams have a word each up to 63 of
+ * them, beyond that they share. */
 int fp4_get_device_error(void* stream, uint32_t* raw);
 
 /*

@@ -337,7 +337,11 @@ at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::
   return d;
 }
 
+// On the stream's own device.
 py::tuple device_error(const py::object& stream) {
+  std::optional<c10::cuda::CUDAGuard> device;
+  if (!stream.is_none() && py::hasattr(stream, "device"))
+    device.emplace(stream.attr("device").cast<at::Device>());
   void* const s = stream.is_none()
                       ? static_cast<void*>(c10::cuda::getCurrentCUDAStream().stream())
                       : reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());

@@ -53,3 +53,19 @@ def test_a_routing_of_another_device_is_refused(ex):
         ex.fp4_quantize(fake(2, 64, dtype=torch.float16), routing=routing(ex, "cuda:1"))
     with pytest.raises(ValueError, match="one device"):
         ex.Fp4Matrix(codes, stored(device="cuda:1")[1], cols=64)
+
+
+def test_the_error_word_is_the_stream_s_device_s(ex):
+    """The word of the stream's own device is read, not the current one's."""
+    class Stream:
+        cuda_stream = 0
+        asked = 0
+
+        @property
+        def device(self):
+            Stream.asked += 1
+            return torch.device("cuda", 63)      # there is none such
+
+    with pytest.raises(RuntimeError):
+        ex.fp4_get_device_error(Stream())
+    assert Stream.asked
