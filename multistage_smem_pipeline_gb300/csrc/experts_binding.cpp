@@ -337,7 +337,7 @@ at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::
   return d;
 }
 
-// On the stream's own device.
+// On the stream's own device; other threads of the interpreter run meanwhile.
 py::tuple device_error(const py::object& stream) {
   std::optional<c10::cuda::CUDAGuard> device;
   if (!stream.is_none() && py::hasattr(stream, "device"))
@@ -346,7 +346,11 @@ py::tuple device_error(const py::object& stream) {
                       ? static_cast<void*>(c10::cuda::getCurrentCUDAStream().stream())
                       : reinterpret_cast<void*>(stream.attr("cuda_stream").cast<uintptr_t>());
   uint32_t raw = 0;
-  const int status = fp4_get_device_error(s, &raw);
+  int status = 0;
+  {
+    const py::gil_scoped_release released;
+    status = fp4_get_device_error(s, &raw);
+  }
   return py::make_tuple(status, raw);
 }
 

@@ -69,3 +69,20 @@ def test_the_error_word_is_the_stream_s_device_s(ex):
     with pytest.raises(RuntimeError):
         ex.fp4_get_device_error(Stream())
     assert Stream.asked
+
+
+@pytest.mark.gpu
+def test_other_threads_run_while_the_stream_is_waited_for(ex):
+    import threading
+    import time
+    s = torch.cuda.Stream()
+    assert ex.fp4_get_device_error(s) == (0, 0)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(600_000_000)           # 0.3 s or so
+    waiter = threading.Thread(target=ex.fp4_get_device_error, args=(s,))
+    waiter.start()
+    steps = 0
+    while waiter.is_alive():
+        time.sleep(0.005)
+        steps += 1
+    assert steps > 10
