@@ -4,7 +4,8 @@
  * same library and with the same conventions: plain C, device pointers on the
  * current device, asynchronous on `stream`, a gemm_status_t value returned,
  * arguments checked on the host before anything is launched, no device memory
- * allocated, every buffer owned by the caller.
+ * allocated, every buffer owned by the caller.  What a call writes overlaps
+ * nothing else of it: no matrix, no weights, none of the routing's arrays.
  *
  * Formats.  Rows are cut into blocks of neighbouring elements that share a
  * scale.  An element is E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.

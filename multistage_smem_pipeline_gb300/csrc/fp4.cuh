@@ -83,6 +83,10 @@ inline uint64_t scale_bytes(const fp4_matrix_t* m) {
          tile_bytes(m->cols, m->format);
 }
 
+inline uint64_t offset_bytes(const fp4_matrix_t* m) {
+  return (static_cast<uint64_t>(m->groups) + 1) * sizeof(int32_t);
+}
+
 inline float power_of_two(int e) {  // |e| <= 126
   const uint32_t bits = static_cast<uint32_t>(e + 127) << 23;
   float f;

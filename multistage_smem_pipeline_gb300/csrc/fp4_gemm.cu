@@ -256,8 +256,10 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   if (!aligned_to(D, 2)) return GEMM_ERR_MISALIGNED;
   const uint64_t dbytes = static_cast<uint64_t>(a->rows) * n_out * 2;
   for (const fp4_matrix_t* m : {a, b})
-    if (m->cols > 0 && (overlaps(D, dbytes, m->codes, code_bytes(m)) ||
-                        overlaps(D, dbytes, m->scales, scale_bytes(m))))
+    if (any_overlap({{D, dbytes, true},
+                     {m->codes, code_bytes(m), false},
+                     {m->scales, scale_bytes(m), false},
+                     {m->offsets, offset_bytes(m), false}}))
       return GEMM_ERR_INVALID_VALUE;
   int sms = 0, device = 0;
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;

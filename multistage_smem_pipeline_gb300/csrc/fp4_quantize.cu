@@ -471,9 +471,10 @@ extern "C" int fp4_quantize(const fp4_matrix_t* out, const void* x, int64_t ldx,
   if (!x) return GEMM_ERR_INVALID_VALUE;
   if (!aligned_to(x, 2)) return GEMM_ERR_MISALIGNED;
   const uint64_t xbytes = (static_cast<uint64_t>(x_rows - 1) * ldx + out->cols) * 2;
-  if (overlaps(x, xbytes, out->codes, code_bytes(out)) ||
-      overlaps(x, xbytes, out->scales, scale_bytes(out)) ||
-      overlaps(out->codes, code_bytes(out), out->scales, scale_bytes(out)))
+  if (any_overlap({{x, xbytes, false},
+                   {out->codes, code_bytes(out), true},
+                   {out->scales, scale_bytes(out), true}},
+                  routing))
     return GEMM_ERR_INVALID_VALUE;
   int sms = 0;
   if ((rc = require_device(&sms)) != GEMM_OK) return rc;
@@ -506,8 +507,10 @@ extern "C" int fp4_dequantize(void* y, int type, const fp4_matrix_t* in, void* s
   if (!y) return GEMM_ERR_INVALID_VALUE;
   if (!aligned_to(y, 2)) return GEMM_ERR_MISALIGNED;
   const uint64_t ybytes = static_cast<uint64_t>(in->rows) * in->cols * 2;
-  if (overlaps(y, ybytes, in->codes, code_bytes(in)) ||
-      overlaps(y, ybytes, in->scales, scale_bytes(in)))
+  if (any_overlap({{y, ybytes, true},
+                   {in->codes, code_bytes(in), false},
+                   {in->scales, scale_bytes(in), false},
+                   {in->offsets, offset_bytes(in), false}}))
     return GEMM_ERR_INVALID_VALUE;
   int sms = 0;
   if ((rc = require_device(&sms)) != GEMM_OK) return rc;

@@ -9,6 +9,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "host.cuh"
 #include "moe_fp4.h"
@@ -33,6 +34,34 @@ inline int check_routing(const moe_routing_t* r) {
   if (!aligned_to(r->offsets, 4) || !aligned_to(r->rows, 4) || !aligned_to(r->ids, 4))
     return GEMM_ERR_MISALIGNED;
   return GEMM_OK;
+}
+
+// An array of a call, and whether the call writes it.
+struct Range {
+  const void* ptr;
+  uint64_t bytes;
+  bool written;
+};
+
+// Whether a written array overlaps any other, the routing's (which later calls
+// still read) among them.  Absent and empty ones overlap nothing.
+inline bool any_overlap(std::initializer_list<Range> arrays, const moe_routing_t* r = nullptr) {
+  const auto meet = [](const Range& a, const Range& b) {
+    return a.ptr && b.ptr && a.bytes && b.bytes && overlaps(a.ptr, a.bytes, b.ptr, b.bytes);
+  };
+  Range of_routing[2] = {};
+  if (r) {
+    of_routing[0] = {r->offsets, (static_cast<uint64_t>(r->experts) + 1) * 4, false};
+    of_routing[1] = {r->rows, static_cast<uint64_t>(r->tokens) * r->top_k * 4, false};
+  }
+  for (const Range& a : arrays) {
+    if (!a.written) continue;
+    for (const Range& b : arrays)
+      if (&a != &b && meet(a, b)) return true;
+    for (const Range& b : of_routing)
+      if (meet(a, b)) return true;
+  }
+  return false;
 }
 
 // A launch with programmatic dependent launch: the kernel's set-up may overlap

@@ -356,33 +356,44 @@ bool rows_aligned(std::initializer_list<const void*> ptrs, int64_t hidden, int64
   return hidden % 8 == 0 && ld % 8 == 0;
 }
 
-// Checks common to the row movers: `per_slot` matrices have tokens * top_k rows.
+// The matrices of the row movers: `per_slot` ones have tokens * top_k rows.
 struct Operand {
   const void* ptr;
   bool per_slot, written, optional;
+
+  Range range(const moe_routing_t* r, int64_t hidden, int64_t ldx) const {
+    uint64_t bytes = 0;
+    if (r->tokens > 0 && hidden > 0)
+      bytes = per_slot ? static_cast<uint64_t>(r->tokens) * r->top_k * hidden * 2
+                       : (static_cast<uint64_t>(r->tokens - 1) * (written ? hidden : ldx) + hidden) * 2;
+    return {ptr, bytes, written};
+  }
 };
 
-int check_rows(std::initializer_list<Operand> ops, int64_t hidden, int64_t ldx, int type,
+// Checks common to them; `weights` and their gradient may be absent.
+int check_rows(const Operand& a, const Operand& b, const Operand& c, const void* weights,
+               const void* grad_weights, int64_t hidden, int64_t ldx, int type,
                const moe_routing_t* r) {
   int rc = check_routing(r);
   if (rc != GEMM_OK) return rc;
   if (!valid_type(type) || hidden < 0 || hidden > MOE_MAX_HIDDEN || ldx < hidden || ldx > INT_MAX)
     return GEMM_ERR_INVALID_VALUE;
-  if (r->tokens == 0 || hidden == 0) return GEMM_OK;
-  const auto bytes = [&](const Operand& o) {
-    if (o.per_slot) return static_cast<uint64_t>(r->tokens) * r->top_k * hidden * 2;
-    return (static_cast<uint64_t>(r->tokens - 1) * (o.written ? hidden : ldx) + hidden) * 2;
-  };
-  for (const Operand& o : ops)
-    if (!o.ptr && !o.optional) return GEMM_ERR_INVALID_VALUE;
-  for (const Operand& o : ops)
-    if (!aligned_to(o.ptr, 2)) return GEMM_ERR_MISALIGNED;
-  for (const Operand& o : ops)
-    for (const Operand& q : ops)
-      if (&o != &q && o.written && o.ptr && q.ptr && overlaps(o.ptr, bytes(o), q.ptr, bytes(q)))
-        return GEMM_ERR_INVALID_VALUE;
+  for (const Operand* o : {&a, &b, &c}) {
+    if (r->tokens == 0 || hidden == 0) break;
+    if (!o->ptr && !o->optional) return GEMM_ERR_INVALID_VALUE;
+  }
+  for (const Operand* o : {&a, &b, &c}) {
+    if (r->tokens == 0 || hidden == 0) break;
+    if (!aligned_to(o->ptr, 2)) return GEMM_ERR_MISALIGNED;
+  }
+  const uint64_t slots = static_cast<uint64_t>(r->tokens) * r->top_k;
+  if (any_overlap({a.range(r, hidden, ldx), b.range(r, hidden, ldx), c.range(r, hidden, ldx),
+                   {weights, 4 * slots, false}, {grad_weights, 4 * slots, true}}, r))
+    return GEMM_ERR_INVALID_VALUE;
   return GEMM_OK;
 }
+
+constexpr Operand kNone{nullptr, false, false, true};
 
 RouteParams route_params(const moe_routing_t* r, int64_t hidden) {
   return RouteParams{r->offsets, r->rows,    r->tokens,
@@ -398,7 +409,8 @@ unsigned slot_blocks(const moe_routing_t* r) {
 template <bool kWeighted>
 int run_combine(void* out, const void* y, const float* weights, int64_t hidden, int type,
                 const moe_routing_t* r, cudaStream_t s) {
-  int rc = check_rows({{out, false, true, false}, {y, true, false, false}}, hidden, hidden, type, r);
+  int rc = check_rows({out, false, true, false}, {y, true, false, false}, kNone, weights, nullptr,
+                      hidden, hidden, type, r);
   if (rc != GEMM_OK) return rc;
   if (r->tokens == 0 || hidden == 0) return GEMM_OK;
   if (kWeighted && !weights) return GEMM_ERR_INVALID_VALUE;
@@ -444,8 +456,7 @@ extern "C" int moe_sort(int32_t* offsets, int32_t* rows, const int32_t* ids, int
     return GEMM_ERR_MISALIGNED;
   const uint64_t bytes = static_cast<uint64_t>(tokens) * top_k * 4;
   const uint64_t offset_bytes = (static_cast<uint64_t>(experts) + 1) * 4;
-  if (tokens > 0 && (overlaps(rows, bytes, ids, bytes) || overlaps(offsets, offset_bytes, ids, bytes) ||
-                     overlaps(offsets, offset_bytes, rows, bytes)))
+  if (any_overlap({{rows, bytes, true}, {offsets, offset_bytes, true}, {ids, bytes, false}}))
     return GEMM_ERR_INVALID_VALUE;
   int device = 0;
   const int rc = require_device(nullptr, &device);
@@ -470,7 +481,7 @@ extern "C" int moe_pairs(int32_t* pairs, const moe_routing_t* r, void* stream) {
   if (!pairs) return GEMM_ERR_INVALID_VALUE;
   if (!aligned_to(pairs, 4)) return GEMM_ERR_MISALIGNED;
   const int n = static_cast<int>(r->tokens * r->top_k);
-  if (overlaps(pairs, 4ull * n, r->rows, 4ull * n)) return GEMM_ERR_INVALID_VALUE;
+  if (any_overlap({{pairs, 4ull * n, true}}, r)) return GEMM_ERR_INVALID_VALUE;
   if ((rc = require_device(nullptr)) != GEMM_OK) return rc;
   return launch_pdl(pairs_kernel, dim3(static_cast<unsigned>((n + kRowThreads - 1) / kRowThreads)),
                     dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), 1u, pairs, r->rows, n);
@@ -478,7 +489,8 @@ extern "C" int moe_pairs(int32_t* pairs, const moe_routing_t* r, void* stream) {
 
 extern "C" int moe_dispatch(void* y, const void* x, int64_t ldx, int64_t hidden, int type,
                             const moe_routing_t* r, void* stream) {
-  int rc = check_rows({{y, true, true, false}, {x, false, false, false}}, hidden, ldx, type, r);
+  int rc = check_rows({y, true, true, false}, {x, false, false, false}, kNone, nullptr, nullptr,
+                      hidden, ldx, type, r);
   if (rc != GEMM_OK) return rc;
   if (r->tokens == 0 || hidden == 0) return GEMM_OK;
   int sms = 0;
@@ -511,10 +523,8 @@ extern "C" int moe_combine(void* out, const void* y, const float* weights, int64
 extern "C" int moe_combine_backward(void* grad_y, float* grad_weights, const void* grad_out,
                                     const void* y, const float* weights, int64_t hidden, int type,
                                     const moe_routing_t* r, void* stream) {
-  int rc = check_rows({{grad_y, true, true, true},
-                       {grad_out, false, false, false},
-                       {y, true, false, false}},
-                      hidden, hidden, type, r);
+  int rc = check_rows({grad_y, true, true, true}, {grad_out, false, false, false},
+                      {y, true, false, false}, weights, grad_weights, hidden, hidden, type, r);
   if (rc != GEMM_OK) return rc;
   const int64_t n = r->tokens * r->top_k;
   if (n == 0 || (!grad_y && !grad_weights)) return GEMM_OK;
