@@ -14,11 +14,20 @@ the program computes itself (here a 16-bit scale per expert, to keep the example
 from __future__ import annotations
 
 import argparse
+import math
 
 import torch
 
 from . import (Fp4Matrix, Routing, fp4_gemm_tn, fp4_quantize, moe_combine, moe_combine_backward,
                moe_dispatch, moe_dispatch_backward, moe_sort)
+
+
+def exponent_for(x: torch.Tensor) -> int:
+    """The exponent of an nvfp4 matrix: the largest block maximum / 6 just within E4M3's 448."""
+    top = float(x.abs().amax()) if x.numel() else 0.0
+    if not math.isfinite(top):
+        raise ValueError("values must be finite")
+    return min(max(math.ceil(math.log2(top / (6 * 448))), -100), 100) if top > 0 else 0
 
 
 class ExpertProjection:
@@ -27,11 +36,7 @@ class ExpertProjection:
     def __init__(self, weights: torch.Tensor, format: str = "nvfp4"):
         experts, out, hidden = weights.shape
         self.experts, self.out = experts, out
-        # one exponent for all weights: the largest block maximum / 6 just below E4M3's 448
-        exponent = 0
-        if format == "nvfp4":
-            top = max(float(weights.abs().amax()), 1e-30)
-            exponent = int(torch.tensor(top / (6 * 448)).log2().ceil())
+        exponent = exponent_for(weights) if format == "nvfp4" else 0
         self.format = format
         self.weights: Fp4Matrix = fp4_quantize(weights.reshape(experts * out, hidden), format=format,
                                                exponent=exponent, group_rows=out)

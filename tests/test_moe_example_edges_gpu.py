@@ -1,0 +1,41 @@
+"""The example's edges: weights without a scale of their own, activations far from 1, and what
+autograd is told (GPU)."""
+import pytest
+import torch
+
+import fp4_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ex():
+    from multistage_smem_pipeline_gb300 import moe_example
+    return moe_example
+
+
+def one_expert(layer, x):
+    """Every token to expert 0 with weight 1."""
+    n = x.shape[0]
+    return layer(x, torch.zeros(n, 1, dtype=torch.int32, device="cuda"), torch.ones(n, 1, device="cuda"))
+
+
+@pytest.mark.parametrize("form", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -110, 2.0 ** -90, 1.0, 2.0 ** 90])
+def test_weights_of_any_size(ex, form, scale):
+    """All zero, so small that the least exponent has to do, and large."""
+    g = torch.Generator().manual_seed(1)
+    w = (torch.randn(2, 40, 64, generator=g) * scale).bfloat16().cuda()
+    x = torch.randn(5, 64, generator=g).bfloat16().cuda()
+    layer = ex.ExpertProjection(w, form)
+    assert -100 <= layer.weights.exponent <= 100
+    got = ref.to_numpy(one_expert(layer, x))
+    a = ref.values(ref.to_numpy(x), form)
+    b = ref.values(ref.to_numpy(w[0]), form, layer.weights.exponent)
+    want = a @ b.T
+    tol = ref.product_tolerance(want, abs(a) @ abs(b).T, 64, torch.bfloat16)
+    tol += ref.half_unit(abs(want) + tol, torch.bfloat16)         # rounded again by combine
+    assert (abs(got - want) <= tol).all()
+    assert got.any() == want.any()
+    with pytest.raises(ValueError):
+        ex.ExpertProjection(torch.full_like(w, float("inf")), "nvfp4")
