@@ -31,20 +31,24 @@ def exponent_for(x: torch.Tensor) -> int:
 
 
 class ExpertProjection:
-    """experts x out x hidden weights (float16 or bfloat16) kept in 4 bits."""
+    """experts x out x hidden weights (float16 or bfloat16) kept in 4 bits.
 
-    def __init__(self, weights: torch.Tensor, format: str = "nvfp4"):
+    activation_exponent: of the activations in nvfp4 (exponent_for a sample of them).  With 0,
+    blocks of 16 whose largest element is below 6 * 2^-10 are zero, and values above 2688 are cut.
+    """
+
+    def __init__(self, weights: torch.Tensor, format: str = "nvfp4", activation_exponent: int = 0):
         experts, out, hidden = weights.shape
         self.experts, self.out = experts, out
         exponent = exponent_for(weights) if format == "nvfp4" else 0
-        self.format = format
+        self.format, self.activation_exponent = format, activation_exponent
         self.weights: Fp4Matrix = fp4_quantize(weights.reshape(experts * out, hidden), format=format,
                                                exponent=exponent, group_rows=out)
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor) -> torch.Tensor:
         """x: tokens x hidden; ids, gates: tokens x top_k experts (int32) and weights (float32)."""
         routing = moe_sort(ids, self.experts)
-        rows = fp4_quantize(x, format=self.format, routing=routing)
+        rows = fp4_quantize(x, format=self.format, exponent=self.activation_exponent, routing=routing)
         y = fp4_gemm_tn(rows, self.weights, dtype=x.dtype)
         return moe_combine(y, routing, gates)
 

@@ -39,3 +39,24 @@ def test_weights_of_any_size(ex, form, scale):
     assert got.any() == want.any()
     with pytest.raises(ValueError):
         ex.ExpertProjection(torch.full_like(w, float("inf")), "nvfp4")
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1e-7, 1e6])
+def test_activations_of_any_size(ex, scale):
+    """With exponent 0 blocks below 6 x 2^-10 are zero and those above 2688 cut: the layer takes the
+    activations' exponent, found on a sample of them."""
+    g = torch.Generator().manual_seed(2)
+    w = (torch.randn(2, 40, 64, generator=g) * 0.1).bfloat16().cuda()
+    x = (torch.randn(50, 64, generator=g) * scale).bfloat16().cuda()
+    exponent = ex.exponent_for(x)
+    layer = ex.ExpertProjection(w, activation_exponent=exponent)
+    got = ref.to_numpy(one_expert(layer, x))
+    a = ref.values(ref.to_numpy(x), "nvfp4", exponent)
+    b = ref.values(ref.to_numpy(w[0]), "nvfp4", layer.weights.exponent)
+    want = a @ b.T
+    tol = ref.product_tolerance(want, abs(a) @ abs(b).T, 64, torch.bfloat16)
+    tol += ref.half_unit(abs(want) + tol, torch.bfloat16)
+    assert (abs(got - want) <= tol).all()
+    # the largest element is 6 scales, whose rounding is 2^-4 at most: not zero, and not cut
+    largest = abs(ref.to_numpy(x)).max()
+    assert abs(abs(a).max() - largest) <= 2.0 ** -4 * largest
