@@ -17,6 +17,7 @@ import argparse
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (Fp4Matrix, Routing, fp4_gemm_tn, fp4_quantize, moe_combine, moe_combine_backward,
                moe_dispatch, moe_dispatch_backward, moe_sort)
@@ -60,6 +61,7 @@ class _Dispatch(torch.autograd.Function):
         return moe_dispatch(x, routing)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y):
         return moe_dispatch_backward(grad_y.contiguous(), ctx.routing), None
 
@@ -72,6 +74,7 @@ class _Combine(torch.autograd.Function):
         return moe_combine(y, routing, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         y, weights = ctx.saved_tensors
         grad_y, grad_w = moe_combine_backward(grad_out.contiguous(), y, ctx.routing, weights)
@@ -79,12 +82,12 @@ class _Combine(torch.autograd.Function):
 
 
 def dispatch(x: torch.Tensor, routing: Routing) -> torch.Tensor:
-    """moe_dispatch with its gradient."""
+    """moe_dispatch with its gradient (of first order)."""
     return _Dispatch.apply(x, routing)
 
 
 def combine(y: torch.Tensor, routing: Routing, weights: torch.Tensor) -> torch.Tensor:
-    """moe_combine with its gradients."""
+    """moe_combine with its gradients (of first order)."""
     return _Combine.apply(y, weights, routing)
 
 

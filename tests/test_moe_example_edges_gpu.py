@@ -60,3 +60,19 @@ def test_activations_of_any_size(ex, scale):
     # the largest element is 6 scales, whose rounding is 2^-4 at most: not zero, and not cut
     largest = abs(ref.to_numpy(x)).max()
     assert abs(abs(a).max() - largest) <= 2.0 ** -4 * largest
+
+
+def test_second_order_is_refused(ex):
+    """The gradients are not differentiable themselves, and say so instead of losing terms."""
+    import multistage_smem_pipeline_gb300 as lib
+    r = lib.moe_sort(torch.tensor([[0, 1], [1, -1], [0, 0]], dtype=torch.int32, device="cuda"), 2)
+    x = torch.randn(3, 16, device="cuda").half().requires_grad_()
+    w = torch.rand(3, 2, device="cuda").requires_grad_()
+    for wrt in (x, w):
+        out = ex.combine(ex.dispatch(x, r), r, w).float()
+        grad, = torch.autograd.grad(out.square().sum(), wrt, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (grad.float().square().sum() + w.square().sum()).backward()
+    out = ex.combine(ex.dispatch(x, r), r, w).float()
+    out.square().sum().backward()                     # the first order is as it was
+    assert x.grad.any() and w.grad.any()
