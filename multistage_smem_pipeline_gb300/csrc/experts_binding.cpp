@@ -231,8 +231,8 @@ struct Fp4Matrix {
     if (g < 0 || (g ? rows % g : rows) != 0)
       value_error(std::to_string(rows) + " rows are not whole groups of " + std::to_string(g));
     c.groups = g ? static_cast<int32_t>(std::max<int64_t>(rows / g, 1)) : 1;
-    c.group_rows = g;
-    tiles = c.groups * ((g + 127) / 128);
+    c.group_rows = rows ? g : 0;  // no rows are whole groups of any size
+    tiles = c.groups * ((c.group_rows + 127) / 128);
   }
 
   const at::Tensor& get_scales() {
@@ -331,7 +331,9 @@ at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::
   if (a.device != b.device) value_error("a and b are on different devices");
   const On on(a.device, stream);
   const at::Tensor d = output(out, a.c.rows, b.c.group_rows, t, a.device);
-  check(fp4_gemm_tn_ex(d.data_ptr(), type, &a.c, &b.c, static_cast<float>(alpha), timeout_ns, inject,
+  fp4_matrix_t rows = a.c;
+  if (rows.rows == 0 && !rows.offsets) rows.groups = b.c.groups;  // ... and any number of them
+  check(fp4_gemm_tn_ex(d.data_ptr(), type, &rows, &b.c, static_cast<float>(alpha), timeout_ns, inject,
                        on.stream()),
         "fp4_gemm_tn");
   return d;
