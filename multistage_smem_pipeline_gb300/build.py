@@ -7,11 +7,13 @@ multistage_smem_pipeline_gb300/lib/libgemm_tn_f16.so (the CUDA runtime is
 linked statically; the driver's cuTensorMapEncodeTiled is fetched at run time
 through the runtime's entry-point query, so no -lcuda is needed).  The Python
 binding of moe_fp4.h, csrc/experts_binding.cpp, is compiled beside them against
-the installed torch's headers and linked to the library.
+the installed torch's headers and linked to the library; without a torch the
+library alone is built.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -48,10 +50,16 @@ def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _has_torch() -> bool:
+    """The binding is left out where there is none to compile it against."""
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    wanted = [LIB] + ([BINDING] if _has_torch() else [])
+    if not all(os.path.exists(w) for w in wanted):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(w) for w in wanted)
     return all(os.path.getmtime(d) <= t for d in _deps() + [BINDING_SRC])
 
 
@@ -77,6 +85,22 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
+def _start(cmd: list[str]) -> subprocess.Popen:
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish(procs, verbose: bool) -> list[str]:
+    """Waits for compilers; what those that failed said."""
+    failed = []
+    for src, p in procs:
+        out, _ = p.communicate()
+        if p.returncode != 0:
+            failed.append(f"{os.path.basename(src)}:\n{out}")
+        elif verbose and out:
+            sys.stdout.write(out)
+    return failed
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
@@ -89,26 +113,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(OBJ_DIR, os.path.basename(src) + ".o")
         objs.append(obj)
         cmd = [exe] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-c", src, "-o", obj]
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                            text=True)))
+        procs.append((src, _start(cmd)))
     binding_obj = os.path.join(OBJ_DIR, "experts_binding.cpp.o")
-    procs.append((BINDING_SRC, subprocess.Popen(_binding_command(binding_obj),
-                                                stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                                text=True)))
-    failed = []
-    for src, p in procs:
-        out, _ = p.communicate()
-        if p.returncode != 0:
-            failed.append(f"{os.path.basename(src)}:\n{out}")
-        elif verbose and out:
-            sys.stdout.write(out)
+    binding = [(BINDING_SRC, _start(_binding_command(binding_obj)))] if _has_torch() else []
+    failed = _finish(procs, verbose)
+    binding_failed = _finish(binding, verbose)
     if failed:
-        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed + binding_failed))
     tmp = LIB + f".{os.getpid()}.tmp"
     subprocess.check_call([exe] + ARCH + ["-shared", "-o", tmp, "-Xlinker",
                                           "-soname=libgemm_tn_f16.so"] + objs)
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    if binding_failed:
+        raise RuntimeError("compilation of the binding failed:\n" + "\n".join(binding_failed))
+    if binding:
+        _link_binding(binding_obj)
+    else:
+        print("no torch: the Python binding of moe_fp4.h is left out", file=sys.stderr)
     return LIB
 
 
