@@ -13,6 +13,7 @@ library alone is built.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -55,9 +56,32 @@ def _has_torch() -> bool:
     return importlib.util.find_spec("torch") is not None
 
 
+def _built_for() -> str:
+    """What the binding's object code depends on beside its sources: torch and Python."""
+    try:
+        version = importlib.metadata.version("torch")   # without the second that importing it takes
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}\n"
+
+
+def _stamp() -> str:
+    return os.path.splitext(BINDING)[0] + ".built_for"
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
 def up_to_date() -> bool:
     wanted = [LIB] + ([BINDING] if _has_torch() else [])
     if not all(os.path.exists(w) for w in wanted):
+        return False
+    if BINDING in wanted and _read(_stamp()) != _built_for():
         return False
     t = min(os.path.getmtime(w) for w in wanted)
     return all(os.path.getmtime(d) <= t for d in _deps() + [BINDING_SRC])
@@ -83,6 +107,8 @@ def _link_binding(obj: str) -> None:
                            "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", "-L" + LIB_DIR,
                            "-l:libgemm_tn_f16.so", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BINDING)
+    with open(_stamp(), "w") as f:
+        f.write(_built_for())
 
 
 def _start(cmd: list[str]) -> subprocess.Popen:

@@ -61,3 +61,21 @@ def test_the_library_is_built_where_the_binding_is_not(compilers):
 def test_both_are_built(compilers):
     done = run(compilers)
     assert "library True binding True again False" in done.stdout, done.stderr
+
+
+def test_the_binding_is_made_anew_for_another_torch(compilers):
+    assert "again False" in run(compilers).stdout
+    assert "again False" in run(compilers).stdout
+    calls = (compilers / "calls").read_text().count("experts_binding.cpp -o")
+    assert calls == 1                                 # the second time nothing was compiled
+    stamp = compilers / "lib" / "_experts.built_for"
+    made_for = stamp.read_text()
+    for other in (made_for.replace("torch", "torch 0.1"), made_for + "x", ""):
+        stamp.write_text(other)
+        assert "again False" in run(compilers).stdout
+        assert stamp.read_text() == made_for
+        calls += 1
+        assert (compilers / "calls").read_text().count("experts_binding.cpp -o") == calls
+    stamp.unlink()
+    run(compilers)
+    assert stamp.read_text() == made_for
