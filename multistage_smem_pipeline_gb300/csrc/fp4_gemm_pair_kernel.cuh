@@ -5,10 +5,11 @@
 // of the two tiles of the activations' scales, which goes to both; the even CTA
 // issues, and each CTA accumulates its 128 outputs in its own tensor memory.
 //
-// What bounds it is shared memory: per 256 columns of k an SM takes in 38 KiB
-// and its MMAs read 32 KiB of codes and 6 KiB of scales in 512 cycles, more
-// than its 128 bytes a cycle; a single CTA's 128 x 256 tile would take in 54
-// and read 54.  At 8192^3 the loads alone take 124 us, the MMAs alone 136 (of
+// What bounds it is how operands get to the MMAs: per 256 columns of k an SM takes
+// in 38 KiB and its MMAs read 32 KiB of codes and 6 KiB of scales in 512 cycles,
+// together more than shared memory's 128 bytes a cycle; a single CTA's 128 x 256
+// tile would take in 54 and read 54.  At 8192^3 the loads alone take 124 us (65
+// bytes a cycle into each SM, which looks like what comes in from L2), the MMAs alone 136 (of
 // which 14 are the accumulator changing hands, as there is no room for two of
 // 256 columns and the scales), both 151, and the stores make it 164
 // (6.7 PFLOP/s).  Codes and scales have rings of their own because tensor memory

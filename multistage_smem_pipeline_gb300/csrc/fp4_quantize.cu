@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kFormat == FP4_NV ? 6 : 4)
 // way to it (4096 tokens of 2880 into 2 slots each of 8 experts 7.5 us, so 8.4; 4096
 // of 4096 into 8 of 64 22.5 and 22.3), but may hold the next step's by now.
 // Neighbouring threads join the four scale bytes of a chunk.  4096 tokens of
-// 4096 columns into 8 slots each take 22 us (5.0 TB/s); what it waits on are
+// 4096 columns into 8 slots each take 22.3 us (4.9 TB/s); what it waits on are
 // the scales, 4 bytes of a row in each 512-byte chunk, as writing codes 16 bytes
 // a thread instead of 8 changed nothing.
 template <typename T, int kFormat, bool kVec>

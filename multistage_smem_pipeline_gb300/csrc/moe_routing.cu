@@ -35,8 +35,8 @@ struct RouteParams {
 // memory), across keys by a scan over the keys, which is `offsets`.  Ranks and
 // keys of a warp's first 256 slots stay in registers; those of later ones wait
 // in `rows`.  Everything is read and written once or twice; what bounds the
-// sort is latency, hence one launch and few steps: 64 slots take 3.1 us, 32,792
-// 7.1 and 65,536 (of 128 experts) 8.9.
+// sort is latency, hence one launch and few steps: 64 slots take 3.3 us, 32,792
+// 7.4 and 65,536 (of 128 experts) 9.2.
 __global__ void __launch_bounds__(kSortThreads)
     sort_kernel(int32_t* __restrict__ offsets, int32_t* rows, const int32_t* __restrict__ ids, int n,
                 int experts) {
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kSortThreads)
   };
   // the rank of a slot among those of its warp so far; lanes with equal keys
   // are found bit by bit (matching them in one instruction took longer:
-  // 16.1 against 13.1 us for 65,536 slots of 128 experts)
+  // 12.1 against 9.2 us for 65,536 slots of 128 experts)
   const int bits = 32 - __clz(keys);
   const auto place = [&](int key) {
     unsigned same = 0xffffffffu;
