@@ -141,9 +141,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [exe] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-c", src, "-o", obj]
         procs.append((src, _start(cmd)))
     binding_obj = os.path.join(OBJ_DIR, "experts_binding.cpp.o")
-    binding = [(BINDING_SRC, _start(_binding_command(binding_obj)))] if _has_torch() else []
+    binding, binding_failed = [], []
+    if _has_torch():
+        try:
+            binding.append((BINDING_SRC, _start(_binding_command(binding_obj))))
+        except Exception as e:  # an installed torch that does not import
+            binding_failed.append(f"{os.path.basename(BINDING_SRC)}: {e!r}")
     failed = _finish(procs, verbose)
-    binding_failed = _finish(binding, verbose)
+    binding_failed += _finish(binding, verbose)
     if failed:
         raise RuntimeError("compilation failed:\n" + "\n".join(failed + binding_failed))
     tmp = LIB + f".{os.getpid()}.tmp"

@@ -79,3 +79,16 @@ def test_the_binding_is_made_anew_for_another_torch(compilers):
     stamp.unlink()
     run(compilers)
     assert stamp.read_text() == made_for
+
+
+def test_the_library_is_built_where_torch_does_not_import(compilers):
+    """A torch that is there and broken is an error, after the library."""
+    broken = compilers / "broken" / "torch"
+    broken.mkdir(parents=True)
+    (broken / "__init__.py").write_text("raise ImportError('a broken torch')\n")
+    script = SCRIPT.format(root=ROOT, out=str(compilers), bin=str(compilers / "bin"), hide=False)
+    env = dict(os.environ, PATH=f"{compilers / 'bin'}:{os.environ['PATH']}",
+               PYTHONPATH=str(compilers / "broken"))
+    done = subprocess.run([sys.executable, "-c", script], env=env, text=True, capture_output=True)
+    assert done.returncode != 0 and "a broken torch" in done.stderr
+    assert (compilers / "lib" / "libgemm_tn_f16.so").exists()
