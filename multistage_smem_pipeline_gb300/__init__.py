@@ -3,8 +3,8 @@
 The compute path is the C-ABI library built from ``csrc/`` (TMA + mbarrier
 stage ring + tcgen05/TMEM kernels for sm_103a).  ``binding`` marshals torch
 tensors into that library; it has no fallback of any kind.  ``experts`` is
-the same for 4-bit matrices, their product and the routing of tokens to
-experts.
+the same for 4-bit matrices, their product, the routing of tokens to experts
+and linear layers in 16 bits.
 """
 _EXPORTS = ("gemm_tn_f16", "gemm_tn_f16_ex", "gemm_f16_scaled", "gemm_tn_f16_from_host",
             "get_device_error",
@@ -12,7 +12,9 @@ _EXPORTS = ("gemm_tn_f16", "gemm_tn_f16_ex", "gemm_f16_scaled", "gemm_tn_f16_fro
             "GemmError")
 _EXPERTS = ("Fp4Matrix", "Routing", "fp4_quantize", "fp4_dequantize", "fp4_gemm_tn",
             "fp4_query_config", "fp4_scale_bytes", "fp4_get_device_error", "moe_sort", "moe_pairs",
-            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward")
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+            "linear", "linear_backward", "moe_linear", "moe_linear_backward", "linear_query_config",
+            "linear_get_device_error")
 __all__ = list(_EXPORTS + _EXPERTS)
 
 

@@ -6,7 +6,7 @@ Each translation unit under csrc/ is compiled in parallel, then linked into
 multistage_smem_pipeline_gb300/lib/libgemm_tn_f16.so (the CUDA runtime is
 linked statically; the driver's cuTensorMapEncodeTiled is fetched at run time
 through the runtime's entry-point query, so no -lcuda is needed).  The Python
-binding of moe_fp4.h, csrc/experts_binding.cpp, is compiled beside them against
+binding of moe_fp4.h and linear.h, csrc/experts_binding.cpp, is compiled beside them against
 the installed torch's headers and linked to the library; without a torch the
 library alone is built.
 """
@@ -28,7 +28,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libgemm_tn_f16.so")
-BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")
+BINDING_SRC = os.path.join(CSRC, "experts_binding.cpp")   # includes linear_binding.h
 BINDING = os.path.join(LIB_DIR, "_experts.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,7 +48,8 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return _sources() + [f for folder, kind in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h"))
+                         for f in glob.glob(os.path.join(folder, kind))]
 
 
 def _has_torch() -> bool:

@@ -1,4 +1,4 @@
-// Python binding of moe_fp4.h: checks and marshals torch tensors, allocates
+// Python binding of moe_fp4.h and linear.h: checks and marshals torch tensors, allocates
 // outputs, and calls the C functions on the current (or a given) stream.  It
 // is compiled because the calls it makes are a few microseconds long on the
 // GPU: marshalled from Python, a call cost the host 7 to 11 us; compiled, 2.6 to
@@ -14,6 +14,7 @@
 #include <memory>
 #include <optional>
 #include <string>
+#include <tuple>
 
 #include "moe_fp4.h"
 
@@ -340,7 +341,7 @@ at::Tensor gemm(const Fp4Matrix& a, const Fp4Matrix& b, double alpha, const py::
 }
 
 // On the stream's own device; other threads of the interpreter run meanwhile.
-py::tuple device_error(const py::object& stream) {
+py::tuple device_error(const py::object& stream, int (*read)(void*, uint32_t*)) {
   std::optional<c10::cuda::CUDAGuard> device;
   if (!stream.is_none() && py::hasattr(stream, "device"))
     device.emplace(stream.attr("device").cast<at::Device>());
@@ -351,7 +352,7 @@ py::tuple device_error(const py::object& stream) {
   int status = 0;
   {
     const py::gil_scoped_release released;
-    status = fp4_get_device_error(s, &raw);
+    status = read(s, &raw);
   }
   return py::make_tuple(status, raw);
 }
@@ -454,6 +455,8 @@ std::pair<at::Tensor, at::Tensor> combine_backward(const at::Tensor& grad_out, c
 
 }  // namespace
 
+#include "linear_binding.h"
+
 PYBIND11_MODULE(_experts, m) {
   const auto none = py::none();
   py::class_<Routing, RoutingPtr>(m, "Routing",
@@ -508,7 +511,9 @@ PYBIND11_MODULE(_experts, m) {
         "g(r) is the group of row r, so with activations in expert order each row meets its "
         "expert's weights; rows of dropped slots give zeros.  b has as many groups as a, each of "
         "b.group_rows outputs.  timeout_ns and inject: see fp4_gemm_tn_ex in moe_fp4.h.");
-  m.def("fp4_get_device_error", &device_error, py::arg("stream") = none,
+  m.def("fp4_get_device_error",
+        [](const py::object& stream) { return device_error(stream, fp4_get_device_error); },
+        py::arg("stream") = none,
         "(status, raw word) of the stream's error word of fp4_gemm_tn; synchronises the stream.");
   m.def("fp4_scale_bytes", &scale_bytes, py::arg("rows"), py::arg("cols"),
         py::arg("format") = "nvfp4", py::arg("groups") = 1, py::arg("by_offsets") = false,
@@ -533,4 +538,6 @@ PYBIND11_MODULE(_experts, m) {
   m.def("moe_combine_backward", &combine_backward, py::arg("grad_out"), py::arg("y"),
         py::arg("routing"), py::arg("weights"), py::arg("stream") = none,
         "moe_combine's gradients: (of y, of weights); zeros for dropped slots.");
+
+  define_linear(m);
 }

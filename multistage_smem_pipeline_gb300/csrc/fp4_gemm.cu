@@ -11,47 +11,6 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-std::mutex g_mu;
-std::atomic<EncodeTiledFn> g_encode{nullptr};
-uintptr_t g_word_stream[kErrorWords];
-int g_words_used = 1;
-
-int get_encoder(EncodeTiledFn* encode) {
-  *encode = g_encode.load(std::memory_order_acquire);
-  if (*encode) return GEMM_OK;
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                       &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess || fn == nullptr) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
-  *encode = reinterpret_cast<EncodeTiledFn>(fn);
-  g_encode.store(*encode, std::memory_order_release);
-  return GEMM_OK;
-}
-
-// Index of a stream's error word: 0 for the legacy default stream, one each
-// for the first 63 others, then shared by a hash.
-int error_index(cudaStream_t s) {
-  const uintptr_t h = reinterpret_cast<uintptr_t>(s);
-  if (h == 0) return 0;
-  std::lock_guard<std::mutex> lk(g_mu);
-  for (int i = 1; i < g_words_used; ++i)
-    if (g_word_stream[i] == h) return i;
-  if (g_words_used < kErrorWords) {
-    g_word_stream[g_words_used] = h;
-    return g_words_used++;
-  }
-  return 1 + static_cast<int>((h >> 4) % (kErrorWords - 1));
-}
-
 // A matrix's codes as rows of bytes; a box is 128 bytes wide.
 int encode_codes(EncodeTiledFn encode, CUtensorMap* map, const fp4_matrix_t* m, uint32_t box_rows) {
   const uint64_t pitch = static_cast<uint64_t>(code_pitch(m->cols));

@@ -37,6 +37,7 @@
 #include <cuda.h>
 
 #include "fp4.cuh"
+#include "tensor_map.cuh"
 
 namespace gb300 {
 
@@ -49,7 +50,6 @@ constexpr int kGemmMaxStages = 8;
 constexpr uint32_t kWBytes = kGemmM * kGemmBytesK;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemScales = 256;  // first column of the scales
-constexpr int kErrorWords = 64;
 constexpr uint32_t kGemmSmemLimit = 232448;
 
 enum GemmWait : uint32_t { kWaitEmpty = 1, kWaitFull = 2, kWaitTmemEmpty = 3, kWaitTmemFull = 4,
@@ -211,15 +211,6 @@ __device__ __forceinline__ bool gemm_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
 // The same wait by a whole warp: it goes on, or gives up, together.
 __device__ __forceinline__ bool gemm_wait_warp(uint32_t bar, uint32_t parity,
                                                volatile int* abort_flag, uint32_t site,
@@ -242,13 +233,6 @@ struct GemmTile {
   int32_t x_tile;   // its scale tile
   int32_t count;    // rows
   int32_t group, m; // weight tile m of the group
-};
-
-// A group by offsets, in shared memory: every role looks each tile's group up
-// (from global memory: 129.0 us for 4096 tokens x 8 of 64 experts, against 128.2).
-struct GroupStart {
-  int32_t tiles;  // row tiles of the groups before it
-  int32_t row;    // its first row
 };
 
 // Tile t: groups in order; in a group, kRaster row tiles at a time walk over the
@@ -306,19 +290,6 @@ __device__ __forceinline__ GemmTile gemm_tile(int t, const Fp4GemmParams& p, con
   o.x_tile += xt * (kBN / kTileRows);
   o.count = min(kBN, rows - xt * kBN);
   return o;
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack_two(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack_two<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -441,35 +412,6 @@ __device__ __forceinline__ void zero_tail(const Fp4GemmParams& p, const GroupSta
     p.d[i] = 0;
 }
 
-// Where each group starts, and the end, by one warp.  All offsets of 128 groups
-// are asked for at once: nothing can be loaded before this is done, and one
-// latency of memory is 0.4 us.
-template <int kBN>
-__device__ __forceinline__ void find_groups(const Fp4GemmParams& p, GroupStart* start, int lane) {
-  constexpr int kAhead = 4;
-  int32_t total = 0;
-  for (int g0 = 0; g0 <= p.groups; g0 += 32 * kAhead) {
-    int32_t row[kAhead + 1];
-#pragma unroll
-    for (int i = 0; i <= kAhead; ++i) row[i] = p.offsets[min(g0 + 32 * i + lane, p.groups)];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int g = g0 + 32 * i + lane;
-      const int32_t next = __shfl_down_sync(0xffffffffu, row[i], 1);
-      const int32_t first = __shfl_sync(0xffffffffu, row[i + 1], 0);
-      const int32_t n = ((lane < 31 ? next : first) - row[i] + kBN - 1) / kBN;  // 0 past the last
-      int32_t upto = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int32_t v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-      }
-      if (g <= p.groups) start[g] = GroupStart{total + upto - n, row[i]};
-      total += __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ kernel
 // kSplit: few tiles.  A cluster of p.split CTAs (2, 4 or 8) shares one tile, each
 // taking its part of k; then every CTA sends each other one its partial sums
@@ -532,7 +474,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) find_groups<kBN>(p, start, lane);
+  if (p.offsets && warp == 2) find_groups<kBN>(p.offsets, p.groups, start, lane);
   tc_fence_before_sync();
   if (kSplit) cluster_sync();  // the others' barriers exist
   else __syncthreads();

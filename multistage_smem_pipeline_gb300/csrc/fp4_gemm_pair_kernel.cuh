@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish_pair();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) find_groups<kBN>(p, start, lane);
+  if (p.offsets && warp == 2) find_groups<kBN>(p.offsets, p.groups, start, lane);
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();

@@ -1,0 +1,545 @@
+// Host side of linear layers: checks, workspaces, the form of a product, tensor
+// maps, launches.
+#include "linear_kernel.cuh"
+#include "linear_pair_kernel.cuh"
+#include "linear_rows.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+// ------------------------------------------------------------------ checks
+bool in_range(int64_t v, int64_t most) { return v >= 0 && v <= most; }
+
+int groups_of(const linear_t* l) { return l->routing ? l->routing->experts : 1; }
+
+// The stride of a single row does not matter: one that the tensor maps take.
+Rows matrix_of(const void* ptr, int64_t rows, int64_t cols, int64_t ld) {
+  return Rows{ptr, rows, cols, rows > 1 ? ld : copy_ld(cols)};
+}
+Rows x_rows(const linear_t* l) { return matrix_of(l->x, l->rows, l->in, l->ldx); }
+Rows w_rows(const linear_t* l) { return matrix_of(l->w, groups_of(l) * l->out, l->in, l->ldw); }
+Rows by_out(const linear_t* l, const void* ptr, int64_t ld) {
+  return matrix_of(ptr, l->rows, l->out, ld);
+}
+
+uint64_t bytes_of(const Rows& r) {
+  return r.rows && r.cols ? (static_cast<uint64_t>(r.rows - 1) * r.ld + r.cols) * 2 : 0;
+}
+Range reads(const Rows& r) { return Range{r.ptr, bytes_of(r), false}; }
+
+// A matrix that a call needs; none of its elements: any pointer.
+int check_rows(const Rows& r) {
+  if (r.ld < r.cols || r.ld > (int64_t{1} << 38)) return GEMM_ERR_INVALID_VALUE;
+  if (r.rows == 0 || r.cols == 0) return GEMM_OK;
+  if (!r.ptr) return GEMM_ERR_INVALID_VALUE;
+  return aligned_to(r.ptr, 2) ? GEMM_OK : GEMM_ERR_MISALIGNED;
+}
+
+int check_layer(const linear_t* l) {
+  if (!l || !in_range(l->rows, LINEAR_MAX_ROWS) || !in_range(l->in, LINEAR_MAX_COLS) ||
+      !in_range(l->out, LINEAR_MAX_COLS) || !valid_type(l->type) || l->activation < LINEAR_NONE ||
+      l->activation > LINEAR_SILU)
+    return GEMM_ERR_INVALID_VALUE;
+  if (l->routing) {
+    const int rc = check_routing(l->routing);
+    if (rc != GEMM_OK) return rc;
+    if (l->rows != l->routing->tokens * l->routing->top_k) return GEMM_ERR_INVALID_VALUE;
+  }
+  return groups_of(l) * l->out <= INT_MAX ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
+bool valid_form(int pair, int tile, int split) {
+  if (pair) return pair == 1 && tile == 256 && split == 1;
+  if (tile != 64 && tile != 128 && tile != 192 && tile != 256) return false;
+  return split == 1 || ((split == 2 || split == 4 || split == 8) && tile / 32 % split == 0);
+}
+
+int check_options(const linear_options_t* o) {
+  if (!o) return GEMM_OK;
+  if (o->inject < 0 || o->inject > 1) return GEMM_ERR_INVALID_VALUE;
+  if (o->tile == 0 && o->cta_pair == 0 && o->split_k == 0) return GEMM_OK;
+  return valid_form(o->cta_pair, o->tile, o->split_k) ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
+// The offsets of a layer's groups; null for one group (and for rows of nobody).
+const int32_t* offsets_of(const linear_t* l) {
+  return l->routing && l->rows > 0 ? l->routing->offsets : nullptr;
+}
+
+// ------------------------------------------------------------------ forms
+// What the choice of a form needs to know of the device.
+struct Machine {
+  int sms;
+  int clusters[3];  // of 2, 4 and 8 CTAs, held at once, a CTA an SM
+};
+
+Machine machine_of(int sms, int device) {
+  static std::once_flag once;
+  static int held[3] = {0, 0, 0};
+  std::call_once(once, [&] {
+    const auto kernel = linear_tc<__half, LINEAR_FORWARD, true>;
+    static std::atomic<uint64_t> granted{0};
+    if (!grant_smem(kernel, kLinSmemLimit, device, granted)) return;
+    for (int i = 0; i < 3; ++i) {
+      cudaLaunchConfig_t cfg;
+      std::memset(&cfg, 0, sizeof(cfg));
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((2u << i) * (sms / (2 << i)));
+      cfg.blockDim = dim3(kLinThreads);
+      cfg.dynamicSmemBytes = kLinSmemLimit;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        held[i] = 0;
+      }
+    }
+  });
+  return Machine{sms, {held[0], held[1], held[2]}};
+}
+
+struct Plan {
+  bool pair;
+  int tile, split;
+  int m_tiles, n_tiles;  // m_tiles: grad_w's, of a group
+  int box_rows;
+  int units;             // CTAs, pairs or clusters
+};
+
+// A product: D's rows (of all groups together, but of one for grad_w) and columns,
+// the sums' length, in groups; `ragged`: by offsets.
+struct Product {
+  int kind;
+  int64_t m, n, k;
+  int64_t groups;
+  bool ragged;
+};
+
+Product product_of(int kind, int64_t rows, int64_t in, int64_t out, int64_t groups, bool ragged) {
+  switch (kind) {
+    case LINEAR_FORWARD: return Product{kind, rows, out, in, groups, ragged};
+    case LINEAR_GRAD_X: return Product{kind, rows, in, out, groups, ragged};
+    default: return Product{kind, out, in, rows, groups, ragged};
+  }
+}
+
+// Row tiles of height `h` of all groups: as many as are expected, or as there can be.
+int64_t row_tiles(const Product& p, int64_t h, bool most) {
+  if (p.kind == LINEAR_GRAD_W) return p.groups * ((p.m + h - 1) / h);
+  if (!p.ragged) return (p.m + h - 1) / h;
+  const int64_t live = std::min(p.groups, p.m);
+  // a group is taken to end half way through its last tile
+  return most ? p.m / h + live : std::max(live, (2 * p.m + live * h) / (2 * h));
+}
+
+int make_plan(const Product& p, const Machine& machine, const linear_options_t* forced, Plan* o) {
+  const bool weight = p.kind == LINEAR_GRAD_W;
+  // of a group, in the mean
+  const int64_t k = weight && p.ragged ? (p.k + p.groups - 1) / p.groups : p.k;
+  const int64_t tile_rows = weight ? p.m : p.ragged ? (p.m + p.groups - 1) / p.groups : p.m;
+  const double kbs = std::max<double>(1.0, static_cast<double>((k + kLinK - 1) / kLinK));
+  const auto n_tiles = [&](int64_t tile) { return (p.n + tile - 1) / tile; };
+  double least = 0.0;
+  o->tile = 0;
+  const auto offer = [&](bool pair, int tile, int split, double cycles) {
+    if (o->tile != 0 && cycles >= least) return;
+    least = cycles;
+    o->pair = pair;
+    o->tile = tile;
+    o->split = split;
+  };
+  if (forced && forced->tile != 0) {
+    offer(forced->cta_pair != 0, forced->tile, forced->split_k, 0.0);
+  } else {
+    // Cycles of the waves of tiles.  Operands come in at about 60 bytes a cycle and
+    // SM; an MMA of 128 rows takes half a cycle a column, and 100 at least.
+    const auto waves = [&](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
+    offer(true, 256, 1, waves(row_tiles(p, 256, false) * n_tiles(256), machine.sms / 2) * (2500 + 540 * kbs));
+    for (int tile : {256, 192, 128, 64}) {
+      const int64_t tiles = row_tiles(p, 128, false) * n_tiles(tile);
+      const double rows = static_cast<double>(std::min<int64_t>(128, tile_rows));
+      const double stage = std::max({2.0 * tile, 400.0, (rows * 128 + tile * 128) / 60.0});
+      offer(false, tile, 1, waves(tiles, machine.sms) * (2500 + stage * kbs));
+      for (int i = 0; i < 3; ++i) {
+        const int split = 2 << i;
+        if (!valid_form(0, tile, split) || row_tiles(p, 128, true) * n_tiles(tile) > machine.clusters[i] ||
+            kbs < 2 * split)
+          continue;
+        offer(false, tile, split, 4500 + 10.0 * rows + stage * kbs / split);
+      }
+    }
+  }
+  const int64_t h = o->pair ? 256 : 128;
+  const int64_t most = row_tiles(p, h, true) * n_tiles(o->tile);
+  // counted in 32 bits, with room for a grid's stride past the last
+  if (most > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
+  o->m_tiles = weight ? static_cast<int>((p.m + h - 1) / h) : 0;
+  o->n_tiles = static_cast<int>(n_tiles(o->tile));
+  // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile loads
+  // little more than it has.
+  o->box_rows = p.ragged || p.m <= 64 ? 32 : 128;
+  o->units = static_cast<int>(o->split > 1 ? most : std::min<int64_t>(o->pair ? machine.sms / 2 : machine.sms, most));
+  return GEMM_OK;
+}
+
+// ------------------------------------------------------------------ launches
+struct Maps {
+  CUtensorMap a, b;
+};
+
+// A matrix of `rows` rows of `cols` as two or three dimensions (matrices of it).
+int encode(EncodeTiledFn fn, CUtensorMap* map, const void* ptr, int64_t cols, int64_t rows,
+           int64_t ld, int64_t matrices, uint32_t box_rows, int rank) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(matrices)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(ld) * 2 * (matrices > 1 ? rows : 1)};
+  const cuuint32_t box[3] = {kLinK, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(ptr), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
+template <typename T, int kProduct>
+int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaStream_t s) {
+  const uint32_t fixed = linear_fixed_bytes(p.groups) + (plan.split > 1 ? 0u : kLinEpiWarps * kLinBufBytes);
+  const uint32_t stage = plan.pair ? kLinPairStage : kLinABytes + plan.tile * (kLinK * 2);
+  p.stages = std::min<int>((kLinSmemLimit - fixed) / stage, kLinMaxStages);
+  const size_t smem = fixed + p.stages * stage;
+  const auto go = [&](auto kernel, std::atomic<uint64_t>& granted, unsigned ctas, unsigned cluster) {
+    if (!grant_smem(kernel, kLinSmemLimit, device, granted)) return static_cast<int>(GEMM_ERR_CUDA);
+    return launch_pdl(kernel, dim3(ctas), dim3(kLinThreads), smem, s, cluster, m.a, m.b, p);
+  };
+  static std::atomic<uint64_t> granted[3];
+  if (plan.pair) return go(linear_pair<T, kProduct>, granted[0], 2 * plan.units, 2);
+  if (plan.split > 1)
+    return go(linear_tc<T, kProduct, true>, granted[1], plan.units * plan.split, plan.split);
+  return go(linear_tc<T, kProduct, false>, granted[2], plan.units, 1);
+}
+
+// One product of operands that the tensor maps take as they are: a is x or dz, b is w
+// or (grad_w) x.
+int launch(const Product& pr, const Rows& a, const Rows& b, LinearParams p, int type,
+           const linear_options_t* opt, int sms, int device, cudaStream_t s) {
+  Plan plan;
+  int rc = make_plan(pr, machine_of(sms, device), opt, &plan);
+  if (rc != GEMM_OK) return rc;
+  p.n = static_cast<int32_t>(pr.n);
+  p.k = static_cast<int32_t>(pr.k);
+  p.m = pr.kind == LINEAR_GRAD_W ? static_cast<int32_t>(pr.m) : 0;
+  p.groups = static_cast<int32_t>(pr.groups);
+  p.tile = plan.tile;
+  p.m_tiles = plan.m_tiles;
+  p.n_tiles = plan.n_tiles;
+  p.box_rows = plan.box_rows;
+  p.split = plan.split;
+  p.inject = opt ? opt->inject : 0;
+  p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : kTimeoutNs;
+  p.error_word = error_index(s);
+  Maps m;
+  std::memset(&m, 0, sizeof(m));
+  if (pr.k > 0) {
+    EncodeTiledFn fn = nullptr;
+    if ((rc = get_encoder(&fn)) != GEMM_OK) return rc;
+    const bool weight = pr.kind == LINEAR_GRAD_W;
+    const uint32_t a_box = weight ? 64 : plan.box_rows;
+    const uint32_t b_box = pr.kind == LINEAR_FORWARD ? (plan.pair ? 128 : plan.tile) : 64;
+    const int64_t matrices = weight ? 1 : pr.groups;
+    if ((rc = encode(fn, &m.a, a.ptr, a.cols, a.rows, a.ld, 1, a_box, 2)) != GEMM_OK ||
+        (rc = encode(fn, &m.b, b.ptr, b.cols, b.rows / matrices, b.ld, matrices, b_box, 3)) != GEMM_OK)
+      return rc;
+  }
+  const auto by_type = [&](auto t) {
+    using T = decltype(t);
+    switch (pr.kind) {
+      case LINEAR_FORWARD: return launch_as<T, LINEAR_FORWARD>(m, p, plan, device, s);
+      case LINEAR_GRAD_X: return launch_as<T, LINEAR_GRAD_X>(m, p, plan, device, s);
+      default: return launch_as<T, LINEAR_GRAD_W>(m, p, plan, device, s);
+    }
+  };
+  return type == MOE_F16 ? by_type(__half{}) : by_type(__nv_bfloat16{});
+}
+
+// ------------------------------------------------------------------ workspaces
+// Pieces of a workspace, one after the other, each on a 16-byte boundary.
+struct Pieces {
+  uint64_t bytes = 0;
+  uint64_t add(uint64_t n) {
+    const uint64_t at = bytes;
+    bytes += (n + 15) & ~uint64_t{15};
+    return at;
+  }
+};
+uint64_t copy_bytes(const Rows& r) { return static_cast<uint64_t>(r.rows) * copy_ld(r.cols) * 2; }
+
+struct ForwardSpace {
+  bool copy_x, copy_w;
+  uint64_t x, w, bytes;
+};
+ForwardSpace forward_space(const linear_t* l) {
+  Pieces p;
+  ForwardSpace f{};
+  const bool sums = l->rows > 0 && l->out > 0 && l->in > 0;
+  f.copy_x = sums && !loads_as_is(x_rows(l));
+  f.copy_w = sums && !loads_as_is(w_rows(l));
+  if (f.copy_x) f.x = p.add(copy_bytes(x_rows(l)));
+  if (f.copy_w) f.w = p.add(copy_bytes(w_rows(l)));
+  f.bytes = p.bytes;
+  return f;
+}
+
+struct BackwardSpace {
+  bool copy_x, copy_w, dz, strips;
+  uint64_t x, w, z, sums, bytes;
+  int strip_rows;
+};
+BackwardSpace backward_space(const linear_t* l, bool grad_x, bool grad_w, bool grad_bias,
+                             const Rows& grad) {
+  Pieces p;
+  BackwardSpace b{};
+  const bool live = l->rows > 0 && l->out > 0;
+  const bool for_x = live && grad_x && l->in > 0, for_w = live && grad_w && l->in > 0;
+  b.copy_w = for_x && !loads_as_is(w_rows(l));
+  b.copy_x = for_w && !loads_as_is(x_rows(l));
+  b.dz = (for_x || for_w) && (l->activation != LINEAR_NONE || !loads_as_is(grad));
+  b.strips = live && grad_bias;
+  b.strip_rows = strip_rows_for(l->rows);
+  if (b.copy_w) b.w = p.add(copy_bytes(w_rows(l)));
+  if (b.copy_x) b.x = p.add(copy_bytes(x_rows(l)));
+  if (b.dz) b.z = p.add(copy_bytes(grad));
+  if (b.strips)
+    b.sums = p.add((l->rows / b.strip_rows + groups_of(l)) * static_cast<uint64_t>(l->out) * 4);
+  b.bytes = p.bytes;
+  return b;
+}
+
+int check_workspace(const void* workspace, uint64_t bytes, uint64_t needed) {
+  if (needed == 0) return GEMM_OK;
+  if (!workspace || bytes < needed) return GEMM_ERR_INVALID_VALUE;
+  return aligned_to(workspace, 16) ? GEMM_OK : GEMM_ERR_MISALIGNED;
+}
+
+// The rows, or their copy at `at` of the workspace.
+int as_loaded(Rows* r, bool copied, void* workspace, uint64_t at, int sms, cudaStream_t s) {
+  if (!copied) return GEMM_OK;
+  void* const dst = static_cast<uint8_t*>(workspace) + at;
+  const int rc = copy_rows(dst, *r, sms, s);
+  r->ptr = dst;
+  r->ld = copy_ld(r->cols);
+  return rc;
+}
+
+bool by_vectors(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
+
+}  // namespace
+}  // namespace gb300
+
+using namespace gb300;
+
+extern "C" int linear_forward_workspace(const linear_t* layer, uint64_t* bytes) {
+  const int rc = check_layer(layer);
+  if (rc != GEMM_OK) return rc;
+  if (!bytes) return GEMM_ERR_INVALID_VALUE;
+  *bytes = forward_space(layer).bytes;
+  return GEMM_OK;
+}
+
+extern "C" int linear_backward_workspace(const void* grad_x, const void* grad_w,
+                                         const void* grad_bias, const linear_t* layer,
+                                         const void* grad_out, int64_t ldg, uint64_t* bytes) {
+  const int rc = check_layer(layer);
+  if (rc != GEMM_OK) return rc;
+  if (!bytes) return GEMM_ERR_INVALID_VALUE;
+  *bytes = backward_space(layer, grad_x != nullptr, grad_w != nullptr, grad_bias != nullptr,
+                          by_out(layer, grad_out, ldg)).bytes;
+  return GEMM_OK;
+}
+
+extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, const void* bias,
+                              const void* residual, int64_t ldr, void* workspace,
+                              uint64_t workspace_bytes, const linear_options_t* opt, void* stream) {
+  int rc = check_layer(layer);
+  if (rc != GEMM_OK) return rc;
+  if ((rc = check_options(opt)) != GEMM_OK) return rc;
+  const Rows result = by_out(layer, out, layer->out);
+  Rows x = x_rows(layer), w = w_rows(layer);
+  const Rows res = by_out(layer, residual, ldr);
+  if (residual && layer->routing) return GEMM_ERR_INVALID_VALUE;
+  for (const Rows* r : {&x, &w})
+    if ((rc = check_rows(*r)) != GEMM_OK) return rc;
+  if (residual && (rc = check_rows(res)) != GEMM_OK) return rc;
+  if (!aligned_to(preact, 2) || !aligned_to(bias, 2)) return GEMM_ERR_MISALIGNED;
+  const ForwardSpace space = forward_space(layer);
+  if ((rc = check_workspace(workspace, workspace_bytes, space.bytes)) != GEMM_OK) return rc;
+  if (layer->rows == 0 || layer->out == 0) return GEMM_OK;
+  if ((rc = check_rows(result)) != GEMM_OK) return rc;
+  const int groups = groups_of(layer);
+  if (any_overlap({{out, bytes_of(result), true},
+                   {preact, bytes_of(result), true},
+                   {space.bytes ? workspace : nullptr, space.bytes, true},
+                   {bias, static_cast<uint64_t>(groups) * layer->out * 2, false},
+                   reads(x), reads(w), reads(res)},
+                  layer->routing))
+    return GEMM_ERR_INVALID_VALUE;
+  int sms = 0, device = 0;
+  if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((rc = as_loaded(&x, space.copy_x, workspace, space.x, sms, s)) != GEMM_OK ||
+      (rc = as_loaded(&w, space.copy_w, workspace, space.w, sms, s)) != GEMM_OK)
+    return rc;
+  LinearParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.out = static_cast<uint16_t*>(out);
+  p.preact = static_cast<uint16_t*>(preact);
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.ldr = res.ld;
+  p.offsets = offsets_of(layer);
+  p.rows = static_cast<int32_t>(layer->rows);
+  p.activation = layer->activation;
+  p.vector = by_vectors(out, layer->out) && by_vectors(preact, 8) && by_vectors(bias, 8) &&
+             (!residual || by_vectors(residual, res.ld));
+  return launch(product_of(LINEAR_FORWARD, layer->rows, layer->in, layer->out, groups,
+                           p.offsets != nullptr),
+                x, w, p, layer->type, opt, sms, device, s);
+}
+
+extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, const linear_t* layer,
+                               const void* grad_out, int64_t ldg, const void* preact,
+                               void* workspace, uint64_t workspace_bytes,
+                               const linear_options_t* opt, void* stream) {
+  int rc = check_layer(layer);
+  if (rc != GEMM_OK) return rc;
+  if ((rc = check_options(opt)) != GEMM_OK) return rc;
+  const int groups = groups_of(layer);
+  Rows x = x_rows(layer), w = w_rows(layer), dz = by_out(layer, grad_out, ldg);
+  const Rows z = by_out(layer, preact, layer->out);
+  const Rows to_x = matrix_of(grad_x, layer->rows, layer->in, layer->in);
+  const Rows to_w = matrix_of(grad_w, groups * layer->out, layer->in, layer->in);
+  const uint64_t bias_bytes = static_cast<uint64_t>(groups) * layer->out * 2;
+  if ((rc = check_rows(dz)) != GEMM_OK) return rc;
+  if (layer->activation != LINEAR_NONE && (rc = check_rows(z)) != GEMM_OK) return rc;
+  if (grad_w && (rc = check_rows(x)) != GEMM_OK) return rc;
+  if (grad_x && (rc = check_rows(w)) != GEMM_OK) return rc;
+  if (!aligned_to(grad_x, 2) || !aligned_to(grad_w, 2) || !aligned_to(grad_bias, 2))
+    return GEMM_ERR_MISALIGNED;
+  const BackwardSpace space =
+      backward_space(layer, grad_x != nullptr, grad_w != nullptr, grad_bias != nullptr, dz);
+  if ((rc = check_workspace(workspace, workspace_bytes, space.bytes)) != GEMM_OK) return rc;
+  if (any_overlap({{grad_x, bytes_of(to_x), true},
+                   {grad_w, bytes_of(to_w), true},
+                   {grad_bias, bias_bytes, true},
+                   {space.bytes ? workspace : nullptr, space.bytes, true},
+                   {grad_w ? x.ptr : nullptr, bytes_of(x), false},
+                   {grad_x ? w.ptr : nullptr, bytes_of(w), false},
+                   {layer->activation != LINEAR_NONE ? preact : nullptr, bytes_of(z), false},
+                   reads(dz)},
+                  layer->routing))
+    return GEMM_ERR_INVALID_VALUE;
+  const bool for_x = grad_x && bytes_of(to_x) > 0, for_w = grad_w && bytes_of(to_w) > 0,
+             for_bias = grad_bias && bias_bytes > 0;
+  if (!for_x && !for_w && !for_bias) return GEMM_OK;
+  int sms = 0, device = 0;
+  if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  LinearParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.offsets = offsets_of(layer);
+  p.rows = static_cast<int32_t>(layer->rows);
+  p.strip_rows = space.strip_rows;
+  const auto at = [&](uint64_t offset) { return static_cast<uint8_t*>(workspace) + offset; };
+  float* const strips = space.strips ? reinterpret_cast<float*>(at(space.sums)) : nullptr;
+  if (space.dz || space.strips) {
+    GradRows g{};
+    g.grad = dz;
+    g.preact = layer->activation == LINEAR_NONE ? nullptr : preact;
+    g.dz = space.dz ? at(space.z) : nullptr;
+    g.strips = strips;
+    g.offsets = p.offsets;
+    g.groups = groups;
+    g.strip_rows = space.strip_rows;
+    g.type = layer->type;
+    g.activation = layer->activation;
+    if ((rc = grad_rows(g, s)) != GEMM_OK) return rc;
+    if (space.dz) {
+      dz.ptr = g.dz;
+      dz.ld = copy_ld(dz.cols);
+    }
+  }
+  if (for_x) {
+    if ((rc = as_loaded(&w, space.copy_w, workspace, space.w, sms, s)) != GEMM_OK) return rc;
+    LinearParams px = p;
+    px.out = static_cast<uint16_t*>(grad_x);
+    px.vector = by_vectors(grad_x, layer->in);
+    rc = launch(product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
+                           p.offsets != nullptr),
+                dz, w, px, layer->type, opt, sms, device, s);
+    if (rc != GEMM_OK) return rc;
+  }
+  p.grad_bias = static_cast<uint16_t*>(grad_bias);
+  if (for_w) {
+    if ((rc = as_loaded(&x, space.copy_x, workspace, space.x, sms, s)) != GEMM_OK) return rc;
+    p.out = static_cast<uint16_t*>(grad_w);
+    p.vector = by_vectors(grad_w, layer->in);
+    p.strips = for_bias ? strips : nullptr;
+    rc = launch(product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
+                           p.offsets != nullptr),
+                dz, x, p, layer->type, opt, sms, device, s);
+    if (rc != GEMM_OK || strips) return rc;
+  }
+  if (!for_bias) return GEMM_OK;
+  // Without grad_w, or without rows: then there are no strips either.
+  p.m = static_cast<int32_t>(layer->out);
+  p.groups = groups;
+  p.strips = strips;
+  return sum_strips(p, layer->type, sms, s);
+}
+
+extern "C" int linear_query_config(int product, int64_t rows, int64_t in, int64_t out, int experts,
+                                   linear_config_t* config) {
+  if (!config || product < LINEAR_FORWARD || product > LINEAR_GRAD_W || rows < 1 || in < 1 ||
+      out < 1 || rows > LINEAR_MAX_ROWS || in > LINEAR_MAX_COLS || out > LINEAR_MAX_COLS ||
+      experts < 0 || experts > MOE_MAX_EXPERTS || std::max(experts, 1) * out > INT_MAX)
+    return GEMM_ERR_INVALID_VALUE;
+  Machine machine{152, {76, 36, 15}};
+  int sms = 0, device = 0;
+  if (require_device(&sms, &device) == GEMM_OK) machine = machine_of(sms, device);
+  else cudaGetLastError();
+  Plan plan;
+  const int rc = make_plan(product_of(product, rows, in, out, std::max(experts, 1), experts > 0),
+                           machine, nullptr, &plan);
+  if (rc != GEMM_OK) return rc;
+  *config = linear_config_t{plan.pair ? 1 : 0, plan.tile, plan.split,
+                            plan.units * (plan.pair ? 2 : plan.split)};
+  return GEMM_OK;
+}
+
+extern "C" int linear_get_device_error(void* stream, uint32_t* raw) {
+  const int rc = require_device(nullptr);
+  if (rc != GEMM_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t word = 0;
+  const uint32_t zero = 0;
+  const size_t off = static_cast<size_t>(error_index(s)) * sizeof(uint32_t);
+  if (cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&word, g_linear_error, sizeof(word), off, cudaMemcpyDeviceToHost,
+                                s) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_linear_error, &zero, sizeof(zero), off, cudaMemcpyHostToDevice, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  if (raw) *raw = word;
+  return static_cast<int>(word & 0xffu);
+}

@@ -1,0 +1,307 @@
+// The products of linear layers on single CTAs: tiles of 128 rows of D by 64 to
+// 256 columns.
+//
+// Inside a CTA, one per SM:
+//   warp 0 -- producer: per 64 of the sum, TMA boxes of both operands into a ring;
+//   warp 1 -- MMA issuer, into two accumulators by turns;
+//   warps 2 .. 9 -- epilogue: two warps for each quadrant of lanes, which take
+//       32 columns by turns (linear_finish).
+// The loops of the issuing warps are run by the whole warp, and one lane issues.
+//
+// kSplit: few tiles.  The CTAs of a cluster share one tile, each taking its part of
+// the sum's stages; with all MMAs done and read by everyone's tensor cores,
+// the rings are free, and every CTA writes its sums for each other one's share of
+// the columns into that one's ring, where they are added in the order of the
+// parts.  No sum depends on who came first.
+#pragma once
+#include "linear.cuh"
+
+namespace gb300 {
+
+template <typename T, int kProduct, bool kSplit>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const LinearParams p) {
+  constexpr bool kAMn = a_mn(kProduct), kBMn = b_mn(kProduct);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
+  const uint32_t stage_bytes = kLinABytes + p.tile * (kLinK * 2);
+  const uint32_t bufs = base + stages * stage_bytes;
+  const uint32_t bars = bufs + (kSplit ? 0u : kLinEpiWarps * kLinBufBytes);
+  const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
+  const int tile_step = kSplit ? INT_MAX / 4 : gridDim.x;  // kSplit: one tile
+  const auto full_bar = [&](int s) { return bars + 8u * s; };
+  const auto empty_bar = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
+  const auto tfull_bar = [&](int b) { return bars + 8u * (2 * kLinMaxStages + b); };
+  const auto tempty_bar = [&](int b) { return bars + 8u * (2 * kLinMaxStages + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (2 * kLinMaxStages + 4);
+  uint8_t* const misc = smem + (bars - base) + 8 * kLinBars;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 8);
+  // columns between the accumulators, and those allocated: a power of two
+  const uint32_t acc_cols = p.tile <= 64 ? 64 : p.tile <= 128 ? 128 : 256;
+  const uint32_t tmem_cols = 2 * acc_cols;
+
+  if (threadIdx.x == 0) {
+    grid_launch_dependents();
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), kLinEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (linear_has_sums<kProduct>(p)) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+    }
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == 2) linear_starts<kLinM>(p, start, lane);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = linear_tiles<kProduct>(p, start);
+  // this CTA's stages of a tile's sum
+  const auto stages_of = [&](const LinearTile& t, int* from, int* end) {
+    const int kbs = (t.k_len + kLinK - 1) / kLinK;
+    *from = kSplit ? static_cast<int>(static_cast<int64_t>(part) * kbs / p.split) : 0;
+    *end = kSplit ? static_cast<int>(static_cast<int64_t>(part + 1) * kbs / p.split) : kbs;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ok = true;
+    for (int t = first_tile; ok && t < tiles; t += tile_step) {
+      const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
+      const int a_boxes =
+          kAMn ? (tile.count + 63) >> 6 : (tile.count + p.box_rows - 1) / p.box_rows;
+      const uint32_t a_box_bytes = kAMn ? kLinChunkBytes : p.box_rows * (kLinK * 2);
+      const int b_boxes = kBMn ? (min(p.tile, p.n - tile.col) + 63) >> 6 : 1;
+      const uint32_t b_box_bytes = kBMn ? kLinChunkBytes : p.tile * (kLinK * 2);
+      const uint32_t bytes = a_boxes * a_box_bytes + b_boxes * b_box_bytes;
+      int from, end;
+      stages_of(tile, &from, &end);
+      for (int kb = from; kb < end; ++kb) {
+        if (!linear_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kLinEmpty, p)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t a = base + stage * stage_bytes, b = a + kLinABytes;
+          const uint32_t full = full_bar(stage);
+          const int k = kb * kLinK;
+          mbar_arrive_expect_tx(full, bytes);
+          if (!(p.inject && issued == 0)) {
+            for (int i = 0; i < a_boxes; ++i) {
+              if (kAMn) tma_load_2d(a + i * a_box_bytes, &tmA, full, tile.row + 64 * i, tile.k_row + k);
+              else tma_load_2d(a + i * a_box_bytes, &tmA, full, k, tile.row + i * p.box_rows);
+            }
+            for (int i = 0; i < b_boxes; ++i) {
+              if (kProduct == LINEAR_FORWARD)
+                tma_load_3d(b, &tmB, full, k, tile.col, tile.group);
+              else if (kProduct == LINEAR_GRAD_X)
+                tma_load_3d(b + i * b_box_bytes, &tmB, full, tile.col + 64 * i, k, tile.group);
+              else
+                tma_load_3d(b + i * b_box_bytes, &tmB, full, tile.col + 64 * i, tile.k_row + k, 0);
+            }
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // every load has landed before the CTA may end
+    const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+    for (uint32_t i = first; i < issued; ++i)
+      linear_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    const uint64_t a_desc0 = linear_desc<kAMn>(base);
+    const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
+    for (int t = first_tile; ok && t < tiles; t += tile_step) {
+      const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
+      const int cols = min(p.tile, p.n - tile.col);
+      const uint32_t idesc = linear_idesc<T, kProduct>(kLinM, (cols + 15) & ~15);
+      if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem + acc * acc_cols;
+      int from, end;
+      stages_of(tile, &from, &end);
+      for (int kb = from; kb < end; ++kb) {
+        if (!linear_wait_warp(full_bar(stage), phase, abort_flag, kLinFull, p)) {
+          ok = false;
+          break;
+        }
+        if (kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb, p)) {
+          const uint32_t a = base + stage * stage_bytes;
+          const int valid = tile.k_len - kb * kLinK;
+          linear_zero_rows(a, kLinM / 64, valid, lane);
+          linear_zero_rows(a + kLinABytes, p.tile / 64, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after_sync();
+        const int steps = linear_steps(tile, kb);
+        if (elect_one()) {
+          const uint64_t at = static_cast<uint64_t>((stage * stage_bytes) >> 4);
+          const uint64_t a_desc = a_desc0 + at, b_desc = b_desc0 + at;
+          if (steps == kLinK / 16) {
+#pragma unroll
+            for (int s = 0; s < kLinK / 16; ++s)
+              umma_f16(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
+                       b_desc + s * linear_desc_step<kBMn>(), idesc, kb != from || s != 0);
+          } else {
+            for (int s = 0; s < steps; ++s)
+              umma_f16(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
+                       b_desc + s * linear_desc_step<kBMn>(), idesc, kb != from || s != 0);
+          }
+          umma_commit(empty_bar(stage));
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(tfull_bar(acc));
+      __syncwarp();
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (elect_one()) umma_commit(drain_bar);
+    __syncwarp();
+    linear_wait_drain(drain_bar, 0, p.timeout_ns);
+  } else if (!kSplit) {
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3;               // the lane quadrant this warp may read
+    const int half = (warp - 2) >> 2;
+    const uint32_t buf = bufs + (warp - 2) * kLinBufBytes;
+    if (kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = first_tile; t < tiles; t += tile_step) {
+      const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
+      const int live = min(32, tile.count - 32 * q);  // rows of this quadrant, if any
+      const int chunks = live > 0 ? (min(p.tile, p.n - tile.col) + 31) >> 5 : 0;
+      const int64_t row = linear_out_row<kProduct>(tile, p) + 32 * q;
+      LinearExtras x;
+      if (half < chunks)
+        x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * half, lane);
+      if (!linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p)) break;
+      tc_fence_after_sync();
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
+      const auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
+      };
+      for (int c = half; c < chunks; c += 2) {
+        uint32_t r[32];
+        linear_sums(t_row + 32 * c, tile.k_len > 0, r);
+        if (c + 2 >= chunks) release();
+        linear_put_row(buf, lane, r);
+        __syncwarp();
+        linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, row, live, tile.col + 32 * c, lane);
+        __syncwarp();
+        if (c + 2 < chunks)
+          x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * (c + 2), lane);
+      }
+      if (half >= chunks) release();
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    linear_zero_tail<kProduct>(p, start);
+  }
+  if (kSplit) {
+    // ---------------------------------------------------------- parts to their owners
+    // Chunk c of 32 columns belongs to CTA c / mine.  A buffer of the ring for each
+    // part, quadrant and chunk of one's own.
+    const bool live_tile = first_tile < tiles;
+    LinearTile tile = {};
+    if (live_tile) tile = linear_tile<kProduct, kLinM>(first_tile, p, start);
+    const int mine = p.tile / 32 / p.split;
+    const int cols = min(p.tile, p.n - tile.col);
+    const int quads = (tile.count + 31) >> 5;
+    const auto slot = [&](int s, int q, int c) {
+      return base + static_cast<uint32_t>((s * 4 + q) * mine + c) * kLinBufBytes;
+    };
+    if (warp >= 2 && kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
+    int ok = 1;
+    if (warp >= 2 && live_tile) ok = linear_wait_warp(tfull_bar(0), 0, abort_flag, kLinTmemFull, p);
+    __syncwarp();
+    cluster_sync();  // all rings are free
+    if (warp >= 2 && live_tile && ok) {
+      tc_fence_after_sync();
+      int from, end;
+      stages_of(tile, &from, &end);
+      const int q = warp & 3, half = (warp - 2) >> 2;
+      for (int c = half; q < quads && 32 * c < cols; c += 2) {
+        uint32_t r[32];
+        linear_sums(tmem + (static_cast<uint32_t>(q * 32) << 16) + 32 * c, end > from, r);
+        const int owner = c / mine;
+        const uint32_t to = mapa_shared(slot(part, q, c - owner * mine), owner);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_cluster_v4(linear_piece(to, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2],
+                        r[4 * j + 3]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // all parts have come
+    if (warp >= 2) {
+      if (live_tile && ok) {
+        for (int i = warp - 2; i < quads * mine; i += kLinEpiWarps) {
+          const int c = i / quads, q = i - c * quads;
+          const int col = tile.col + 32 * (part * mine + c);
+          if (col >= p.n) break;
+          const int live = min(32, tile.count - 32 * q);
+          const int64_t row = linear_out_row<kProduct>(tile, p) + 32 * q;
+          LinearExtras x = linear_extras<kProduct>(p, tile.group, row, live, col, lane);
+          linear_finish<T, kProduct>(slot(0, q, c), p.split, 4 * mine * kLinBufBytes, p, x,
+                                     tile.group, row, live, col, lane);
+        }
+      }
+      linear_zero_tail<kProduct>(p, start);
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+}  // namespace gb300

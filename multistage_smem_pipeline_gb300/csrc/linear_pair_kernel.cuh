@@ -1,0 +1,312 @@
+// The products of linear layers over CTA pairs (tcgen05 cta_group::2): tiles of
+// 256 rows of D by 256 columns.
+//
+// Each CTA loads its own 128 rows of A and its half of B's columns, 32 KiB per 64 of
+// the sum where a single CTA's 128 x 256 tile takes 48; the even CTA issues, and
+// each accumulates its 128 rows in its own tensor memory, in two accumulators by
+// turns.
+//
+// Barriers as in the other pair kernels: `full` in the even CTA counts both CTAs'
+// bytes; `empty` and `tfull` are in both, committed to both; `tempty` in the even
+// CTA takes every epilogue warp of both.  grad_w's ragged stages (see linear.cuh)
+// are different: each CTA has to zero rows of its own, so their loads count on
+// each CTA's own `full`, and the odd CTA's second warp, idle otherwise, zeroes its
+// rows and says so on `ready` of the even one.
+#pragma once
+#include "linear.cuh"
+
+namespace gb300 {
+
+constexpr int kLinPairTile = 256;
+constexpr uint32_t kLinPairStage = kLinABytes + kLinPairTile / 2 * kLinK * 2;
+
+template <typename T, int kProduct>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const LinearParams p) {
+  constexpr bool kAMn = a_mn(kProduct), kBMn = b_mn(kProduct);
+  constexpr bool kWeight = kProduct == LINEAR_GRAD_W;
+  constexpr int kHeight = 2 * kLinM;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stages = p.stages;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  constexpr uint16_t kBoth = 0x3;
+  const uint32_t bufs = base + stages * kLinPairStage;
+  const uint32_t bars = bufs + kLinEpiWarps * kLinBufBytes;
+  const auto full_bar = [&](int s) { return bars + 8u * s; };
+  const auto empty_bar = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
+  const auto ready_bar = [&](int s) { return bars + 8u * (2 * kLinMaxStages + s); };
+  const auto tfull_bar = [&](int b) { return bars + 8u * (3 * kLinMaxStages + b); };
+  const auto tempty_bar = [&](int b) { return bars + 8u * (3 * kLinMaxStages + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (3 * kLinMaxStages + 4);
+  uint8_t* const misc = smem + (bars - base) + 8 * kLinBars;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 8);
+
+  if (threadIdx.x == 0) {
+    grid_launch_dependents();
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(ready_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * kLinEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (linear_has_sums<kProduct>(p)) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers exist, and both are running
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * kLinPairTile);
+    tmem_relinquish_pair();
+  }
+  grid_dependency_wait();
+  if (warp == 2) linear_starts<kHeight>(p, start, lane);
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = linear_tiles<kProduct>(p, start);
+  // columns of B that a CTA holds: half of the tile's, to 16
+  const auto half_cols = [&](const LinearTile& t) {
+    return (min(kLinPairTile, p.n - t.col) + 31) >> 5 << 4;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0, issued = 0;
+    uint32_t own_phase = 0;  // odd CTA: bit s is the parity of its own full_bar(s)
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
+      const int mine = min(kLinM, tile.count - rank * kLinM);  // rows; may be none
+      const int theirs = min(kLinM, tile.count - (1 - rank) * kLinM);
+      const int half = half_cols(tile);
+      // boxes of a CTA with `rows` rows: at least one, so that both always load
+      const auto a_boxes_of = [&](int rows) {
+        return max(1, kAMn ? (rows + 63) >> 6 : (rows + p.box_rows - 1) / p.box_rows);
+      };
+      const int a_boxes = a_boxes_of(mine);
+      const uint32_t a_box_bytes = kAMn ? kLinChunkBytes : p.box_rows * (kLinK * 2);
+      const int b_boxes = kBMn ? (half + 63) >> 6 : 1;
+      const uint32_t b_bytes = kBMn ? b_boxes * kLinChunkBytes : kLinPairTile / 2 * kLinK * 2;
+      const uint32_t own_bytes = a_boxes * a_box_bytes + b_bytes;
+      const uint32_t both_bytes = own_bytes + a_boxes_of(theirs) * a_box_bytes + b_bytes;
+      const int row = tile.row + rank * kLinM;
+      const int col = tile.col + rank * half;
+      const int kbs = (tile.k_len + kLinK - 1) / kLinK;
+      for (int kb = 0; kb < kbs; ++kb) {
+        if (!linear_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kLinEmpty, p)) {
+          ok = false;
+          break;
+        }
+        const bool ragged = kWeight && linear_ragged(tile, kb, p);
+        if (elect_one()) {
+          const uint32_t a = base + stage * kLinPairStage, b = a + kLinABytes;
+          const uint32_t full = ragged ? mapa_shared(full_bar(stage), rank)
+                                       : mapa_shared(full_bar(stage), 0);
+          const int k = kb * kLinK;
+          if (ragged) mbar_arrive_expect_tx(full_bar(stage), own_bytes);
+          else if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), both_bytes);
+          if (!(p.inject && issued == 0 && rank == 0)) {
+            for (int i = 0; i < a_boxes; ++i) {
+              if (kAMn) tma_load_2d_pair(a + i * a_box_bytes, &tmA, full, row + 64 * i, tile.k_row + k);
+              else tma_load_2d_pair(a + i * a_box_bytes, &tmA, full, k, row + i * p.box_rows);
+            }
+            for (int i = 0; i < b_boxes; ++i) {
+              if (kProduct == LINEAR_FORWARD)
+                tma_load_3d_pair(b, &tmB, full, k, col, tile.group);
+              else if (kProduct == LINEAR_GRAD_X)
+                tma_load_3d_pair(b + i * kLinChunkBytes, &tmB, full, col + 64 * i, k, tile.group);
+              else
+                tma_load_3d_pair(b + i * kLinChunkBytes, &tmB, full, col + 64 * i, tile.k_row + k, 0);
+            }
+          }
+        }
+        __syncwarp();
+        if (ragged) own_phase ^= 1u << stage;
+        ++issued;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (rank == 0) {  // both CTAs' bytes, but for those of ragged stages
+      const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+      for (uint32_t i = first; i < issued; ++i)
+        linear_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
+    } else if (kWeight) {
+      for (int s = 0; s < stages; ++s)  // the last ragged load of each slot
+        linear_wait_drain(full_bar(s), ((own_phase >> s) & 1u) ^ 1u, p.timeout_ns);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------------------------------------------------- MMA issuer
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0, ready_phase = 0;
+    bool ok = true;
+    const uint64_t a_desc0 = linear_desc<kAMn>(base);
+    const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
+      const uint32_t idesc = linear_idesc<T, kProduct>(kHeight, 2 * half_cols(tile));
+      if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
+      tc_fence_after_sync();
+      const uint32_t d_tmem = tmem + acc * kLinPairTile;
+      const int kbs = (tile.k_len + kLinK - 1) / kLinK;
+      for (int kb = 0; kb < kbs; ++kb) {
+        if (!linear_wait_warp(full_bar(stage), phase, abort_flag, kLinFull, p)) {
+          ok = false;
+          break;
+        }
+        if (kWeight && linear_ragged(tile, kb, p)) {
+          const uint32_t a = base + stage * kLinPairStage;
+          const int valid = tile.k_len - kb * kLinK;
+          linear_zero_rows(a, kLinM / 64, valid, lane);
+          linear_zero_rows(a + kLinABytes, kLinPairTile / 128, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (!linear_wait_warp<true>(ready_bar(stage), (ready_phase >> stage) & 1u, abort_flag,
+                                      kLinPeer, p)) {
+            ok = false;
+            break;
+          }
+          ready_phase ^= 1u << stage;
+        }
+        tc_fence_after_sync();
+        const int steps = linear_steps(tile, kb);
+        if (elect_one()) {
+          const uint64_t at = static_cast<uint64_t>((stage * kLinPairStage) >> 4);
+          const uint64_t a_desc = a_desc0 + at, b_desc = b_desc0 + at;
+          if (steps == kLinK / 16) {
+#pragma unroll
+            for (int s = 0; s < kLinK / 16; ++s)
+              umma_f16_pair(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
+                            b_desc + s * linear_desc_step<kBMn>(), idesc, (kb | s) != 0);
+          } else {
+            for (int s = 0; s < steps; ++s)
+              umma_f16_pair(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
+                            b_desc + s * linear_desc_step<kBMn>(), idesc, (kb | s) != 0);
+          }
+          umma_commit_pair_mc(empty_bar(stage), kBoth);
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kBoth);
+      __syncwarp();
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (elect_one()) umma_commit_pair_mc(drain_bar, 0x1);
+    __syncwarp();
+    linear_wait_drain(drain_bar, 0, p.timeout_ns);
+    // the last remote arrivals on this CTA's barriers have landed
+    for (int b = 0; b < 2; ++b) {
+      linear_wait_drain(tempty_bar(acc), acc_phase ^ 1u, p.timeout_ns);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- odd CTA's ragged stages
+    if (kWeight && p.offsets) {
+      int stage = 0;
+      uint32_t own_phase = 0;
+      for (int t = pair; t < tiles; t += pairs) {
+        const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
+        const int kbs = (tile.k_len + kLinK - 1) / kLinK;
+        if (kbs == 0) continue;
+        stage = (stage + kbs - 1) % stages;  // that of the tile's last
+        if (linear_ragged(tile, kbs - 1, p)) {
+          if (!linear_wait_warp(full_bar(stage), (own_phase >> stage) & 1u, abort_flag, kLinFull, p))
+            break;
+          own_phase ^= 1u << stage;
+          const uint32_t a = base + stage * kLinPairStage;
+          const int valid = tile.k_len - (kbs - 1) * kLinK;
+          linear_zero_rows(a, kLinM / 64, valid, lane);
+          linear_zero_rows(a + kLinABytes, kLinPairTile / 128, valid, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(ready_bar(stage), 0));
+          __syncwarp();
+        }
+        if (++stage == stages) stage = 0;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue (both CTAs)
+    const int q = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const uint32_t buf = bufs + (warp - 2) * kLinBufBytes;
+    if (kWeight) linear_sum_strips<T>(p, start);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = pair; t < tiles; t += pairs) {
+      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
+      const int live = min(32, tile.count - rank * kLinM - 32 * q);
+      const int chunks = live > 0 ? (min(kLinPairTile, p.n - tile.col) + 31) >> 5 : 0;
+      const int64_t row = linear_out_row<kProduct>(tile, p) + rank * kLinM + 32 * q;
+      LinearExtras x;
+      if (half < chunks)
+        x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * half, lane);
+      if (!linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p)) break;
+      tc_fence_after_sync();
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kLinPairTile;
+      const uint32_t leader_tempty = mapa_shared(tempty_bar(acc), 0);
+      const auto release = [&] {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(leader_tempty);
+      };
+      for (int c = half; c < chunks; c += 2) {
+        uint32_t r[32];
+        linear_sums(t_row + 32 * c, tile.k_len > 0, r);
+        if (c + 2 >= chunks) release();
+        linear_put_row(buf, lane, r);
+        __syncwarp();
+        linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, row, live, tile.col + 32 * c, lane);
+        __syncwarp();
+        if (c + 2 < chunks)
+          x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * (c + 2), lane);
+      }
+      if (half >= chunks) release();
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    linear_zero_tail<kProduct>(p, start);
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 2 * kLinPairTile);
+  }
+}
+
+}  // namespace gb300

@@ -1,0 +1,42 @@
+// What linear layers do with rows before their products (linear_rows.cu).
+#pragma once
+#include "linear.cuh"
+
+namespace gb300 {
+
+// Rows of `cols` elements, `ld` apart.
+struct Rows {
+  const void* ptr;
+  int64_t rows, cols, ld;
+};
+
+// The kernels' tensor maps take these rows as they are.
+inline bool loads_as_is(const Rows& r) { return aligned_to(r.ptr, 16) && r.ld % 8 == 0; }
+// Elements between the rows of a copy that they can take.
+__host__ __device__ inline int64_t copy_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+// dst (16-byte aligned, copy_ld(src.cols) between rows) = src.
+int copy_rows(void* dst, const Rows& src, int sms, cudaStream_t stream);
+
+// Rows of a strip for `rows` rows: 64, more where that would be over 512 strips.
+inline int strip_rows_for(int64_t rows) {
+  int64_t s = 64;
+  while (rows / s > 512) s *= 2;
+  return static_cast<int>(s);
+}
+
+// dz = grad_out act'(preact), for the rows that are in a group.
+struct GradRows {
+  Rows grad;                 // grad_out
+  const void* preact;        // contiguous; null for LINEAR_NONE
+  void* dz;                  // copy_ld(cols) between rows; or null
+  float* strips;             // sums of dz over strips of rows; or null
+  const int32_t* offsets;    // or null: one group
+  int groups, strip_rows, type, activation;
+};
+int grad_rows(const GradRows& g, cudaStream_t stream);
+
+// grad_bias from the strips alone (else a product's kernel does that).
+int sum_strips(const LinearParams& p, int type, int sms, cudaStream_t stream);
+
+}  // namespace gb300

@@ -133,6 +133,19 @@ __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 
+template <typename T>
+__device__ __forceinline__ uint32_t pack_two(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack_two<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack_two<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Eight neighbouring 16-bit elements.
 struct alignas(16) Pack {
   uint32_t w[4];
@@ -220,6 +233,44 @@ __device__ __forceinline__ void clip8(float (&f)[8], int e, int n) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (e + i < 0 || e + i >= n) f[i] = 0.0f;
+}
+
+// ------------------------------------------------------------------ groups by offsets
+// A group by offsets, in shared memory: every role looks each tile's group up
+// (from global memory: 129.0 us for 4096 tokens x 8 of 64 experts, against 128.2).
+struct GroupStart {
+  int32_t tiles;  // row tiles of the groups before it
+  int32_t row;    // its first row
+};
+
+// Where each group starts, and the end, by one warp.  All offsets of 128 groups
+// are asked for at once: nothing can be loaded before this is done, and one
+// latency of memory is 0.4 us.
+template <int kBN>
+__device__ __forceinline__ void find_groups(const int32_t* offsets, int groups, GroupStart* start,
+                                            int lane) {
+  constexpr int kAhead = 4;
+  int32_t total = 0;
+  for (int g0 = 0; g0 <= groups; g0 += 32 * kAhead) {
+    int32_t row[kAhead + 1];
+#pragma unroll
+    for (int i = 0; i <= kAhead; ++i) row[i] = offsets[min(g0 + 32 * i + lane, groups)];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int g = g0 + 32 * i + lane;
+      const int32_t next = __shfl_down_sync(0xffffffffu, row[i], 1);
+      const int32_t first = __shfl_sync(0xffffffffu, row[i + 1], 0);
+      const int32_t n = ((lane < 31 ? next : first) - row[i] + kBN - 1) / kBN;  // 0 past the last
+      int32_t upto = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      if (g <= groups) start[g] = GroupStart{total + upto - n, row[i]};
+      total += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
 }
 
 }  // namespace gb300

@@ -188,22 +188,6 @@ __device__ __forceinline__ void store_chunk_direct(uint32_t buf, uint16_t* D, in
   }
 }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // The C term of the scaled epilogue for the warp's 32 x 32 chunk (rows
 // [m0, m0 + 32), columns [col, col + 32)), copied into the warp's staging
 // buffer `buf` (free to overwrite) with cp.async, in the layout of the
