@@ -281,6 +281,21 @@ __device__ __forceinline__ void linear_zero_rows(uint32_t at, int chunks, int va
 }
 
 // ------------------------------------------------------------------ epilogue
+// 1 / (1 + e^-u) and 1 / (1 + e^u), with their relative accuracy on both sides: the
+// exponential is at most 1, the denominator between 1 and 2.
+struct Sigmoids {
+  float up, down;
+};
+__device__ __forceinline__ Sigmoids sigmoids(float u) {
+  const float e = __expf(-fabsf(u)), r = __fdividef(1.0f, 1.0f + e), s = e * r;
+  return u < 0.0f ? Sigmoids{s, r} : Sigmoids{r, s};
+}
+
+// (1 + tanh u) / 2 is the sigmoid of 2u; 1.5957691 = 2 sqrt(2 / pi).
+__device__ __forceinline__ float gelu_tanh_argument(float z) {
+  return 1.5957691f * z * fmaf(0.044715f, z * z, 1.0f);
+}
+
 __device__ __forceinline__ float activate(float z, int activation) {
   switch (activation) {
     case LINEAR_RELU:
@@ -288,10 +303,9 @@ __device__ __forceinline__ float activate(float z, int activation) {
     case LINEAR_GELU:
       return 0.5f * z * erfcf(z * -0.70710678f);  // erfc: no cancellation far below 0
     case LINEAR_GELU_TANH:
-      // z (1 + tanh u) / 2 = z / (1 + e^(-2u)), again without cancellation
-      return __fdividef(z, 1.0f + __expf(-1.5957691f * z * fmaf(0.044715f, z * z, 1.0f)));
+      return z * sigmoids(gelu_tanh_argument(z)).up;
     case LINEAR_SILU:
-      return __fdividef(z, 1.0f + __expf(-z));
+      return z * sigmoids(z).up;
     default:
       return z;
   }
@@ -307,16 +321,12 @@ __device__ __forceinline__ float activation_slope(float z, int activation) {
     case LINEAR_GELU:
       return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678f));
     case LINEAR_GELU_TANH: {
-      const float u = 1.5957691f * z * fmaf(0.044715f, z * z, 1.0f);
-      const float du = fmaf(0.21406459f, z * z, 1.5957691f);
-      const float up = __fdividef(1.0f, 1.0f + __expf(-u));
-      const float down = __fdividef(1.0f, 1.0f + __expf(u));
-      return up + z * du * (up * down);
+      const Sigmoids s = sigmoids(gelu_tanh_argument(z));
+      return fmaf(z * fmaf(0.21406445f, z * z, 1.5957691f), s.up * s.down, s.up);
     }
     case LINEAR_SILU: {
-      const float up = __fdividef(1.0f, 1.0f + __expf(-z));
-      const float down = __fdividef(1.0f, 1.0f + __expf(z));
-      return up * fmaf(z, down, 1.0f);
+      const Sigmoids s = sigmoids(z);
+      return s.up * fmaf(z, s.down, 1.0f);
     }
     default:
       return 1.0f;
