@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const Fp4GemmParams p) {
   constexpr int kBN = kGemmBN;
   static_assert(kBN == kTileRows, "a row tile is a scale tile");
+  static_assert(kBN == 1 << 7, "find_groups below");
   using S = Fp4GemmShape<kFormat>;
   constexpr int kChunks = chunks_per_stage(kFormat);
   extern __shared__ uint8_t smem_raw[];
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) find_groups<kBN>(p.offsets, p.groups, start, lane);
+  if (p.offsets && warp == 2) find_groups(p.offsets, p.groups, start, lane, 7);
   tc_fence_before_sync();
   if (kSplit) cluster_sync();  // the others' barriers exist
   else __syncthreads();

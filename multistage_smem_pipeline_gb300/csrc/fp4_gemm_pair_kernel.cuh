@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                   const __grid_constant__ CUtensorMap tmSX, const Fp4GemmParams p) {
   using S = Fp4PairShape<kFormat>;
   constexpr int kBN = S::kBN;
+  static_assert(kBN == 1 << 8, "find_groups below");
   constexpr int kChunks = chunks_per_stage(kFormat);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tmem_relinquish_pair();
   }
   grid_dependency_wait();
-  if (p.offsets && warp == 2) find_groups<kBN>(p.offsets, p.groups, start, lane);
+  if (p.offsets && warp == 2) find_groups(p.offsets, p.groups, start, lane, 8);
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();

@@ -50,17 +50,18 @@ int check_layer(const linear_t* l) {
   return groups_of(l) * l->out <= INT_MAX ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
-bool valid_form(int pair, int tile, int split) {
+// `product`: LINEAR_*, or -1 for any.
+bool valid_form(int product, int pair, int tile, int split) {
   if (pair) return pair == 1 && tile == 256 && split == 1;
-  if (tile != 64 && tile != 128 && tile != 192 && tile != 256) return false;
-  return split == 1 || ((split == 2 || split == 4 || split == 8) && tile / 32 % split == 0);
+  if (tile != 64 && tile != 128 && tile != 256 && (tile != 32 || product == LINEAR_GRAD_W)) return false;
+  return split == 1 || split == 2 || split == 4 || split == 8;
 }
 
 int check_options(const linear_options_t* o) {
   if (!o) return GEMM_OK;
   if (o->inject < 0 || o->inject > 1) return GEMM_ERR_INVALID_VALUE;
   if (o->tile == 0 && o->cta_pair == 0 && o->split_k == 0) return GEMM_OK;
-  return valid_form(o->cta_pair, o->tile, o->split_k) ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+  return valid_form(-1, o->cta_pair, o->tile, o->split_k) ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }
 
 // The offsets of a layer's groups; null for one group (and for rows of nobody).
@@ -107,13 +108,13 @@ Machine machine_of(int sms, int device) {
 struct Plan {
   bool pair;
   int tile, split;
-  int m_tiles, n_tiles;  // m_tiles: grad_w's, of a group
+  int m_tiles, n_tiles;  // n_tiles: grad_w's, of a group
   int box_rows;
   int units;             // CTAs, pairs or clusters
 };
 
-// A product: D's rows (of all groups together, but of one for grad_w) and columns,
-// the sums' length, in groups; `ragged`: by offsets.
+// A product as the tensor cores see it: m by n, n over all groups but for grad_w, whose
+// sums are (k); `ragged`: groups by offsets.
 struct Product {
   int kind;
   int64_t m, n, k;
@@ -123,28 +124,28 @@ struct Product {
 
 Product product_of(int kind, int64_t rows, int64_t in, int64_t out, int64_t groups, bool ragged) {
   switch (kind) {
-    case LINEAR_FORWARD: return Product{kind, rows, out, in, groups, ragged};
-    case LINEAR_GRAD_X: return Product{kind, rows, in, out, groups, ragged};
+    case LINEAR_FORWARD: return Product{kind, out, rows, in, groups, ragged};
+    case LINEAR_GRAD_X: return Product{kind, in, rows, out, groups, ragged};
     default: return Product{kind, out, in, rows, groups, ragged};
   }
 }
 
-// Row tiles of height `h` of all groups: as many as are expected, or as there can be.
-int64_t row_tiles(const Product& p, int64_t h, bool most) {
-  if (p.kind == LINEAR_GRAD_W) return p.groups * ((p.m + h - 1) / h);
-  if (!p.ragged) return (p.m + h - 1) / h;
-  const int64_t live = std::min(p.groups, p.m);
+// Tiles of N of all groups: as many as are expected, or as there can be.
+int64_t n_tiles(const Product& p, int64_t tile, bool most) {
+  if (p.kind == LINEAR_GRAD_W) return p.groups * ((p.n + tile - 1) / tile);
+  if (!p.ragged) return (p.n + tile - 1) / tile;
+  const int64_t live = std::min(p.groups, p.n);
   // a group is taken to end half way through its last tile
-  return most ? p.m / h + live : std::max(live, (2 * p.m + live * h) / (2 * h));
+  return most ? p.n / tile + live : std::max(live, (2 * p.n + live * tile) / (2 * tile));
 }
 
 int make_plan(const Product& p, const Machine& machine, const linear_options_t* forced, Plan* o) {
   const bool weight = p.kind == LINEAR_GRAD_W;
   // of a group, in the mean
   const int64_t k = weight && p.ragged ? (p.k + p.groups - 1) / p.groups : p.k;
-  const int64_t tile_rows = weight ? p.m : p.ragged ? (p.m + p.groups - 1) / p.groups : p.m;
+  const int64_t n = !weight && p.ragged ? (p.n + p.groups - 1) / p.groups : p.n;
   const double kbs = std::max<double>(1.0, static_cast<double>((k + kLinK - 1) / kLinK));
-  const auto n_tiles = [&](int64_t tile) { return (p.n + tile - 1) / tile; };
+  const auto m_tiles = [&](bool pair) { return pair ? (p.m + 255) / 256 : (p.m + 127) / 128; };
   double least = 0.0;
   o->tile = 0;
   const auto offer = [&](bool pair, int tile, int split, double cycles) {
@@ -155,35 +156,35 @@ int make_plan(const Product& p, const Machine& machine, const linear_options_t* 
     o->split = split;
   };
   if (forced && forced->tile != 0) {
+    if (!valid_form(p.kind, forced->cta_pair, forced->tile, forced->split_k))
+      return GEMM_ERR_INVALID_VALUE;
     offer(forced->cta_pair != 0, forced->tile, forced->split_k, 0.0);
   } else {
     // Cycles of the waves of tiles.  Operands come in at about 60 bytes a cycle and
-    // SM; an MMA of 128 rows takes half a cycle a column, and 100 at least.
+    // SM; an MMA takes half a cycle a column, and 100 at least.
     const auto waves = [&](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    offer(true, 256, 1, waves(row_tiles(p, 256, false) * n_tiles(256), machine.sms / 2) * (2500 + 540 * kbs));
-    for (int tile : {256, 192, 128, 64}) {
-      const int64_t tiles = row_tiles(p, 128, false) * n_tiles(tile);
-      const double rows = static_cast<double>(std::min<int64_t>(128, tile_rows));
-      const double stage = std::max({2.0 * tile, 400.0, (rows * 128 + tile * 128) / 60.0});
+    offer(true, 256, 1, waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) * (2500 + 540 * kbs));
+    for (int tile : {256, 128, 64, 32}) {
+      if (!valid_form(p.kind, 0, tile, 1)) continue;
+      const int64_t tiles = n_tiles(p, tile, false) * m_tiles(false);
+      const double cols = static_cast<double>(std::min<int64_t>(tile, n));
+      const double stage = std::max({2.0 * cols, 400.0, (kLinABytes + cols * 128) / 60.0});
       offer(false, tile, 1, waves(tiles, machine.sms) * (2500 + stage * kbs));
       for (int i = 0; i < 3; ++i) {
         const int split = 2 << i;
-        if (!valid_form(0, tile, split) || row_tiles(p, 128, true) * n_tiles(tile) > machine.clusters[i] ||
-            kbs < 2 * split)
-          continue;
-        offer(false, tile, split, 4500 + 10.0 * rows + stage * kbs / split);
+        if (n_tiles(p, tile, true) * m_tiles(false) > machine.clusters[i] || kbs < 2 * split) continue;
+        offer(false, tile, split, 4500 + 10.0 * cols + stage * kbs / split);
       }
     }
   }
-  const int64_t h = o->pair ? 256 : 128;
-  const int64_t most = row_tiles(p, h, true) * n_tiles(o->tile);
+  const int64_t most = n_tiles(p, o->tile, true) * m_tiles(o->pair);
   // counted in 32 bits, with room for a grid's stride past the last
   if (most > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
-  o->m_tiles = weight ? static_cast<int>((p.m + h - 1) / h) : 0;
-  o->n_tiles = static_cast<int>(n_tiles(o->tile));
+  o->m_tiles = static_cast<int>(m_tiles(o->pair));
+  o->n_tiles = weight ? static_cast<int>((p.n + o->tile - 1) / o->tile) : 0;
   // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile loads
   // little more than it has.
-  o->box_rows = p.ragged || p.m <= 64 ? 32 : 128;
+  o->box_rows = std::min(p.ragged || p.n <= 64 ? 32 : 128, o->tile);
   o->units = static_cast<int>(o->split > 1 ? most : std::min<int64_t>(o->pair ? machine.sms / 2 : machine.sms, most));
   return GEMM_OK;
 }
@@ -226,18 +227,20 @@ int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaS
   return go(linear_tc<T, kProduct, false>, granted[2], plan.units, 1);
 }
 
-// One product of operands that the tensor maps take as they are: a is x or dz, b is w
-// or (grad_w) x.
+// One product of operands that the tensor maps take as they are: `a` is that of M, w or
+// (grad_w) dz, and `b` that of N, x or dz.
 int launch(const Product& pr, const Rows& a, const Rows& b, LinearParams p, int type,
            const linear_options_t* opt, int sms, int device, cudaStream_t s) {
   Plan plan;
   int rc = make_plan(pr, machine_of(sms, device), opt, &plan);
   if (rc != GEMM_OK) return rc;
-  p.n = static_cast<int32_t>(pr.n);
+  const bool weight = pr.kind == LINEAR_GRAD_W;
+  p.n = static_cast<int32_t>(weight ? pr.n : pr.m);
+  p.m = weight ? static_cast<int32_t>(pr.m) : 0;
   p.k = static_cast<int32_t>(pr.k);
-  p.m = pr.kind == LINEAR_GRAD_W ? static_cast<int32_t>(pr.m) : 0;
   p.groups = static_cast<int32_t>(pr.groups);
   p.tile = plan.tile;
+  while (1 << p.tile_shift < p.tile) ++p.tile_shift;
   p.m_tiles = plan.m_tiles;
   p.n_tiles = plan.n_tiles;
   p.box_rows = plan.box_rows;
@@ -250,12 +253,11 @@ int launch(const Product& pr, const Rows& a, const Rows& b, LinearParams p, int 
   if (pr.k > 0) {
     EncodeTiledFn fn = nullptr;
     if ((rc = get_encoder(&fn)) != GEMM_OK) return rc;
-    const bool weight = pr.kind == LINEAR_GRAD_W;
-    const uint32_t a_box = weight ? 64 : plan.box_rows;
-    const uint32_t b_box = pr.kind == LINEAR_FORWARD ? (plan.pair ? 128 : plan.tile) : 64;
     const int64_t matrices = weight ? 1 : pr.groups;
-    if ((rc = encode(fn, &m.a, a.ptr, a.cols, a.rows, a.ld, 1, a_box, 2)) != GEMM_OK ||
-        (rc = encode(fn, &m.b, b.ptr, b.cols, b.rows / matrices, b.ld, matrices, b_box, 3)) != GEMM_OK)
+    if ((rc = encode(fn, &m.a, a.ptr, a.cols, a.rows / matrices, a.ld, matrices,
+                     pr.kind == LINEAR_FORWARD ? kLinM : 64, 3)) != GEMM_OK ||
+        (rc = encode(fn, &m.b, b.ptr, b.cols, b.rows, b.ld, 1, weight ? 64 : plan.box_rows, 2)) !=
+            GEMM_OK)
       return rc;
   }
   const auto by_type = [&](auto t) {
@@ -328,14 +330,12 @@ int check_workspace(const void* workspace, uint64_t bytes, uint64_t needed) {
   return aligned_to(workspace, 16) ? GEMM_OK : GEMM_ERR_MISALIGNED;
 }
 
-// The rows, or their copy at `at` of the workspace.
-int as_loaded(Rows* r, bool copied, void* workspace, uint64_t at, int sms, cudaStream_t s) {
-  if (!copied) return GEMM_OK;
-  void* const dst = static_cast<uint8_t*>(workspace) + at;
-  const int rc = copy_rows(dst, *r, sms, s);
-  r->ptr = dst;
+// Has rows copied to `at` of the workspace, and takes them from there.
+void copied(Rows* r, PrepareRows* p, int which, void* workspace, uint64_t at) {
+  p->from[which] = *r;
+  p->to[which] = static_cast<uint8_t*>(workspace) + at;
+  r->ptr = p->to[which];
   r->ld = copy_ld(r->cols);
-  return rc;
 }
 
 bool by_vectors(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
@@ -393,9 +393,11 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
   int sms = 0, device = 0;
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if ((rc = as_loaded(&x, space.copy_x, workspace, space.x, sms, s)) != GEMM_OK ||
-      (rc = as_loaded(&w, space.copy_w, workspace, space.w, sms, s)) != GEMM_OK)
-    return rc;
+  PrepareRows prepare{};
+  prepare.type = layer->type;
+  if (space.copy_x) copied(&x, &prepare, 0, workspace, space.x);
+  if (space.copy_w) copied(&w, &prepare, 1, workspace, space.w);
+  if ((rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
   LinearParams p;
   std::memset(&p, 0, sizeof(p));
   p.out = static_cast<uint16_t*>(out);
@@ -410,7 +412,7 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
              (!residual || by_vectors(residual, res.ld));
   return launch(product_of(LINEAR_FORWARD, layer->rows, layer->in, layer->out, groups,
                            p.offsets != nullptr),
-                x, w, p, layer->type, opt, sms, device, s);
+                w, x, p, layer->type, opt, sms, device, s);
 }
 
 extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, const linear_t* layer,
@@ -459,36 +461,36 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   p.strip_rows = space.strip_rows;
   const auto at = [&](uint64_t offset) { return static_cast<uint8_t*>(workspace) + offset; };
   float* const strips = space.strips ? reinterpret_cast<float*>(at(space.sums)) : nullptr;
+  PrepareRows prepare{};
+  prepare.type = layer->type;
   if (space.dz || space.strips) {
-    GradRows g{};
-    g.grad = dz;
-    g.preact = layer->activation == LINEAR_NONE ? nullptr : preact;
-    g.dz = space.dz ? at(space.z) : nullptr;
-    g.strips = strips;
-    g.offsets = p.offsets;
-    g.groups = groups;
-    g.strip_rows = space.strip_rows;
-    g.type = layer->type;
-    g.activation = layer->activation;
-    if ((rc = grad_rows(g, s)) != GEMM_OK) return rc;
+    prepare.grad = dz;
+    prepare.preact = layer->activation == LINEAR_NONE ? nullptr : preact;
+    prepare.dz = space.dz ? at(space.z) : nullptr;
+    prepare.strips = strips;
+    prepare.offsets = p.offsets;
+    prepare.groups = groups;
+    prepare.strip_rows = space.strip_rows;
+    prepare.activation = layer->activation;
     if (space.dz) {
-      dz.ptr = g.dz;
+      dz.ptr = prepare.dz;
       dz.ld = copy_ld(dz.cols);
     }
   }
+  if (space.copy_w) copied(&w, &prepare, 0, workspace, space.w);
+  if (space.copy_x) copied(&x, &prepare, 1, workspace, space.x);
+  if ((rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
   if (for_x) {
-    if ((rc = as_loaded(&w, space.copy_w, workspace, space.w, sms, s)) != GEMM_OK) return rc;
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);
     px.vector = by_vectors(grad_x, layer->in);
     rc = launch(product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
                            p.offsets != nullptr),
-                dz, w, px, layer->type, opt, sms, device, s);
+                w, dz, px, layer->type, opt, sms, device, s);
     if (rc != GEMM_OK) return rc;
   }
   p.grad_bias = static_cast<uint16_t*>(grad_bias);
   if (for_w) {
-    if ((rc = as_loaded(&x, space.copy_x, workspace, space.x, sms, s)) != GEMM_OK) return rc;
     p.out = static_cast<uint16_t*>(grad_w);
     p.vector = by_vectors(grad_w, layer->in);
     p.strips = for_bias ? strips : nullptr;

@@ -5,23 +5,24 @@
 //   forward  z = x w^T        D rows x out, sums over in
 //   grad_x   dz w             D rows x in,  sums over out
 //   grad_w   dz^T x           D out x in,   sums over rows
-// The tensor cores take D = A B^T, each operand either with the summed index
-// contiguous (K-major) or with the other one (MN-major), so nothing is
-// transposed in memory:
-//              A                      B
-//   forward    x       K-major        w        K-major
-//   grad_x     dz      K-major        w        MN-major
-//   grad_w     dz^T    MN-major       x^T      MN-major
-// D's rows are the instruction's M, so that an accumulator lane is a row of D
-// and a row's columns lie next to each other for the epilogue.
-//
-// Groups are ragged in rows: in D's rows for the first two, in the summed index
-// for grad_w.  A tile of D ends with its group; the rows of the next group that
-// its last box of A brings along end in accumulator lanes that are not stored.
-// grad_w has to keep them out of the sums: it stops at the group's last 16 rows
-// and zeroes, in shared memory, what of those is not the group's, in both
-// operands (a NaN there would come through a zero in the other).  w is a
-// tensor of three dimensions, so that boxes past an expert's rows read zeros.
+// The tensor cores take operands either with the summed index contiguous (K-major) or
+// with the other one (MN-major), so nothing is transposed in memory.  One operand has
+// their M, 128 a CTA, the other their N, any multiple of 16:
+//              M                              N
+//   forward    outputs, w       K-major       rows, x       K-major
+//   grad_x     inputs, w^T      MN-major      rows, dz      K-major
+//   grad_w     outputs, dz^T    MN-major      inputs, x^T   MN-major
+// Rows are the N of the first two because groups are ragged in rows: a tile of 5 rows
+// costs an instruction of 16 columns, and one that ends with its group what it
+// has.  (With rows as M, in steps of 128 or 256, 4096 tokens x 8 of 64 experts,
+// 4096 -> 2048, took 392 us.)  The rows of the next group that its last copy of rows brings
+// along are not multiplied, or end in columns of the accumulator that are not
+// stored.
+// grad_w has the rows in the sum, and has to keep other groups' out of it: it stops at
+// the group's last 16 rows and zeroes, in shared memory, what of those is not the
+// group's, in both operands (a NaN there would come through a zero in the
+// other).  w is a tensor of three dimensions, so that copies past an expert's
+// rows bring zeros.
 #pragma once
 #include <cuda.h>
 
@@ -33,12 +34,11 @@
 
 namespace gb300 {
 
-constexpr int kLinM = 128;            // rows of D per CTA: one accumulator lane each
+constexpr int kLinM = 128;            // the M of a CTA: one accumulator lane each
 constexpr int kLinK = 64;             // summed elements of a stage: 128 bytes, a swizzle row
 constexpr int kLinEpiWarps = 8;
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
 constexpr int kLinMaxStages = 12;
-constexpr int kLinMaxTile = 256;      // columns of D
 constexpr uint32_t kLinABytes = kLinM * kLinK * 2;
 constexpr uint32_t kLinChunkBytes = 64 * kLinK * 2;  // MN-major: 64 columns by 64 of the sum
 constexpr uint32_t kLinBufBytes = 32 * 32 * 4;       // an epilogue warp's 32 x 32 sums
@@ -59,9 +59,10 @@ struct LinearParams {
   int32_t n;                 // columns of D
   int32_t k;                 // forward, grad_x: length of the sums
   int32_t groups;
-  int32_t tile;              // columns of a tile
-  int32_t m_tiles, n_tiles;  // of D; m_tiles: grad_w's, of a group
-  int32_t box_rows;          // forward, grad_x: rows that one copy of A loads
+  int32_t tile;              // the N of a tile, at most
+  int32_t tile_shift;        // forward, grad_x: its logarithm
+  int32_t m_tiles, n_tiles;  // M: of a group; N: grad_w's, of a group
+  int32_t box_rows;          // forward, grad_x: rows that one copy loads
   int32_t stages, split;
   int32_t activation;
   int32_t vector;            // D, bias and residual can be accessed 16 bytes at a time
@@ -70,8 +71,9 @@ struct LinearParams {
   uint64_t timeout_ns;
 };
 
-__host__ __device__ constexpr bool a_mn(int product) { return product == LINEAR_GRAD_W; }
-__host__ __device__ constexpr bool b_mn(int product) { return product != LINEAR_FORWARD; }
+// MN-major operands, of M and of N
+__host__ __device__ constexpr bool a_mn(int product) { return product != LINEAR_FORWARD; }
+__host__ __device__ constexpr bool b_mn(int product) { return product == LINEAR_GRAD_W; }
 
 // Shared memory past the ring and the epilogue's buffers: barriers, the tensor
 // memory address, the abort flag, and where each group starts; 1 KiB to align.
@@ -176,42 +178,42 @@ __device__ __forceinline__ void linear_wait_drain(uint32_t bar, uint32_t parity,
 }
 
 // ------------------------------------------------------------------ tiles
+// forward and grad_x: M is columns of D, N its rows; grad_w: the other way about.
 struct LinearTile {
   int32_t group;
-  int32_t row;     // of D: first row (grad_w: within the group's D)
-  int32_t count;   // rows of the tile, at most its height
-  int32_t col;     // first column
-  int32_t k_row;   // grad_w: the first summed row
-  int32_t k_len;   // length of the sums
+  int32_t m, m_count;   // first of the group's, and how many, at most the tile's
+  int32_t n, n_count;   // the same of N; forward and grad_x: first of all rows
+  int32_t k_row;        // grad_w: the first summed row
+  int32_t k_len;        // length of the sums
 };
 
-// Row tiles that walk over the columns together, so that what runs at once
-// shares operands in L2.
+// Row tiles (grad_w: tiles of outputs) that walk over the others together, so that
+// what runs at once shares operands in L2.
 constexpr int kLinRaster = 8;
 
-// Row tile and column tile of tile t among m_tiles x n_tiles.
-__device__ __forceinline__ void linear_raster(int t, int m_tiles, int n_tiles, int* mt, int* nt) {
-  if (m_tiles == 1) {
-    *mt = 0;
-    *nt = t;
+// Tile t among `slow` x `fast`: bands of kLinRaster of the first, over all of the second.
+__device__ __forceinline__ void linear_raster(int t, int slow, int fast, int* s, int* f) {
+  if (slow == 1) {
+    *s = 0;
+    *f = t;
     return;
   }
-  const int band = t / (kLinRaster * n_tiles);
-  const int in = t - band * kLinRaster * n_tiles;
-  const int wide = min(kLinRaster, m_tiles - band * kLinRaster);
-  *nt = wide == kLinRaster ? in / kLinRaster : in / wide;
-  *mt = band * kLinRaster + in - *nt * wide;
+  const int band = t / (kLinRaster * fast);
+  const int in = t - band * kLinRaster * fast;
+  const int wide = min(kLinRaster, slow - band * kLinRaster);
+  *f = wide == kLinRaster ? in / kLinRaster : in / wide;
+  *s = band * kLinRaster + in - *f * wide;
 }
 
 // Tiles of all groups.
 template <int kProduct>
 __device__ __forceinline__ int linear_tiles(const LinearParams& p, const GroupStart* start) {
   return kProduct == LINEAR_GRAD_W ? p.groups * p.m_tiles * p.n_tiles
-                                   : start[p.groups].tiles * p.n_tiles;
+                                   : start[p.groups].tiles * p.m_tiles;
 }
 
-// kHeight: rows of a tile.
-template <int kProduct, int kHeight>
+// kM: the M of a tile.
+template <int kProduct, int kM>
 __device__ __forceinline__ LinearTile linear_tile(int t, const LinearParams& p,
                                                   const GroupStart* start) {
   LinearTile o;
@@ -220,38 +222,41 @@ __device__ __forceinline__ LinearTile linear_tile(int t, const LinearParams& p,
     const int per = p.m_tiles * p.n_tiles;
     o.group = p.groups > 1 ? t / per : 0;
     linear_raster(t - o.group * per, p.m_tiles, p.n_tiles, &mt, &nt);
-    o.row = mt * kHeight;
-    o.count = min(kHeight, p.m - o.row);
+    o.n = nt * p.tile;
+    o.n_count = min(p.tile, p.n - o.n);
     o.k_row = start[o.group].row;
     o.k_len = start[o.group + 1].row - o.k_row;
+    o.m = mt * kM;
+    o.m_count = min(kM, p.m - o.m);
   } else {
-    int lo = 0, hi = p.groups - 1;  // the last group with tiles * n_tiles <= t before it
+    int lo = 0, hi = p.groups - 1;  // the last group with tiles * m_tiles <= t before it
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (start[mid].tiles * p.n_tiles <= t) lo = mid;
+      if (start[mid].tiles * p.m_tiles <= t) lo = mid;
       else hi = mid - 1;
     }
     const int first = start[lo].row, rows = start[lo + 1].row - first;
-    linear_raster(t - start[lo].tiles * p.n_tiles, (rows + kHeight - 1) / kHeight, p.n_tiles, &mt,
-                  &nt);
+    linear_raster(t - start[lo].tiles * p.m_tiles, (rows + p.tile - 1) >> p.tile_shift, p.m_tiles,
+                  &nt, &mt);
     o.group = lo;
-    o.row = first + mt * kHeight;
-    o.count = min(kHeight, rows - mt * kHeight);
+    o.n = first + (nt << p.tile_shift);
+    o.n_count = min(p.tile, rows - (nt << p.tile_shift));
     o.k_row = 0;
     o.k_len = p.k;
+    o.m = mt * kM;
+    o.m_count = min(kM, p.n - o.m);
   }
-  o.col = nt * p.tile;
   return o;
 }
 
 // Where each group starts, by one warp.
-template <int kHeight>
 __device__ __forceinline__ void linear_starts(const LinearParams& p, GroupStart* start, int lane) {
   if (p.offsets) {
-    find_groups<kHeight>(p.offsets, p.groups, start, lane);
+    find_groups(p.offsets, p.groups, start, lane, p.tile_shift);
   } else {  // one group, or none of any rows
     for (int g = lane; g <= p.groups; g += 32)
-      start[g] = g ? GroupStart{(p.rows + kHeight - 1) / kHeight, p.rows} : GroupStart{0, 0};
+      start[g] = g ? GroupStart{(p.rows + (1 << p.tile_shift) - 1) >> p.tile_shift, p.rows}
+                   : GroupStart{0, 0};
   }
 }
 
@@ -280,6 +285,56 @@ __device__ __forceinline__ void linear_zero_rows(uint32_t at, int chunks, int va
       st_shared_v4(at + c * kLinChunkBytes + valid * 128u + i * 16u, 0, 0, 0, 0);
 }
 
+// ------------------------------------------------------------------ loads
+// What a CTA loads for each stage of a tile: of M from m on, of N from n on.
+struct LinearLoads {
+  int32_t m, n;
+  int32_t a_boxes, b_boxes;
+  uint32_t a_box_bytes, b_box_bytes, bytes;
+};
+
+// At least a box of each, also where there is nothing (past the ends they are zeros).
+template <int kProduct>
+__device__ __forceinline__ LinearLoads linear_loads(int m, int m_count, int n, int n_count,
+                                                    const LinearParams& p) {
+  LinearLoads l;
+  l.m = m;
+  l.n = n;
+  l.a_boxes = a_mn(kProduct) ? min(max(1, (m_count + 63) >> 6), kLinM / 64) : 1;
+  l.a_box_bytes = a_mn(kProduct) ? kLinChunkBytes : kLinABytes;
+  l.b_boxes = max(1, b_mn(kProduct) ? (n_count + 63) >> 6 : (n_count + p.box_rows - 1) / p.box_rows);
+  l.b_box_bytes = b_mn(kProduct) ? kLinChunkBytes : p.box_rows * (kLinK * 2);
+  l.bytes = l.a_boxes * l.a_box_bytes + l.b_boxes * l.b_box_bytes;
+  return l;
+}
+
+// A stage's, from k of the sum on, to shared memory at `dst`; by one lane.
+template <int kProduct, bool kPair>
+__device__ __forceinline__ void linear_load(const LinearLoads& l, uint32_t dst, const void* tmA,
+                                            const void* tmB, uint32_t full, int k,
+                                            const LinearTile& t, const LinearParams& p) {
+  const auto load_a = [&](uint32_t at, int x, int y, int z) {
+    if (kPair) tma_load_3d_pair(at, tmA, full, x, y, z);
+    else tma_load_3d(at, tmA, full, x, y, z);
+  };
+  const auto load_b = [&](uint32_t at, int x, int y) {
+    if (kPair) tma_load_2d_pair(at, tmB, full, x, y);
+    else tma_load_2d(at, tmB, full, x, y);
+  };
+  if (kProduct == LINEAR_FORWARD) {
+    load_a(dst, k, l.m, t.group);
+  } else {
+    for (int i = 0; i < l.a_boxes; ++i)
+      load_a(dst + i * l.a_box_bytes, l.m + 64 * i, t.k_row + k,
+             kProduct == LINEAR_GRAD_X ? t.group : 0);
+  }
+  const uint32_t b = dst + kLinABytes;
+  for (int i = 0; i < l.b_boxes; ++i) {
+    if (kProduct == LINEAR_GRAD_W) load_b(b + i * l.b_box_bytes, l.n + 64 * i, t.k_row + k);
+    else load_b(b + i * l.b_box_bytes, k, l.n + i * p.box_rows);
+  }
+}
+
 // ------------------------------------------------------------------ epilogue
 // 1 / (1 + e^-u) and 1 / (1 + e^u), with their relative accuracy on both sides: the
 // exponential is at most 1, the denominator between 1 and 2.
@@ -296,45 +351,76 @@ __device__ __forceinline__ float gelu_tanh_argument(float z) {
   return 1.5957691f * z * fmaf(0.044715f, z * z, 1.0f);
 }
 
-__device__ __forceinline__ float activate(float z, int activation) {
-  switch (activation) {
-    case LINEAR_RELU:
-      return z < 0.0f ? 0.0f : z;  // a NaN stays
-    case LINEAR_GELU:
-      return 0.5f * z * erfcf(z * -0.70710678f);  // erfc: no cancellation far below 0
-    case LINEAR_GELU_TANH:
-      return z * sigmoids(gelu_tanh_argument(z)).up;
-    case LINEAR_SILU:
-      return z * sigmoids(z).up;
-    default:
-      return z;
+// P(Z <= z) of a standard normal Z, and its density there times sqrt(2 pi).  Below 0
+// it is e^(-z^2/2) f(|z|) with f(s) = erfcx(s / sqrt 2) / 2, here a polynomial in
+// t = 1 / (1 + 0.3 s) that was fitted to f by weighted least squares (relative
+// error 1.5e-7 for s up to 14, 4.7e-7 as evaluated in fp32): a subtraction from 1
+// would have no accuracy left there.  (With erfcf the slopes of 8192 x 4096 cost
+// more time than their memory.)
+struct Normal {
+  float below, density;
+};
+__device__ __forceinline__ Normal normal(float z) {
+  const float s = fabsf(z), t = __fdividef(1.0f, fmaf(0.3f, s, 1.0f));
+  float f = 0.035674453f;
+  f = fmaf(f, t, -0.15720180f);
+  f = fmaf(f, t, 0.20635141f);
+  f = fmaf(f, t, -0.053681802f);
+  f = fmaf(f, t, 0.12856069f);
+  f = fmaf(f, t, 0.099913761f);
+  f = fmaf(f, t, 0.12075391f);
+  f = fmaf(f, t, 0.11962930f);
+  const float e = __expf(-0.5f * z * z), tail = e * (f * t);
+  return Normal{z < 0.0f ? tail : 1.0f - tail, e};
+}
+
+template <int kActivation>
+__device__ __forceinline__ float activate(float z) {
+  switch (kActivation) {
+    case LINEAR_RELU: return z < 0.0f ? 0.0f : z;  // a NaN stays
+    case LINEAR_GELU: return z * normal(z).below;
+    case LINEAR_GELU_TANH: return z * sigmoids(gelu_tanh_argument(z)).up;
+    case LINEAR_SILU: return z * sigmoids(z).up;
+    default: return z;
   }
 }
 
 // act'(z).  Past 100 it is 0 or 1 in fp32, and products of what overflows and what
 // vanishes there would be NaN.
-__device__ __forceinline__ float activation_slope(float z, int activation) {
+template <int kActivation>
+__device__ __forceinline__ float activation_slope(float z) {
+  if (kActivation == LINEAR_NONE) return 1.0f;
+  if (kActivation == LINEAR_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if (fabsf(z) > 100.0f) z = copysignf(100.0f, z);
+  if (kActivation == LINEAR_GELU) {
+    const Normal n = normal(z);
+    return fmaf(z * 0.39894228f, n.density, n.below);
+  }
+  if (kActivation == LINEAR_GELU_TANH) {
+    const Sigmoids s = sigmoids(gelu_tanh_argument(z));
+    return fmaf(z * fmaf(0.21406445f, z * z, 1.5957691f), s.up * s.down, s.up);
+  }
+  const Sigmoids s = sigmoids(z);
+  return s.up * fmaf(z, s.down, 1.0f);
+}
+
+// The activation of some values; the choice is made once for them.
+template <int kN>
+__device__ __forceinline__ void activate_all(float (&v)[kN], int activation) {
+  const auto all = [&](auto a) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) v[e] = activate<decltype(a)::value>(v[e]);
+  };
   switch (activation) {
-    case LINEAR_RELU:
-      return z > 0.0f ? 1.0f : 0.0f;
-    case LINEAR_GELU:
-      return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678f));
-    case LINEAR_GELU_TANH: {
-      const Sigmoids s = sigmoids(gelu_tanh_argument(z));
-      return fmaf(z * fmaf(0.21406445f, z * z, 1.5957691f), s.up * s.down, s.up);
-    }
-    case LINEAR_SILU: {
-      const Sigmoids s = sigmoids(z);
-      return s.up * fmaf(z, s.down, 1.0f);
-    }
-    default:
-      return 1.0f;
+    case LINEAR_RELU: return all(std::integral_constant<int, LINEAR_RELU>{});
+    case LINEAR_GELU: return all(std::integral_constant<int, LINEAR_GELU>{});
+    case LINEAR_GELU_TANH: return all(std::integral_constant<int, LINEAR_GELU_TANH>{});
+    case LINEAR_SILU: return all(std::integral_constant<int, LINEAR_SILU>{});
   }
 }
 
 // An epilogue warp's 32 x 32 sums pass through shared memory from the layout of
-// the accumulator (a lane is a row) to that of memory (four lanes are a row's 32
+// the accumulator (a lane is a column of D, or a row) to that of memory (four lanes are a row's 32
 // columns, eight of them each), so that bias, residual, z and D are read and
 // written 16 bytes a lane, 64 bytes of a row at once.  Piece j (of 16 bytes) of row r
 // is at j ^ (r & 7): neither side has bank conflicts.
@@ -364,10 +450,61 @@ __device__ __forceinline__ void linear_sums(uint32_t taddr, bool any, uint32_t (
   for (int i = 0; i < 32; ++i) r[i] = any ? r[i] : 0u;
 }
 
-__device__ __forceinline__ void linear_put_row(uint32_t buf, int lane, const uint32_t (&r)[32]) {
+// A lane is a row of D (grad_w), or a column.
+template <int kProduct>
+__device__ __forceinline__ void linear_put(uint32_t buf, int lane, const uint32_t (&r)[32]) {
+  if (kProduct == LINEAR_GRAD_W) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    st_shared_v4(linear_piece(buf, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+    for (int j = 0; j < 8; ++j)
+      st_shared_v4(linear_piece(buf, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) + 4u * (lane & 3)),
+                   "r"(r[i])
+                   : "memory");
+  }
+}
+
+// The same into another CTA's shared memory (a shared::cluster address).
+template <int kProduct>
+__device__ __forceinline__ void linear_send(uint32_t buf, int lane, const uint32_t (&r)[32]) {
+  if (kProduct == LINEAR_GRAD_W) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      st_cluster_v4(linear_piece(buf, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) +
+                                                           4u * (lane & 3)),
+                   "r"(r[i])
+                   : "memory");
+  }
+}
+
+// 32 x 32 sums of a tile: lanes 32 q on of the accumulator, and columns 32 c on, `m` being
+// the first of the M of the CTA.
+struct LinearChunk {
+  int64_t row;     // of D
+  int32_t live;    // rows; none: not stored
+  int32_t col;
+};
+template <int kProduct>
+__device__ __forceinline__ LinearChunk linear_chunk(const LinearTile& t, int m, int q, int c,
+                                                    const LinearParams& p) {
+  LinearChunk o;
+  if (kProduct == LINEAR_GRAD_W) {
+    o.row = static_cast<int64_t>(t.group) * p.m + m + 32 * q;
+    o.live = min(32, p.m - (m + 32 * q));
+    o.col = t.n + 32 * c;
+  } else {
+    o.row = t.n + 32 * c;
+    o.live = min(32, t.n_count - 32 * c);
+    o.col = m + 32 * q;
+  }
+  if (o.col >= p.n) o.live = 0;
+  return o;
 }
 
 // What a chunk's epilogue reads from memory, asked for before its sums are there.
@@ -377,11 +514,12 @@ struct LinearExtras {
 };
 
 template <int kProduct>
-__device__ __forceinline__ LinearExtras linear_extras(const LinearParams& p, int group, int64_t row,
-                                                      int live, int col, int lane) {
+__device__ __forceinline__ LinearExtras linear_extras(const LinearParams& p, int group,
+                                                      const LinearChunk& at, int lane) {
   LinearExtras x = {};
   if (kProduct != LINEAR_FORWARD || !p.vector) return x;
-  const int c = col + 8 * (lane & 3);
+  const int64_t row = at.row;
+  const int live = at.live, c = at.col + 8 * (lane & 3);
   if (c >= p.n) return x;
   if (p.bias)
     x.bias = *reinterpret_cast<const Pack*>(p.bias + static_cast<int64_t>(group) * p.n + c);
@@ -396,13 +534,15 @@ __device__ __forceinline__ LinearExtras linear_extras(const LinearParams& p, int
   return x;
 }
 
-// The chunk whose first row of D is `row` and first column `col`; `live` of its rows are
-// the tile's.  Its sums are those of `parts` buffers `part_bytes` apart, added in order.
+// A chunk's part of D.  Its sums are those of `parts` buffers `part_bytes` apart, added
+// in order.
 template <typename T, int kProduct>
 __device__ __forceinline__ void linear_finish(uint32_t buf, int parts, uint32_t part_bytes,
                                               const LinearParams& p, LinearExtras& x, int group,
-                                              int64_t row, int live, int col, int lane) {
+                                              const LinearChunk& chunk, int lane) {
   constexpr bool kForward = kProduct == LINEAR_FORWARD;
+  const int64_t row = chunk.row;
+  const int live = chunk.live, col = chunk.col;
   if (p.vector) {
     const int c = col + 8 * (lane & 3);
     float bias[8];
@@ -427,10 +567,7 @@ __device__ __forceinline__ void linear_finish(uint32_t buf, int parts, uint32_t 
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += bias[e];
           if (p.preact) *reinterpret_cast<Pack*>(p.preact + at) = pack<T>(v);
-          if (p.activation != LINEAR_NONE) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = activate(v[e], p.activation);
-          }
+          activate_all(v, p.activation);
           if (p.residual) {
             float res[8];
             unpack<T>(x.residual[0], res);
@@ -462,28 +599,38 @@ __device__ __forceinline__ void linear_finish(uint32_t buf, int parts, uint32_t 
         if (r0 + i < live)
           res[i] = reinterpret_cast<const T*>(p.residual)[(row + r0 + i) * p.ldr + c];
     }
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + i;
-      float v = 0.0f;
+      v[i] = 0.0f;
       for (int s = 0; s < parts; ++s) {
         float part;
         asm volatile("ld.shared.f32 %0, [%1];"
                      : "=f"(part)
-                     : "r"(linear_piece(buf + s * part_bytes, r, lane >> 2) + 4u * (lane & 3))
+                     : "r"(linear_piece(buf + s * part_bytes, r0 + i, lane >> 2) + 4u * (lane & 3))
                      : "memory");
-        v += part;
+        v[i] += part;
       }
-      if (r >= live) continue;
-      const int64_t at = (row + r) * p.n + c;
-      if (kForward) {
-        v += bias;
-        if (p.preact) reinterpret_cast<T*>(p.preact)[at] = from_float<T>(v);
-        v = activate(v, p.activation);
-        if (p.residual) v += to_float(res[i]);
-      }
-      reinterpret_cast<T*>(p.out)[at] = from_float<T>(v);
+      v[i] += bias;
     }
+    const int64_t at = (row + r0) * p.n + c;
+    if (kForward) {
+      if (p.preact) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < live)
+            reinterpret_cast<T*>(p.preact)[at + static_cast<int64_t>(i) * p.n] = from_float<T>(v[i]);
+      }
+      activate_all(v, p.activation);
+      if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += to_float(res[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + i < live)
+        reinterpret_cast<T*>(p.out)[at + static_cast<int64_t>(i) * p.n] = from_float<T>(v[i]);
   }
 }
 
@@ -529,11 +676,40 @@ __device__ __forceinline__ void linear_sum_strips(const LinearParams& p, const G
                        static_cast<int64_t>(gridDim.x) * (32 * kLinEpiWarps));
 }
 
-// First row of a tile's part of D in memory.
-template <int kProduct>
-__device__ __forceinline__ int64_t linear_out_row(const LinearTile& t, const LinearParams& p) {
-  return kProduct == LINEAR_GRAD_W ? static_cast<int64_t>(t.group) * p.m + t.row
-                                   : static_cast<int64_t>(t.row);
+// An epilogue warp's chunks of a tile: those of lane quadrant q, columns 32 half, 32 (half + 2)
+// ...  `wait` waits for the accumulator and `release` gives it back, by one lane, once
+// the warp's last chunk of it is in registers.  False: the wait gave up.
+template <typename T, int kProduct, typename Wait, typename Release>
+__device__ __forceinline__ bool linear_epilogue(const LinearTile& tile, int m, int q, int half,
+                                                uint32_t t_row, uint32_t buf, const LinearParams& p,
+                                                int lane, Wait wait, Release release) {
+  const auto let_go = [&] {
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) release();
+  };
+  int chunks = (tile.n_count + 31) >> 5;
+  LinearChunk at = linear_chunk<kProduct>(tile, m, q, half, p);
+  if (at.live <= 0) chunks = 0;     // then so are the warp's others
+  LinearExtras x;
+  if (chunks > half) x = linear_extras<kProduct>(p, tile.group, at, lane);
+  if (!wait()) return false;
+  tc_fence_after_sync();
+  if (chunks <= half) let_go();
+  for (int c = half; c < chunks; c += 2) {
+    uint32_t r[32];
+    linear_sums(t_row + 32 * c, tile.k_len > 0, r);
+    if (c + 2 >= chunks) let_go();
+    linear_put<kProduct>(buf, lane, r);
+    __syncwarp();
+    linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, at, lane);
+    __syncwarp();
+    if (c + 2 < chunks) {
+      at = linear_chunk<kProduct>(tile, m, q, c + 2, p);
+      x = linear_extras<kProduct>(p, tile.group, at, lane);
+    }
+  }
+  return true;
 }
 
 // Rows of no group are zero, by every epilogue thread of the grid.

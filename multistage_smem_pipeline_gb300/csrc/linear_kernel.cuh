@@ -1,5 +1,5 @@
-// The products of linear layers on single CTAs: tiles of 128 rows of D by 64 to
-// 256 columns.
+// The products of linear layers on single CTAs: tiles of an M of 128 and an N of 32
+// to 256.
 //
 // Inside a CTA, one per SM:
 //   warp 0 -- producer: per 64 of the sum, TMA boxes of both operands into a ring;
@@ -9,10 +9,9 @@
 // The loops of the issuing warps are run by the whole warp, and one lane issues.
 //
 // kSplit: few tiles.  The CTAs of a cluster share one tile, each taking its part of
-// the sum's stages; with all MMAs done and read by everyone's tensor cores,
-// the rings are free, and every CTA writes its sums for each other one's share of
-// the columns into that one's ring, where they are added in the order of the
-// parts.  No sum depends on who came first.
+// the sum's stages; with all MMAs done, the rings are free, and every CTA writes its
+// sums for each other one's share of the chunks into that one's ring, where they
+// are added in the order of the parts.  No sum depends on who came first.
 #pragma once
 #include "linear.cuh"
 
@@ -44,8 +43,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 8);
-  // columns between the accumulators, and those allocated: a power of two
-  const uint32_t acc_cols = p.tile <= 64 ? 64 : p.tile <= 128 ? 128 : 256;
+  // columns between the accumulators: tiles are powers of two
+  const uint32_t acc_cols = p.tile;
   const uint32_t tmem_cols = 2 * acc_cols;
 
   if (threadIdx.x == 0) {
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (warp == 2) linear_starts<kLinM>(p, start, lane);
+  if (warp == 2) linear_starts(p, start, lane);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -92,12 +91,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     bool ok = true;
     for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
-      const int a_boxes =
-          kAMn ? (tile.count + 63) >> 6 : (tile.count + p.box_rows - 1) / p.box_rows;
-      const uint32_t a_box_bytes = kAMn ? kLinChunkBytes : p.box_rows * (kLinK * 2);
-      const int b_boxes = kBMn ? (min(p.tile, p.n - tile.col) + 63) >> 6 : 1;
-      const uint32_t b_box_bytes = kBMn ? kLinChunkBytes : p.tile * (kLinK * 2);
-      const uint32_t bytes = a_boxes * a_box_bytes + b_boxes * b_box_bytes;
+      const LinearLoads loads = linear_loads<kProduct>(tile.m, tile.m_count, tile.n, tile.n_count, p);
       int from, end;
       stages_of(tile, &from, &end);
       for (int kb = from; kb < end; ++kb) {
@@ -106,24 +100,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           break;
         }
         if (elect_one()) {
-          const uint32_t a = base + stage * stage_bytes, b = a + kLinABytes;
           const uint32_t full = full_bar(stage);
-          const int k = kb * kLinK;
-          mbar_arrive_expect_tx(full, bytes);
-          if (!(p.inject && issued == 0)) {
-            for (int i = 0; i < a_boxes; ++i) {
-              if (kAMn) tma_load_2d(a + i * a_box_bytes, &tmA, full, tile.row + 64 * i, tile.k_row + k);
-              else tma_load_2d(a + i * a_box_bytes, &tmA, full, k, tile.row + i * p.box_rows);
-            }
-            for (int i = 0; i < b_boxes; ++i) {
-              if (kProduct == LINEAR_FORWARD)
-                tma_load_3d(b, &tmB, full, k, tile.col, tile.group);
-              else if (kProduct == LINEAR_GRAD_X)
-                tma_load_3d(b + i * b_box_bytes, &tmB, full, tile.col + 64 * i, k, tile.group);
-              else
-                tma_load_3d(b + i * b_box_bytes, &tmB, full, tile.col + 64 * i, tile.k_row + k, 0);
-            }
-          }
+          mbar_arrive_expect_tx(full, loads.bytes);
+          if (!(p.inject && issued == 0))
+            linear_load<kProduct, false>(loads, base + stage * stage_bytes, &tmA, &tmB, full,
+                                         kb * kLinK, tile, p);
         }
         __syncwarp();
         ++issued;
@@ -146,8 +127,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
     for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
-      const int cols = min(p.tile, p.n - tile.col);
-      const uint32_t idesc = linear_idesc<T, kProduct>(kLinM, (cols + 15) & ~15);
+      const uint32_t idesc = linear_idesc<T, kProduct>(kLinM, (tile.n_count + 15) & ~15);
       if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
       tc_fence_after_sync();
       const uint32_t d_tmem = tmem + acc * acc_cols;
@@ -210,32 +190,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint32_t acc_phase = 0;
     for (int t = first_tile; t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
-      const int live = min(32, tile.count - 32 * q);  // rows of this quadrant, if any
-      const int chunks = live > 0 ? (min(p.tile, p.n - tile.col) + 31) >> 5 : 0;
-      const int64_t row = linear_out_row<kProduct>(tile, p) + 32 * q;
-      LinearExtras x;
-      if (half < chunks)
-        x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * half, lane);
-      if (!linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p)) break;
-      tc_fence_after_sync();
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols;
-      const auto release = [&] {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(acc));
-      };
-      for (int c = half; c < chunks; c += 2) {
-        uint32_t r[32];
-        linear_sums(t_row + 32 * c, tile.k_len > 0, r);
-        if (c + 2 >= chunks) release();
-        linear_put_row(buf, lane, r);
-        __syncwarp();
-        linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, row, live, tile.col + 32 * c, lane);
-        __syncwarp();
-        if (c + 2 < chunks)
-          x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * (c + 2), lane);
-      }
-      if (half >= chunks) release();
+      const bool ok = linear_epilogue<T, kProduct>(
+          tile, tile.m, q, half, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols, buf,
+          p, lane,
+          [&] { return linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p); },
+          [&] { mbar_arrive(tempty_bar(acc)); });
+      if (!ok) break;
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
@@ -245,16 +205,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   if (kSplit) {
     // ---------------------------------------------------------- parts to their owners
-    // Chunk c of 32 columns belongs to CTA c / mine.  A buffer of the ring for each
-    // part, quadrant and chunk of one's own.
+    // Chunk (q, c) is the 4 c + q-th, and CTA u / mine owns the u-th.  Of one's own there
+    // is a buffer in the ring for each part.
     const bool live_tile = first_tile < tiles;
     LinearTile tile = {};
     if (live_tile) tile = linear_tile<kProduct, kLinM>(first_tile, p, start);
-    const int mine = p.tile / 32 / p.split;
-    const int cols = min(p.tile, p.n - tile.col);
-    const int quads = (tile.count + 31) >> 5;
-    const auto slot = [&](int s, int q, int c) {
-      return base + static_cast<uint32_t>((s * 4 + q) * mine + c) * kLinBufBytes;
+    const int mine = max(1, p.tile / 8 / p.split);
+    const int chunks = (tile.n_count + 31) >> 5;
+    const auto slot = [&](int s, int i) {
+      return base + static_cast<uint32_t>(s * mine + i) * kLinBufBytes;
     };
     if (warp >= 2 && kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
     int ok = 1;
@@ -266,30 +225,26 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int from, end;
       stages_of(tile, &from, &end);
       const int q = warp & 3, half = (warp - 2) >> 2;
-      for (int c = half; q < quads && 32 * c < cols; c += 2) {
+      for (int c = half; c < chunks; c += 2) {
+        if (linear_chunk<kProduct>(tile, tile.m, q, c, p).live <= 0) continue;
         uint32_t r[32];
         linear_sums(tmem + (static_cast<uint32_t>(q * 32) << 16) + 32 * c, end > from, r);
-        const int owner = c / mine;
-        const uint32_t to = mapa_shared(slot(part, q, c - owner * mine), owner);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          st_cluster_v4(linear_piece(to, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2],
-                        r[4 * j + 3]);
+        const int u = 4 * c + q, owner = u / mine;
+        linear_send<kProduct>(mapa_shared(slot(part, u - owner * mine), owner), lane, r);
       }
     }
     __syncwarp();
     cluster_sync();  // all parts have come
     if (warp >= 2) {
       if (live_tile && ok) {
-        for (int i = warp - 2; i < quads * mine; i += kLinEpiWarps) {
-          const int c = i / quads, q = i - c * quads;
-          const int col = tile.col + 32 * (part * mine + c);
-          if (col >= p.n) break;
-          const int live = min(32, tile.count - 32 * q);
-          const int64_t row = linear_out_row<kProduct>(tile, p) + 32 * q;
-          LinearExtras x = linear_extras<kProduct>(p, tile.group, row, live, col, lane);
-          linear_finish<T, kProduct>(slot(0, q, c), p.split, 4 * mine * kLinBufBytes, p, x,
-                                     tile.group, row, live, col, lane);
+        for (int i = warp - 2; i < mine; i += kLinEpiWarps) {
+          const int u = part * mine + i;
+          if (u >= 4 * chunks) break;
+          const LinearChunk at = linear_chunk<kProduct>(tile, tile.m, u & 3, u >> 2, p);
+          if (at.live <= 0) continue;
+          LinearExtras x = linear_extras<kProduct>(p, tile.group, at, lane);
+          linear_finish<T, kProduct>(slot(0, i), p.split, mine * kLinBufBytes, p, x, tile.group, at,
+                                     lane);
         }
       }
       linear_zero_tail<kProduct>(p, start);

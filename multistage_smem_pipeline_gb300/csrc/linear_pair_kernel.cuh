@@ -1,10 +1,9 @@
-// The products of linear layers over CTA pairs (tcgen05 cta_group::2): tiles of
-// 256 rows of D by 256 columns.
+// The products of linear layers over CTA pairs (tcgen05 cta_group::2): tiles of an M
+// of 256 and an N of 256 at most.
 //
-// Each CTA loads its own 128 rows of A and its half of B's columns, 32 KiB per 64 of
-// the sum where a single CTA's 128 x 256 tile takes 48; the even CTA issues, and
-// each accumulates its 128 rows in its own tensor memory, in two accumulators by
-// turns.
+// Each CTA loads its own 128 of M and its half of N, 32 KiB per 64 of the sum where a
+// single CTA's 128 x 256 tile takes 48; the even CTA issues, and each accumulates
+// its 128 of M in its own tensor memory, in two accumulators by turns.
 //
 // Barriers as in the other pair kernels: `full` in the even CTA counts both CTAs'
 // bytes; `empty` and `tfull` are in both, committed to both; `tempty` in the even
@@ -26,7 +25,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 const LinearParams p) {
   constexpr bool kAMn = a_mn(kProduct), kBMn = b_mn(kProduct);
   constexpr bool kWeight = kProduct == LINEAR_GRAD_W;
-  constexpr int kHeight = 2 * kLinM;
+  constexpr int kM = 2 * kLinM;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -75,16 +74,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_relinquish_pair();
   }
   grid_dependency_wait();
-  if (warp == 2) linear_starts<kHeight>(p, start, lane);
+  if (warp == 2) linear_starts(p, start, lane);
   tc_fence_before_sync();
   cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int tiles = linear_tiles<kProduct>(p, start);
-  // columns of B that a CTA holds: half of the tile's, to 16
-  const auto half_cols = [&](const LinearTile& t) {
-    return (min(kLinPairTile, p.n - t.col) + 31) >> 5 << 4;
-  };
+  // the N that a CTA holds: half of the tile's, to 16
+  const auto half_n = [&](const LinearTile& t) { return (t.n_count + 31) >> 5 << 4; };
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer (both CTAs)
@@ -93,22 +90,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint32_t own_phase = 0;  // odd CTA: bit s is the parity of its own full_bar(s)
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
-      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
-      const int mine = min(kLinM, tile.count - rank * kLinM);  // rows; may be none
-      const int theirs = min(kLinM, tile.count - (1 - rank) * kLinM);
-      const int half = half_cols(tile);
-      // boxes of a CTA with `rows` rows: at least one, so that both always load
-      const auto a_boxes_of = [&](int rows) {
-        return max(1, kAMn ? (rows + 63) >> 6 : (rows + p.box_rows - 1) / p.box_rows);
+      const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
+      const int half = half_n(tile);
+      const auto loads_of = [&](int r) {
+        return linear_loads<kProduct>(tile.m + r * kLinM, tile.m_count - r * kLinM,
+                                      tile.n + r * half, half, p);
       };
-      const int a_boxes = a_boxes_of(mine);
-      const uint32_t a_box_bytes = kAMn ? kLinChunkBytes : p.box_rows * (kLinK * 2);
-      const int b_boxes = kBMn ? (half + 63) >> 6 : 1;
-      const uint32_t b_bytes = kBMn ? b_boxes * kLinChunkBytes : kLinPairTile / 2 * kLinK * 2;
-      const uint32_t own_bytes = a_boxes * a_box_bytes + b_bytes;
-      const uint32_t both_bytes = own_bytes + a_boxes_of(theirs) * a_box_bytes + b_bytes;
-      const int row = tile.row + rank * kLinM;
-      const int col = tile.col + rank * half;
+      const LinearLoads loads = loads_of(rank);
+      const uint32_t both_bytes = loads.bytes + loads_of(1 - rank).bytes;
       const int kbs = (tile.k_len + kLinK - 1) / kLinK;
       for (int kb = 0; kb < kbs; ++kb) {
         if (!linear_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kLinEmpty, p)) {
@@ -117,26 +106,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         const bool ragged = kWeight && linear_ragged(tile, kb, p);
         if (elect_one()) {
-          const uint32_t a = base + stage * kLinPairStage, b = a + kLinABytes;
-          const uint32_t full = ragged ? mapa_shared(full_bar(stage), rank)
-                                       : mapa_shared(full_bar(stage), 0);
-          const int k = kb * kLinK;
-          if (ragged) mbar_arrive_expect_tx(full_bar(stage), own_bytes);
+          const uint32_t full = mapa_shared(full_bar(stage), ragged ? rank : 0);
+          if (ragged) mbar_arrive_expect_tx(full_bar(stage), loads.bytes);
           else if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), both_bytes);
-          if (!(p.inject && issued == 0 && rank == 0)) {
-            for (int i = 0; i < a_boxes; ++i) {
-              if (kAMn) tma_load_2d_pair(a + i * a_box_bytes, &tmA, full, row + 64 * i, tile.k_row + k);
-              else tma_load_2d_pair(a + i * a_box_bytes, &tmA, full, k, row + i * p.box_rows);
-            }
-            for (int i = 0; i < b_boxes; ++i) {
-              if (kProduct == LINEAR_FORWARD)
-                tma_load_3d_pair(b, &tmB, full, k, col, tile.group);
-              else if (kProduct == LINEAR_GRAD_X)
-                tma_load_3d_pair(b + i * kLinChunkBytes, &tmB, full, col + 64 * i, k, tile.group);
-              else
-                tma_load_3d_pair(b + i * kLinChunkBytes, &tmB, full, col + 64 * i, tile.k_row + k, 0);
-            }
-          }
+          if (!(p.inject && issued == 0 && rank == 0))
+            linear_load<kProduct, true>(loads, base + stage * kLinPairStage, &tmA, &tmB, full,
+                                        kb * kLinK, tile, p);
         }
         __syncwarp();
         if (ragged) own_phase ^= 1u << stage;
@@ -163,8 +138,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint64_t a_desc0 = linear_desc<kAMn>(base);
     const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
     for (int t = pair; ok && t < tiles; t += pairs) {
-      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
-      const uint32_t idesc = linear_idesc<T, kProduct>(kHeight, 2 * half_cols(tile));
+      const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
+      const uint32_t idesc = linear_idesc<T, kProduct>(kM, 2 * half_n(tile));
       if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
       tc_fence_after_sync();
       const uint32_t d_tmem = tmem + acc * kLinPairTile;
@@ -236,7 +211,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int stage = 0;
       uint32_t own_phase = 0;
       for (int t = pair; t < tiles; t += pairs) {
-        const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
+        const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
         const int kbs = (tile.k_len + kLinK - 1) / kLinK;
         if (kbs == 0) continue;
         stage = (stage + kbs - 1) % stages;  // that of the tile's last
@@ -265,34 +240,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = pair; t < tiles; t += pairs) {
-      const LinearTile tile = linear_tile<kProduct, kHeight>(t, p, start);
-      const int live = min(32, tile.count - rank * kLinM - 32 * q);
-      const int chunks = live > 0 ? (min(kLinPairTile, p.n - tile.col) + 31) >> 5 : 0;
-      const int64_t row = linear_out_row<kProduct>(tile, p) + rank * kLinM + 32 * q;
-      LinearExtras x;
-      if (half < chunks)
-        x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * half, lane);
-      if (!linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p)) break;
-      tc_fence_after_sync();
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kLinPairTile;
-      const uint32_t leader_tempty = mapa_shared(tempty_bar(acc), 0);
-      const auto release = [&] {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader_tempty);
-      };
-      for (int c = half; c < chunks; c += 2) {
-        uint32_t r[32];
-        linear_sums(t_row + 32 * c, tile.k_len > 0, r);
-        if (c + 2 >= chunks) release();
-        linear_put_row(buf, lane, r);
-        __syncwarp();
-        linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, row, live, tile.col + 32 * c, lane);
-        __syncwarp();
-        if (c + 2 < chunks)
-          x = linear_extras<kProduct>(p, tile.group, row, live, tile.col + 32 * (c + 2), lane);
-      }
-      if (half >= chunks) release();
+      const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
+      const bool ok = linear_epilogue<T, kProduct>(
+          tile, tile.m + rank * kLinM, q, half,
+          tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kLinPairTile, buf, p, lane,
+          [&] { return linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p); },
+          [&] { mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0)); });
+      if (!ok) break;
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;

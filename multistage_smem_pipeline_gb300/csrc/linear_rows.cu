@@ -9,61 +9,99 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Elements [e, e + 8) of a row of n that starts at any 2-byte address.
-template <bool kAligned>
-__device__ __forceinline__ Pack window(const uint16_t* row, int e, int n) {
-  return load8<kAligned>(row, e, n);
+constexpr int kCopyAhead = 4;
+constexpr int kCopyPieces = kCopyAhead * kThreads;  // of 16 bytes, that a block copies
+
+// Blocks of a launch: first those of dz, then those of each copy.
+struct PrepareParams {
+  PrepareRows p;
+  int col_blocks;            // of dz: 256 columns each
+  int64_t first_copy[2];     // block
+};
+
+__device__ void copy_block(const Rows& src, uint16_t* dst, int64_t block) {
+  const int n = static_cast<int>(src.cols);
+  const int64_t ld = copy_ld(n);
+  const uint32_t per = static_cast<uint32_t>(ld / 8);
+  const int64_t row0 = block * kCopyPieces / per;
+  const uint32_t piece0 = static_cast<uint32_t>(block * kCopyPieces - row0 * per);
+  Pack v[kCopyAhead];
+  int64_t row[kCopyAhead];
+  int e[kCopyAhead];
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i) {
+    const uint32_t at = piece0 + threadIdx.x + i * kThreads;
+    row[i] = row0 + at / per;
+    e[i] = static_cast<int>(at % per) * 8;
+    if (row[i] < src.rows)
+      v[i] = load8<false>(static_cast<const uint16_t*>(src.ptr) + row[i] * src.ld, e[i], n);
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i)
+    if (row[i] < src.rows) *reinterpret_cast<Pack*>(dst + row[i] * ld + e[i]) = v[i];
 }
 
-// One block: 256 columns (a lane has eight) of a strip of rows, which its warps take by
-// turns, four rows of loads in flight each.  Memory bounds it: reads of grad_out
-// and z and the write of dz.
-template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kThreads)
-    grad_rows_kernel(const GradRows p) {
-  constexpr int kAhead = 4;
+// A block of dz: 256 columns (a lane has eight) of a strip of rows, which its warps
+// take by turns, four rows of loads in flight each (two, of two loads, where rows are
+// not aligned).  Memory bounds it: reads of
+// grad_out and z and the write of dz.
+template <typename T, bool kAligned, int kActivation>
+__global__ void __launch_bounds__(kThreads, 3)
+    prepare_kernel(const __grid_constant__ PrepareParams q) {
+  constexpr int kAhead = kAligned ? 4 : 2;
+  constexpr bool kSlope = kActivation != LINEAR_NONE;
   __shared__ float partial[kWarps][256 + 8];
-  __shared__ int found[3];   // group, first row, rows
-  grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int strip = blockIdx.y;
-  const int n = static_cast<int>(p.grad.cols);
-  if (threadIdx.x == 0) found[2] = 0;
-  __syncthreads();
+  __shared__ int found[2];   // first row, rows
+  const PrepareRows& p = q.p;
+  if (threadIdx.x == 0) {
+    grid_launch_dependents();
+    found[1] = 0;
+  }
   grid_dependency_wait();
+  const int64_t block = blockIdx.x;
+  if (block >= q.first_copy[0]) {
+    const int which = block >= q.first_copy[1];
+    copy_block(p.from[which], static_cast<uint16_t*>(p.to[which]), block - q.first_copy[which]);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int strip = static_cast<int>(block / q.col_blocks);
+  const int col0 = static_cast<int>(block - static_cast<int64_t>(strip) * q.col_blocks) * 256;
+  const int n = static_cast<int>(p.grad.cols);
+  int64_t row0;
+  int rows;
   if (p.offsets) {
     // the group whose strips this one is among
+    __syncthreads();
     for (int g = threadIdx.x; g < p.groups; g += kThreads) {
       const int first = p.offsets[g], end = p.offsets[g + 1];
       const int at = strip_of(first, g, p.strip_rows);
       if (at <= strip && strip < strip_of(end, g + 1, p.strip_rows)) {
-        found[0] = g;
-        found[1] = first + (strip - at) * p.strip_rows;
-        found[2] = min(p.strip_rows, end - found[1]);   // none: a group's spare strip
+        found[0] = first + (strip - at) * p.strip_rows;
+        found[1] = min(p.strip_rows, end - found[0]);   // none: a group's spare strip
       }
     }
-  } else if (threadIdx.x == 0) {
-    found[1] = strip * p.strip_rows;
-    found[2] = min(p.strip_rows, static_cast<int>(p.grad.rows) - found[1]);
+    __syncthreads();
+    row0 = found[0];
+    rows = found[1];
+  } else {
+    row0 = static_cast<int64_t>(strip) * p.strip_rows;
+    rows = static_cast<int>(min(static_cast<int64_t>(p.strip_rows), p.grad.rows - row0));
   }
-  __syncthreads();
-  const int rows = found[2];
   if (rows <= 0) return;
-  const int64_t row0 = found[1];
-  const int c = blockIdx.x * 256 + 8 * lane;
-  const bool live = c < n;
+  const int c = col0 + 8 * lane;
   const uint16_t* const grad = static_cast<const uint16_t*>(p.grad.ptr);
   const uint16_t* const z = static_cast<const uint16_t*>(p.preact);
   const int64_t dz_ld = copy_ld(n);
   float sum[8] = {};
-  for (int r0 = warp; live && r0 < rows; r0 += kAhead * kWarps) {
+  for (int r0 = warp; c < n && r0 < rows; r0 += kAhead * kWarps) {
     Pack g[kAhead], s[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int r = r0 + i * kWarps;
       if (r < rows) {
-        g[i] = window<kAligned>(grad + (row0 + r) * p.grad.ld, c, n);
-        if (z) s[i] = window<kAligned>(z + (row0 + r) * n, c, n);
+        g[i] = load8<kAligned>(grad + (row0 + r) * p.grad.ld, c, n);
+        if (kSlope) s[i] = load8<kAligned>(z + (row0 + r) * n, c, n);
       }
     }
 #pragma unroll
@@ -72,11 +110,11 @@ __global__ void __launch_bounds__(kThreads)
       if (r >= rows) break;
       float v[8];
       unpack<T>(g[i], v);
-      if (z) {
+      if (kSlope) {
         float zs[8];
         unpack<T>(s[i], zs);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= activation_slope(zs[e], p.activation);
+        for (int e = 0; e < 8; ++e) v[e] *= activation_slope<kActivation>(zs[e]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
@@ -89,7 +127,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int e = 0; e < 8; ++e) partial[warp][e * 32 + lane] = sum[e];
   __syncthreads();
-  const int col = blockIdx.x * 256 + threadIdx.x;
+  const int col = col0 + threadIdx.x;
   if (col >= n) return;
   float total = 0.0f;
 #pragma unroll
@@ -98,18 +136,17 @@ __global__ void __launch_bounds__(kThreads)
   p.strips[static_cast<int64_t>(strip) * n + col] = total;
 }
 
-__global__ void __launch_bounds__(kThreads) copy_rows_kernel(uint16_t* dst, const Rows src) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int n = static_cast<int>(src.cols);
-  const int64_t ld = copy_ld(n);
-  const int64_t per = ld / 8, total = src.rows * per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-    const int64_t r = i / per;
-    const int e = static_cast<int>(i - r * per) * 8;
-    const uint16_t* const row = static_cast<const uint16_t*>(src.ptr) + r * src.ld;
-    *reinterpret_cast<Pack*>(dst + r * ld + e) = window<false>(row, e, n);
+template <typename T, bool kAligned>
+int launch_prepare(const PrepareParams& q, unsigned blocks, cudaStream_t s) {
+  const auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, 1u, q);
+  };
+  switch (q.p.activation) {
+    case LINEAR_RELU: return go(prepare_kernel<T, kAligned, LINEAR_RELU>);
+    case LINEAR_GELU: return go(prepare_kernel<T, kAligned, LINEAR_GELU>);
+    case LINEAR_GELU_TANH: return go(prepare_kernel<T, kAligned, LINEAR_GELU_TANH>);
+    case LINEAR_SILU: return go(prepare_kernel<T, kAligned, LINEAR_SILU>);
+    default: return go(prepare_kernel<T, kAligned, LINEAR_NONE>);
   }
 }
 
@@ -118,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) sum_strips_kernel(const LinearParams
   extern __shared__ GroupStart start[];
   grid_launch_dependents();
   grid_dependency_wait();
-  if (threadIdx.x < 32) linear_starts<kLinM>(p, start, threadIdx.x);
+  if (threadIdx.x < 32) linear_starts(p, start, threadIdx.x);
   __syncthreads();
   linear_sum_strips<T>(p, start, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
                        static_cast<int64_t>(gridDim.x) * kThreads);
@@ -126,26 +163,27 @@ __global__ void __launch_bounds__(kThreads) sum_strips_kernel(const LinearParams
 
 }  // namespace
 
-int copy_rows(void* dst, const Rows& src, int sms, cudaStream_t stream) {
-  const int64_t pieces = src.rows * (copy_ld(src.cols) / 8);
-  const int64_t blocks = std::min<int64_t>((pieces + kThreads - 1) / kThreads, 8LL * sms);
-  return launch_pdl(copy_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream,
-                    1u, static_cast<uint16_t*>(dst), src);
-}
-
-int grad_rows(const GradRows& g, cudaStream_t stream) {
-  const bool aligned = loads_as_is(g.grad) && (!g.preact || (aligned_to(g.preact, 16) && g.grad.cols % 8 == 0)) &&
-                       g.grad.cols % 8 == 0;
-  const int64_t strips = g.offsets ? g.grad.rows / g.strip_rows + g.groups
-                                   : (g.grad.rows + g.strip_rows - 1) / g.strip_rows;
-  const dim3 grid(static_cast<unsigned>((g.grad.cols + 255) / 256), static_cast<unsigned>(strips));
-  const auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, 1u, g);
-  };
-  if (g.type == MOE_F16)
-    return aligned ? go(grad_rows_kernel<__half, true>) : go(grad_rows_kernel<__half, false>);
-  return aligned ? go(grad_rows_kernel<__nv_bfloat16, true>)
-                 : go(grad_rows_kernel<__nv_bfloat16, false>);
+int prepare_rows(const PrepareRows& p, cudaStream_t stream) {
+  PrepareParams q;
+  q.p = p;
+  q.col_blocks = static_cast<int>((p.grad.cols + 255) / 256);
+  const int64_t strips = p.offsets ? p.grad.rows / p.strip_rows + p.groups
+                                   : (p.grad.rows + p.strip_rows - 1) / std::max(p.strip_rows, 1);
+  int64_t blocks = p.grad.rows > 0 ? q.col_blocks * strips : 0;
+  for (int i = 0; i < 2; ++i) {
+    q.first_copy[i] = blocks;
+    if (p.to[i])
+      blocks += (p.from[i].rows * (copy_ld(p.from[i].cols) / 8) + kCopyPieces - 1) / kCopyPieces;
+  }
+  if (blocks == 0) return GEMM_OK;
+  if (blocks > INT_MAX) return GEMM_ERR_INVALID_VALUE;
+  const bool aligned = loads_as_is(p.grad) && p.grad.cols % 8 == 0 && aligned_to(p.preact, 16);
+  const unsigned n = static_cast<unsigned>(blocks);
+  if (p.type == MOE_F16)
+    return aligned ? launch_prepare<__half, true>(q, n, stream)
+                   : launch_prepare<__half, false>(q, n, stream);
+  return aligned ? launch_prepare<__nv_bfloat16, true>(q, n, stream)
+                 : launch_prepare<__nv_bfloat16, false>(q, n, stream);
 }
 
 int sum_strips(const LinearParams& p, int type, int sms, cudaStream_t stream) {

@@ -15,9 +15,6 @@ inline bool loads_as_is(const Rows& r) { return aligned_to(r.ptr, 16) && r.ld % 
 // Elements between the rows of a copy that they can take.
 __host__ __device__ inline int64_t copy_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
-// dst (16-byte aligned, copy_ld(src.cols) between rows) = src.
-int copy_rows(void* dst, const Rows& src, int sms, cudaStream_t stream);
-
 // Rows of a strip for `rows` rows: 64, more where that would be over 512 strips.
 inline int strip_rows_for(int64_t rows) {
   int64_t s = 64;
@@ -25,16 +22,20 @@ inline int strip_rows_for(int64_t rows) {
   return static_cast<int>(s);
 }
 
-// dz = grad_out act'(preact), for the rows that are in a group.
-struct GradRows {
-  Rows grad;                 // grad_out
+// What a call has to do with rows before its products, in one launch.
+struct PrepareRows {
+  // dz = grad_out act'(preact), for the rows that are in a group
+  Rows grad;                 // grad_out; no rows: nothing of this
   const void* preact;        // contiguous; null for LINEAR_NONE
   void* dz;                  // copy_ld(cols) between rows; or null
   float* strips;             // sums of dz over strips of rows; or null
   const int32_t* offsets;    // or null: one group
   int groups, strip_rows, type, activation;
+  // copies, copy_ld(cols) between rows, 16-byte aligned; null: none
+  Rows from[2];
+  void* to[2];
 };
-int grad_rows(const GradRows& g, cudaStream_t stream);
+int prepare_rows(const PrepareRows& p, cudaStream_t stream);
 
 // grad_bias from the strips alone (else a product's kernel does that).
 int sum_strips(const LinearParams& p, int type, int sms, cudaStream_t stream);

@@ -246,9 +246,9 @@ struct GroupStart {
 // Where each group starts, and the end, by one warp.  All offsets of 128 groups
 // are asked for at once: nothing can be loaded before this is done, and one
 // latency of memory is 0.4 us.
-template <int kBN>
+// Tiles of 2^shift rows.
 __device__ __forceinline__ void find_groups(const int32_t* offsets, int groups, GroupStart* start,
-                                            int lane) {
+                                            int lane, int shift) {
   constexpr int kAhead = 4;
   int32_t total = 0;
   for (int g0 = 0; g0 <= groups; g0 += 32 * kAhead) {
@@ -260,7 +260,7 @@ __device__ __forceinline__ void find_groups(const int32_t* offsets, int groups, 
       const int g = g0 + 32 * i + lane;
       const int32_t next = __shfl_down_sync(0xffffffffu, row[i], 1);
       const int32_t first = __shfl_sync(0xffffffffu, row[i + 1], 0);
-      const int32_t n = ((lane < 31 ? next : first) - row[i] + kBN - 1) / kBN;  // 0 past the last
+      const int32_t n = ((lane < 31 ? next : first) - row[i] + (1 << shift) - 1) >> shift;  // 0 past the last
       int32_t upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
