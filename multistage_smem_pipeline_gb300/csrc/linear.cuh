@@ -119,6 +119,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
+// Arrive on an mbarrier of the cluster without a release: it does not wait for this
+// thread's stores to be performed.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b,
                                               uint32_t c, uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a),
@@ -236,11 +243,13 @@ __device__ __forceinline__ LinearTile linear_tile(int t, const LinearParams& p,
       else hi = mid - 1;
     }
     const int first = start[lo].row, rows = start[lo + 1].row - first;
-    linear_raster(t - start[lo].tiles * p.m_tiles, (rows + p.tile - 1) >> p.tile_shift, p.m_tiles,
-                  &nt, &mt);
+    const int n_tiles = (rows + p.tile - 1) >> p.tile_shift;
+    linear_raster(t - start[lo].tiles * p.m_tiles, n_tiles, p.m_tiles, &nt, &mt);
+    // a group's tiles are of one size, to 32 rows, so that what runs at once ends at once
+    const int each = n_tiles > 1 ? ((rows + n_tiles - 1) / n_tiles + 31) & ~31 : rows;
     o.group = lo;
-    o.n = first + (nt << p.tile_shift);
-    o.n_count = min(p.tile, rows - (nt << p.tile_shift));
+    o.n = first + nt * each;
+    o.n_count = min(each, rows - nt * each);
     o.k_row = 0;
     o.k_len = p.k;
     o.m = mt * kM;
@@ -351,6 +360,16 @@ __device__ __forceinline__ float gelu_tanh_argument(float z) {
   return 1.5957691f * z * fmaf(0.044715f, z * z, 1.0f);
 }
 
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // P(Z <= z) of a standard normal Z, and its density there times sqrt(2 pi).  Below 0
 // it is e^(-z^2/2) f(|z|) with f(s) = erfcx(s / sqrt 2) / 2, here a polynomial in
 // t = 1 / (1 + 0.3 s) that was fitted to f by weighted least squares (relative
@@ -361,7 +380,7 @@ struct Normal {
   float below, density;
 };
 __device__ __forceinline__ Normal normal(float z) {
-  const float s = fabsf(z), t = __fdividef(1.0f, fmaf(0.3f, s, 1.0f));
+  const float s = fabsf(z), t = rcp_ftz(fmaf(0.3f, s, 1.0f));
   float f = 0.035674453f;
   f = fmaf(f, t, -0.15720180f);
   f = fmaf(f, t, 0.20635141f);
@@ -385,23 +404,35 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
+// z within -100 and 100, a NaN as it is.
+__device__ __forceinline__ float within_100(float z) {
+  float y;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2C80000;\n\tmin.NaN.f32 %0, t, 0f42C80000;\n\t}"
+      : "=f"(y)
+      : "f"(z));
+  return y;
+}
+
 // act'(z).  Past 100 it is 0 or 1 in fp32, and products of what overflows and what
-// vanishes there would be NaN.
+// vanishes there would be NaN.  The sigmoid p keeps its relative accuracy below 0,
+// where the slope vanishes with it, and 1 - p has an absolute one that is enough where
+// the slope is near 1.  Results below fp32's normal numbers are 0.
 template <int kActivation>
 __device__ __forceinline__ float activation_slope(float z) {
   if (kActivation == LINEAR_NONE) return 1.0f;
   if (kActivation == LINEAR_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  if (fabsf(z) > 100.0f) z = copysignf(100.0f, z);
+  z = within_100(z);
   if (kActivation == LINEAR_GELU) {
     const Normal n = normal(z);
     return fmaf(z * 0.39894228f, n.density, n.below);
   }
-  if (kActivation == LINEAR_GELU_TANH) {
-    const Sigmoids s = sigmoids(gelu_tanh_argument(z));
-    return fmaf(z * fmaf(0.21406445f, z * z, 1.5957691f), s.up * s.down, s.up);
+  if (kActivation == LINEAR_GELU_TANH) {  // factors of -log2(e) in front
+    const float zz = z * z;
+    const float p = rcp_ftz(1.0f + exp2_ftz(z * fmaf(-0.10294324f, zz, -2.3022082f)));
+    return fmaf(z * fmaf(0.21406445f, zz, 1.5957691f), p * (1.0f - p), p);
   }
-  const Sigmoids s = sigmoids(z);
-  return s.up * fmaf(z, s.down, 1.0f);
+  const float p = rcp_ftz(1.0f + exp2_ftz(-1.4426950f * z));
+  return p * fmaf(z, 1.0f - p, 1.0f);
 }
 
 // The activation of some values; the choice is made once for them.

@@ -42,13 +42,12 @@ __device__ void copy_block(const Rows& src, uint16_t* dst, int64_t block) {
 }
 
 // A block of dz: 256 columns (a lane has eight) of a strip of rows, which its warps
-// take by turns, four rows of loads in flight each (two, of two loads, where rows are
-// not aligned).  Memory bounds it: reads of
+// take by turns, two rows of loads in flight each.  Memory bounds it: reads of
 // grad_out and z and the write of dz.
 template <typename T, bool kAligned, int kActivation>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     prepare_kernel(const __grid_constant__ PrepareParams q) {
-  constexpr int kAhead = kAligned ? 4 : 2;
+  constexpr int kAhead = 2;
   constexpr bool kSlope = kActivation != LINEAR_NONE;
   __shared__ float partial[kWarps][256 + 8];
   __shared__ int found[2];   // first row, rows
