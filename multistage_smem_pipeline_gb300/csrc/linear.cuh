@@ -37,7 +37,8 @@ namespace gb300 {
 constexpr int kLinM = 128;            // the M of a CTA: one accumulator lane each
 constexpr int kLinK = 64;             // summed elements of a stage: 128 bytes, a swizzle row
 constexpr int kLinEpiWarps = 8;
-constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;
+constexpr int kLinZeroWarp = 2 + kLinEpiWarps;  // grad_w: zeroes what is no group's in a stage
+constexpr int kLinThreads = 96 + 32 * kLinEpiWarps;
 constexpr int kLinMaxStages = 12;
 constexpr uint32_t kLinABytes = kLinM * kLinK * 2;
 constexpr uint32_t kLinChunkBytes = 64 * kLinK * 2;  // MN-major: 64 columns by 64 of the sum
@@ -77,7 +78,7 @@ __host__ __device__ constexpr bool b_mn(int product) { return product == LINEAR_
 
 // Shared memory past the ring and the epilogue's buffers: barriers, the tensor
 // memory address, the abort flag, and where each group starts; 1 KiB to align.
-constexpr uint32_t kLinBars = 3 * kLinMaxStages + 5;
+constexpr uint32_t kLinBars = 4 * kLinMaxStages + 5;
 __host__ __device__ constexpr uint32_t linear_fixed_bytes(int groups) {
   return 8 * kLinBars + 24 + 8 * (groups + 1) + 1024;
 }
@@ -285,8 +286,18 @@ __device__ __forceinline__ bool linear_ragged(const LinearTile& t, int kb, const
   return p.offsets && (t.k_len & 15) && t.k_len - kb * kLinK < kLinK;
 }
 
+// Waits, in grad_w, for the last loads of ragged stages, on the way out; bit s of
+// `phases` is the parity of the slot's next.
+__device__ __forceinline__ void linear_drain_ragged(uint32_t first_bar, int stages, uint32_t phases,
+                                                    uint64_t timeout_ns) {
+  for (int s = 0; s < stages; ++s)
+    linear_wait_drain(first_bar + 8u * s, ((phases >> s) & 1u) ^ 1u, timeout_ns);
+}
+
 // Zeroes, in `chunks` chunks of 64 columns, the rows of the stage's last step that
-// are past the sum's end.  By a warp; the MMAs see it after the proxy fence.
+// are past the sum's end.  By a warp of its own, which is ahead of the MMAs as the
+// loads are (on single CTAs with 128 columns 759 us for 4096 tokens x 8 of 64 experts
+// by the MMAs' warp, 719 so); they see it after the proxy fence.
 __device__ __forceinline__ void linear_zero_rows(uint32_t at, int chunks, int valid, int lane) {
   const int pieces = (((valid + 15) & ~15) - valid) * 8;
   for (int c = 0; c < chunks; ++c)

@@ -5,7 +5,8 @@
 //   warp 0 -- producer: per 64 of the sum, TMA boxes of both operands into a ring;
 //   warp 1 -- MMA issuer, into two accumulators by turns;
 //   warps 2 .. 9 -- epilogue: two warps for each quadrant of lanes, which take
-//       32 columns by turns (linear_finish).
+//       32 columns by turns (linear_finish);
+//   warp 10 -- grad_w: zeroes the rows of other groups in a sum's last stage.
 // The loops of the issuing warps are run by the whole warp, and one lane issues.
 //
 // kSplit: few tiles.  The CTAs of a cluster share one tile, each taking its part of
@@ -36,9 +37,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int tile_step = kSplit ? INT_MAX / 4 : gridDim.x;  // kSplit: one tile
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
-  const auto tfull_bar = [&](int b) { return bars + 8u * (2 * kLinMaxStages + b); };
-  const auto tempty_bar = [&](int b) { return bars + 8u * (2 * kLinMaxStages + 2 + b); };
-  const uint32_t drain_bar = bars + 8u * (2 * kLinMaxStages + 4);
+  // grad_w's ragged stages: loaded; and zeroed
+  const auto ragged_bar = [&](int s) { return bars + 8u * (2 * kLinMaxStages + s); };
+  const auto ready_bar = [&](int s) { return bars + 8u * (3 * kLinMaxStages + s); };
+  const auto tfull_bar = [&](int b) { return bars + 8u * (4 * kLinMaxStages + b); };
+  const auto tempty_bar = [&](int b) { return bars + 8u * (4 * kLinMaxStages + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (4 * kLinMaxStages + 4);
   uint8_t* const misc = smem + (bars - base) + 8 * kLinBars;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -52,6 +56,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+      mbar_init(ragged_bar(s), 1);
+      mbar_init(ready_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
@@ -87,7 +93,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     int stage = 0;
-    uint32_t phase = 0, issued = 0;
+    uint32_t phase = 0, issued = 0, ragged_phase = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
@@ -99,14 +105,18 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           ok = false;
           break;
         }
+        const bool ragged = kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb, p);
         if (elect_one()) {
-          const uint32_t full = full_bar(stage);
+          // a ragged stage is full at once, and ready once it has landed and is zeroed
+          const uint32_t full = ragged ? ragged_bar(stage) : full_bar(stage);
           mbar_arrive_expect_tx(full, loads.bytes);
+          if (ragged) mbar_arrive(full_bar(stage));
           if (!(p.inject && issued == 0))
             linear_load<kProduct, false>(loads, base + stage * stage_bytes, &tmA, &tmB, full,
                                          kb * kLinK, tile, p);
         }
         __syncwarp();
+        if (ragged) ragged_phase ^= 1u << stage;
         ++issued;
         if (++stage == stages) {
           stage = 0;
@@ -118,10 +128,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
     for (uint32_t i = first; i < issued; ++i)
       linear_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
+    if (kProduct == LINEAR_GRAD_W)
+      linear_drain_ragged(ragged_bar(0), stages, ragged_phase, p.timeout_ns);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    uint32_t phase = 0, acc_phase = 0, ready_phase = 0;
     bool ok = true;
     const uint64_t a_desc0 = linear_desc<kAMn>(base);
     const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
@@ -139,12 +151,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           break;
         }
         if (kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb, p)) {
-          const uint32_t a = base + stage * stage_bytes;
-          const int valid = tile.k_len - kb * kLinK;
-          linear_zero_rows(a, kLinM / 64, valid, lane);
-          linear_zero_rows(a + kLinABytes, p.tile / 64, valid, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
+          if (!linear_wait_warp(ready_bar(stage), (ready_phase >> stage) & 1u, abort_flag, kLinPeer, p)) {
+            ok = false;
+            break;
+          }
+          ready_phase ^= 1u << stage;
         }
         tc_fence_after_sync();
         const int steps = linear_steps(tile, kb);
@@ -180,6 +191,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (elect_one()) umma_commit(drain_bar);
     __syncwarp();
     linear_wait_drain(drain_bar, 0, p.timeout_ns);
+  } else if (warp == kLinZeroWarp) {
+    // ---------------------------------------------------------- grad_w's ragged stages
+    if (kProduct == LINEAR_GRAD_W && p.offsets) {
+      int done = 0;  // stages of tiles before
+      uint32_t ragged_phase = 0;
+      for (int t = first_tile; t < tiles; t += tile_step) {
+        const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
+        int from, end;
+        stages_of(tile, &from, &end);
+        done += end - from;
+        if (end == from || !linear_ragged(tile, end - 1, p)) continue;
+        const int stage = (done - 1) % stages;
+        if (!linear_wait_warp(ragged_bar(stage), (ragged_phase >> stage) & 1u, abort_flag, kLinFull, p))
+          break;
+        ragged_phase ^= 1u << stage;
+        const uint32_t a = base + stage * stage_bytes;
+        const int valid = tile.k_len - (end - 1) * kLinK;
+        linear_zero_rows(a, kLinM / 64, valid, lane);
+        linear_zero_rows(a + kLinABytes, p.tile / 64, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready_bar(stage));
+      }
+    }
   } else if (!kSplit) {
     // ---------------------------------------------------------- epilogue
     const int q = warp & 3;               // the lane quadrant this warp may read
@@ -208,6 +243,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // Chunk (q, c) is the 4 c + q-th, and CTA u / mine owns the u-th.  Of one's own there
     // is a buffer in the ring for each part.
     const bool live_tile = first_tile < tiles;
+    const bool epilogue = warp >= 2 && warp != kLinZeroWarp;
     LinearTile tile = {};
     if (live_tile) tile = linear_tile<kProduct, kLinM>(first_tile, p, start);
     const int mine = max(1, p.tile / 8 / p.split);
@@ -215,12 +251,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const auto slot = [&](int s, int i) {
       return base + static_cast<uint32_t>(s * mine + i) * kLinBufBytes;
     };
-    if (warp >= 2 && kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
+    if (epilogue && kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
     int ok = 1;
-    if (warp >= 2 && live_tile) ok = linear_wait_warp(tfull_bar(0), 0, abort_flag, kLinTmemFull, p);
+    if (epilogue && live_tile) ok = linear_wait_warp(tfull_bar(0), 0, abort_flag, kLinTmemFull, p);
     __syncwarp();
     cluster_sync();  // all rings are free
-    if (warp >= 2 && live_tile && ok) {
+    if (epilogue && live_tile && ok) {
       tc_fence_after_sync();
       int from, end;
       stages_of(tile, &from, &end);
@@ -235,7 +271,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     __syncwarp();
     cluster_sync();  // all parts have come
-    if (warp >= 2) {
+    if (epilogue) {
       if (live_tile && ok) {
         for (int i = warp - 2; i < mine; i += kLinEpiWarps) {
           const int u = part * mine + i;

@@ -9,8 +9,8 @@
 // bytes; `empty` and `tfull` are in both, committed to both; `tempty` in the even
 // CTA takes every epilogue warp of both.  grad_w's ragged stages (see linear.cuh)
 // are different: each CTA has to zero rows of its own, so their loads count on
-// each CTA's own `full`, and the odd CTA's second warp, idle otherwise, zeroes its
-// rows and says so on `ready` of the even one.
+// `ragged` of each CTA, and a warp of each zeroes its rows and says so on `ready`
+// of the even one; `full` of such a stage is passed at once.
 #pragma once
 #include "linear.cuh"
 
@@ -39,10 +39,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t bars = bufs + kLinEpiWarps * kLinBufBytes;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
-  const auto ready_bar = [&](int s) { return bars + 8u * (2 * kLinMaxStages + s); };
-  const auto tfull_bar = [&](int b) { return bars + 8u * (3 * kLinMaxStages + b); };
-  const auto tempty_bar = [&](int b) { return bars + 8u * (3 * kLinMaxStages + 2 + b); };
-  const uint32_t drain_bar = bars + 8u * (3 * kLinMaxStages + 4);
+  // grad_w's ragged stages: loaded; and zeroed
+  const auto ragged_bar = [&](int s) { return bars + 8u * (2 * kLinMaxStages + s); };
+  const auto ready_bar = [&](int s) { return bars + 8u * (3 * kLinMaxStages + s); };
+  const auto tfull_bar = [&](int b) { return bars + 8u * (4 * kLinMaxStages + b); };
+  const auto tempty_bar = [&](int b) { return bars + 8u * (4 * kLinMaxStages + 2 + b); };
+  const uint32_t drain_bar = bars + 8u * (4 * kLinMaxStages + 4);
   uint8_t* const misc = smem + (bars - base) + 8 * kLinBars;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
@@ -53,7 +55,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(ready_bar(s), 1);
+      mbar_init(ragged_bar(s), 1);
+      mbar_init(ready_bar(s), 2);  // both CTAs
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------- producer (both CTAs)
     int stage = 0;
     uint32_t phase = 0, issued = 0;
-    uint32_t own_phase = 0;  // odd CTA: bit s is the parity of its own full_bar(s)
+    uint32_t ragged_phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
@@ -106,15 +109,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         const bool ragged = kWeight && linear_ragged(tile, kb, p);
         if (elect_one()) {
-          const uint32_t full = mapa_shared(full_bar(stage), ragged ? rank : 0);
-          if (ragged) mbar_arrive_expect_tx(full_bar(stage), loads.bytes);
-          else if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), both_bytes);
+          const uint32_t full = ragged ? mapa_shared(ragged_bar(stage), rank)
+                                       : mapa_shared(full_bar(stage), 0);
+          if (ragged) mbar_arrive_expect_tx(ragged_bar(stage), loads.bytes);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), ragged ? 0 : both_bytes);
           if (!(p.inject && issued == 0 && rank == 0))
             linear_load<kProduct, true>(loads, base + stage * kLinPairStage, &tmA, &tmB, full,
                                         kb * kLinK, tile, p);
         }
         __syncwarp();
-        if (ragged) own_phase ^= 1u << stage;
+        if (ragged) ragged_phase ^= 1u << stage;
         ++issued;
         if (++stage == stages) {
           stage = 0;
@@ -122,14 +126,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
       }
     }
-    if (rank == 0) {  // both CTAs' bytes, but for those of ragged stages
+    if (rank == 0) {  // both CTAs' bytes
       const uint32_t first = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
       for (uint32_t i = first; i < issued; ++i)
         linear_wait_drain(full_bar(i % stages), (i / stages) & 1u, p.timeout_ns);
-    } else if (kWeight) {
-      for (int s = 0; s < stages; ++s)  // the last ragged load of each slot
-        linear_wait_drain(full_bar(s), ((own_phase >> s) & 1u) ^ 1u, p.timeout_ns);
     }
+    if (kWeight) linear_drain_ragged(ragged_bar(0), stages, ragged_phase, p.timeout_ns);
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------- MMA issuer
     int stage = 0, acc = 0;
@@ -150,12 +152,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           break;
         }
         if (kWeight && linear_ragged(tile, kb, p)) {
-          const uint32_t a = base + stage * kLinPairStage;
-          const int valid = tile.k_len - kb * kLinK;
-          linear_zero_rows(a, kLinM / 64, valid, lane);
-          linear_zero_rows(a + kLinABytes, kLinPairTile / 128, valid, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
           if (!linear_wait_warp<true>(ready_bar(stage), (ready_phase >> stage) & 1u, abort_flag,
                                       kLinPeer, p)) {
             ok = false;
@@ -205,33 +201,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         acc_phase ^= 1u;
       }
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- odd CTA's ragged stages
+  } else if (warp == kLinZeroWarp) {
+    // ---------------------------------------------------------- grad_w's ragged stages (both CTAs)
     if (kWeight && p.offsets) {
-      int stage = 0;
-      uint32_t own_phase = 0;
+      int done = 0;  // stages of tiles before
+      uint32_t ragged_phase = 0;
       for (int t = pair; t < tiles; t += pairs) {
         const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
         const int kbs = (tile.k_len + kLinK - 1) / kLinK;
-        if (kbs == 0) continue;
-        stage = (stage + kbs - 1) % stages;  // that of the tile's last
-        if (linear_ragged(tile, kbs - 1, p)) {
-          if (!linear_wait_warp(full_bar(stage), (own_phase >> stage) & 1u, abort_flag, kLinFull, p))
-            break;
-          own_phase ^= 1u << stage;
-          const uint32_t a = base + stage * kLinPairStage;
-          const int valid = tile.k_len - (kbs - 1) * kLinK;
-          linear_zero_rows(a, kLinM / 64, valid, lane);
-          linear_zero_rows(a + kLinABytes, kLinPairTile / 128, valid, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(ready_bar(stage), 0));
-          __syncwarp();
-        }
-        if (++stage == stages) stage = 0;
+        done += kbs;
+        if (kbs == 0 || !linear_ragged(tile, kbs - 1, p)) continue;
+        const int stage = (done - 1) % stages;
+        if (!linear_wait_warp(ragged_bar(stage), (ragged_phase >> stage) & 1u, abort_flag, kLinFull, p))
+          break;
+        ragged_phase ^= 1u << stage;
+        const uint32_t a = base + stage * kLinPairStage;
+        const int valid = tile.k_len - (kbs - 1) * kLinK;
+        linear_zero_rows(a, kLinM / 64, valid, lane);
+        linear_zero_rows(a + kLinABytes, kLinPairTile / 128, valid, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(ready_bar(stage), 0));
       }
     }
-  } else {
+  } else if (warp >= 2) {
     // ---------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;
     const int half = (warp - 2) >> 2;
