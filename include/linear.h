@@ -107,7 +107,7 @@ enum { LINEAR_FORWARD = 0, LINEAR_GRAD_X = 1, LINEAR_GRAD_W = 2 };
 /* How a product is cut. */
 typedef struct {
   int cta_pair;              /* 1: 256 x 256 tiles on CTA pairs; 0: 128 x tile on single CTAs */
-  int tile;                  /* rows of a tile (grad_w: inputs): 256; on single CTAs also 64, 128
+  int tile;                  /* rows of a tile (grad_w: outputs): 256; on single CTAs also 64, 128
                                 and, but for grad_w, 32 */
   int split_k;               /* CTAs of a cluster that share a tile's sums; 1: none do */
   int ctas;                  /* launched */

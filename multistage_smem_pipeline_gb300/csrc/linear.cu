@@ -114,7 +114,7 @@ struct Plan {
 };
 
 // A product as the tensor cores see it: m by n, n over all groups but for grad_w, whose
-// sums are (k); `ragged`: groups by offsets.
+// sums (k) are; `ragged`: groups by offsets.
 struct Product {
   int kind;
   int64_t m, n, k;
@@ -126,7 +126,7 @@ Product product_of(int kind, int64_t rows, int64_t in, int64_t out, int64_t grou
   switch (kind) {
     case LINEAR_FORWARD: return Product{kind, out, rows, in, groups, ragged};
     case LINEAR_GRAD_X: return Product{kind, in, rows, out, groups, ragged};
-    default: return Product{kind, out, in, rows, groups, ragged};
+    default: return Product{kind, in, out, rows, groups, ragged};
   }
 }
 
@@ -212,7 +212,7 @@ int encode(EncodeTiledFn fn, CUtensorMap* map, const void* ptr, int64_t cols, in
 
 template <typename T, int kProduct>
 int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaStream_t s) {
-  const uint32_t fixed = linear_fixed_bytes(p.groups) + (plan.split > 1 ? 0u : kLinEpiWarps * kLinBufBytes);
+  const uint32_t fixed = linear_fixed_bytes(p.groups);
   const uint32_t stage = plan.pair ? kLinPairStage : kLinABytes + plan.tile * (kLinK * 2);
   p.stages = std::min<int>((kLinSmemLimit - fixed) / stage, kLinMaxStages);
   const size_t smem = fixed + p.stages * stage;
@@ -228,15 +228,15 @@ int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaS
 }
 
 // One product of operands that the tensor maps take as they are: `a` is that of M, w or
-// (grad_w) dz, and `b` that of N, x or dz.
+// (grad_w) x, and `b` that of N, x or dz.
 int launch(const Product& pr, const Rows& a, const Rows& b, LinearParams p, int type,
            const linear_options_t* opt, int sms, int device, cudaStream_t s) {
   Plan plan;
   int rc = make_plan(pr, machine_of(sms, device), opt, &plan);
   if (rc != GEMM_OK) return rc;
   const bool weight = pr.kind == LINEAR_GRAD_W;
-  p.n = static_cast<int32_t>(weight ? pr.n : pr.m);
-  p.m = weight ? static_cast<int32_t>(pr.m) : 0;
+  p.n = static_cast<int32_t>(pr.m);
+  p.m = weight ? static_cast<int32_t>(pr.n) : 0;
   p.k = static_cast<int32_t>(pr.k);
   p.groups = static_cast<int32_t>(pr.groups);
   p.tile = plan.tile;
@@ -496,7 +496,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
     p.strips = for_bias ? strips : nullptr;
     rc = launch(product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
                            p.offsets != nullptr),
-                dz, x, p, layer->type, opt, sms, device, s);
+                x, dz, p, layer->type, opt, sms, device, s);
     if (rc != GEMM_OK || strips) return rc;
   }
   if (!for_bias) return GEMM_OK;

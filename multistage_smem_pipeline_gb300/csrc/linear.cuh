@@ -7,12 +7,14 @@
 //   grad_w   dz^T x           D out x in,   sums over rows
 // The tensor cores take operands either with the summed index contiguous (K-major) or
 // with the other one (MN-major), so nothing is transposed in memory.  One operand has
-// their M, 128 a CTA, the other their N, any multiple of 16:
+// their M, 128 a CTA, the other their N, any multiple of 16.  M are D's columns and N its
+// rows, so that a lane of the accumulator is a column of D, and what a warp stores at once
+// lies next to each other:
 //              M                              N
 //   forward    outputs, w       K-major       rows, x       K-major
 //   grad_x     inputs, w^T      MN-major      rows, dz      K-major
-//   grad_w     outputs, dz^T    MN-major      inputs, x^T   MN-major
-// Rows are the N of the first two because groups are ragged in rows: a tile of 5 rows
+//   grad_w     inputs, x^T      MN-major      outputs, dz^T MN-major
+// Groups are ragged in rows, the N of the first two: a tile of 5 rows
 // costs an instruction of 16 columns, and one that ends with its group what it
 // has.  (With rows as M, in steps of 128 or 256, 4096 tokens x 8 of 64 experts,
 // 4096 -> 2048, took 392 us.)  The rows of the next group that its last copy of rows brings
@@ -42,7 +44,7 @@ constexpr int kLinThreads = 96 + 32 * kLinEpiWarps;
 constexpr int kLinMaxStages = 12;
 constexpr uint32_t kLinABytes = kLinM * kLinK * 2;
 constexpr uint32_t kLinChunkBytes = 64 * kLinK * 2;  // MN-major: 64 columns by 64 of the sum
-constexpr uint32_t kLinBufBytes = 32 * 32 * 4;       // an epilogue warp's 32 x 32 sums
+constexpr uint32_t kLinBufBytes = 32 * 32 * 4;       // kSplit: 32 x 32 sums
 constexpr uint32_t kLinSmemLimit = 232448;
 
 struct LinearParams {
@@ -56,7 +58,7 @@ struct LinearParams {
   uint16_t* grad_bias;
   int32_t strip_rows;
   int32_t rows;              // of all groups, and those of none
-  int32_t m;                 // grad_w: rows of a group's D
+  int32_t m;                 // grad_w: rows of a group's D (outputs)
   int32_t n;                 // columns of D
   int32_t k;                 // forward, grad_x: length of the sums
   int32_t groups;
@@ -66,7 +68,7 @@ struct LinearParams {
   int32_t box_rows;          // forward, grad_x: rows that one copy loads
   int32_t stages, split;
   int32_t activation;
-  int32_t vector;            // D, bias and residual can be accessed 16 bytes at a time
+  int32_t vector;            // kSplit: D, bias and residual can be accessed 16 bytes at a time
   int32_t inject;            // 1: leave out each CTA's first loads
   int32_t error_word;
   uint64_t timeout_ns;
@@ -76,7 +78,7 @@ struct LinearParams {
 __host__ __device__ constexpr bool a_mn(int product) { return product != LINEAR_FORWARD; }
 __host__ __device__ constexpr bool b_mn(int product) { return product == LINEAR_GRAD_W; }
 
-// Shared memory past the ring and the epilogue's buffers: barriers, the tensor
+// Shared memory past the ring: barriers, the tensor
 // memory address, the abort flag, and where each group starts; 1 KiB to align.
 constexpr uint32_t kLinBars = 4 * kLinMaxStages + 5;
 __host__ __device__ constexpr uint32_t linear_fixed_bytes(int groups) {
@@ -124,13 +126,6 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 // thread's stores to be performed.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b,
-                                              uint32_t c, uint32_t d) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a),
-               "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 
@@ -186,17 +181,16 @@ __device__ __forceinline__ void linear_wait_drain(uint32_t bar, uint32_t parity,
 }
 
 // ------------------------------------------------------------------ tiles
-// forward and grad_x: M is columns of D, N its rows; grad_w: the other way about.
 struct LinearTile {
   int32_t group;
-  int32_t m, m_count;   // first of the group's, and how many, at most the tile's
-  int32_t n, n_count;   // the same of N; forward and grad_x: first of all rows
+  int32_t m, m_count;   // columns of D: first, and how many
+  int32_t n, n_count;   // rows: forward, grad_x of all groups; grad_w of its own
   int32_t k_row;        // grad_w: the first summed row
   int32_t k_len;        // length of the sums
 };
 
-// Row tiles (grad_w: tiles of outputs) that walk over the others together, so that
-// what runs at once shares operands in L2.
+// Tiles of rows that walk over the columns together, so that what runs at once shares
+// operands in L2.
 constexpr int kLinRaster = 8;
 
 // Tile t among `slow` x `fast`: bands of kLinRaster of the first, over all of the second.
@@ -229,13 +223,11 @@ __device__ __forceinline__ LinearTile linear_tile(int t, const LinearParams& p,
   if (kProduct == LINEAR_GRAD_W) {
     const int per = p.m_tiles * p.n_tiles;
     o.group = p.groups > 1 ? t / per : 0;
-    linear_raster(t - o.group * per, p.m_tiles, p.n_tiles, &mt, &nt);
+    linear_raster(t - o.group * per, p.n_tiles, p.m_tiles, &nt, &mt);
     o.n = nt * p.tile;
-    o.n_count = min(p.tile, p.n - o.n);
+    o.n_count = min(p.tile, p.m - o.n);
     o.k_row = start[o.group].row;
     o.k_len = start[o.group + 1].row - o.k_row;
-    o.m = mt * kM;
-    o.m_count = min(kM, p.m - o.m);
   } else {
     int lo = 0, hi = p.groups - 1;  // the last group with tiles * m_tiles <= t before it
     while (lo < hi) {
@@ -253,9 +245,9 @@ __device__ __forceinline__ LinearTile linear_tile(int t, const LinearParams& p,
     o.n_count = min(each, rows - nt * each);
     o.k_row = 0;
     o.k_len = p.k;
-    o.m = mt * kM;
-    o.m_count = min(kM, p.n - o.m);
   }
+  o.m = mt * kM;
+  o.m_count = min(kM, p.n - o.m);
   return o;
 }
 
@@ -461,16 +453,7 @@ __device__ __forceinline__ void activate_all(float (&v)[kN], int activation) {
   }
 }
 
-// An epilogue warp's 32 x 32 sums pass through shared memory from the layout of
-// the accumulator (a lane is a column of D, or a row) to that of memory (four lanes are a row's 32
-// columns, eight of them each), so that bias, residual, z and D are read and
-// written 16 bytes a lane, 64 bytes of a row at once.  Piece j (of 16 bytes) of row r
-// is at j ^ (r & 7): neither side has bank conflicts.
-__device__ __forceinline__ uint32_t linear_piece(uint32_t buf, int row, int piece) {
-  return buf + row * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
-}
-
-// 32 columns of a warp's 32 rows from the accumulator; zeros where nothing was summed
+// 32 columns of a warp's 32 lanes of the accumulator, 32 rows of D's; zeros where nothing was summed
 // (`any`).  The load and the wait for it are one statement: until the wait its registers
 // are still being written, and the compiler, which does not know that, would move
 // what it found in them, or use them for something else, in between.
@@ -492,39 +475,6 @@ __device__ __forceinline__ void linear_sums(uint32_t taddr, bool any, uint32_t (
   for (int i = 0; i < 32; ++i) r[i] = any ? r[i] : 0u;
 }
 
-// A lane is a row of D (grad_w), or a column.
-template <int kProduct>
-__device__ __forceinline__ void linear_put(uint32_t buf, int lane, const uint32_t (&r)[32]) {
-  if (kProduct == LINEAR_GRAD_W) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      st_shared_v4(linear_piece(buf, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) + 4u * (lane & 3)),
-                   "r"(r[i])
-                   : "memory");
-  }
-}
-
-// The same into another CTA's shared memory (a shared::cluster address).
-template <int kProduct>
-__device__ __forceinline__ void linear_send(uint32_t buf, int lane, const uint32_t (&r)[32]) {
-  if (kProduct == LINEAR_GRAD_W) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      st_cluster_v4(linear_piece(buf, lane, j), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) +
-                                                           4u * (lane & 3)),
-                   "r"(r[i])
-                   : "memory");
-  }
-}
-
 // 32 x 32 sums of a tile: lanes 32 q on of the accumulator, and columns 32 c on, `m` being
 // the first of the M of the CTA.
 struct LinearChunk {
@@ -536,17 +486,59 @@ template <int kProduct>
 __device__ __forceinline__ LinearChunk linear_chunk(const LinearTile& t, int m, int q, int c,
                                                     const LinearParams& p) {
   LinearChunk o;
-  if (kProduct == LINEAR_GRAD_W) {
-    o.row = static_cast<int64_t>(t.group) * p.m + m + 32 * q;
-    o.live = min(32, p.m - (m + 32 * q));
-    o.col = t.n + 32 * c;
-  } else {
-    o.row = t.n + 32 * c;
-    o.live = min(32, t.n_count - 32 * c);
-    o.col = m + 32 * q;
-  }
+  o.row = (kProduct == LINEAR_GRAD_W ? static_cast<int64_t>(t.group) * p.m : 0) + t.n + 32 * c;
+  o.live = min(32, t.n_count - 32 * c);
+  o.col = m + 32 * q;
   if (o.col >= p.n) o.live = 0;
   return o;
+}
+
+// A chunk of D from the sums in registers, a column of it for each lane: each store of
+// the warp is 64 neighbouring bytes of a row, whatever its alignment.  (Through shared
+// memory, for 16 bytes a lane, the sums took as much of its bandwidth as the MMAs leave: grad_w of
+// 4096 tokens x 8 of 64 experts 468 us, of which 104 were the epilogue's.)
+template <typename T, int kProduct>
+__device__ __forceinline__ void linear_store(float (&v)[32], const LinearParams& p, float bias,
+                                             const T (&residual)[32], const LinearChunk& at,
+                                             int lane) {
+  if (at.col + lane >= p.n) return;
+  const int64_t first = at.row * p.n + at.col + lane;
+  const auto store = [&](uint16_t* to) {
+    T* o = reinterpret_cast<T*>(to) + first;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i < at.live) *o = from_float<T>(v[i]);
+      o += p.n;
+    }
+  };
+  if (kProduct == LINEAR_FORWARD) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += bias;
+    if (p.preact) store(p.preact);
+    activate_all(v, p.activation);
+    if (p.residual) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += to_float(residual[i]);
+    }
+  }
+  store(p.out);
+}
+
+// kSplit: 32 x 32 sums in shared memory, rows of D of 128 bytes, so that bias, residual, z and D
+// are read and written 16 bytes a lane.  Piece j (of 16 bytes) of row r is at j ^ (r & 7):
+// neither side has bank conflicts.
+__device__ __forceinline__ uint32_t linear_piece(uint32_t buf, int row, int piece) {
+  return buf + row * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
+}
+
+// To another CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ void linear_send(uint32_t buf, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) +
+                                                         4u * (lane & 3)),
+                 "r"(r[i])
+                 : "memory");
 }
 
 // What a chunk's epilogue reads from memory, asked for before its sums are there.
@@ -723,33 +715,40 @@ __device__ __forceinline__ void linear_sum_strips(const LinearParams& p, const G
 // the warp's last chunk of it is in registers.  False: the wait gave up.
 template <typename T, int kProduct, typename Wait, typename Release>
 __device__ __forceinline__ bool linear_epilogue(const LinearTile& tile, int m, int q, int half,
-                                                uint32_t t_row, uint32_t buf, const LinearParams& p,
-                                                int lane, Wait wait, Release release) {
+                                                uint32_t t_row, const LinearParams& p, int lane,
+                                                Wait wait, Release release) {
+  constexpr bool kForward = kProduct == LINEAR_FORWARD;
   const auto let_go = [&] {
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) release();
   };
-  int chunks = (tile.n_count + 31) >> 5;
-  LinearChunk at = linear_chunk<kProduct>(tile, m, q, half, p);
-  if (at.live <= 0) chunks = 0;     // then so are the warp's others
-  LinearExtras x;
-  if (chunks > half) x = linear_extras<kProduct>(p, tile.group, at, lane);
+  const int col = m + 32 * q + lane;
+  const int chunks = m + 32 * q < p.n ? (tile.n_count + 31) >> 5 : 0;
+  float bias = 0.0f;
+  if (kForward && p.bias && col < p.n)
+    bias = to_float(reinterpret_cast<const T*>(p.bias)[static_cast<int64_t>(tile.group) * p.n + col]);
   if (!wait()) return false;
   tc_fence_after_sync();
   if (chunks <= half) let_go();
   for (int c = half; c < chunks; c += 2) {
+    const LinearChunk at = linear_chunk<kProduct>(tile, m, q, c, p);
+    T residual[32];
+    if (kForward && p.residual && col < p.n) {
+      const T* from = reinterpret_cast<const T*>(p.residual) + at.row * p.ldr + col;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i < at.live) residual[i] = *from;
+        from += p.ldr;
+      }
+    }
     uint32_t r[32];
     linear_sums(t_row + 32 * c, tile.k_len > 0, r);
     if (c + 2 >= chunks) let_go();
-    linear_put<kProduct>(buf, lane, r);
-    __syncwarp();
-    linear_finish<T, kProduct>(buf, 1, 0, p, x, tile.group, at, lane);
-    __syncwarp();
-    if (c + 2 < chunks) {
-      at = linear_chunk<kProduct>(tile, m, q, c + 2, p);
-      x = linear_extras<kProduct>(p, tile.group, at, lane);
-    }
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    linear_store<T, kProduct>(v, p, bias, residual, at, lane);
   }
   return true;
 }

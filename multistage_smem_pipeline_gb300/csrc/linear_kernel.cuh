@@ -5,7 +5,7 @@
 //   warp 0 -- producer: per 64 of the sum, TMA boxes of both operands into a ring;
 //   warp 1 -- MMA issuer, into two accumulators by turns;
 //   warps 2 .. 9 -- epilogue: two warps for each quadrant of lanes, which take
-//       32 columns by turns (linear_finish);
+//       32 columns by turns, and store from registers;
 //   warp 10 -- grad_w: zeroes the rows of other groups in a sum's last stage.
 // The loops of the issuing warps are run by the whole warp, and one lane issues.
 //
@@ -30,8 +30,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
   const uint32_t stage_bytes = kLinABytes + p.tile * (kLinK * 2);
-  const uint32_t bufs = base + stages * stage_bytes;
-  const uint32_t bars = bufs + (kSplit ? 0u : kLinEpiWarps * kLinBufBytes);
+  const uint32_t bars = base + stages * stage_bytes;
   const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
   const int first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
   const int tile_step = kSplit ? INT_MAX / 4 : gridDim.x;  // kSplit: one tile
@@ -219,15 +218,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------- epilogue
     const int q = warp & 3;               // the lane quadrant this warp may read
     const int half = (warp - 2) >> 2;
-    const uint32_t buf = bufs + (warp - 2) * kLinBufBytes;
     if (kProduct == LINEAR_GRAD_W) linear_sum_strips<T>(p, start);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = first_tile; t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
       const bool ok = linear_epilogue<T, kProduct>(
-          tile, tile.m, q, half, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols, buf,
-          p, lane,
+          tile, tile.m, q, half, tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * acc_cols, p,
+          lane,
           [&] { return linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p); },
           [&] { mbar_arrive(tempty_bar(acc)); });
       if (!ok) break;
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         uint32_t r[32];
         linear_sums(tmem + (static_cast<uint32_t>(q * 32) << 16) + 32 * c, end > from, r);
         const int u = 4 * c + q, owner = u / mine;
-        linear_send<kProduct>(mapa_shared(slot(part, u - owner * mine), owner), lane, r);
+        linear_send(mapa_shared(slot(part, u - owner * mine), owner), lane, r);
       }
     }
     __syncwarp();

@@ -35,8 +35,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   constexpr uint16_t kBoth = 0x3;
-  const uint32_t bufs = base + stages * kLinPairStage;
-  const uint32_t bars = bufs + kLinEpiWarps * kLinBufBytes;
+  const uint32_t bars = base + stages * kLinPairStage;
   const auto full_bar = [&](int s) { return bars + 8u * s; };
   const auto empty_bar = [&](int s) { return bars + 8u * (kLinMaxStages + s); };
   // grad_w's ragged stages: loaded; and zeroed
@@ -228,7 +227,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // ---------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;
     const int half = (warp - 2) >> 2;
-    const uint32_t buf = bufs + (warp - 2) * kLinBufBytes;
     if (kWeight) linear_sum_strips<T>(p, start);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
       const bool ok = linear_epilogue<T, kProduct>(
           tile, tile.m + rank * kLinM, q, half,
-          tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kLinPairTile, buf, p, lane,
+          tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * kLinPairTile, p, lane,
           [&] { return linear_wait_warp(tfull_bar(acc), acc_phase, abort_flag, kLinTmemFull, p); },
           // Nothing in memory goes with it: the accumulator has been read.  With a release
           // the arrival waits until D's stores are performed, and the next tile with it
