@@ -96,7 +96,7 @@ int linear_backward(void* grad_x, void* grad_w, void* grad_bias, const linear_t*
  * dereferenced; their alignment counts).  It is 16-byte aligned, its contents do
  * not matter before or after, and calls that may run at once need one each.
  * Host only. */
-int linear_forward_workspace(const linear_t* layer, uint64_t* bytes);
+int linear_forward_workspace(const linear_t* layer, const linear_options_t* opt, uint64_t* bytes);
 int linear_backward_workspace(const void* grad_x, const void* grad_w, const void* grad_bias,
                               const linear_t* layer, const void* grad_out, int64_t ldg,
                               uint64_t* bytes);
@@ -108,8 +108,10 @@ enum { LINEAR_FORWARD = 0, LINEAR_GRAD_X = 1, LINEAR_GRAD_W = 2 };
 typedef struct {
   int cta_pair;              /* 1: 256 x 256 tiles on CTA pairs; 0: 128 x tile on single CTAs */
   int tile;                  /* rows of a tile (grad_w: outputs): 256; on single CTAs also 64, 128
-                                and, but for grad_w, 32 */
-  int split_k;               /* CTAs of a cluster that share a tile's sums; 1: none do */
+                                and, but for grad_w, 32; forward without the tensor cores: 1, 2,
+                                4, 8 rows at a time */
+  int split_k;               /* CTAs of a cluster (there: warps) that share a tile's sums, 1, 2, 4
+                                or 8; 1: none do */
   int ctas;                  /* launched */
 } linear_config_t;
 

@@ -1,5 +1,8 @@
 // Host side of linear layers: checks, workspaces, the form of a product, tensor
 // maps, launches.
+#include <cmath>
+
+#include "linear_few_kernel.cuh"
 #include "linear_kernel.cuh"
 #include "linear_pair_kernel.cuh"
 #include "linear_rows.cuh"
@@ -53,8 +56,9 @@ int check_layer(const linear_t* l) {
 // `product`: LINEAR_*, or -1 for any.
 bool valid_form(int product, int pair, int tile, int split) {
   if (pair) return pair == 1 && tile == 256 && split == 1;
-  if (tile != 64 && tile != 128 && tile != 256 && (tile != 32 || product == LINEAR_GRAD_W)) return false;
-  return split == 1 || split == 2 || split == 4 || split == 8;
+  if (split != 1 && split != 2 && split != 4 && split != 8) return false;
+  if (tile == 1 || tile == 2 || tile == 4 || tile == 8) return product <= LINEAR_FORWARD;
+  return tile == 64 || tile == 128 || tile == 256 || (tile == 32 && product != LINEAR_GRAD_W);
 }
 
 int check_options(const linear_options_t* o) {
@@ -107,7 +111,7 @@ Machine machine_of(int sms, int device) {
 
 struct Plan {
   bool pair;
-  int tile, split;
+  int tile, split;       // tile up to 8: linear_few
   int m_tiles, n_tiles;  // n_tiles: grad_w's, of a group
   int box_rows;
   int units;             // CTAs, pairs or clusters
@@ -130,13 +134,38 @@ Product product_of(int kind, int64_t rows, int64_t in, int64_t out, int64_t grou
   }
 }
 
+Product forward_of(const linear_t* l) {
+  return product_of(LINEAR_FORWARD, l->rows, l->in, l->out, groups_of(l), offsets_of(l) != nullptr);
+}
+
 // Tiles of N of all groups: as many as are expected, or as there can be.
 int64_t n_tiles(const Product& p, int64_t tile, bool most) {
   if (p.kind == LINEAR_GRAD_W) return p.groups * ((p.n + tile - 1) / tile);
   if (!p.ragged) return (p.n + tile - 1) / tile;
   const int64_t live = std::min(p.groups, p.n);
-  // a group is taken to end half way through its last tile
-  return most ? p.n / tile + live : std::max(live, (2 * p.n + live * tile) / (2 * tile));
+  if (most) return p.n / tile + live;
+  // of groups whose sizes are spread as the intervals of a random process are
+  return std::llround(live / (1.0 - std::exp(-static_cast<double>(tile) * live / p.n)));
+}
+
+// The rows that linear_few takes at a time, where the product is its: by sizes alone, so
+// that the workspace does not depend on the device.  0: it is not.  In millions of
+// multiplications, from 160 shapes of 1 to 16 rows, or 0.02 to 4 for each of 8 to 64 experts:
+// up to 4 rows always (4 x 14336 x 4096 23.7 us, tensor cores 23.4; 4 x 448 x 2376 3.1 and 6.2);
+// 8 rows up to 32 (8 x 1136 x 3376 4.9 and 8.1; 8 x 4096 x 4096 12.3 and 9.9); up to a row for
+// each expert up to 30 (33 rows, 40 experts, 3264 -> 176 10.8 and 12.3; 14, 28, 3584 -> 1760
+// 26.9 and 25.5), and up to 4 rows for each up to 4 (20, 11, 832 -> 104 3.3 and 6.0; 96, 32,
+// 384 -> 600 10.8 and 6.1).
+int few_rows(const Product& p, const linear_options_t* forced) {
+  if (p.kind != LINEAR_FORWARD) return 0;
+  if (forced && forced->tile != 0) return forced->tile <= 8 ? forced->tile : 0;
+  const double work = 1e-6 * static_cast<double>(p.n) * static_cast<double>(p.m) * static_cast<double>(p.k);
+  if (!p.ragged) {
+    if (p.n <= 4) return p.n <= 1 ? 1 : p.n == 2 ? 2 : 4;
+    return p.n <= 8 && work <= 32 ? 8 : 0;
+  }
+  if (p.n <= p.groups) return work > 30 ? 0 : 4 * p.n <= p.groups ? 1 : 2 * p.n <= p.groups ? 2 : 4;
+  return p.n <= 4 * p.groups && work <= 4 ? 8 : 0;
 }
 
 int make_plan(const Product& p, const Machine& machine, const linear_options_t* forced, Plan* o) {
@@ -159,23 +188,46 @@ int make_plan(const Product& p, const Machine& machine, const linear_options_t* 
     if (!valid_form(p.kind, forced->cta_pair, forced->tile, forced->split_k))
       return GEMM_ERR_INVALID_VALUE;
     offer(forced->cta_pair != 0, forced->tile, forced->split_k, 0.0);
+  } else if (const int rows = few_rows(p, nullptr)) {
+    // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
+    // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
+    // with four).
+    const int64_t units = std::min(p.groups, p.n) * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
+    int split = 1;
+    while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
+    offer(false, rows, split, 0.0);
   } else {
-    // Cycles of the waves of tiles.  Operands come in at about 60 bytes a cycle and
-    // SM; an MMA takes half a cycle a column, and 100 at least.
+    // Cycles, for waves of tiles: a beginning and an end, with what an epilogue takes of them
+    // by its rows, and stages of 64 of the sum.  These come in at 60 bytes a cycle and SM,
+    // and an MMA takes 107 at least.  Clusters that share sums meet twice, and send them.
+    // Fitted to 900 products of 300 layers (rows 1 to 32768, inputs and outputs 64 to 8192,
+    // half of them with 8 to 64 experts): 2.5 % over the best form of each in the mean, 26 at worst.
     const auto waves = [&](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    offer(true, 256, 1, waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) * (2500 + 540 * kbs));
+    const auto cols = [&](int64_t tile) { return static_cast<double>((std::min(tile, n) + 31) / 32 * 32); };
+    offer(true, 256, 1,
+          690 + waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) *
+                    (2110 + 15.7 * cols(256) + kbs * std::max(2.6 * cols(256), 480.0)));
     for (int tile : {256, 128, 64, 32}) {
       if (!valid_form(p.kind, 0, tile, 1)) continue;
-      const int64_t tiles = n_tiles(p, tile, false) * m_tiles(false);
-      const double cols = static_cast<double>(std::min<int64_t>(tile, n));
-      const double stage = std::max({2.0 * cols, 400.0, (kLinABytes + cols * 128) / 60.0});
-      offer(false, tile, 1, waves(tiles, machine.sms) * (2500 + stage * kbs));
+      const double c = cols(tile);
+      const double stage = std::max({1.6 * c, 480.0, (kLinABytes + c * 128) / 60.0});
+      offer(false, tile, 1,
+            waves(n_tiles(p, tile, false) * m_tiles(false), machine.sms) * (1770 + 15.7 * c + stage * kbs));
       for (int i = 0; i < 3; ++i) {
         const int split = 2 << i;
         if (n_tiles(p, tile, true) * m_tiles(false) > machine.clusters[i] || kbs < 2 * split) continue;
-        offer(false, tile, split, 4500 + 10.0 * cols + stage * kbs / split);
+        offer(false, tile, split, 3990 + 42.6 * c + 100 * split + stage * std::ceil(kbs / split));
       }
     }
+  }
+  if (o->tile <= 8) {
+    const int64_t units = p.groups * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t blocks = (units * o->split + kFewWarps - 1) / kFewWarps;
+    if (blocks > INT_MAX / kFewWarps) return GEMM_ERR_INVALID_VALUE;
+    o->m_tiles = o->n_tiles = o->box_rows = 0;
+    o->units = static_cast<int>(blocks);
+    return GEMM_OK;
   }
   const int64_t most = n_tiles(p, o->tile, true) * m_tiles(o->pair);
   // counted in 32 bits, with room for a grid's stride past the last
@@ -227,13 +279,41 @@ int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaS
   return go(linear_tc<T, kProduct, false>, granted[2], plan.units, 1);
 }
 
+template <typename T, int kRows>
+int launch_few(const FewParams& f, const LinearParams& p, bool aligned, int blocks,
+               cudaStream_t s) {
+  const auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), 0, s, 1u, f, p);
+  };
+  return aligned ? go(linear_few<T, kRows, true>) : go(linear_few<T, kRows, false>);
+}
+
+// The forward product of few rows: x and w as the caller has them.
+int launch_few(const Plan& plan, const Rows& w, const Rows& x, LinearParams p, int type,
+               cudaStream_t s) {
+  const FewParams f{static_cast<const uint16_t*>(x.ptr), static_cast<const uint16_t*>(w.ptr), x.ld,
+                    w.ld};
+  p.n = static_cast<int32_t>(w.rows / p.groups);
+  p.k = static_cast<int32_t>(w.cols);
+  p.split = plan.split;
+  const bool aligned = loads_as_is(x) && loads_as_is(w) && p.k % 8 == 0;
+  const auto by_type = [&](auto t) {
+    using T = decltype(t);
+    switch (plan.tile) {
+      case 1: return launch_few<T, 1>(f, p, aligned, plan.units, s);
+      case 2: return launch_few<T, 2>(f, p, aligned, plan.units, s);
+      case 4: return launch_few<T, 4>(f, p, aligned, plan.units, s);
+      default: return launch_few<T, 8>(f, p, aligned, plan.units, s);
+    }
+  };
+  return type == MOE_F16 ? by_type(__half{}) : by_type(__nv_bfloat16{});
+}
+
 // One product of operands that the tensor maps take as they are: `a` is that of M, w or
 // (grad_w) x, and `b` that of N, x or dz.
-int launch(const Product& pr, const Rows& a, const Rows& b, LinearParams p, int type,
-           const linear_options_t* opt, int sms, int device, cudaStream_t s) {
-  Plan plan;
-  int rc = make_plan(pr, machine_of(sms, device), opt, &plan);
-  if (rc != GEMM_OK) return rc;
+int launch(const Product& pr, const Plan& plan, const Rows& a, const Rows& b, LinearParams p,
+           int type, const linear_options_t* opt, int device, cudaStream_t s) {
+  int rc = GEMM_OK;
   const bool weight = pr.kind == LINEAR_GRAD_W;
   p.n = static_cast<int32_t>(pr.m);
   p.m = weight ? static_cast<int32_t>(pr.n) : 0;
@@ -287,10 +367,10 @@ struct ForwardSpace {
   bool copy_x, copy_w;
   uint64_t x, w, bytes;
 };
-ForwardSpace forward_space(const linear_t* l) {
+ForwardSpace forward_space(const linear_t* l, bool few) {
   Pieces p;
   ForwardSpace f{};
-  const bool sums = l->rows > 0 && l->out > 0 && l->in > 0;
+  const bool sums = !few && l->rows > 0 && l->out > 0 && l->in > 0;
   f.copy_x = sums && !loads_as_is(x_rows(l));
   f.copy_w = sums && !loads_as_is(w_rows(l));
   if (f.copy_x) f.x = p.add(copy_bytes(x_rows(l)));
@@ -345,11 +425,13 @@ bool by_vectors(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 
 
 using namespace gb300;
 
-extern "C" int linear_forward_workspace(const linear_t* layer, uint64_t* bytes) {
-  const int rc = check_layer(layer);
+extern "C" int linear_forward_workspace(const linear_t* layer, const linear_options_t* opt,
+                                        uint64_t* bytes) {
+  int rc = check_layer(layer);
   if (rc != GEMM_OK) return rc;
+  if ((rc = check_options(opt)) != GEMM_OK) return rc;
   if (!bytes) return GEMM_ERR_INVALID_VALUE;
-  *bytes = forward_space(layer).bytes;
+  *bytes = forward_space(layer, few_rows(forward_of(layer), opt) > 0).bytes;
   return GEMM_OK;
 }
 
@@ -378,7 +460,8 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
     if ((rc = check_rows(*r)) != GEMM_OK) return rc;
   if (residual && (rc = check_rows(res)) != GEMM_OK) return rc;
   if (!aligned_to(preact, 2) || !aligned_to(bias, 2)) return GEMM_ERR_MISALIGNED;
-  const ForwardSpace space = forward_space(layer);
+  const Product pr = forward_of(layer);
+  const ForwardSpace space = forward_space(layer, few_rows(pr, opt) > 0);
   if ((rc = check_workspace(workspace, workspace_bytes, space.bytes)) != GEMM_OK) return rc;
   if (layer->rows == 0 || layer->out == 0) return GEMM_OK;
   if ((rc = check_rows(result)) != GEMM_OK) return rc;
@@ -393,11 +476,6 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
   int sms = 0, device = 0;
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  PrepareRows prepare{};
-  prepare.type = layer->type;
-  if (space.copy_x) copied(&x, &prepare, 0, workspace, space.x);
-  if (space.copy_w) copied(&w, &prepare, 1, workspace, space.w);
-  if ((rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
   LinearParams p;
   std::memset(&p, 0, sizeof(p));
   p.out = static_cast<uint16_t*>(out);
@@ -410,9 +488,16 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
   p.activation = layer->activation;
   p.vector = by_vectors(out, layer->out) && by_vectors(preact, 8) && by_vectors(bias, 8) &&
              (!residual || by_vectors(residual, res.ld));
-  return launch(product_of(LINEAR_FORWARD, layer->rows, layer->in, layer->out, groups,
-                           p.offsets != nullptr),
-                w, x, p, layer->type, opt, sms, device, s);
+  p.groups = groups;
+  Plan plan;
+  if ((rc = make_plan(pr, machine_of(sms, device), opt, &plan)) != GEMM_OK) return rc;
+  if (plan.tile <= 8) return launch_few(plan, w, x, p, layer->type, s);
+  PrepareRows prepare{};
+  prepare.type = layer->type;
+  if (space.copy_x) copied(&x, &prepare, 0, workspace, space.x);
+  if (space.copy_w) copied(&w, &prepare, 1, workspace, space.w);
+  if ((rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
+  return launch(pr, plan, w, x, p, layer->type, opt, device, s);
 }
 
 extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, const linear_t* layer,
@@ -453,6 +538,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   int sms = 0, device = 0;
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Machine machine = machine_of(sms, device);
 
   LinearParams p;
   std::memset(&p, 0, sizeof(p));
@@ -484,20 +570,24 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);
     px.vector = by_vectors(grad_x, layer->in);
-    rc = launch(product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
-                           p.offsets != nullptr),
-                w, dz, px, layer->type, opt, sms, device, s);
-    if (rc != GEMM_OK) return rc;
+    const Product pr = product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
+                                  p.offsets != nullptr);
+    Plan plan;
+    if ((rc = make_plan(pr, machine, opt, &plan)) != GEMM_OK ||
+        (rc = launch(pr, plan, w, dz, px, layer->type, opt, device, s)) != GEMM_OK)
+      return rc;
   }
   p.grad_bias = static_cast<uint16_t*>(grad_bias);
   if (for_w) {
     p.out = static_cast<uint16_t*>(grad_w);
     p.vector = by_vectors(grad_w, layer->in);
     p.strips = for_bias ? strips : nullptr;
-    rc = launch(product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
-                           p.offsets != nullptr),
-                x, dz, p, layer->type, opt, sms, device, s);
-    if (rc != GEMM_OK || strips) return rc;
+    const Product pr = product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
+                                  p.offsets != nullptr);
+    Plan plan;
+    if ((rc = make_plan(pr, machine, opt, &plan)) != GEMM_OK ||
+        (rc = launch(pr, plan, x, dz, p, layer->type, opt, device, s)) != GEMM_OK || strips)
+      return rc;
   }
   if (!for_bias) return GEMM_OK;
   // Without grad_w, or without rows: then there are no strips either.
@@ -522,7 +612,7 @@ extern "C" int linear_query_config(int product, int64_t rows, int64_t in, int64_
                            machine, nullptr, &plan);
   if (rc != GEMM_OK) return rc;
   *config = linear_config_t{plan.pair ? 1 : 0, plan.tile, plan.split,
-                            plan.units * (plan.pair ? 2 : plan.split)};
+                            plan.units * (plan.pair ? 2 : plan.tile <= 8 ? 1 : plan.split)};
   return GEMM_OK;
 }
 

@@ -116,10 +116,10 @@ py::object forward(const at::Tensor& x, const Routing* routing, const at::Tensor
   const On on(l.device, stream);
   const at::Tensor o = output(out, l.c.rows, l.c.out, l.type, l.device);
   const at::Tensor z = save_preact ? fresh({l.c.rows, l.c.out}, l.type, l.device) : at::Tensor();
-  uint64_t bytes = 0;
-  check(linear_forward_workspace(&l.c, &bytes), "linear");
-  const at::Tensor space = l.workspace(bytes);
   const linear_options_t opt = options_of(form, timeout_ns, inject);
+  uint64_t bytes = 0;
+  check(linear_forward_workspace(&l.c, &opt, &bytes), "linear");
+  const at::Tensor space = l.workspace(bytes);
   check(linear_forward(o.data_ptr(), save_preact ? z.data_ptr() : nullptr, &l.c, b,
                        residual ? residual->data_ptr() : nullptr, ldr,
                        bytes ? space.data_ptr() : nullptr, bytes, &opt, on.stream()),

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 DTYPES = [torch.float16, torch.bfloat16]
 # every way of cutting a product: (cta_pair, tile, split_k)
 FORMS = [(1, 256, 1)] + [(0, tile, split) for tile in (32, 64, 128, 256) for split in (1, 2, 4, 8)]
+FEW = [(0, rows, split) for rows in (1, 2, 4, 8) for split in (1, 2, 4, 8)]   # forward alone
 
 # rows, out, in
 SHAPES = [(1, 8, 8), (1, 1, 1), (1, 300, 64), (2, 64, 72), (31, 33, 63), (32, 256, 64), (33, 40, 65),
@@ -99,6 +100,23 @@ def test_every_form(lib, form, rows, out, hidden):
     m = make(rows, out, hidden, dtype, seed=7)
     check_forward(lib, m, "silu", form=form)
     check_backward(lib, m, "silu", form=form)
+
+
+@pytest.mark.parametrize("form", FEW)
+@pytest.mark.parametrize("rows,out,hidden", [(1, 8, 8), (1, 1, 1), (3, 257, 1000), (8, 72, 2056), (9, 30, 4097),
+                                             (21, 3, 513), (5, 1003, 24)])
+def test_few_rows(lib, form, rows, out, hidden):
+    for dtype in DTYPES:
+        m = make(rows, out, hidden, dtype, seed=17)
+        check_forward(lib, m, "gelu", form=form)
+        counts = (2, 0, rows, 1)
+        m = make(rows + 5, out, hidden, dtype, experts=4, seed=19)
+        routing, offsets = routing_of(lib, counts, 2)
+        m["x"][offsets[-1]:] = float("nan")
+        got, z = lib.moe_linear(m["x"], routing, m["w"], m["bias"], activation="silu", save_preact=True, form=form)
+        want, err, wz, zerr = ref.forward(m["x"], m["w"], m["bias"], None, "silu", offsets)
+        ref.check(got, want, err, "out")
+        ref.check(z, wz, zerr, "z")
 
 
 @pytest.mark.parametrize("form", [None] + FORMS)
