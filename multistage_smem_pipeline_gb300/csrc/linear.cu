@@ -149,23 +149,27 @@ int64_t n_tiles(const Product& p, int64_t tile, bool most) {
 }
 
 // The rows that linear_few takes at a time, where the product is its: by sizes alone, so
-// that the workspace does not depend on the device.  0: it is not.  In millions of
-// multiplications, from 160 shapes of 1 to 16 rows, or 0.02 to 4 for each of 8 to 64 experts:
-// up to 4 rows always (4 x 14336 x 4096 23.7 us, tensor cores 23.4; 4 x 448 x 2376 3.1 and 6.2);
-// 8 rows up to 32 (8 x 1136 x 3376 4.9 and 8.1; 8 x 4096 x 4096 12.3 and 9.9); up to a row for
-// each expert up to 30 (33 rows, 40 experts, 3264 -> 176 10.8 and 12.3; 14, 28, 3584 -> 1760
-// 26.9 and 25.5), and up to 4 rows for each up to 4 (20, 11, 832 -> 104 3.3 and 6.0; 96, 32,
-// 384 -> 600 10.8 and 6.1).
+// that the workspace does not depend on the device.  0: it is not.  From 200 shapes of 1 to 16
+// rows, or 0.02 to 4 for each of 8 to 64 experts; us, then those of the tensor cores' best form:
+//   a row, always (1 x 14336 x 4096 21.0, 22.2; 1 x 4096 x 4096 7.5, 11.6);
+//   2 to 4 rows, up to 100 and 80 million multiplications (2 x 13032 x 3768 19.0, 21.2; 3 x 4168 x 7832
+//   20.8, 16.8; 4 x 448 x 2376 3.1, 6.2); 8 up to 32 (8 x 1136 x 3376 4.9, 8.1; 8 x 4096 x 4096
+//   12.3, 9.9); 16, eight at a time, up to 8 with few outputs (16 x 312 x 1216 4.2, 5.9; 14 x 2552 x 184
+//   4.4, 3.8);
+//   experts' rows one by one, up to 4 for each, up to 30 and 5000 warps (33 rows, 40 experts,
+//   3264 -> 176 8.7, 12.3; 45, 15, 1256 -> 160 4.4, 7.0; 14, 28, 3584 -> 1760 28.9, 25.5; 26, 34,
+//   288 -> 888 6.8, 5.1).
 int few_rows(const Product& p, const linear_options_t* forced) {
   if (p.kind != LINEAR_FORWARD) return 0;
   if (forced && forced->tile != 0) return forced->tile <= 8 ? forced->tile : 0;
-  const double work = 1e-6 * static_cast<double>(p.n) * static_cast<double>(p.m) * static_cast<double>(p.k);
-  if (!p.ragged) {
-    if (p.n <= 4) return p.n <= 1 ? 1 : p.n == 2 ? 2 : 4;
-    return p.n <= 8 && work <= 32 ? 8 : 0;
-  }
-  if (p.n <= p.groups) return work > 30 ? 0 : 4 * p.n <= p.groups ? 1 : 2 * p.n <= p.groups ? 2 : 4;
-  return p.n <= 4 * p.groups && work <= 4 ? 8 : 0;
+  const double outputs = static_cast<double>(p.n) * static_cast<double>(p.m);
+  const double work = 1e-6 * outputs * static_cast<double>(p.k);
+  if (p.ragged) return p.n <= 4 * p.groups && work <= 30 && outputs <= 5000 * kFewOuts ? 1 : 0;
+  if (p.n <= 1) return 1;
+  if (p.n <= 2) return work <= 100 ? 2 : 0;
+  if (p.n <= 4) return work <= 80 ? 4 : 0;
+  if (p.n <= 8) return work <= 32 ? 8 : 0;
+  return p.n <= 16 && p.m <= 512 && work <= 8 ? 8 : 0;
 }
 
 int make_plan(const Product& p, const Machine& machine, const linear_options_t* forced, Plan* o) {
@@ -192,7 +196,7 @@ int make_plan(const Product& p, const Machine& machine, const linear_options_t* 
     // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
     // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
     // with four).
-    const int64_t units = std::min(p.groups, p.n) * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t units = (p.ragged ? p.n : 1) * ((p.m + kFewOuts - 1) / kFewOuts);
     const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
     int split = 1;
     while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
@@ -201,28 +205,29 @@ int make_plan(const Product& p, const Machine& machine, const linear_options_t* 
     // Cycles, for waves of tiles: a beginning and an end, with what an epilogue takes of them
     // by its rows, and stages of 64 of the sum.  These come in at 60 bytes a cycle and SM,
     // and an MMA takes 107 at least.  Clusters that share sums meet twice, and send them.
-    // Fitted to 900 products of 300 layers (rows 1 to 32768, inputs and outputs 64 to 8192,
-    // half of them with 8 to 64 experts): 2.5 % over the best form of each in the mean, 26 at worst.
+    // Fitted to 1680 products of 560 layers (rows 1 to 32768, inputs and outputs 64 to 8192,
+    // half of them with 8 to 64 experts): 2.2 % over the best form of each in the mean, 26 at worst.
     const auto waves = [&](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
     const auto cols = [&](int64_t tile) { return static_cast<double>((std::min(tile, n) + 31) / 32 * 32); };
     offer(true, 256, 1,
-          690 + waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) *
-                    (2110 + 15.7 * cols(256) + kbs * std::max(2.6 * cols(256), 480.0)));
-    for (int tile : {256, 128, 64, 32}) {
+          410 + waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) *
+                    (2110 + 15 * cols(256) + kbs * std::max(2.6 * cols(256), 480.0)));
+    for (int tile : {32, 64, 128, 256}) {
       if (!valid_form(p.kind, 0, tile, 1)) continue;
       const double c = cols(tile);
-      const double stage = std::max({1.6 * c, 480.0, (kLinABytes + c * 128) / 60.0});
-      offer(false, tile, 1,
-            waves(n_tiles(p, tile, false) * m_tiles(false), machine.sms) * (1770 + 15.7 * c + stage * kbs));
+      const double stage = std::max({1.4 * c, 480.0, (kLinABytes + c * 128) / 60.0});
+      const int64_t tiles = n_tiles(p, tile, false) * m_tiles(false);
+      offer(false, tile, 1, waves(tiles, machine.sms) * (1770 + 15 * c + stage * kbs));
       for (int i = 0; i < 3; ++i) {
         const int split = 2 << i;
         if (n_tiles(p, tile, true) * m_tiles(false) > machine.clusters[i] || kbs < 2 * split) continue;
-        offer(false, tile, split, 3990 + 42.6 * c + 100 * split + stage * std::ceil(kbs / split));
+        offer(false, tile, split,
+              4070 + 38 * c + (36.0 + 14.0 * tiles) * split + stage * std::ceil(kbs / split));
       }
     }
   }
   if (o->tile <= 8) {
-    const int64_t units = p.groups * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t units = (p.ragged && o->tile == 1 ? p.n : p.groups) * ((p.m + kFewOuts - 1) / kFewOuts);
     const int64_t blocks = (units * o->split + kFewWarps - 1) / kFewWarps;
     if (blocks > INT_MAX / kFewWarps) return GEMM_ERR_INVALID_VALUE;
     o->m_tiles = o->n_tiles = o->box_rows = 0;

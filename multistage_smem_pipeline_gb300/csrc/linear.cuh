@@ -41,7 +41,9 @@ constexpr int kLinK = 64;             // summed elements of a stage: 128 bytes, 
 constexpr int kLinEpiWarps = 8;
 constexpr int kLinZeroWarp = 2 + kLinEpiWarps;  // grad_w: zeroes what is no group's in a stage
 constexpr int kLinThreads = 96 + 32 * kLinEpiWarps;
-constexpr int kLinMaxStages = 12;
+// Deeper rings begin later: all of them are asked for at once, and the first lands with the
+// others (64 x 1704 x 656 with a tile of 32: 6.3 us with 8, 6.9 with 11).
+constexpr int kLinMaxStages = 8;
 constexpr uint32_t kLinABytes = kLinM * kLinK * 2;
 constexpr uint32_t kLinChunkBytes = 64 * kLinK * 2;  // MN-major: 64 columns by 64 of the sum
 constexpr uint32_t kLinBufBytes = 32 * 32 * 4;       // kSplit: 32 x 32 sums

@@ -95,10 +95,17 @@ __global__ void __launch_bounds__(kFewThreads, few_blocks(kRows, kAligned))
   const int team = warp / p.split, part = warp - team * p.split;
   const int per_group = (p.n + kOuts - 1) / kOuts;
   const int unit = static_cast<int>(blockIdx.x) * (kFewWarps / p.split) + team;
-  const int group = unit / per_group;
+  int group = unit / per_group;
   const int n0 = (unit - group * per_group) * kOuts;
   int row = 0, end = group < p.groups ? p.rows : 0;
-  if (p.offsets && group < p.groups) {
+  if (p.offsets && kRows == 1) {
+    // a row, whose group its warps find: most groups have none
+    row = group;
+    int before = 0;  // groups that end at the row or before it
+    for (int g = lane; g < p.groups; g += 32) before += p.offsets[g + 1] <= row;
+    group = min(__reduce_add_sync(0xffffffffu, before), p.groups - 1);
+    end = min(row + 1, p.offsets[p.groups]);
+  } else if (p.offsets && group < p.groups) {
     row = p.offsets[group];
     end = p.offsets[group + 1];
   }
