@@ -575,6 +575,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);
     px.vector = by_vectors(grad_x, layer->in);
+    px.overlap = for_w ? kOverlapFirst : kOverlapNone;
     const Product pr = product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
                                   p.offsets != nullptr);
     Plan plan;
@@ -587,6 +588,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
     p.out = static_cast<uint16_t*>(grad_w);
     p.vector = by_vectors(grad_w, layer->in);
     p.strips = for_bias ? strips : nullptr;
+    p.overlap = for_x ? kOverlapSecond : kOverlapNone;
     const Product pr = product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
                                   p.offsets != nullptr);
     Plan plan;

@@ -71,10 +71,30 @@ struct LinearParams {
   int32_t stages, split;
   int32_t activation;
   int32_t vector;            // kSplit: D, bias and residual can be accessed 16 bytes at a time
+  int32_t overlap;           // kOverlap*
   int32_t inject;            // 1: leave out each CTA's first loads
   int32_t error_word;
   uint64_t timeout_ns;
 };
+
+// grad_w runs beside grad_x, whose SMs it takes over as they get free (1021 x 1000 x 1411,
+// with everything before: 26 us one after the other).  Both need what came before them and
+// nothing of each other.  So grad_x lets grad_w start only once all of its own CTAs have
+// waited for that (kOverlapFirst), grad_w begins without waiting, and waits for grad_x at
+// its end (kOverlapSecond), so that what follows it follows both.
+enum { kOverlapNone = 0, kOverlapFirst = 1, kOverlapSecond = 2 };
+
+__device__ __forceinline__ void linear_begin_early(const LinearParams& p) {
+  if (p.overlap != kOverlapFirst) grid_launch_dependents();
+}
+__device__ __forceinline__ void linear_begin(const LinearParams& p) {
+  if (p.overlap == kOverlapSecond) return;
+  grid_dependency_wait();
+  if (p.overlap == kOverlapFirst) grid_launch_dependents();
+}
+__device__ __forceinline__ void linear_end(const LinearParams& p) {
+  if (p.overlap == kOverlapSecond) grid_dependency_wait();
+}
 
 // MN-major operands, of M and of N
 __host__ __device__ constexpr bool a_mn(int product) { return product != LINEAR_FORWARD; }

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t tmem_cols = 2 * acc_cols;
 
   if (threadIdx.x == 0) {
-    grid_launch_dependents();
+    linear_begin_early(p);
     for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
-  grid_dependency_wait();
+  linear_begin(p);
   if (warp == 2) linear_starts(p, start, lane);
   tc_fence_before_sync();
   __syncthreads();
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
+  linear_end(p);
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, tmem_cols);

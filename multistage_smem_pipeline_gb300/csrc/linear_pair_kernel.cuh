@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   GroupStart* const start = reinterpret_cast<GroupStart*>(misc + 8);
 
   if (threadIdx.x == 0) {
-    grid_launch_dependents();
+    linear_begin_early(p);
     for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * kLinPairTile);
     tmem_relinquish_pair();
   }
-  grid_dependency_wait();
+  linear_begin(p);
   if (warp == 2) linear_starts(p, start, lane);
   tc_fence_before_sync();
   cluster_sync();
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   __syncwarp();
   tc_fence_before_sync();
   cluster_sync();
+  linear_end(p);
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem, 2 * kLinPairTile);
