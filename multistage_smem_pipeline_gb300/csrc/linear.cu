@@ -399,12 +399,12 @@ BackwardSpace backward_space(const linear_t* l, bool grad_x, bool grad_w, bool g
   b.copy_x = for_w && !loads_as_is(x_rows(l));
   b.dz = (for_x || for_w) && (l->activation != LINEAR_NONE || !loads_as_is(grad));
   b.strips = live && grad_bias;
-  b.strip_rows = strip_rows_for(l->rows);
+  b.strip_rows = strip_rows_for(l->rows, l->out);
   if (b.copy_w) b.w = p.add(copy_bytes(w_rows(l)));
   if (b.copy_x) b.x = p.add(copy_bytes(x_rows(l)));
   if (b.dz) b.z = p.add(copy_bytes(grad));
   if (b.strips)
-    b.sums = p.add((l->rows / b.strip_rows + groups_of(l)) * static_cast<uint64_t>(l->out) * 4);
+    b.sums = p.add((l->rows / b.strip_rows + groups_of(l)) * strip_ld(l->out) * 4);
   b.bytes = p.bytes;
   return b;
 }

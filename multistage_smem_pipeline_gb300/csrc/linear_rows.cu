@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
   for (int w = 0; w < kWarps; ++w)
     total += partial[w][(threadIdx.x & 7) * 32 + (threadIdx.x >> 3)];
-  p.strips[static_cast<int64_t>(strip) * n + col] = total;
+  p.strips[strip * strip_ld(n) + col] = total;
 }
 
 template <typename T, bool kAligned>
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) sum_strips_kernel(const LinearParams
   grid_dependency_wait();
   if (threadIdx.x < 32) linear_starts(p, start, threadIdx.x);
   __syncthreads();
-  linear_sum_strips<T>(p, start, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
-                       static_cast<int64_t>(gridDim.x) * kThreads);
+  linear_sum_strips<T>(p, start, static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+                       static_cast<int64_t>(gridDim.x) * kWarps, threadIdx.x & 31);
 }
 
 }  // namespace
@@ -186,8 +186,8 @@ int prepare_rows(const PrepareRows& p, cudaStream_t stream) {
 }
 
 int sum_strips(const LinearParams& p, int type, int sms, cudaStream_t stream) {
-  const int64_t n = static_cast<int64_t>(p.groups) * p.m;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 8LL * sms)));
+  const int64_t units = static_cast<int64_t>(p.groups) * ((p.m + 31) / 32);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((units + kWarps - 1) / kWarps, 8LL * sms)));
   const size_t smem = (p.groups + 1) * sizeof(GroupStart);
   return type == MOE_F16
              ? launch_pdl(sum_strips_kernel<__half>, grid, dim3(kThreads), smem, stream, 1u, p)

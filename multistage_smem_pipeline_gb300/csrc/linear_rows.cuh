@@ -15,10 +15,11 @@ inline bool loads_as_is(const Rows& r) { return aligned_to(r.ptr, 16) && r.ld % 
 // Elements between the rows of a copy that they can take.
 __host__ __device__ inline int64_t copy_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
-// Rows of a strip for `rows` rows: 64, more where that would be over 512 strips.
-inline int strip_rows_for(int64_t rows) {
-  int64_t s = 64;
-  while (rows / s > 512) s *= 2;
+// Rows of a strip for rows x cols: 32, more where there are blocks enough (of 256 columns
+// each) to fill the GPU's SMs twice over.
+inline int strip_rows_for(int64_t rows, int64_t cols) {
+  int64_t s = 32;
+  while (rows / (2 * s) * ((cols + 255) / 256) >= 1216 || rows / s > 4096) s *= 2;
   return static_cast<int>(s);
 }
 
