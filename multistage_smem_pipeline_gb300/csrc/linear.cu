@@ -423,8 +423,6 @@ void copied(Rows* r, PrepareRows* p, int which, void* workspace, uint64_t at) {
   r->ld = copy_ld(r->cols);
 }
 
-bool by_vectors(const void* p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0; }
-
 }  // namespace
 }  // namespace gb300
 
@@ -491,8 +489,6 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
   p.offsets = offsets_of(layer);
   p.rows = static_cast<int32_t>(layer->rows);
   p.activation = layer->activation;
-  p.vector = by_vectors(out, layer->out) && by_vectors(preact, 8) && by_vectors(bias, 8) &&
-             (!residual || by_vectors(residual, res.ld));
   p.groups = groups;
   Plan plan;
   if ((rc = make_plan(pr, machine_of(sms, device), opt, &plan)) != GEMM_OK) return rc;
@@ -574,7 +570,6 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   if (for_x) {
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);
-    px.vector = by_vectors(grad_x, layer->in);
     px.overlap = for_w ? kOverlapFirst : kOverlapNone;
     const Product pr = product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
                                   p.offsets != nullptr);
@@ -586,7 +581,6 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   p.grad_bias = static_cast<uint16_t*>(grad_bias);
   if (for_w) {
     p.out = static_cast<uint16_t*>(grad_w);
-    p.vector = by_vectors(grad_w, layer->in);
     p.strips = for_bias ? strips : nullptr;
     p.overlap = for_x ? kOverlapSecond : kOverlapNone;
     const Product pr = product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,

@@ -70,7 +70,6 @@ struct LinearParams {
   int32_t box_rows;          // forward, grad_x: rows that one copy loads
   int32_t stages, split;
   int32_t activation;
-  int32_t vector;            // kSplit: D, bias and residual can be accessed 16 bytes at a time
   int32_t overlap;           // kOverlap*
   int32_t inject;            // 1: leave out each CTA's first loads
   int32_t error_word;
@@ -551,147 +550,32 @@ __device__ __forceinline__ void linear_store(float (&v)[32], const LinearParams&
   store(p.out);
 }
 
-// kSplit: 32 x 32 sums in shared memory, rows of D of 128 bytes, so that bias, residual, z and D
-// are read and written 16 bytes a lane.  Piece j (of 16 bytes) of row r is at j ^ (r & 7):
-// neither side has bank conflicts.
-__device__ __forceinline__ uint32_t linear_piece(uint32_t buf, int row, int piece) {
-  return buf + row * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
-}
-
-// To another CTA's shared memory (a shared::cluster address).
+// kSplit: 32 x 32 sums in shared memory, rows of D of 128 bytes.  They go to another CTA's
+// (a shared::cluster address) by whole rows: 16 bytes a lane, in 32 rows at once, took longer
+// (128 x 512 x 2048 by eight CTAs, a tile of 256: 13.0 us, and 10.2 so).
 __device__ __forceinline__ void linear_send(uint32_t buf, int lane, const uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(linear_piece(buf, i, lane >> 2) +
-                                                         4u * (lane & 3)),
-                 "r"(r[i])
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(buf + 128u * i + 4u * lane), "r"(r[i])
                  : "memory");
 }
 
-// What a chunk's epilogue reads from memory, asked for before its sums are there.
-struct LinearExtras {
-  Pack bias;
-  Pack residual[4];
-};
-
-template <int kProduct>
-__device__ __forceinline__ LinearExtras linear_extras(const LinearParams& p, int group,
-                                                      const LinearChunk& at, int lane) {
-  LinearExtras x = {};
-  if (kProduct != LINEAR_FORWARD || !p.vector) return x;
-  const int64_t row = at.row;
-  const int live = at.live, c = at.col + 8 * (lane & 3);
-  if (c >= p.n) return x;
-  if (p.bias)
-    x.bias = *reinterpret_cast<const Pack*>(p.bias + static_cast<int64_t>(group) * p.n + c);
-  if (p.residual) {
+// The sums of `parts` buffers `part_bytes` apart, added in order.
+__device__ __forceinline__ void linear_add_parts(uint32_t buf, int parts, uint32_t part_bytes,
+                                                 int lane, float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      if (r < live)
-        x.residual[i] = *reinterpret_cast<const Pack*>(p.residual + (row + r) * p.ldr + c);
-    }
-  }
-  return x;
-}
-
-// A chunk's part of D.  Its sums are those of `parts` buffers `part_bytes` apart, added
-// in order.
-template <typename T, int kProduct>
-__device__ __forceinline__ void linear_finish(uint32_t buf, int parts, uint32_t part_bytes,
-                                              const LinearParams& p, LinearExtras& x, int group,
-                                              const LinearChunk& chunk, int lane) {
-  constexpr bool kForward = kProduct == LINEAR_FORWARD;
-  const int64_t row = chunk.row;
-  const int live = chunk.live, col = chunk.col;
-  if (p.vector) {
-    const int c = col + 8 * (lane & 3);
-    float bias[8];
-    if (kForward) unpack<T>(x.bias, bias);
+  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      if (8 * i >= live) break;
-      const int r = 8 * i + (lane >> 2);
-      float v[8] = {};
-      for (int s = 0; s < parts; ++s) {
+  for (int s = 0; s < parts; ++s) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 q = ld_shared_v4(linear_piece(buf + s * part_bytes, r, 2 * (lane & 3) + h));
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * h + e] += __uint_as_float(w[e]);
-        }
-      }
-      if (r < live && c < p.n) {
-        const int64_t at = (row + r) * p.n + c;
-        if (kForward) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += bias[e];
-          if (p.preact) *reinterpret_cast<Pack*>(p.preact + at) = pack<T>(v);
-          activate_all(v, p.activation);
-          if (p.residual) {
-            float res[8];
-            unpack<T>(x.residual[0], res);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += res[e];
-          }
-        }
-        *reinterpret_cast<Pack*>(p.out + at) = pack<T>(v);
-      }
-      if (kForward) {
-#pragma unroll
-        for (int e = 0; e < 3; ++e) x.residual[e] = x.residual[e + 1];
-      }
+    for (int i = 0; i < 32; ++i) {
+      float part;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(part)
+                   : "r"(buf + s * part_bytes + 128u * i + 4u * lane)
+                   : "memory");
+      v[i] += part;
     }
-    return;
-  }
-  // Rows that are not aligned: a lane is a column, a row at a time.
-  const int c = col + lane;
-  if (c >= p.n) return;
-  const float bias = kForward && p.bias
-                         ? to_float(reinterpret_cast<const T*>(p.bias)[static_cast<int64_t>(group) * p.n + c])
-                         : 0.0f;
-#pragma unroll 1
-  for (int r0 = 0; r0 < live; r0 += 8) {
-    T res[8] = {};
-    if (kForward && p.residual) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r0 + i < live)
-          res[i] = reinterpret_cast<const T*>(p.residual)[(row + r0 + i) * p.ldr + c];
-    }
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      for (int s = 0; s < parts; ++s) {
-        float part;
-        asm volatile("ld.shared.f32 %0, [%1];"
-                     : "=f"(part)
-                     : "r"(linear_piece(buf + s * part_bytes, r0 + i, lane >> 2) + 4u * (lane & 3))
-                     : "memory");
-        v[i] += part;
-      }
-      v[i] += bias;
-    }
-    const int64_t at = (row + r0) * p.n + c;
-    if (kForward) {
-      if (p.preact) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (r0 + i < live)
-            reinterpret_cast<T*>(p.preact)[at + static_cast<int64_t>(i) * p.n] = from_float<T>(v[i]);
-      }
-      activate_all(v, p.activation);
-      if (p.residual) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += to_float(res[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r0 + i < live)
-        reinterpret_cast<T*>(p.out)[at + static_cast<int64_t>(i) * p.n] = from_float<T>(v[i]);
   }
 }
 
@@ -763,6 +647,25 @@ __device__ __forceinline__ void linear_sum_strips(const LinearParams& p, const G
                        static_cast<int64_t>(gridDim.x) * kLinEpiWarps, threadIdx.x & 31);
 }
 
+// What a lane's column of D has added to it.
+template <typename T, int kProduct>
+__device__ __forceinline__ float linear_bias(const LinearParams& p, int group, int col) {
+  if (kProduct != LINEAR_FORWARD || !p.bias || col >= p.n) return 0.0f;
+  return to_float(reinterpret_cast<const T*>(p.bias)[static_cast<int64_t>(group) * p.n + col]);
+}
+template <typename T, int kProduct>
+__device__ __forceinline__ void linear_residual(T (&residual)[32], const LinearParams& p,
+                                                const LinearChunk& at, int lane) {
+  const int col = at.col + lane;
+  if (kProduct != LINEAR_FORWARD || !p.residual || col >= p.n) return;
+  const T* from = reinterpret_cast<const T*>(p.residual) + at.row * p.ldr + col;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i < at.live) residual[i] = *from;
+    from += p.ldr;
+  }
+}
+
 // An epilogue warp's chunks of a tile: those of lane quadrant q, columns 32 half, 32 (half + 2)
 // ...  `wait` waits for the accumulator and `release` gives it back, by one lane, once
 // the warp's last chunk of it is in registers.  False: the wait gave up.
@@ -770,31 +673,20 @@ template <typename T, int kProduct, typename Wait, typename Release>
 __device__ __forceinline__ bool linear_epilogue(const LinearTile& tile, int m, int q, int half,
                                                 uint32_t t_row, const LinearParams& p, int lane,
                                                 Wait wait, Release release) {
-  constexpr bool kForward = kProduct == LINEAR_FORWARD;
   const auto let_go = [&] {
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) release();
   };
-  const int col = m + 32 * q + lane;
   const int chunks = m + 32 * q < p.n ? (tile.n_count + 31) >> 5 : 0;
-  float bias = 0.0f;
-  if (kForward && p.bias && col < p.n)
-    bias = to_float(reinterpret_cast<const T*>(p.bias)[static_cast<int64_t>(tile.group) * p.n + col]);
+  const float bias = linear_bias<T, kProduct>(p, tile.group, m + 32 * q + lane);
   if (!wait()) return false;
   tc_fence_after_sync();
   if (chunks <= half) let_go();
   for (int c = half; c < chunks; c += 2) {
     const LinearChunk at = linear_chunk<kProduct>(tile, m, q, c, p);
     T residual[32];
-    if (kForward && p.residual && col < p.n) {
-      const T* from = reinterpret_cast<const T*>(p.residual) + at.row * p.ldr + col;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (i < at.live) residual[i] = *from;
-        from += p.ldr;
-      }
-    }
+    linear_residual<T, kProduct>(residual, p, at, lane);
     uint32_t r[32];
     linear_sums(t_row + 32 * c, tile.k_len > 0, r);
     if (c + 2 >= chunks) let_go();

@@ -276,9 +276,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (u >= 4 * chunks) break;
           const LinearChunk at = linear_chunk<kProduct>(tile, tile.m, u & 3, u >> 2, p);
           if (at.live <= 0) continue;
-          LinearExtras x = linear_extras<kProduct>(p, tile.group, at, lane);
-          linear_finish<T, kProduct>(slot(0, i), p.split, mine * kLinBufBytes, p, x, tile.group, at,
-                                     lane);
+          T residual[32];
+          linear_residual<T, kProduct>(residual, p, at, lane);
+          float v[32];
+          linear_add_parts(slot(0, i), p.split, mine * kLinBufBytes, lane, v);
+          linear_store<T, kProduct>(v, p, linear_bias<T, kProduct>(p, tile.group, at.col + lane),
+                                    residual, at, lane);
         }
       }
       linear_zero_tail<kProduct>(p, start);
