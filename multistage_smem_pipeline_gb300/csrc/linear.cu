@@ -84,7 +84,7 @@ Machine machine_of(int sms, int device) {
   static std::once_flag once;
   static int held[3] = {0, 0, 0};
   std::call_once(once, [&] {
-    const auto kernel = linear_tc<__half, LINEAR_FORWARD, true>;
+    const auto kernel = linear_tc<__half, LINEAR_FORWARD, true, 2>;
     static std::atomic<uint64_t> granted{0};
     if (!grant_smem(kernel, kLinSmemLimit, device, granted)) return;
     for (int i = 0; i < 3; ++i) {
@@ -270,18 +270,23 @@ int encode(EncodeTiledFn fn, CUtensorMap* map, const void* ptr, int64_t cols, in
 template <typename T, int kProduct>
 int launch_as(const Maps& m, LinearParams p, const Plan& plan, int device, cudaStream_t s) {
   const uint32_t fixed = linear_fixed_bytes(p.groups);
-  const uint32_t stage = plan.pair ? kLinPairStage : kLinABytes + plan.tile * (kLinK * 2);
-  p.stages = std::min<int>((kLinSmemLimit - fixed) / stage, kLinMaxStages);
+  const uint32_t block = plan.pair ? kLinPairStage : kLinABytes + plan.tile * (kLinK * 2);
+  const int blocks = plan.pair || plan.tile > 64 ? 1 : 2;
+  const uint32_t stage = blocks * block;
+  p.stages = std::min<int>((kLinSmemLimit - fixed) / stage, kLinMaxStages / blocks);
   const size_t smem = fixed + p.stages * stage;
   const auto go = [&](auto kernel, std::atomic<uint64_t>& granted, unsigned ctas, unsigned cluster) {
     if (!grant_smem(kernel, kLinSmemLimit, device, granted)) return static_cast<int>(GEMM_ERR_CUDA);
     return launch_pdl(kernel, dim3(ctas), dim3(kLinThreads), smem, s, cluster, m.a, m.b, p);
   };
-  static std::atomic<uint64_t> granted[3];
+  static std::atomic<uint64_t> granted[5];
   if (plan.pair) return go(linear_pair<T, kProduct>, granted[0], 2 * plan.units, 2);
   if (plan.split > 1)
-    return go(linear_tc<T, kProduct, true>, granted[1], plan.units * plan.split, plan.split);
-  return go(linear_tc<T, kProduct, false>, granted[2], plan.units, 1);
+    return blocks == 2
+               ? go(linear_tc<T, kProduct, true, 2>, granted[1], plan.units * plan.split, plan.split)
+               : go(linear_tc<T, kProduct, true, 1>, granted[2], plan.units * plan.split, plan.split);
+  return blocks == 2 ? go(linear_tc<T, kProduct, false, 2>, granted[3], plan.units, 1)
+                     : go(linear_tc<T, kProduct, false, 1>, granted[4], plan.units, 1);
 }
 
 template <typename T, int kRows>

@@ -37,10 +37,11 @@
 namespace gb300 {
 
 constexpr int kLinM = 128;            // the M of a CTA: one accumulator lane each
-constexpr int kLinK = 64;             // summed elements of a stage: 128 bytes, a swizzle row
+constexpr int kLinK = 64;             // summed elements of a block: 128 bytes, a swizzle row
 constexpr int kLinEpiWarps = 8;
 constexpr int kLinZeroWarp = 2 + kLinEpiWarps;  // grad_w: zeroes what is no group's in a stage
-constexpr int kLinThreads = 96 + 32 * kLinEpiWarps;
+constexpr int kLinNWarp = 3 + kLinEpiWarps;     // the second producer
+constexpr int kLinThreads = 128 + 32 * kLinEpiWarps;
 // Deeper rings begin later: all of them are asked for at once, and the first lands with the
 // others (64 x 1704 x 656 with a tile of 32: 6.3 us with 8, 6.9 with 11).
 constexpr int kLinMaxStages = 8;
@@ -318,6 +319,115 @@ __device__ __forceinline__ void linear_zero_rows(uint32_t at, int chunks, int va
       st_shared_v4(at + c * kLinChunkBytes + valid * 128u + i * 16u, 0, 0, 0, 0);
 }
 
+// ------------------------------------------------------------------ products of a tile
+// True if the phase with the given parity has completed; does not wait.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The ring as a warp goes through it: a stage, and what its next barrier said already.
+struct LinearRing {
+  uint32_t bars;                 // the first of those that the warp waits on
+  int stages;
+  int stage;
+  uint32_t phase;
+  bool open;                     // the stage's has been seen to be complete
+
+  __device__ __forceinline__ void look(uint32_t flip) { open = mbar_test_wait(bars + 8u * stage, phase ^ flip); }
+  __device__ __forceinline__ void step() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// By the whole warp: the stage's barrier, of the phase before for a producer (flip 1).
+__device__ __forceinline__ bool linear_enter(const LinearRing& ring, uint32_t flip,
+                                             volatile int* abort_flag, uint32_t site,
+                                             const LinearParams& p) {
+  return __all_sync(0xffffffffu, ring.open) ||
+         linear_wait_warp(ring.bars + 8u * ring.stage, ring.phase ^ flip, abort_flag, site, p);
+}
+
+// Blocks from .. end - 1 of a tile's sum, kBlocks a stage; by a whole warp, of which one lane
+// issues.  False: a wait gave up.  What bounds it with small tiles is the issuing: about 30 cycles an
+// MMA (which takes 40 for an N of 32), 66 a commit, and the wait, 95; so the next stage's barrier is
+// looked at before this one's MMAs are issued, whole stages have no branches, and stages have
+// two blocks where there is room.
+template <typename T, int kProduct, bool kPair, int kBlocks>
+__device__ __forceinline__ bool linear_multiply(const LinearTile& tile, int from, int end,
+                                                LinearRing& ring, uint32_t empty_bars,
+                                                uint32_t ready_bars, uint32_t& ready_phase,
+                                                uint32_t block_units, uint64_t a_desc0,
+                                                uint64_t b_desc0, uint32_t d_tmem, uint32_t idesc,
+                                                volatile int* abort_flag, const LinearParams& p) {
+  constexpr uint32_t kA = linear_desc_step<a_mn(kProduct)>(), kB = linear_desc_step<b_mn(kProduct)>();
+  constexpr int kSteps = kLinK / 16;
+  if (from >= end) return true;
+  const int left = end - from;
+  const int whole = (left - 1) / kBlocks;           // stages before the last
+  const auto mma = [&](uint64_t da, uint64_t db, int s, uint32_t accumulate) {
+    if (kPair) umma_f16_pair(d_tmem, da + s * kA, db + s * kB, idesc, accumulate);
+    else umma_f16(d_tmem, da + s * kA, db + s * kB, idesc, accumulate);
+  };
+  const auto commit = [&](int stage) {
+    if (kPair) umma_commit_pair_mc(empty_bars + 8u * stage, 0x3);
+    else umma_commit(empty_bars + 8u * stage);
+  };
+  ring.look(0);
+  uint32_t accumulate = 0;
+  for (int i = 0; i < whole; ++i) {
+    if (!linear_enter(ring, 0, abort_flag, kLinFull, p)) return false;
+    tc_fence_after_sync();
+    const int stage = ring.stage;
+    ring.step();
+    ring.look(0);
+    if (elect_one()) {
+      const uint32_t at = stage * kBlocks * block_units;
+      const uint64_t da = a_desc0 + at, db = b_desc0 + at;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          mma(da + b * block_units, db + b * block_units, s, b + s > 0 ? 1u : accumulate);
+      commit(stage);
+    }
+    __syncwarp();
+    accumulate = 1;
+  }
+  // the last: of fewer blocks or steps, and in grad_w ragged
+  if (!linear_enter(ring, 0, abort_flag, kLinFull, p)) return false;
+  const int stage = ring.stage;
+  if (kProduct == LINEAR_GRAD_W && linear_ragged(tile, end - 1, p)) {
+    if (!linear_wait_warp<kPair>(ready_bars + 8u * stage, (ready_phase >> stage) & 1u, abort_flag,
+                                 kLinPeer, p))
+      return false;
+    ready_phase ^= 1u << stage;
+  }
+  tc_fence_after_sync();
+  ring.step();
+  const int steps = (left - 1 - whole * kBlocks) * kSteps + linear_steps(tile, end - 1);
+  if (elect_one()) {
+    const uint32_t at = stage * kBlocks * block_units;
+    const uint64_t da = a_desc0 + at, db = b_desc0 + at;
+    for (int s = 0; s < steps; ++s)
+      mma(da + s / kSteps * block_units, db + s / kSteps * block_units, s % kSteps,
+          s > 0 ? 1u : accumulate);
+    commit(stage);
+  }
+  __syncwarp();
+  return true;
+}
+
 // ------------------------------------------------------------------ loads
 // What a CTA loads for each stage of a tile: of M from m on, of N from n on.
 struct LinearLoads {
@@ -341,30 +451,32 @@ __device__ __forceinline__ LinearLoads linear_loads(int m, int m_count, int n, i
   return l;
 }
 
-// A stage's, from k of the sum on, to shared memory at `dst`; by one lane.
+// A stage's operand of M, or of N, from k of the sum on, to the stage at `dst`; by one lane.
 template <int kProduct, bool kPair>
-__device__ __forceinline__ void linear_load(const LinearLoads& l, uint32_t dst, const void* tmA,
-                                            const void* tmB, uint32_t full, int k,
-                                            const LinearTile& t, const LinearParams& p) {
-  const auto load_a = [&](uint32_t at, int x, int y, int z) {
-    if (kPair) tma_load_3d_pair(at, tmA, full, x, y, z);
-    else tma_load_3d(at, tmA, full, x, y, z);
-  };
-  const auto load_b = [&](uint32_t at, int x, int y) {
-    if (kPair) tma_load_2d_pair(at, tmB, full, x, y);
-    else tma_load_2d(at, tmB, full, x, y);
+__device__ __forceinline__ void linear_load_m(const LinearLoads& l, uint32_t dst, const void* tm,
+                                              uint32_t full, int k, const LinearTile& t) {
+  const auto load = [&](uint32_t at, int x, int y, int z) {
+    if (kPair) tma_load_3d_pair(at, tm, full, x, y, z);
+    else tma_load_3d(at, tm, full, x, y, z);
   };
   if (kProduct == LINEAR_FORWARD) {
-    load_a(dst, k, l.m, t.group);
+    load(dst, k, l.m, t.group);
   } else {
-    for (int i = 0; i < l.a_boxes; ++i)
-      load_a(dst + i * l.a_box_bytes, l.m + 64 * i, t.k_row + k,
-             kProduct == LINEAR_GRAD_X ? t.group : 0);
+    const int group = kProduct == LINEAR_GRAD_X ? t.group : 0;
+    load(dst, l.m, t.k_row + k, group);
+    if (l.a_boxes > 1) load(dst + kLinChunkBytes, l.m + 64, t.k_row + k, group);
   }
-  const uint32_t b = dst + kLinABytes;
+}
+template <int kProduct, bool kPair>
+__device__ __forceinline__ void linear_load_n(const LinearLoads& l, uint32_t dst, const void* tm,
+                                              uint32_t full, int k, const LinearTile& t,
+                                              const LinearParams& p) {
   for (int i = 0; i < l.b_boxes; ++i) {
-    if (kProduct == LINEAR_GRAD_W) load_b(b + i * l.b_box_bytes, l.n + 64 * i, t.k_row + k);
-    else load_b(b + i * l.b_box_bytes, k, l.n + i * p.box_rows);
+    const uint32_t at = dst + kLinABytes + i * l.b_box_bytes;
+    const int x = kProduct == LINEAR_GRAD_W ? l.n + 64 * i : k;
+    const int y = kProduct == LINEAR_GRAD_W ? t.k_row + k : l.n + i * p.box_rows;
+    if (kPair) tma_load_2d_pair(at, tm, full, x, y);
+    else tma_load_2d(at, tm, full, x, y);
   }
 }
 

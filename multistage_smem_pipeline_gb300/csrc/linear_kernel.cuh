@@ -2,7 +2,8 @@
 // to 256.
 //
 // Inside a CTA, one per SM:
-//   warp 0 -- producer: per 64 of the sum, TMA boxes of both operands into a ring;
+//   warps 0 and 11 -- producers, of M and of N: per 64 of the sum, TMA boxes into a ring
+//       (one warp for both took 440 cycles a stage, whatever the tile);
 //   warp 1 -- MMA issuer, into two accumulators by turns;
 //   warps 2 .. 9 -- epilogue: two warps for each quadrant of lanes, which take
 //       32 columns by turns, and store from registers;
@@ -18,7 +19,9 @@
 
 namespace gb300 {
 
-template <typename T, int kProduct, bool kSplit>
+// kBlocks: of 64 of the sum in a stage, 2 for tiles up to 64 (32 x 4096 x 4096 in tiles of 32: 15.2 us
+// and 17.2; but 128 x 4096 x 4096 in tiles of 128, for which there are three such stages, 19.3 and 17.8).
+template <typename T, int kProduct, bool kSplit, int kBlocks>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const LinearParams p) {
@@ -29,7 +32,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint8_t* const smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = p.stages;
-  const uint32_t stage_bytes = kLinABytes + p.tile * (kLinK * 2);
+  const uint32_t block_bytes = kLinABytes + p.tile * (kLinK * 2);
+  const uint32_t stage_bytes = kBlocks * block_bytes;
   const uint32_t bars = base + stages * stage_bytes;
   const int part = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
   const int first_tile = kSplit ? blockIdx.x / p.split : blockIdx.x;
@@ -89,38 +93,47 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     *end = kSplit ? static_cast<int>(static_cast<int64_t>(part + 1) * kbs / p.split) : kbs;
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, ragged_phase = 0;
+  if (warp == 0 || warp == kLinNWarp) {
+    // ---------------------------------------------------------- producers
+    LinearRing ring{empty_bar(0), stages, 0, 0, true};
+    uint32_t issued = 0, ragged_phase = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
       const LinearLoads loads = linear_loads<kProduct>(tile.m, tile.m_count, tile.n, tile.n_count, p);
       int from, end;
       stages_of(tile, &from, &end);
-      for (int kb = from; kb < end; ++kb) {
-        if (!linear_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kLinEmpty, p)) {
+      for (int kb = from; kb < end; kb += kBlocks) {
+        if (!linear_enter(ring, 1, abort_flag, kLinEmpty, p)) {
           ok = false;
           break;
         }
-        const bool ragged = kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb, p);
+        const int blocks = kBlocks == 1 ? 1 : min(kBlocks, end - kb);
+        const int stage = ring.stage;
+        const bool ragged = kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb + blocks - 1, p);
+        ring.step();
+        ring.look(1);
         if (elect_one()) {
           // a ragged stage is full at once, and ready once it has landed and is zeroed
           const uint32_t full = ragged ? ragged_bar(stage) : full_bar(stage);
-          mbar_arrive_expect_tx(full, loads.bytes);
-          if (ragged) mbar_arrive(full_bar(stage));
-          if (!(p.inject && issued == 0))
-            linear_load<kProduct, false>(loads, base + stage * stage_bytes, &tmA, &tmB, full,
-                                         kb * kLinK, tile, p);
+          const uint32_t dst = base + stage * stage_bytes;
+          if (warp == 0) {
+            mbar_arrive_expect_tx(full, blocks * loads.bytes);
+            if (ragged) mbar_arrive(full_bar(stage));
+          }
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            if (b >= blocks) break;
+            const uint32_t at = dst + b * block_bytes;
+            const int k = (kb + b) * kLinK;
+            if (warp != 0) linear_load_n<kProduct, false>(loads, at, &tmB, full, k, tile, p);
+            else if (!(p.inject && issued == 0))
+              linear_load_m<kProduct, false>(loads, at, &tmA, full, k, tile);
+          }
         }
         __syncwarp();
         if (ragged) ragged_phase ^= 1u << stage;
         ++issued;
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
     }
     // every load has landed before the CTA may end
@@ -131,55 +144,23 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       linear_drain_ragged(ragged_bar(0), stages, ragged_phase, p.timeout_ns);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0, ready_phase = 0;
-    bool ok = true;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t ready_phase = 0;
+    LinearRing ring{full_bar(0), stages, 0, 0, false};
     const uint64_t a_desc0 = linear_desc<kAMn>(base);
     const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
-    for (int t = first_tile; ok && t < tiles; t += tile_step) {
+    for (int t = first_tile; t < tiles; t += tile_step) {
       const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
       const uint32_t idesc = linear_idesc<T, kProduct>(kLinM, (tile.n_count + 15) & ~15);
       if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
       tc_fence_after_sync();
-      const uint32_t d_tmem = tmem + acc * acc_cols;
       int from, end;
       stages_of(tile, &from, &end);
-      for (int kb = from; kb < end; ++kb) {
-        if (!linear_wait_warp(full_bar(stage), phase, abort_flag, kLinFull, p)) {
-          ok = false;
-          break;
-        }
-        if (kProduct == LINEAR_GRAD_W && linear_ragged(tile, kb, p)) {
-          if (!linear_wait_warp(ready_bar(stage), (ready_phase >> stage) & 1u, abort_flag, kLinPeer, p)) {
-            ok = false;
-            break;
-          }
-          ready_phase ^= 1u << stage;
-        }
-        tc_fence_after_sync();
-        const int steps = linear_steps(tile, kb);
-        if (elect_one()) {
-          const uint64_t at = static_cast<uint64_t>((stage * stage_bytes) >> 4);
-          const uint64_t a_desc = a_desc0 + at, b_desc = b_desc0 + at;
-          if (steps == kLinK / 16) {
-#pragma unroll
-            for (int s = 0; s < kLinK / 16; ++s)
-              umma_f16(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
-                       b_desc + s * linear_desc_step<kBMn>(), idesc, kb != from || s != 0);
-          } else {
-            for (int s = 0; s < steps; ++s)
-              umma_f16(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
-                       b_desc + s * linear_desc_step<kBMn>(), idesc, kb != from || s != 0);
-          }
-          umma_commit(empty_bar(stage));
-        }
-        __syncwarp();
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
+      if (!linear_multiply<T, kProduct, false, kBlocks>(
+              tile, from, end, ring, empty_bar(0), ready_bar(0), ready_phase, block_bytes >> 4,
+              a_desc0, b_desc0, tmem + acc * acc_cols, idesc, abort_flag, p))
+        break;
       if (elect_one()) umma_commit(tfull_bar(acc));
       __syncwarp();
       if (++acc == 2) {
@@ -199,13 +180,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const LinearTile tile = linear_tile<kProduct, kLinM>(t, p, start);
         int from, end;
         stages_of(tile, &from, &end);
-        done += end - from;
+        done += (end - from + kBlocks - 1) / kBlocks;
         if (end == from || !linear_ragged(tile, end - 1, p)) continue;
         const int stage = (done - 1) % stages;
         if (!linear_wait_warp(ragged_bar(stage), (ragged_phase >> stage) & 1u, abort_flag, kLinFull, p))
           break;
         ragged_phase ^= 1u << stage;
-        const uint32_t a = base + stage * stage_bytes;
+        const uint32_t a = base + stage * stage_bytes + (end - from - 1) % kBlocks * block_bytes;
         const int valid = tile.k_len - (end - 1) * kLinK;
         linear_zero_rows(a, kLinM / 64, valid, lane);
         linear_zero_rows(a + kLinABytes, p.tile / 64, valid, lane);
@@ -241,7 +222,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // Chunk (q, c) is the 4 c + q-th, and CTA u / mine owns the u-th.  Of one's own there
     // is a buffer in the ring for each part.
     const bool live_tile = first_tile < tiles;
-    const bool epilogue = warp >= 2 && warp != kLinZeroWarp;
+    const bool epilogue = warp >= 2 && warp < kLinZeroWarp;
     LinearTile tile = {};
     if (live_tile) tile = linear_tile<kProduct, kLinM>(first_tile, p, start);
     const int mine = max(1, p.tile / 8 / p.split);

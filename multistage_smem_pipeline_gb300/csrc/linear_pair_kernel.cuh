@@ -85,11 +85,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // the N that a CTA holds: half of the tile's, to 16
   const auto half_n = [&](const LinearTile& t) { return (t.n_count + 31) >> 5 << 4; };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer (both CTAs)
-    int stage = 0;
-    uint32_t phase = 0, issued = 0;
-    uint32_t ragged_phase = 0;
+  if (warp == 0 || warp == kLinNWarp) {
+    // ---------------------------------------------------------- producers (both CTAs)
+    LinearRing ring{empty_bar(0), stages, 0, 0, true};
+    uint32_t issued = 0, ragged_phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
@@ -102,27 +101,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const uint32_t both_bytes = loads.bytes + loads_of(1 - rank).bytes;
       const int kbs = (tile.k_len + kLinK - 1) / kLinK;
       for (int kb = 0; kb < kbs; ++kb) {
-        if (!linear_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, kLinEmpty, p)) {
+        if (!linear_enter(ring, 1, abort_flag, kLinEmpty, p)) {
           ok = false;
           break;
         }
+        const int stage = ring.stage;
         const bool ragged = kWeight && linear_ragged(tile, kb, p);
+        ring.step();
+        ring.look(1);
         if (elect_one()) {
           const uint32_t full = ragged ? mapa_shared(ragged_bar(stage), rank)
                                        : mapa_shared(full_bar(stage), 0);
-          if (ragged) mbar_arrive_expect_tx(ragged_bar(stage), loads.bytes);
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), ragged ? 0 : both_bytes);
-          if (!(p.inject && issued == 0 && rank == 0))
-            linear_load<kProduct, true>(loads, base + stage * kLinPairStage, &tmA, &tmB, full,
-                                        kb * kLinK, tile, p);
+          const uint32_t dst = base + stage * kLinPairStage;
+          if (warp == 0) {
+            if (ragged) mbar_arrive_expect_tx(ragged_bar(stage), loads.bytes);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), ragged ? 0 : both_bytes);
+            if (!(p.inject && issued == 0 && rank == 0))
+              linear_load_m<kProduct, true>(loads, dst, &tmA, full, kb * kLinK, tile);
+          } else {
+            linear_load_n<kProduct, true>(loads, dst, &tmB, full, kb * kLinK, tile, p);
+          }
         }
         __syncwarp();
         if (ragged) ragged_phase ^= 1u << stage;
         ++issued;
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
     }
     if (rank == 0) {  // both CTAs' bytes
@@ -133,55 +135,22 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (kWeight) linear_drain_ragged(ragged_bar(0), stages, ragged_phase, p.timeout_ns);
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------- MMA issuer
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0, ready_phase = 0;
-    bool ok = true;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t ready_phase = 0;
+    LinearRing ring{full_bar(0), stages, 0, 0, false};
     const uint64_t a_desc0 = linear_desc<kAMn>(base);
     const uint64_t b_desc0 = linear_desc<kBMn>(base + kLinABytes);
-    for (int t = pair; ok && t < tiles; t += pairs) {
+    for (int t = pair; t < tiles; t += pairs) {
       const LinearTile tile = linear_tile<kProduct, kM>(t, p, start);
       const uint32_t idesc = linear_idesc<T, kProduct>(kM, 2 * half_n(tile));
       if (!linear_wait_warp(tempty_bar(acc), acc_phase ^ 1u, abort_flag, kLinTmemEmpty, p)) break;
       tc_fence_after_sync();
-      const uint32_t d_tmem = tmem + acc * kLinPairTile;
-      const int kbs = (tile.k_len + kLinK - 1) / kLinK;
-      for (int kb = 0; kb < kbs; ++kb) {
-        if (!linear_wait_warp(full_bar(stage), phase, abort_flag, kLinFull, p)) {
-          ok = false;
-          break;
-        }
-        if (kWeight && linear_ragged(tile, kb, p)) {
-          if (!linear_wait_warp<true>(ready_bar(stage), (ready_phase >> stage) & 1u, abort_flag,
-                                      kLinPeer, p)) {
-            ok = false;
-            break;
-          }
-          ready_phase ^= 1u << stage;
-        }
-        tc_fence_after_sync();
-        const int steps = linear_steps(tile, kb);
-        if (elect_one()) {
-          const uint64_t at = static_cast<uint64_t>((stage * kLinPairStage) >> 4);
-          const uint64_t a_desc = a_desc0 + at, b_desc = b_desc0 + at;
-          if (steps == kLinK / 16) {
-#pragma unroll
-            for (int s = 0; s < kLinK / 16; ++s)
-              umma_f16_pair(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
-                            b_desc + s * linear_desc_step<kBMn>(), idesc, (kb | s) != 0);
-          } else {
-            for (int s = 0; s < steps; ++s)
-              umma_f16_pair(d_tmem, a_desc + s * linear_desc_step<kAMn>(),
-                            b_desc + s * linear_desc_step<kBMn>(), idesc, (kb | s) != 0);
-          }
-          umma_commit_pair_mc(empty_bar(stage), kBoth);
-        }
-        __syncwarp();
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
+      if (!linear_multiply<T, kProduct, true, 1>(
+              tile, 0, (tile.k_len + kLinK - 1) / kLinK, ring, empty_bar(0), ready_bar(0),
+              ready_phase, kLinPairStage >> 4, a_desc0, b_desc0, tmem + acc * kLinPairTile, idesc,
+              abort_flag, p))
+        break;
       if (elect_one()) umma_commit_pair_mc(tfull_bar(acc), kBoth);
       __syncwarp();
       if (++acc == 2) {
