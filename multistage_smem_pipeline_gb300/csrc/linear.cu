@@ -172,60 +172,61 @@ int few_rows(const Product& p, const linear_options_t* forced) {
   return p.n <= 16 && p.m <= 512 && work <= 8 ? 8 : 0;
 }
 
-int make_plan(const Product& p, const Machine& machine, const linear_options_t* forced, Plan* o) {
+// A way of cutting a product, the cycles that it is expected to take, and the SMs that
+// it has meanwhile.
+struct Form {
+  bool pair;
+  int tile, split;
+  double cycles;
+  int64_t ctas;
+};
+constexpr int kMostForms = 17;
+
+int64_t m_tiles(const Product& p, bool pair) { return pair ? (p.m + 255) / 256 : (p.m + 127) / 128; }
+
+// The forms on the tensor cores.  Cycles, for waves of tiles: a beginning and an end, with what an
+// epilogue takes of them by its rows, and blocks of 64 of the sum.  These come in at 60 bytes a
+// cycle and SM, and cost 480 at least to be issued.  Clusters that share sums meet twice, and send them.
+// Fitted to 1680 products of 560 layers (rows 1 to 32768, inputs and outputs 64 to 8192, half of them
+// with 8 to 64 experts): 2.2 % over the best form of each in the mean, 26 at worst.
+int list_forms(const Product& p, const Machine& machine, Form (&forms)[kMostForms]) {
   const bool weight = p.kind == LINEAR_GRAD_W;
   // of a group, in the mean
   const int64_t k = weight && p.ragged ? (p.k + p.groups - 1) / p.groups : p.k;
   const int64_t n = !weight && p.ragged ? (p.n + p.groups - 1) / p.groups : p.n;
-  const double kbs = std::max<double>(1.0, static_cast<double>((k + kLinK - 1) / kLinK));
-  const auto m_tiles = [&](bool pair) { return pair ? (p.m + 255) / 256 : (p.m + 127) / 128; };
-  double least = 0.0;
-  o->tile = 0;
-  const auto offer = [&](bool pair, int tile, int split, double cycles) {
-    if (o->tile != 0 && cycles >= least) return;
-    least = cycles;
-    o->pair = pair;
-    o->tile = tile;
-    o->split = split;
-  };
-  if (forced && forced->tile != 0) {
-    if (!valid_form(p.kind, forced->cta_pair, forced->tile, forced->split_k))
-      return GEMM_ERR_INVALID_VALUE;
-    offer(forced->cta_pair != 0, forced->tile, forced->split_k, 0.0);
-  } else if (const int rows = few_rows(p, nullptr)) {
-    // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
-    // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
-    // with four).
-    const int64_t units = (p.ragged ? p.n : 1) * ((p.m + kFewOuts - 1) / kFewOuts);
-    const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
-    int split = 1;
-    while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
-    offer(false, rows, split, 0.0);
-  } else {
-    // Cycles, for waves of tiles: a beginning and an end, with what an epilogue takes of them
-    // by its rows, and stages of 64 of the sum.  These come in at 60 bytes a cycle and SM,
-    // and an MMA takes 107 at least.  Clusters that share sums meet twice, and send them.
-    // Fitted to 1680 products of 560 layers (rows 1 to 32768, inputs and outputs 64 to 8192,
-    // half of them with 8 to 64 experts): 2.2 % over the best form of each in the mean, 26 at worst.
-    const auto waves = [&](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
-    const auto cols = [&](int64_t tile) { return static_cast<double>((std::min(tile, n) + 31) / 32 * 32); };
-    offer(true, 256, 1,
-          410 + waves(n_tiles(p, 256, false) * m_tiles(true), machine.sms / 2) *
-                    (2110 + 15 * cols(256) + kbs * std::max(2.6 * cols(256), 480.0)));
-    for (int tile : {32, 64, 128, 256}) {
-      if (!valid_form(p.kind, 0, tile, 1)) continue;
-      const double c = cols(tile);
-      const double stage = std::max({1.4 * c, 480.0, (kLinABytes + c * 128) / 60.0});
-      const int64_t tiles = n_tiles(p, tile, false) * m_tiles(false);
-      offer(false, tile, 1, waves(tiles, machine.sms) * (1770 + 15 * c + stage * kbs));
-      for (int i = 0; i < 3; ++i) {
-        const int split = 2 << i;
-        if (n_tiles(p, tile, true) * m_tiles(false) > machine.clusters[i] || kbs < 2 * split) continue;
-        offer(false, tile, split,
-              4070 + 38 * c + (36.0 + 14.0 * tiles) * split + stage * std::ceil(kbs / split));
-      }
+  const double blocks = std::max<double>(1.0, static_cast<double>((k + kLinK - 1) / kLinK));
+  const auto cols = [&](int64_t tile) { return static_cast<double>((std::min(tile, n) + 31) / 32 * 32); };
+  const auto waves = [](int64_t tiles, int64_t slots) { return static_cast<double>((tiles + slots - 1) / slots); };
+  int count = 0;
+  const int64_t pairs = machine.sms / 2, pair_tiles = n_tiles(p, 256, false) * m_tiles(p, true);
+  forms[count++] = Form{true, 256, 1,
+                        410 + waves(pair_tiles, pairs) * (2110 + 15 * cols(256) +
+                                                          blocks * std::max(2.6 * cols(256), 480.0)),
+                        2 * std::min(pair_tiles, pairs)};
+  for (int tile : {32, 64, 128, 256}) {
+    if (!valid_form(p.kind, 0, tile, 1)) continue;
+    const double c = cols(tile);
+    const double block = std::max({1.4 * c, 480.0, (kLinABytes + c * 128) / 60.0});
+    const int64_t tiles = n_tiles(p, tile, false) * m_tiles(p, false);
+    const int64_t most = n_tiles(p, tile, true) * m_tiles(p, false);
+    forms[count++] = Form{false, tile, 1, waves(tiles, machine.sms) * (1770 + 15 * c + block * blocks),
+                          std::min<int64_t>(tiles, machine.sms)};
+    for (int i = 0; i < 3; ++i) {
+      const int split = 2 << i;
+      if (most > machine.clusters[i] || blocks < 2 * split) continue;
+      forms[count++] = Form{false, tile, split,
+                            4070 + 38 * c + (36.0 + 14.0 * tiles) * split + block * std::ceil(blocks / split),
+                            most * split};
     }
   }
+  return count;
+}
+
+// The plan of a form that there is.
+int plan_of(const Product& p, const Machine& machine, const Form& form, Plan* o) {
+  o->pair = form.pair;
+  o->tile = form.tile;
+  o->split = form.split;
   if (o->tile <= 8) {
     const int64_t units = (p.ragged && o->tile == 1 ? p.n : p.groups) * ((p.m + kFewOuts - 1) / kFewOuts);
     const int64_t blocks = (units * o->split + kFewWarps - 1) / kFewWarps;
@@ -234,16 +235,74 @@ int make_plan(const Product& p, const Machine& machine, const linear_options_t* 
     o->units = static_cast<int>(blocks);
     return GEMM_OK;
   }
-  const int64_t most = n_tiles(p, o->tile, true) * m_tiles(o->pair);
+  const int64_t most = n_tiles(p, o->tile, true) * m_tiles(p, o->pair);
   // counted in 32 bits, with room for a grid's stride past the last
   if (most > INT_MAX / 4) return GEMM_ERR_INVALID_VALUE;
-  o->m_tiles = static_cast<int>(m_tiles(o->pair));
-  o->n_tiles = weight ? static_cast<int>((p.n + o->tile - 1) / o->tile) : 0;
+  o->m_tiles = static_cast<int>(m_tiles(p, o->pair));
+  o->n_tiles = p.kind == LINEAR_GRAD_W ? static_cast<int>((p.n + o->tile - 1) / o->tile) : 0;
   // Boxes of 32 rows where a group may end anywhere in a tile, so that a tile loads
   // little more than it has.
   o->box_rows = std::min(p.ragged || p.n <= 64 ? 32 : 128, o->tile);
   o->units = static_cast<int>(o->split > 1 ? most : std::min<int64_t>(o->pair ? machine.sms / 2 : machine.sms, most));
   return GEMM_OK;
+}
+
+bool is_forced(const linear_options_t* opt) { return opt && opt->tile != 0; }
+
+int forced_plan(const Product& p, const Machine& machine, const linear_options_t* opt, Plan* o) {
+  if (!valid_form(p.kind, opt->cta_pair, opt->tile, opt->split_k)) return GEMM_ERR_INVALID_VALUE;
+  return plan_of(p, machine, Form{opt->cta_pair != 0, opt->tile, opt->split_k, 0.0, 0}, o);
+}
+
+int make_plan(const Product& p, const Machine& machine, const linear_options_t* opt, Plan* o) {
+  if (is_forced(opt)) return forced_plan(p, machine, opt, o);
+  if (const int rows = few_rows(p, nullptr)) {
+    // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
+    // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
+    // with four).
+    const int64_t units = (p.ragged ? p.n : 1) * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
+    int split = 1;
+    while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
+    return plan_of(p, machine, Form{false, rows, split, 0.0, 0}, o);
+  }
+  Form forms[kMostForms];
+  const int count = list_forms(p, machine, forms);
+  const Form* best = &forms[0];
+  for (int i = 1; i < count; ++i)
+    if (forms[i].cycles < best->cycles) best = &forms[i];
+  return plan_of(p, machine, *best, o);
+}
+
+// grad_x and grad_w, which run beside each other where the SMs suffice for both (1021 x 1000 x
+// 1000: with the form that is best for each alone, 128 CTAs and 128, 17.3 us).  Where memory
+// bounds them that does not help.
+int make_plans(const Product& x, const Product& w, const Machine& machine,
+               const linear_options_t* opt, Plan* plan_x, Plan* plan_w) {
+  if (is_forced(opt)) {
+    const int rc = forced_plan(x, machine, opt, plan_x);
+    return rc != GEMM_OK ? rc : forced_plan(w, machine, opt, plan_w);
+  }
+  Form fx[kMostForms], fw[kMostForms];
+  const int nx = list_forms(x, machine, fx), nw = list_forms(w, machine, fw);
+  // each weight once, each row of x, dz and their gradients: 16 bits, at 3500 bytes a cycle
+  const double weights = static_cast<double>(std::min(x.groups, x.n)) * static_cast<double>(x.m) * static_cast<double>(x.k);
+  const double rows = static_cast<double>(x.n) * static_cast<double>(x.m + x.k);
+  const double memory = 4.0 * (weights + rows) / 3500.0;
+  const Form *best_x = nullptr, *best_w = nullptr;
+  double least = 0.0;
+  for (int i = 0; i < nx; ++i)
+    for (int j = 0; j < nw; ++j) {
+      const double cycles = fx[i].ctas + fw[j].ctas <= machine.sms
+                                ? std::max({fx[i].cycles, fw[j].cycles, memory}) + 500
+                                : fx[i].cycles + fw[j].cycles;
+      if (best_x && cycles >= least) continue;
+      least = cycles;
+      best_x = &fx[i];
+      best_w = &fw[j];
+    }
+  const int rc = plan_of(x, machine, *best_x, plan_x);
+  return rc != GEMM_OK ? rc : plan_of(w, machine, *best_w, plan_w);
 }
 
 // ------------------------------------------------------------------ launches
@@ -571,29 +630,28 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   }
   if (space.copy_w) copied(&w, &prepare, 0, workspace, space.w);
   if (space.copy_x) copied(&x, &prepare, 1, workspace, space.x);
-  if ((rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
+  const Product pr_x = product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
+                                  p.offsets != nullptr);
+  const Product pr_w = product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
+                                  p.offsets != nullptr);
+  Plan plan_x, plan_w;
+  if (for_x && for_w) rc = make_plans(pr_x, pr_w, machine, opt, &plan_x, &plan_w);
+  else if (for_x) rc = make_plan(pr_x, machine, opt, &plan_x);
+  else if (for_w) rc = make_plan(pr_w, machine, opt, &plan_w);
+  if (rc != GEMM_OK || (rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
   if (for_x) {
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);
     px.overlap = for_w ? kOverlapFirst : kOverlapNone;
-    const Product pr = product_of(LINEAR_GRAD_X, layer->rows, layer->in, layer->out, groups,
-                                  p.offsets != nullptr);
-    Plan plan;
-    if ((rc = make_plan(pr, machine, opt, &plan)) != GEMM_OK ||
-        (rc = launch(pr, plan, w, dz, px, layer->type, opt, device, s)) != GEMM_OK)
-      return rc;
+    if ((rc = launch(pr_x, plan_x, w, dz, px, layer->type, opt, device, s)) != GEMM_OK) return rc;
   }
   p.grad_bias = static_cast<uint16_t*>(grad_bias);
   if (for_w) {
     p.out = static_cast<uint16_t*>(grad_w);
     p.strips = for_bias ? strips : nullptr;
     p.overlap = for_x ? kOverlapSecond : kOverlapNone;
-    const Product pr = product_of(LINEAR_GRAD_W, layer->rows, layer->in, layer->out, groups,
-                                  p.offsets != nullptr);
-    Plan plan;
-    if ((rc = make_plan(pr, machine, opt, &plan)) != GEMM_OK ||
-        (rc = launch(pr, plan, x, dz, p, layer->type, opt, device, s)) != GEMM_OK || strips)
-      return rc;
+    rc = launch(pr_w, plan_w, x, dz, p, layer->type, opt, device, s);
+    if (rc != GEMM_OK || strips) return rc;
   }
   if (!for_bias) return GEMM_OK;
   // Without grad_w, or without rows: then there are no strips either.
