@@ -186,9 +186,10 @@ int64_t m_tiles(const Product& p, bool pair) { return pair ? (p.m + 255) / 256 :
 
 // The forms on the tensor cores.  Cycles, for waves of tiles: a beginning and an end, with what an
 // epilogue takes of them by its rows, and blocks of 64 of the sum.  These come in at 60 bytes a
-// cycle and SM, and cost 480 at least to be issued.  Clusters that share sums meet twice, and send them.
-// Fitted to 1680 products of 560 layers (rows 1 to 32768, inputs and outputs 64 to 8192, half of them
-// with 8 to 64 experts): 2.2 % over the best form of each in the mean, 26 at worst.
+// cycle and SM, and cost something to be issued.  Clusters that share sums meet twice, and send them.
+// Fitted to 1200 products of 400 layers (rows 1 to 32768, inputs and outputs 64 to 8192, half of them
+// with 8 to 64 experts): 1.2 % over the best form of each in the mean, and half again as long at worst
+// (grad_w of 18 experts with 12803 rows, 112 -> 72).
 int list_forms(const Product& p, const Machine& machine, Form (&forms)[kMostForms]) {
   const bool weight = p.kind == LINEAR_GRAD_W;
   // of a group, in the mean
@@ -200,22 +201,22 @@ int list_forms(const Product& p, const Machine& machine, Form (&forms)[kMostForm
   int count = 0;
   const int64_t pairs = machine.sms / 2, pair_tiles = n_tiles(p, 256, false) * m_tiles(p, true);
   forms[count++] = Form{true, 256, 1,
-                        410 + waves(pair_tiles, pairs) * (2110 + 15 * cols(256) +
-                                                          blocks * std::max(2.6 * cols(256), 480.0)),
+                        360 + waves(pair_tiles, pairs) * (2110 + 19 * cols(256) +
+                                                          blocks * std::max(2.6 * cols(256), 520.0)),
                         2 * std::min(pair_tiles, pairs)};
   for (int tile : {32, 64, 128, 256}) {
     if (!valid_form(p.kind, 0, tile, 1)) continue;
     const double c = cols(tile);
-    const double block = std::max({1.4 * c, 480.0, (kLinABytes + c * 128) / 60.0});
+    const double block = std::max({1.5 * c, tile > 64 ? 535.0 : 240.0, (kLinABytes + c * 128) / 60.0});
     const int64_t tiles = n_tiles(p, tile, false) * m_tiles(p, false);
     const int64_t most = n_tiles(p, tile, true) * m_tiles(p, false);
-    forms[count++] = Form{false, tile, 1, waves(tiles, machine.sms) * (1770 + 15 * c + block * blocks),
+    forms[count++] = Form{false, tile, 1, waves(tiles, machine.sms) * (1770 + 19 * c + block * blocks),
                           std::min<int64_t>(tiles, machine.sms)};
     for (int i = 0; i < 3; ++i) {
       const int split = 2 << i;
       if (most > machine.clusters[i] || blocks < 2 * split) continue;
       forms[count++] = Form{false, tile, split,
-                            4070 + 38 * c + (36.0 + 14.0 * tiles) * split + block * std::ceil(blocks / split),
+                            4850 + 36 * c + (68.0 + 9.0 * tiles) * split + block * std::ceil(blocks / split),
                             most * split};
     }
   }
