@@ -1,4 +1,4 @@
-"""One projection of a mixture-of-experts layer, served and trained, on the package's kernels.
+"""Layers of a mixture of experts, served in 4 bits and trained in 16, on the package's kernels.
 
     python -m multistage_smem_pipeline_gb300.moe_example [--tokens T] [--experts E] [--top-k K]
         [--hidden H] [--out N] [--format nvfp4|mxfp4]
@@ -8,8 +8,9 @@ slots by expert, quantises each token once into the rows of its slots, multiplie
 its expert's weights and sums the slots back into token order with the router's weights.  The
 forward is also captured into a CUDA graph, as a decoding loop would run it.
 
-Training: `dispatch` and `combine` are the same moves as autograd functions around experts that
-the program computes itself (here a 16-bit scale per expert, to keep the example short).
+Training: `dispatch`, `expert_linear`, `linear` and `combine` are the package's moves and 16-bit layers as
+autograd functions; two layers of experts with an activation between them, the way back to the
+tokens, and a dense layer onto the residual stream, forward and backward.
 """
 from __future__ import annotations
 
@@ -19,8 +20,9 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (Fp4Matrix, Routing, fp4_gemm_tn, fp4_quantize, moe_combine, moe_combine_backward,
-               moe_dispatch, moe_dispatch_backward, moe_sort)
+from . import (Fp4Matrix, Routing, fp4_gemm_tn, fp4_quantize, linear as _linear, linear_backward,
+               moe_combine, moe_combine_backward, moe_dispatch, moe_dispatch_backward, moe_linear,
+               moe_linear_backward, moe_sort)
 
 
 def exponent_for(x: torch.Tensor) -> int:
@@ -81,6 +83,48 @@ class _Combine(torch.autograd.Function):
         return grad_y, grad_w, None
 
 
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, routing, activation):
+        keep = activation != "none" and any(ctx.needs_input_grad[:3])
+        if routing is None:
+            got = _linear(x, weight, bias, activation=activation, residual=residual, save_preact=keep)
+        else:
+            got = moe_linear(x, routing, weight, bias, activation=activation, save_preact=keep)
+        out, preact = got if keep else (got, None)
+        ctx.routing, ctx.activation = routing, activation
+        need_x, need_weight = ctx.needs_input_grad[:2]
+        ctx.save_for_backward(x if need_weight else None, weight if need_x else None, preact)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        x, weight, preact = ctx.saved_tensors
+        need = dict(zip(("need_x", "need_weight", "need_bias"), ctx.needs_input_grad))
+        kw = dict(activation=ctx.activation, preact=preact, **need)
+        grad = grad_out.contiguous()
+        if not any(need.values()):
+            grads = (None, None, None)
+        elif ctx.routing is None:
+            grads = linear_backward(grad, x, weight, **kw)
+        else:
+            grads = moe_linear_backward(grad, x, ctx.routing, weight, **kw)
+        return (*grads, grad_out if ctx.needs_input_grad[3] else None, None, None)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+           residual: torch.Tensor | None = None, activation: str = "none") -> torch.Tensor:
+    """act(x @ weight^T + bias) + residual with its gradients (of first order)."""
+    return _Linear.apply(x, weight, bias, residual, None, activation)
+
+
+def expert_linear(x: torch.Tensor, routing: Routing, weight: torch.Tensor,
+                  bias: torch.Tensor | None = None, activation: str = "none") -> torch.Tensor:
+    """moe_linear with its gradients (of first order): x in expert order, a matrix for each expert."""
+    return _Linear.apply(x, weight, bias, None, routing, activation)
+
+
 def dispatch(x: torch.Tensor, routing: Routing) -> torch.Tensor:
     """moe_dispatch with its gradient (of first order)."""
     return _Dispatch.apply(x, routing)
@@ -128,17 +172,24 @@ def main(argv=None) -> None:
     same = torch.equal(captured, y)
     print(f"as a graph: {start.elapsed_time(end) * 10:.1f} us a forward, same result: {same}")
 
+    def parameter(*sizes, scale):
+        return (torch.randn(*sizes, device=dev) * scale).bfloat16().requires_grad_()
+
     x16 = x.clone().requires_grad_()
     g16 = gates.clone().requires_grad_()
-    scale = torch.randn(a.experts, 1, device=dev).bfloat16().requires_grad_()
+    up = w.clone().requires_grad_()
+    up_bias = parameter(a.experts, a.out, scale=0.1)
+    down = parameter(a.experts, a.hidden, a.out, scale=a.out ** -0.5)
+    last, last_bias = parameter(a.hidden, a.hidden, scale=a.hidden ** -0.5), parameter(a.hidden, scale=0.1)
     routing = moe_sort(ids, a.experts)
-    rows = dispatch(x16, routing)
-    counts = routing.offsets.diff()
-    rows = rows * scale.repeat_interleave(counts, dim=0, output_size=rows.shape[0])
-    loss = combine(rows, routing, g16).float().square().mean()
+    rows = expert_linear(dispatch(x16, routing), routing, up, up_bias, activation="silu")
+    rows = expert_linear(rows, routing, down)
+    y16 = linear(combine(rows, routing, g16), last, last_bias, residual=x16)
+    loss = y16.float().square().mean()
     loss.backward()
     print(f"trained: loss {loss.item():.4f}, gradient norms: x {x16.grad.float().norm():.4f}, "
-          f"router weights {g16.grad.norm():.4f}, experts {scale.grad.float().norm():.4f}")
+          f"router weights {g16.grad.norm():.4f}, experts {up.grad.float().norm():.4f} and "
+          f"{down.grad.float().norm():.4f}, dense layer {last.grad.float().norm():.4f}")
 
 
 if __name__ == "__main__":
