@@ -47,7 +47,8 @@ enum {
 /* The layer.  Matrices are row by row, 2-byte aligned at least, with rows that do
  * not overlap: a row stride (elements) is at least the width, and the arrays
  * without one are contiguous.  Rows that start on 16-byte boundaries (pointer
- * and stride) are read where they are; others are first copied to `workspace`. */
+ * and stride) are read where they are, and so are all rows of forward products of few
+ * rows; others are first copied to `workspace`. */
 typedef struct {
   int64_t rows;              /* of x and out */
   int64_t in, out;           /* elements of their rows */

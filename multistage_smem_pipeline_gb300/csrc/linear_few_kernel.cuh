@@ -1,13 +1,13 @@
 // The forward product for a few rows, without the tensor cores: out[r][n] for up to kRows
 // rows of a group at a time.
 //
-// An MMA takes 107 cycles for any N up to 128 or so, as many as for 128 outputs by 16 of
-// the sum, so that a CTA takes in 38 bytes of weights a cycle at most, and tiles of 128 outputs
-// are too few to fill the SMs (1 x 4096 x 4096: 32).  Here a warp has four outputs, whose
+// On the tensor cores the issue loop takes about 356 cycles for a stage, 16 KiB of weights,
+// however few the rows are, and tiles of 128 outputs are too few to fill the SMs
+// (1 x 4096 x 4096: 32 tiles, 11.6 us; 7.5 so).  Here a warp has four outputs, whose
 // weights it reads 16 bytes a lane along the sum; a lane's products go to 4 x kRows
 // sums in registers, which the warp's lanes add up at the end, halving the number of
-// sums as they halve the distance.  What bounds it is memory (1 x 14336 x 4096: 21.7 us,
-// 5.4 TB/s), and for 8 rows the multiplications (35).  `split` warps share a sum where outputs
+// sums as they halve the distance.  What bounds it is memory (1 x 14336 x 4096: 21.1 us,
+// 5.6 TB/s), and for 8 rows the multiplications (35).  `split` warps share a sum where outputs
 // are few, and add their parts in order.  x comes from the first-level cache, and is used for four
 // outputs at a time.  Rows may start at any 2-byte address: nothing is copied first.
 #pragma once

@@ -14,6 +14,9 @@
 // the sum's stages; with all MMAs done, the rings are free, and every CTA writes its
 // sums for each other one's share of the chunks into that one's ring, where they
 // are added in the order of the parts.  No sum depends on who came first.
+//
+// What bounds it: with small tiles the issue loop (see linear_multiply), and for few blocks
+// a launch's two ends, about 3 us (517 x 1001 x 1411: 12.8 us with its copies).
 #pragma once
 #include "linear.cuh"
 
