@@ -359,6 +359,70 @@ def test_on_other_streams_at_once(lib):
     assert all(lib.linear_get_device_error(s) == (0, 0) for s in streams)
 
 
+@pytest.mark.parametrize("form", [None, (1, 256, 1), (0, 64, 1), (0, 128, 8), (0, 256, 2)])
+def test_the_most_experts(lib, form):
+    """1024 experts, most of them without a row, one with many."""
+    counts = [0] * 1024
+    for e, rows in ((0, 1), (1, 17), (500, 300), (501, 2), (1023, 33)):
+        counts[e] = rows
+    m = make(sum(counts) + 5, 40, 72, torch.bfloat16, experts=1024, seed=21)
+    routing, offsets = routing_of(lib, counts, 5)
+    for t in ("x", "grad", "z"):
+        m[t][offsets[-1]:] = float("nan")
+    got, z = lib.moe_linear(m["x"], routing, m["w"], m["bias"], activation="silu", save_preact=True, form=form)
+    want, err, wz, zerr = ref.forward(m["x"], m["w"], m["bias"], None, "silu", offsets)
+    ref.check(got, want, err, "out")
+    ref.check(z, wz, zerr, "z")
+    check_backward(lib, m, "silu", routing, offsets, form)
+
+
+def test_two_graphs_replayed_at_once(lib):
+    """Each has workspaces of its own (unaligned rows are copied to them, dz and strips are there)."""
+    sets = [make(230, 201, 335, torch.float16, seed=60 + i) for i in range(2)]
+    calls = [lambda m=m: (lib.linear(m["x"], m["w"], m["bias"], activation="gelu"),
+                          *lib.linear_backward(m["grad"], m["x"], m["w"], preact=m["z"], activation="gelu", need_bias=True))
+             for m in sets]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for c in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(c())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,out,hidden", [(300, 264, 520), (2000, 1000, 1411)])
+def test_what_follows_a_backward_pass_follows_all_of_it(lib, rows, out, hidden):
+    """grad_w may run beside grad_x: the next kernels still come after both, and what came before, before."""
+    m = make(rows, out, hidden, torch.bfloat16, seed=70)
+    w2 = values(71, 64, hidden, dtype=torch.bfloat16, scale=0.05)
+    kw = dict(preact=m["z"], activation="silu", need_bias=True)
+    want = [t.clone() for t in lib.linear_backward(m["grad"], m["x"], m["w"], **kw)]
+    then = lib.linear(want[0], w2)
+    torch.cuda.synchronize()
+    d = {k: torch.empty_like(m[k]) for k in ("x", "w", "grad", "z")}
+    kw["preact"] = d["z"]
+    results = []
+    for _ in range(10):
+        for k in d:
+            d[k].copy_(m[k])
+        g = lib.linear_backward(d["grad"], d["x"], d["w"], **kw)
+        results.append((*g, lib.linear(g[0], w2)))
+        for k in d:
+            d[k].fill_(float("nan"))
+    for r in results:
+        assert all(torch.equal(a, b) for a, b in zip(r, (*want, then)))
+
+
 @pytest.mark.parametrize("form", [(1, 256, 1), (0, 128, 1), (0, 256, 4)])
 def test_a_wait_that_runs_out_is_reported(lib, form):
     m = make(300, 264, 400, torch.float16)
