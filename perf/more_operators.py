@@ -261,8 +261,7 @@ def _exact_act(z, name):
         p = torch.special.expit(z)
         return z * p, p * (1 + z * torch.special.expit(-z))
     if name == "gelu":
-        tail = torch.special.erfcx(z.abs() / math.sqrt(2)) * torch.exp(-z * z / 2) / 2
-        p = torch.where(z < 0, tail, 1 - tail)
+        p = torch.special.ndtr(z)
         return z * p, p + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     t = torch.tanh(math.sqrt(2 / math.pi) * (z + CUBIC * z ** 3))
     # (1 + t) / 2 without the cancellation where t is near -1
