@@ -102,8 +102,15 @@ int linear_backward_workspace(const void* grad_x, const void* grad_w, const void
                               const linear_t* layer, const void* grad_out, int64_t ldg,
                               uint64_t* bytes);
 
-/* The products of these calls. */
-enum { LINEAR_FORWARD = 0, LINEAR_GRAD_X = 1, LINEAR_GRAD_W = 2 };
+/* The products of these calls.  grad_x and grad_w of one call share the GPU, and may be cut in
+ * another way than either in a call without the other one: _OF_BOTH is the former. */
+enum {
+  LINEAR_FORWARD = 0,
+  LINEAR_GRAD_X = 1,
+  LINEAR_GRAD_W = 2,
+  LINEAR_GRAD_X_OF_BOTH = 3,
+  LINEAR_GRAD_W_OF_BOTH = 4
+};
 
 /* How a product is cut. */
 typedef struct {

@@ -255,35 +255,11 @@ int forced_plan(const Product& p, const Machine& machine, const linear_options_t
   return plan_of(p, machine, Form{opt->cta_pair != 0, opt->tile, opt->split_k, 0.0, 0}, o);
 }
 
-int make_plan(const Product& p, const Machine& machine, const linear_options_t* opt, Plan* o) {
-  if (is_forced(opt)) return forced_plan(p, machine, opt, o);
-  if (const int rows = few_rows(p, nullptr)) {
-    // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
-    // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
-    // with four).
-    const int64_t units = (p.ragged ? p.n : 1) * ((p.m + kFewOuts - 1) / kFewOuts);
-    const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
-    int split = 1;
-    while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
-    return plan_of(p, machine, Form{false, rows, split, 0.0, 0}, o);
-  }
-  Form forms[kMostForms];
-  const int count = list_forms(p, machine, forms);
-  const Form* best = &forms[0];
-  for (int i = 1; i < count; ++i)
-    if (forms[i].cycles < best->cycles) best = &forms[i];
-  return plan_of(p, machine, *best, o);
-}
-
 // grad_x and grad_w, which run beside each other where the SMs suffice for both (1021 x 1000 x
 // 1000: with the form that is best for each alone, 128 CTAs and 128, 17.3 us).  Where memory
 // bounds them that does not help.
-int make_plans(const Product& x, const Product& w, const Machine& machine,
-               const linear_options_t* opt, Plan* plan_x, Plan* plan_w) {
-  if (is_forced(opt)) {
-    const int rc = forced_plan(x, machine, opt, plan_x);
-    return rc != GEMM_OK ? rc : forced_plan(w, machine, opt, plan_w);
-  }
+void choose_both(const Product& x, const Product& w, const Machine& machine, Form* form_x,
+                 Form* form_w) {
   Form fx[kMostForms], fw[kMostForms];
   const int nx = list_forms(x, machine, fx), nw = list_forms(w, machine, fw);
   // each weight once, each row of x, dz and their gradients: 16 bits, at 3500 bytes a cycle
@@ -302,8 +278,40 @@ int make_plans(const Product& x, const Product& w, const Machine& machine,
       best_x = &fx[i];
       best_w = &fw[j];
     }
-  const int rc = plan_of(x, machine, *best_x, plan_x);
-  return rc != GEMM_OK ? rc : plan_of(w, machine, *best_w, plan_w);
+  *form_x = *best_x;
+  *form_w = *best_w;
+}
+
+int make_plans(const Product& x, const Product& w, const Machine& machine,
+               const linear_options_t* opt, Plan* plan_x, Plan* plan_w) {
+  if (is_forced(opt)) {
+    const int rc = forced_plan(x, machine, opt, plan_x);
+    return rc != GEMM_OK ? rc : forced_plan(w, machine, opt, plan_w);
+  }
+  Form fx, fw;
+  choose_both(x, w, machine, &fx, &fw);
+  const int rc = plan_of(x, machine, fx, plan_x);
+  return rc != GEMM_OK ? rc : plan_of(w, machine, fw, plan_w);
+}
+
+int make_plan(const Product& p, const Machine& machine, const linear_options_t* opt, Plan* o) {
+  if (is_forced(opt)) return forced_plan(p, machine, opt, o);
+  if (const int rows = few_rows(p, nullptr)) {
+    // As many warps for a sum as give each lane 16 bytes of it, and can all run at once
+    // (2 x 9112 x 2624: 11.9 us with one, 15.5 with two; 1 x 4096 x 4096: 8.8 with two, 7.5
+    // with four).
+    const int64_t units = (p.ragged ? p.n : 1) * ((p.m + kFewOuts - 1) / kFewOuts);
+    const int64_t warps = machine.sms * kFewWarps * few_blocks(rows, true);
+    int split = 1;
+    while (split < 8 && 2 * split * units <= warps && split * 256 < p.k) split *= 2;
+    return plan_of(p, machine, Form{false, rows, split, 0.0, 0}, o);
+  }
+  Form forms[kMostForms];
+  const int count = list_forms(p, machine, forms);
+  const Form* best = &forms[0];
+  for (int i = 1; i < count; ++i)
+    if (forms[i].cycles < best->cycles) best = &forms[i];
+  return plan_of(p, machine, *best, o);
 }
 
 // ------------------------------------------------------------------ launches
@@ -664,7 +672,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
 
 extern "C" int linear_query_config(int product, int64_t rows, int64_t in, int64_t out, int experts,
                                    linear_config_t* config) {
-  if (!config || product < LINEAR_FORWARD || product > LINEAR_GRAD_W || rows < 1 || in < 1 ||
+  if (!config || product < LINEAR_FORWARD || product > LINEAR_GRAD_W_OF_BOTH || rows < 1 || in < 1 ||
       out < 1 || rows > LINEAR_MAX_ROWS || in > LINEAR_MAX_COLS || out > LINEAR_MAX_COLS ||
       experts < 0 || experts > MOE_MAX_EXPERTS || std::max(experts, 1) * out > INT_MAX)
     return GEMM_ERR_INVALID_VALUE;
@@ -672,9 +680,17 @@ extern "C" int linear_query_config(int product, int64_t rows, int64_t in, int64_
   int sms = 0, device = 0;
   if (require_device(&sms, &device) == GEMM_OK) machine = machine_of(sms, device);
   else cudaGetLastError();
-  Plan plan;
-  const int rc = make_plan(product_of(product, rows, in, out, std::max(experts, 1), experts > 0),
-                           machine, nullptr, &plan);
+  const auto of = [&](int kind) {
+    return product_of(kind, rows, in, out, std::max(experts, 1), experts > 0);
+  };
+  Plan plan, beside;
+  int rc;
+  if (product == LINEAR_GRAD_X_OF_BOTH)
+    rc = make_plans(of(LINEAR_GRAD_X), of(LINEAR_GRAD_W), machine, nullptr, &plan, &beside);
+  else if (product == LINEAR_GRAD_W_OF_BOTH)
+    rc = make_plans(of(LINEAR_GRAD_X), of(LINEAR_GRAD_W), machine, nullptr, &beside, &plan);
+  else
+    rc = make_plan(of(product), machine, nullptr, &plan);
   if (rc != GEMM_OK) return rc;
   *config = linear_config_t{plan.pair ? 1 : 0, plan.tile, plan.split,
                             plan.units * (plan.pair ? 2 : plan.tile <= 8 ? 1 : plan.split)};

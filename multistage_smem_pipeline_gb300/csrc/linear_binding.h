@@ -184,10 +184,10 @@ py::tuple backward(const at::Tensor& grad_out, const Out& x, const Routing* rout
 }
 
 py::dict linear_config(const std::string& product, int64_t rows, int64_t in, int64_t out,
-                       int experts) {
+                       int experts, bool both) {
   const int kind = product == "forward"  ? LINEAR_FORWARD
-                   : product == "grad_x" ? LINEAR_GRAD_X
-                   : product == "grad_w" ? LINEAR_GRAD_W
+                   : product == "grad_x" ? (both ? LINEAR_GRAD_X_OF_BOTH : LINEAR_GRAD_X)
+                   : product == "grad_w" ? (both ? LINEAR_GRAD_W_OF_BOTH : LINEAR_GRAD_W)
                                          : -1;
   linear_config_t c{};
   check(linear_query_config(kind, rows, in, out, experts, &c), "linear_query_config");
@@ -266,8 +266,10 @@ void define_linear(py::module_& m) {
       "zero for one without; rows of dropped slots have zeros in grad_x and count in nothing.");
   m.def("linear_query_config", &linear_config, py::arg("product"), py::arg("rows"),
         py::arg("in_features"), py::arg("out_features"), py::arg("experts") = 0,
+        py::kw_only(), py::arg("both") = false,
         "The form that a product (forward, grad_x or grad_w) of a layer of these sizes takes, "
-        "without running it; experts: 0 for a dense one.");
+        "without running it; experts: 0 for a dense one; both: grad_x or grad_w in a call for "
+        "both of them, where it may be another.");
   m.def(
       "linear_get_device_error",
       [](const py::object& stream) { return device_error(stream, linear_get_device_error); },
