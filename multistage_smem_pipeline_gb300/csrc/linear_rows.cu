@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         float zs[8];
         unpack<T>(s[i], zs);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= activation_slope<kActivation>(zs[e]);
+        for (int e = 0; e < 8; ++e)  // rounded, also where nothing but the sum takes it
+          v[e] = __fmul_rn(v[e], activation_slope<kActivation>(zs[e]));
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
