@@ -88,7 +88,8 @@ int linear_forward(void* out, void* preact, const linear_t* layer, const void* b
  * (experts x out) that are not NULL, all contiguous.  grad_out: rows x out, row stride
  * ldg.  preact: rows x out, contiguous, as linear_forward wrote it; NULL for
  * LINEAR_NONE.  layer->x is read for grad_w alone and layer->w for grad_x alone,
- * and may be NULL otherwise.  The gradients of an expert without rows are zero. */
+ * and may be NULL otherwise.  The gradients of an expert without rows are zero.  The bits of a
+ * gradient do not depend on which others the call is for. */
 int linear_backward(void* grad_x, void* grad_w, void* grad_bias, const linear_t* layer,
                     const void* grad_out, int64_t ldg, const void* preact, void* workspace,
                     uint64_t workspace_bytes, const linear_options_t* opt, void* stream);

@@ -28,3 +28,12 @@ def test_both_gradients_are_cut_to_run_beside_each_other(ex):
             assert c["ctas"] >= 1 and c["tile"] >= (64 if product == "grad_w" else 32)
     # of the forward product there is one form
     assert ex.linear_query_config("forward", 64, 2048, 2048, both=True) == ex.linear_query_config("forward", 64, 2048, 2048)
+
+
+def test_a_gradient_s_sums_are_shared_as_beside_the_other_one(ex):
+    """The bits of a gradient depend on how many CTAs share its sums, and not on what else is asked for."""
+    for rows, out, hidden, experts in SIZES:
+        for product in ("grad_x", "grad_w"):
+            alone = ex.linear_query_config(product, rows, hidden, out, experts)
+            both = ex.linear_query_config(product, rows, hidden, out, experts, both=True)
+            assert alone["split_k"] == both["split_k"], (product, rows, out, hidden, experts, alone, both)
