@@ -52,40 +52,10 @@ int launch_single(const CUtensorMap& w, const CUtensorMap& x, Fp4GemmParams p, i
                     fixed + p.stages * S::kStageBytes, s, static_cast<unsigned>(p.split), w, x, p);
 }
 
-// What the choice of a form needs to know of the device.
-struct Machine {
-  int sms;
-  int clusters[3];  // of 2, 4 and 8 CTAs, held at once, a CTA an SM (clusters lie
-                    // within a GPC, so some SMs may be left out)
-};
-
-Machine machine_of(int sms, int device) {
-  static std::once_flag once;
-  static int held[3] = {0, 0, 0};
-  std::call_once(once, [&] {
-    const auto kernel = fp4_gemm_tc<__half, FP4_NV, true>;
-    static std::atomic<uint64_t> granted{0};
-    if (!grant_smem(kernel, kGemmSmemLimit, device, granted)) return;
-    for (int i = 0; i < 3; ++i) {
-      cudaLaunchConfig_t cfg;
-      std::memset(&cfg, 0, sizeof(cfg));
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2u << i;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3((2u << i) * (sms / (2 << i)));
-      cfg.blockDim = dim3(kGemmThreads);
-      cfg.dynamicSmemBytes = kGemmSmemLimit;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        held[i] = 0;
-      }
-    }
-  });
-  return Machine{sms, {held[0], held[1], held[2]}};
+int machine_of(int sms, int device, Machine* machine) {
+  static PerDevice<Machine> known;
+  return machine_by(fp4_gemm_tc<__half, FP4_NV, true>, kGemmThreads, kGemmSmemLimit, sms, device,
+                    known, machine);
 }
 
 // CTAs that share each of `tiles` tiles' k.  Measured on GB300: a 256-column
@@ -253,9 +223,11 @@ extern "C" int fp4_gemm_tn_ex(void* D, int type, const fp4_matrix_t* a, const fp
   p.inject = inject;
   p.error_word = error_index(s);
 
+  Machine machine;
+  if ((rc = machine_of(sms, device, &machine)) != GEMM_OK) return rc;
   Plan plan;
-  rc = make_plan(a->rows, n_out, a->cols, a->format, a->groups, a->offsets != nullptr,
-                 machine_of(sms, device), &plan);
+  rc = make_plan(a->rows, n_out, a->cols, a->format, a->groups, a->offsets != nullptr, machine,
+                 &plan);
   if (rc != GEMM_OK) return rc;
   p.m_tiles = plan.m_tiles;
   p.box_rows = plan.box_rows;
@@ -287,11 +259,11 @@ extern "C" int fp4_query_config(int64_t rows, int64_t n, int64_t cols, int forma
       (by_offsets ? groups > MOE_MAX_EXPERTS : rows % groups != 0) || n > INT_MAX / groups)
     return GEMM_ERR_INVALID_VALUE;
   Machine machine{152, {76, 36, 15}};
-  int sms = 0, device = 0;
-  if (require_device(&sms, &device) == GEMM_OK) machine = machine_of(sms, device);
-  else cudaGetLastError();
+  int sms = 0, device = 0, rc = GEMM_OK;
+  if (require_device(&sms, &device) != GEMM_OK) cudaGetLastError();
+  else if ((rc = machine_of(sms, device, &machine)) != GEMM_OK) return rc;
   Plan plan;
-  const int rc = make_plan(rows, n, cols, format, groups, by_offsets != 0, machine, &plan);
+  rc = make_plan(rows, n, cols, format, groups, by_offsets != 0, machine, &plan);
   if (rc != GEMM_OK) return rc;
   *out = fp4_config_t{plan.pair ? 1 : 0, plan.split, plan.tile, plan.box_rows,
                       plan.units * (plan.pair ? 2 : plan.split)};

@@ -74,39 +74,10 @@ const int32_t* offsets_of(const linear_t* l) {
 }
 
 // ------------------------------------------------------------------ forms
-// What the choice of a form needs to know of the device.
-struct Machine {
-  int sms;
-  int clusters[3];  // of 2, 4 and 8 CTAs, held at once, a CTA an SM
-};
-
-Machine machine_of(int sms, int device) {
-  static std::once_flag once;
-  static int held[3] = {0, 0, 0};
-  std::call_once(once, [&] {
-    const auto kernel = linear_tc<__half, LINEAR_FORWARD, true, 2>;
-    static std::atomic<uint64_t> granted{0};
-    if (!grant_smem(kernel, kLinSmemLimit, device, granted)) return;
-    for (int i = 0; i < 3; ++i) {
-      cudaLaunchConfig_t cfg;
-      std::memset(&cfg, 0, sizeof(cfg));
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2u << i;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3((2u << i) * (sms / (2 << i)));
-      cfg.blockDim = dim3(kLinThreads);
-      cfg.dynamicSmemBytes = kLinSmemLimit;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&held[i], kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        held[i] = 0;
-      }
-    }
-  });
-  return Machine{sms, {held[0], held[1], held[2]}};
+int machine_of(int sms, int device, Machine* machine) {
+  static PerDevice<Machine> known;
+  return machine_by(linear_tc<__half, LINEAR_FORWARD, true, 2>, kLinThreads, kLinSmemLimit, sms,
+                    device, known, machine);
 }
 
 struct Plan {
@@ -583,8 +554,11 @@ extern "C" int linear_forward(void* out, void* preact, const linear_t* layer, co
   p.rows = static_cast<int32_t>(layer->rows);
   p.activation = layer->activation;
   p.groups = groups;
+  Machine machine;
   Plan plan;
-  if ((rc = make_plan(pr, machine_of(sms, device), opt, &plan)) != GEMM_OK) return rc;
+  if ((rc = machine_of(sms, device, &machine)) != GEMM_OK ||
+      (rc = make_plan(pr, machine, opt, &plan)) != GEMM_OK)
+    return rc;
   if (plan.tile <= 8) return launch_few(plan, w, x, p, layer->type, s);
   PrepareRows prepare{};
   prepare.type = layer->type;
@@ -632,7 +606,8 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   int sms = 0, device = 0;
   if ((rc = require_device(&sms, &device)) != GEMM_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Machine machine = machine_of(sms, device);
+  Machine machine;
+  if ((rc = machine_of(sms, device, &machine)) != GEMM_OK) return rc;
 
   LinearParams p;
   std::memset(&p, 0, sizeof(p));
@@ -697,14 +672,13 @@ extern "C" int linear_query_config(int product, int64_t rows, int64_t in, int64_
       experts < 0 || experts > MOE_MAX_EXPERTS || std::max(experts, 1) * out > INT_MAX)
     return GEMM_ERR_INVALID_VALUE;
   Machine machine{152, {76, 36, 15}};
-  int sms = 0, device = 0;
-  if (require_device(&sms, &device) == GEMM_OK) machine = machine_of(sms, device);
-  else cudaGetLastError();
+  int sms = 0, device = 0, rc = GEMM_OK;
+  if (require_device(&sms, &device) != GEMM_OK) cudaGetLastError();
+  else if ((rc = machine_of(sms, device, &machine)) != GEMM_OK) return rc;
   const auto of = [&](int kind) {
     return product_of(kind, rows, in, out, std::max(experts, 1), experts > 0);
   };
   Plan plan, beside;
-  int rc;
   if (product == LINEAR_GRAD_X_OF_BOTH)
     rc = make_plans(of(LINEAR_GRAD_X), of(LINEAR_GRAD_W), machine, nullptr, &plan, &beside);
   else if (product == LINEAR_GRAD_W_OF_BOTH)

@@ -13,6 +13,7 @@
 
 #include "host.cuh"
 #include "moe_fp4.h"
+#include "per_device.h"
 #include "ptx.cuh"
 
 namespace gb300 {
@@ -116,6 +117,45 @@ bool grant_smem(Kernel kernel, size_t bytes, int device, std::atomic<uint64_t>& 
   }
   done.fetch_or(bit, std::memory_order_release);
   return true;
+}
+
+// What the choice of a product's form needs to know of the device.
+struct Machine {
+  int sms;
+  int clusters[3];  // of 2, 4 and 8 CTAs, held at once, a CTA an SM (clusters lie
+                    // within a GPC, so some SMs may be left out)
+};
+
+// That of the current device, by a kernel that has `smem` bytes in each of its CTAs; `known` is
+// the kernel's.
+template <typename Kernel>
+int machine_by(Kernel kernel, int threads, size_t smem, int sms, int device,
+               PerDevice<Machine>& known, Machine* machine) {
+  const auto ask = [&](Machine* m) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return false;
+    m->sms = sms;
+    for (int i = 0; i < 3; ++i) {
+      cudaLaunchConfig_t cfg;
+      std::memset(&cfg, 0, sizeof(cfg));
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3((2u << i) * (sms / (2 << i)));
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&m->clusters[i], kernel, &cfg) != cudaSuccess) return false;
+    }
+    return true;
+  };
+  if (known.get(device, machine, ask)) return GEMM_OK;
+  cudaGetLastError();
+  return GEMM_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ device
