@@ -536,44 +536,50 @@ __device__ __forceinline__ float activate(float z) {
   }
 }
 
-// z within -100 and 100, a NaN as it is.
-__device__ __forceinline__ float within_100(float z) {
+// z within -110 and 110, a NaN as it is.
+__device__ __forceinline__ float within_110(float z) {
   float y;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2C80000;\n\tmin.NaN.f32 %0, t, 0f42C80000;\n\t}"
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, 0fC2DC0000;\n\tmin.NaN.f32 %0, t, 0f42DC0000;\n\t}"
       : "=f"(y)
       : "f"(z));
   return y;
 }
 
-// act'(z).  Past 100 it is 0 or 1 in fp32, and products of what overflows and what
-// vanishes there would be NaN.  The sigmoid p keeps its relative accuracy below 0,
-// where the slope vanishes with it, and 1 - p has an absolute one that is enough where
-// the slope is near 1.  Results below fp32's normal numbers are 0.
+// act'(z).  Below 0, where it vanishes, it keeps its relative accuracy (but where it crosses zero):
+// it is a product of an exponential, or a sigmoid, and a sum, and those carry a factor of 2^32 until
+// the end, since the slope is up to 230 times the exponential and would be lost where that alone is
+// below fp32's normal numbers (silu from -87.4 on, gelu from -13.2, gelu_tanh from -9.9).  Above 0 its
+// accuracy is an absolute one; it is near 1 there.  Past 110 it is 0 or 1 in fp32, and products of
+// what overflows and what vanishes there would be NaN.
 template <int kActivation>
 __device__ __forceinline__ float activation_slope(float z) {
+  constexpr float kScale = 32.0f, kUnscale = 0x1p-32f;  // the factor, as an exponent, and its inverse
   if (kActivation == LINEAR_NONE) return 1.0f;
   if (kActivation == LINEAR_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  z = within_100(z);
+  z = within_110(z);
   if (kActivation == LINEAR_GELU) {
     // as in `normal`, with a polynomial of degree 6: relative error 8.5e-6 (dz and bias of 8192 x
-    // 4096 50 us with that of `normal`)
-    const float t = rcp_ftz(fmaf(0.3f, fabsf(z), 1.0f));
+    // 4096 50 us with that of `normal`); act'(-|z|), of which act'(|z|) is the rest to 1
+    const float s = fabsf(z), t = rcp_ftz(fmaf(0.3f, s, 1.0f));
     float f = -0.077096712f;
     f = fmaf(f, t, 0.21603487f);
     f = fmaf(f, t, -0.016945807f);
     f = fmaf(f, t, 0.14419527f);
     f = fmaf(f, t, 0.11374218f);
     f = fmaf(f, t, 0.12007421f);
-    const float e = exp2_ftz(z * z * -0.72134752f), tail = e * (f * t);
-    return fmaf(z * 0.39894228f, e, z < 0.0f ? tail : 1.0f - tail);
+    const float e = exp2_ftz(fmaf(s * s, -0.72134752f, kScale));
+    const float low = e * (fmaf(s, -0.39894228f, f * t) * kUnscale);
+    return z < 0.0f ? low : 1.0f - low;
   }
-  if (kActivation == LINEAR_GELU_TANH) {  // factors of -log2(e) in front
+  // P (1 + z u' (1 - P)) with the sigmoid P of u(z); factors of -log2(e) in the exponent
+  float exponent = fmaf(-1.4426950f, z, -kScale), zu = z;
+  if (kActivation == LINEAR_GELU_TANH) {
     const float zz = z * z;
-    const float p = rcp_ftz(1.0f + exp2_ftz(z * fmaf(-0.10294324f, zz, -2.3022082f)));
-    return fmaf(z * fmaf(0.21406445f, zz, 1.5957691f), p * (1.0f - p), p);
+    exponent = fmaf(z, fmaf(-0.10294324f, zz, -2.3022082f), -kScale);
+    zu = z * fmaf(0.21406445f, zz, 1.5957691f);
   }
-  const float p = rcp_ftz(1.0f + exp2_ftz(-1.4426950f * z));
-  return p * fmaf(z, 1.0f - p, 1.0f);
+  const float p = rcp_ftz(exp2_ftz(exponent) + kUnscale);  // 2^32 P
+  return p * (fmaf(zu, fmaf(p, -kUnscale, 1.0f), 1.0f) * kUnscale);
 }
 
 // The activation of some values; the choice is made once for them.
