@@ -643,6 +643,7 @@ extern "C" int linear_backward(void* grad_x, void* grad_w, void* grad_bias, cons
   else if (for_x) rc = make_plan(pr_x, machine, opt, &plan_x);
   else if (for_w) rc = make_plan(pr_w, machine, opt, &plan_w);
   if (rc != GEMM_OK || (rc = prepare_rows(prepare, s)) != GEMM_OK) return rc;
+  // Between the launches of the two products there is no other (see launch_pdl).
   if (for_x) {
     LinearParams px = p;
     px.out = static_cast<uint16_t*>(grad_x);

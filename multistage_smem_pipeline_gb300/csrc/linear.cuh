@@ -82,15 +82,25 @@ struct LinearParams {
 // nothing of each other.  So grad_x lets grad_w start only once all of its own CTAs have
 // waited for that (kOverlapFirst), grad_w begins without waiting, and waits for grad_x at
 // its end (kOverlapSecond), so that what follows it follows both.
+// What came before is complete when grad_x's waits return, and a CTA of grad_w starts after that.
+// The instructions promise grad_x alone to see it; fences on both sides of the start carry that
+// on to grad_w, whose loads of it are ordinary ones and TMA's.
 enum { kOverlapNone = 0, kOverlapFirst = 1, kOverlapSecond = 2 };
 
 __device__ __forceinline__ void linear_begin_early(const LinearParams& p) {
   if (p.overlap != kOverlapFirst) grid_launch_dependents();
 }
 __device__ __forceinline__ void linear_begin(const LinearParams& p) {
-  if (p.overlap == kOverlapSecond) return;
+  if (p.overlap == kOverlapSecond) {
+    __threadfence();
+    fence_proxy_async_global();
+    return;
+  }
   grid_dependency_wait();
-  if (p.overlap == kOverlapFirst) grid_launch_dependents();
+  if (p.overlap == kOverlapFirst) {
+    __threadfence();
+    grid_launch_dependents();
+  }
 }
 __device__ __forceinline__ void linear_end(const LinearParams& p) {
   if (p.overlap == kOverlapSecond) grid_dependency_wait();

@@ -67,7 +67,10 @@ inline bool any_overlap(std::initializer_list<Range> arrays, const moe_routing_t
 
 // A launch with programmatic dependent launch: the kernel's set-up may overlap
 // the end of the one before it in the stream, and every kernel here waits for
-// that one (grid_dependency_wait) before its first access to memory.
+// that one (grid_dependency_wait) before its first access to memory.  The exception is
+// a grad_w of linear layers that runs beside grad_x: the launch before it has to
+// trigger after its own wait and nowhere else, and grad_w has to wait for it before it ends,
+// so that what comes next follows both.
 // `cluster` blocks form a cluster.
 template <typename... Params, typename... Args>
 int launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

@@ -89,6 +89,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 __device__ __forceinline__ void tc_fence_before_sync() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -117,7 +121,8 @@ __device__ __forceinline__ void tma_prefetch_l2_2d(const void* tmap, int32_t x, 
 // the stream (if it was launched with programmatic serialization) be
 // scheduled before this one ends; wait blocks until every prerequisite grid
 // has completed and its memory is visible, so it must precede this kernel's
-// first global-memory access.
+// first global-memory access.  (One kernel begins without it: grad_w beside grad_x, which
+// triggers after its own wait; see kOverlapSecond in linear.cuh.)
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
