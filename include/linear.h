@@ -68,9 +68,10 @@ typedef struct {
 
 /* For tests and measurements; NULL, or all zero, chooses.  `tile` not 0: the call's
  * products take the form of these three (see linear_config_t; one that there is
- * not is GEMM_ERR_INVALID_VALUE).  timeout_ns: the limit of a wait in the
- * kernels, 0: 2 s.  inject = 1: the first stage of every CTA is never loaded, so
- * that a wait runs out, the results are undefined and the error word is set. */
+ * not is GEMM_ERR_INVALID_VALUE).  timeout_ns: the limit of a wait in the kernels,
+ * 0: 2 s, and 1 us for each 64 elements of a product's sums.  inject = 1: the first
+ * stage of every CTA is never loaded, so that a wait runs out, the results are
+ * undefined and the error word is set. */
 typedef struct {
   int cta_pair, tile, split_k;
   int inject;

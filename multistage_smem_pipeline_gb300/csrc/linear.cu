@@ -10,7 +10,9 @@
 namespace gb300 {
 namespace {
 
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+// The limit of a wait that the caller leaves open.  One CTA takes 0.2 us for 64 of a sum, and some
+// waits are for a whole sum: that of 2^30 rows of one expert takes 3.3 s.
+constexpr uint64_t kTimeoutNs = 2000000000ull, kTimeoutNsPerBlock = 1000;
 
 // ------------------------------------------------------------------ checks
 bool in_range(int64_t v, int64_t most) { return v >= 0 && v <= most; }
@@ -395,7 +397,9 @@ int launch(const Product& pr, const Plan& plan, const Rows& a, const Rows& b, Li
   p.box_rows = plan.box_rows;
   p.split = plan.split;
   p.inject = opt ? opt->inject : 0;
-  p.timeout_ns = opt && opt->timeout_ns ? opt->timeout_ns : kTimeoutNs;
+  p.timeout_ns = opt && opt->timeout_ns
+                     ? opt->timeout_ns
+                     : kTimeoutNs + kTimeoutNsPerBlock * static_cast<uint64_t>(pr.k / kLinK);
   p.error_word = error_index(s);
   Maps m;
   std::memset(&m, 0, sizeof(m));
