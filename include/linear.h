@@ -62,7 +62,7 @@ typedef struct {
    * tokens * top_k, and expert e has its own out x in weights (and `out` biases),
    * one expert's after the other's: expert e's begin at row e * out.  Of the
    * routing the offsets are read alone.  Rows past the last offset are in no
-   * expert: they give zeros and are not read otherwise. */
+   * expert: they give zeros, and their values affect nothing. */
   const moe_routing_t* routing;
 } linear_t;
 

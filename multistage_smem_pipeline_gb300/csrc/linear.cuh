@@ -519,8 +519,8 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 // P(Z <= z) of a standard normal Z.  Below 0
 // it is e^(-z^2/2) f(|z|) with f(s) = erfcx(s / sqrt 2) / 2, here a polynomial in
 // t = 1 / (1 + 0.3 s) that was fitted to f by weighted least squares (relative
-// error 1.5e-7 for s up to 14, 4.7e-7 as evaluated in fp32): a subtraction from 1
-// would have no accuracy left there.
+// error 1.5e-7 for s up to 14, 4.7e-7 as evaluated in fp32; the whole has up to 2e-5
+// at -13, by the exponential's argument): a subtraction from 1 would have no accuracy left there.
 __device__ __forceinline__ float normal(float z) {
   const float s = fabsf(z), t = rcp_ftz(fmaf(0.3f, s, 1.0f));
   float f = 0.035674453f;

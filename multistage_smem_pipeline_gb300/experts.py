@@ -13,7 +13,8 @@ In 16 bits, with gradients:
     h = moe_linear(moe_dispatch(x, routing), routing, w, bias, activation="gelu")
     y = linear(x, w, bias, residual=x)                  # dense
 
-Tensors given as `out` are written in place; without it one is allocated.
+Tensors given as `out` are written in place; without it one is allocated.  The calls record no
+gradients, whatever their inputs require: the package's moe_example has them as autograd functions.
 """
 from __future__ import annotations
 
